@@ -11,6 +11,12 @@
  *   attn_decode_paged_append  kv_store of the new rows + attn_decode_paged, fused
  *   attn_prefill_varlen_append  kv_store of the new rows + attn_prefill_varlen, fused
  *   attn_mixed_step      a step of prefill chunks and decode rows, the two side by side
+ *   attn_shared_plan, attn_decode_shared, attn_decode_shared_append
+ *                        decode of a batch whose sequences share leading pages,
+ *                        every shared page read once for all of them
+ *   kv_pages_fork, kv_pages_extend, kv_pages_compact
+ *                        block tables, reference counts and pages handled on
+ *                        the device: fork / reorder / free, grow, compact
  *
  * Sources: "nano-vLLM-1" (Senjl's Digital Garden), ModelRunner sections
  * "3. KV cache 分配", "4. prefill 输入打包", "5. deocde 输入打包" and BlockManager
@@ -399,6 +405,189 @@ int attn_decode_paged_noalloc(const kvp_bf16 *q, int64_t q_stride_tok, const kvp
                               const int32_t *context_lens, int num_seqs, int max_context_len,
                               int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
                               kvp_bf16 *out, int64_t out_stride_tok, kvp_stream_t stream);
+
+/*
+ * attn_shared_plan - finds the leading pages that the sequences of a decode
+ * batch share, for attn_decode_shared / attn_decode_shared_append.
+ *
+ * Prefix-cache hits and forked sequences map their first logical blocks to
+ * the same physical blocks ("【nano-vllm 学习】04 - 自顶向下的引擎调度层源码学习2",
+ * section "场景优化1：Parallel Memory Shared").  Sequences b - 1 and b share
+ * the leading entries in which their block-table rows agree, up to (not
+ * including) the block of either sequence's last token.  A group is a maximal
+ * run of neighbours that share at least min_shared_len tokens (and at least
+ * half of what the next pair on either side shares); its prefix is what all
+ * of its members share.  Sharing is found by comparing block ids, so the
+ * attention's result is that of attn_decode_paged for any tables; batches
+ * gain when sequences with a common prefix are neighbours.
+ *
+ *   block_tables     [num_seqs, max_blocks_per_seq] int32
+ *   context_lens     [num_seqs] int32 (0: padding row); a length outside
+ *                    [0, max_blocks_per_seq * block_size] is clamped and
+ *                    records KVP_ERR_DEVICE_DATA
+ *   min_shared_len   tokens (0: the library's default, 128)
+ *   plan             device buffer of at least attn_shared_plan_size() bytes,
+ *                    16-byte aligned.  It holds the step's context lengths
+ *                    too: one plan serves every layer of the step, and the
+ *                    next step needs a new one.
+ * Supported: num_heads / num_kv_heads in {1, 2, 4, 8}, num_kv_heads in
+ * {1, 2, 4, 8}; block_size 16 * 2^k (16..4096); num_seqs < 2^20.
+ * num_seqs == 0 is a no-op.
+ */
+size_t attn_shared_plan_size(int num_seqs, int num_heads, int num_kv_heads);
+
+int attn_shared_plan(const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int num_seqs, int64_t num_blocks, int block_size,
+                     int num_heads, int num_kv_heads, int min_shared_len, void *plan,
+                     size_t plan_bytes, kvp_stream_t stream);
+
+/* Bytes of device workspace the two attention calls below need for this
+ * shape on the current device (0 on error; see kvp_last_error). */
+size_t attn_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                         int head_dim);
+
+/*
+ * attn_decode_shared - attn_decode_paged over a planned batch: one query
+ * token per sequence, every group's shared prefix read once for the whole
+ * group.
+ *
+ * Arguments as attn_decode_paged, with the context lengths taken from `plan`:
+ * the buffer that attn_shared_plan filled, earlier on the stream, from the
+ * same block_tables for the same num_seqs, num_heads, num_kv_heads,
+ * block_size and max_blocks_per_seq.  A plan made for another shape records
+ * KVP_ERR_DEVICE_DATA and nothing is written.
+ *   workspace   device scratch of at least attn_decode_shared_workspace_size()
+ *               bytes, 16-byte aligned, garbage afterwards; two calls that run
+ *               at the same time must not share one (they may share a plan)
+ * Supported: as attn_shared_plan, head_dim in {64, 128}, fewer than 2^31
+ * slots in the pool.
+ */
+int attn_decode_shared(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k_cache,
+                       const kvp_bf16 *v_cache, int64_t num_blocks, int block_size,
+                       const int32_t *block_tables, int max_blocks_per_seq, const void *plan,
+                       size_t plan_bytes, int num_seqs, int num_heads, int num_kv_heads,
+                       int head_dim, float softmax_scale, void *workspace, size_t workspace_bytes,
+                       kvp_bf16 *out, int64_t out_stride_tok, kvp_stream_t stream);
+
+/*
+ * attn_decode_shared_append - kv_store of the step's new rows and
+ * attn_decode_shared in one call, as attn_decode_paged_append is to
+ * attn_decode_paged (same k, v and slot_mapping, same requirements: the slot
+ * of a sequence's last context token, and no sequence reads another one's new
+ * slot; a slot that is not that token's records KVP_ERR_DEVICE_DATA).
+ */
+int attn_decode_shared_append(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k,
+                              const kvp_bf16 *v, int64_t k_stride_tok, int64_t v_stride_tok,
+                              const int32_t *slot_mapping, kvp_bf16 *k_cache, kvp_bf16 *v_cache,
+                              int64_t num_blocks, int block_size, const int32_t *block_tables,
+                              int max_blocks_per_seq, const void *plan, size_t plan_bytes,
+                              int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                              float softmax_scale, void *workspace, size_t workspace_bytes,
+                              kvp_bf16 *out, int64_t out_stride_tok, kvp_stream_t stream);
+
+/*
+ * Pages on the device.  The three calls below keep a pool's bookkeeping in
+ * device memory, for loops that decide on the device which sequence goes on
+ * (parallel sampling, beam search) or replay CUDA graphs:
+ *
+ *   block_tables  [num_rows, max_blocks_per_seq] int32; row r's pages are its
+ *                 first ceil(context_lens[r] / block_size) entries, the others
+ *                 are not read.  Output tables hold -1 there.
+ *   context_lens  [num_rows] int32, 0 = empty row
+ *   ref_counts    [num_blocks] int32: how many rows (or other holders, e.g. a
+ *                 kept prefix) use a page; 0 = free
+ *
+ * Free pages are taken lowest id first, rows are served in order, so results
+ * are deterministic.  Lengths outside [0, max_blocks_per_seq * block_size]
+ * make a row empty, page ids outside [0, num_blocks) are dropped; both record
+ * KVP_ERR_DEVICE_DATA, as does a pool without enough free pages.  Outputs are
+ * separate arrays that must not overlap the inputs (except as noted).
+ *   workspace     device scratch of kv_pages_workspace_size(num_blocks, rows)
+ *                 bytes (rows: the larger of num_rows and num_out), 16-byte
+ *                 aligned, garbage afterwards; not shared by calls that run at
+ *                 the same time
+ * num_blocks * block_size must be below 2^31 and num_rows, num_out below 2^20.
+ */
+size_t kv_pages_workspace_size(int64_t num_blocks, int num_rows);
+
+/*
+ * kv_pages_fork - new rows made from old ones: fork, reorder, free.
+ *
+ * New row r < num_out continues old row parents[r] (-1: an empty row); the
+ * old rows end.  Reference counts change accordingly: every page of an old
+ * row loses one holder, every page of a new row gains one, and pages left
+ * without a holder become free (their contents stay).  So parents = identity
+ * with one entry -1 frees a row, a repeated parent forks it, a beam step
+ * reorders rows.
+ * An unfilled last page (context_lens % block_size != 0) that several new
+ * rows would write to is copied ("场景优化1：Parallel Memory Shared", copy on
+ * write): the lowest such row keeps the page, each other one gets a free page
+ * of its own with the filled tokens copied in every plane.  A row that finds
+ * no free page becomes empty and records KVP_ERR_DEVICE_DATA.  An unfilled
+ * last page must have no holders besides the rows of block_tables.
+ *
+ *   cache, num_planes, plane_stride   as kv_copy_blocks, with
+ *                 block_elems = block_size * row_elems (row_elems =
+ *                 num_kv_heads * head_dim)
+ *   parents       [num_out] int32 in [-1, num_rows); others act as -1 and
+ *                 record KVP_ERR_DEVICE_DATA
+ *   out_tables [num_out, max_blocks_per_seq], out_context_lens [num_out],
+ *   out_ref_counts [num_blocks]
+ */
+int kv_pages_fork(kvp_bf16 *cache, int64_t num_planes, int64_t plane_stride, int64_t num_blocks,
+                  int block_size, int64_t row_elems, const int32_t *block_tables,
+                  int max_blocks_per_seq, const int32_t *context_lens, int num_rows,
+                  const int32_t *ref_counts, const int32_t *parents, int num_out,
+                  int32_t *out_tables, int32_t *out_context_lens, int32_t *out_ref_counts,
+                  void *workspace, size_t workspace_bytes, kvp_stream_t stream);
+
+/*
+ * kv_pages_extend - room for new tokens: row r grows by new_tokens[r] (>= 0).
+ *
+ * Each row gets the pages that its new length needs, its new length, and the
+ * cache slots of its new tokens, which slot_mapping lists row after row (the
+ * form kv_store, attn_decode_shared_append and the prefill calls take).
+ * Entries of slot_mapping past the last new token are -1.
+ * A row that cannot grow keeps its length, takes -1 for its slots, and
+ * records KVP_ERR_DEVICE_DATA: when the free pages run out before its turn
+ * ends (then no later row gets pages either), when its last page is unfilled
+ * and has other holders, or when the new length does not fit its table row
+ * (such a row takes no slots at all).
+ *
+ *   new_tokens    [num_rows] int32
+ *   num_slots     entries of slot_mapping; the new tokens' total, or more
+ *                 (fewer: the slots past the end are not written, and
+ *                 KVP_ERR_DEVICE_DATA is recorded)
+ *   out_tables, out_context_lens, out_ref_counts   may each be the
+ *                 corresponding input itself (an update in place)
+ */
+int kv_pages_extend(const int32_t *block_tables, int max_blocks_per_seq,
+                    const int32_t *context_lens, int num_rows, const int32_t *ref_counts,
+                    int64_t num_blocks, int block_size, const int32_t *new_tokens,
+                    int64_t num_slots, int32_t *out_tables, int32_t *out_context_lens,
+                    int32_t *out_ref_counts, int32_t *slot_mapping, void *workspace,
+                    size_t workspace_bytes, kvp_stream_t stream);
+
+/*
+ * kv_pages_compact - moves the pages in use to the front of the pool.
+ *
+ * With n pages in use (ref_counts > 0), the k-th page in use with an id >= n
+ * moves to the k-th free page with an id < n, in every plane; afterwards the
+ * pages in use are exactly 0 .. n - 1 and the rest of the pool can be given
+ * back or used in one piece.  Tables and reference counts follow.
+ *
+ *   out_tables      [num_rows, max_blocks_per_seq]
+ *   out_ref_counts  [num_blocks]
+ *   places          [num_blocks] int32: the new id of each page that was in
+ *                   use, -1 for free ones (for holders outside block_tables)
+ * A row that lists a free page gets -1 there and records KVP_ERR_DEVICE_DATA.
+ */
+int kv_pages_compact(kvp_bf16 *cache, int64_t num_planes, int64_t plane_stride, int64_t num_blocks,
+                     int block_size, int64_t row_elems, const int32_t *block_tables,
+                     int max_blocks_per_seq, const int32_t *context_lens, int num_rows,
+                     const int32_t *ref_counts, int32_t *out_tables, int32_t *out_ref_counts,
+                     int32_t *places, void *workspace, size_t workspace_bytes,
+                     kvp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -12,6 +12,8 @@ PyTorch fallback: if the library cannot be loaded, every call raises.
     attn_prefill_varlen(q, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, ...)
     attn_prefill_varlen_append(q, k, v, slot_mapping, cu_seqlens_q, cu_seqlens_k, ...)
     attn_decode_paged(q, k_cache, v_cache, block_tables, context_lens, max_context_len, ...)
+    attn_shared_plan(block_tables, context_lens, ...) + attn_decode_shared(q, ..., plan)
+    kv_pages_fork / kv_pages_extend / kv_pages_compact(..., block_tables, context_lens, ref_counts, ...)
 """
 from __future__ import annotations
 
@@ -24,6 +26,9 @@ __all__ = ["kv_store", "kv_copy_blocks", "attn_prefill_varlen", "attn_prefill_va
            "attn_mixed_step",
            "attn_decode_paged", "attn_decode_workspace_size", "attn_decode_paged_noalloc",
            "attn_decode_paged_append",
+           "attn_shared_plan", "attn_shared_plan_size", "attn_decode_shared",
+           "attn_decode_shared_append", "attn_decode_shared_workspace_size",
+           "kv_pages_fork", "kv_pages_extend", "kv_pages_compact", "kv_pages_workspace_size",
            "device_status", "selftest_wait", "library", "library_path", "KvpError"]
 
 _LIB_LOCK = threading.Lock()
@@ -58,6 +63,20 @@ SIGNATURES = {
     "attn_mixed_step": (_I32, [_P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I32, _P, _I32, _P, _P,
                                _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P, _SZ, _P, _I64,
                                _P]),
+    "attn_shared_plan_size": (_SZ, [_I32, _I32, _I32]),
+    "attn_shared_plan": (_I32, [_P, _I32, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
+    "attn_decode_shared_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "attn_decode_shared": (_I32, [_P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _SZ, _I32, _I32, _I32,
+                                  _I32, _F32, _P, _SZ, _P, _I64, _P]),
+    "attn_decode_shared_append": (_I32, [_P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _I32,
+                                         _P, _SZ, _I32, _I32, _I32, _I32, _F32, _P, _SZ, _P, _I64, _P]),
+    "kv_pages_workspace_size": (_SZ, [_I64, _I32]),
+    "kv_pages_fork": (_I32, [_P, _I64, _I64, _I64, _I32, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _P, _P,
+                             _P, _P, _SZ, _P]),
+    "kv_pages_extend": (_I32, [_P, _I32, _P, _I32, _P, _I64, _I32, _P, _I64, _P, _P, _P, _P, _P, _SZ,
+                               _P]),
+    "kv_pages_compact": (_I32, [_P, _I64, _I64, _I64, _I32, _I64, _P, _I32, _P, _I32, _P, _P, _P, _P,
+                                _P, _SZ, _P]),
 }
 
 
@@ -437,3 +456,236 @@ def attn_mixed_step(q, k, v, slot_mapping, cu_seqlens_q, cu_seqlens_k, max_seqle
         int(max_seqlen_k), nseq, int(num_decode_seqs), int(decode_sms), hq, hkv, d, scale, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(out), os_, _stream(q)))
     return out
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on the tensors' device and its current stream."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _sized(fn, device, *args) -> int:
+    """A size query of the library (on `device` where it matters)."""
+    import torch
+    if device is None or device.index == torch.cuda.current_device():
+        n = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            n = fn(*args)
+    if n == 0:
+        _check(-1)
+    return int(n)
+
+
+def _int32(t, name, shape, device):
+    import torch
+    _require(t, name, torch.int32, len(shape), device)
+    if any(w is not None and n != w for n, w in zip(t.shape, shape)) or not t.is_contiguous():
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must be contiguous [{want}], got {tuple(t.shape)}")
+
+
+def _scratch(t, name, nbytes, device):
+    """The caller's buffer, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    _require(t, name, torch.uint8, 1, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def attn_shared_plan_size(num_seqs: int, num_heads: int, num_kv_heads: int) -> int:
+    return _sized(library().attn_shared_plan_size, None, num_seqs, num_heads, num_kv_heads)
+
+
+def attn_shared_plan(block_tables, context_lens, block_size: int, num_heads: int, num_kv_heads: int,
+                     num_blocks: int, min_shared_len: int = 0, plan=None):
+    """Finds the leading pages that neighbouring sequences of a decode batch
+    share (see include/kvpaged.h) and returns the plan, a uint8 device tensor
+    that attn_decode_shared / attn_decode_shared_append of every layer of this
+    step take.  ``plan``: a buffer to fill (attn_shared_plan_size bytes)."""
+    import torch
+    _require(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
+    b = block_tables.shape[0]
+    _int32(block_tables, "block_tables", (b, None), dev)
+    _int32(context_lens, "context_lens", (b,), dev)
+    plan = _scratch(plan, "plan", attn_shared_plan_size(b, num_heads, num_kv_heads), dev)
+    _call(dev, library().attn_shared_plan, block_tables.data_ptr(), block_tables.shape[1],
+          context_lens.data_ptr(), b, num_blocks, block_size, num_heads, num_kv_heads, min_shared_len,
+          plan.data_ptr(), plan.numel())
+    return plan
+
+
+def attn_decode_shared_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                      device=None) -> int:
+    return _sized(library().attn_decode_shared_workspace_size, device, num_seqs, num_heads,
+                  num_kv_heads, head_dim)
+
+
+def _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale, workspace, out):
+    """Checks what attn_decode_shared and its append form have in common;
+    -> (device, [q, stride], [caches .. plan], [shape .. out])."""
+    import torch
+    nb, bs, hkv, d = _cache_dims(k_cache, v_cache)
+    dev = k_cache.device
+    _require(q, "q", torch.bfloat16, 3, dev)
+    b, hq = q.shape[0], q.shape[1]
+    qs = _rows(q, "q", hq, d)
+    _int32(block_tables, "block_tables", (b, None), dev)
+    _require(plan, "plan", torch.uint8, 1, dev)
+    if not plan.is_contiguous():
+        raise ValueError("plan must be contiguous")
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=dev)
+    _require(out, "out", torch.bfloat16, 3, dev)
+    if out.shape[0] != b:
+        raise ValueError("out must have one row per sequence")
+    os_ = _rows(out, "out", hq, d)
+    if workspace is None:
+        workspace = torch.empty((attn_decode_shared_workspace_size(b, hq, hkv, d, dev),),
+                                dtype=torch.uint8, device=dev)
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    return (dev, out, (q.data_ptr(), qs),
+            (k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, block_tables.data_ptr(),
+             block_tables.shape[1], plan.data_ptr(), plan.numel(), b, hq, hkv, d, scale,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(), os_))
+
+
+def attn_decode_shared(q, k_cache, v_cache, block_tables, plan, softmax_scale: float | None = None,
+                       workspace=None, out=None):
+    """attn_decode_paged over a batch planned by attn_shared_plan (which has
+    the context lengths): the pages that a group of neighbouring sequences
+    share are read once for the group."""
+    dev, out, qa, rest = _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale, workspace,
+                                      out)
+    _call(dev, library().attn_decode_shared, *qa, *rest)
+    return out
+
+
+def attn_decode_shared_append(q, k, v, slot_mapping, k_cache, v_cache, block_tables, plan,
+                              softmax_scale: float | None = None, workspace=None, out=None):
+    """kv_store(k, v, slot_mapping, k_cache, v_cache) followed by
+    attn_decode_shared, in one call (see include/kvpaged.h).  Row b of k / v
+    is sequence b's new token, stored at slot_mapping[b]."""
+    import torch
+    dev, out, qa, rest = _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale, workspace,
+                                      out)
+    _require(k, "k", torch.bfloat16, 3, dev)
+    _require(v, "v", torch.bfloat16, 3, dev)
+    b, hkv, d = q.shape[0], k_cache.shape[2], k_cache.shape[3]
+    ks, vs = _rows(k, "k", hkv, d), _rows(v, "v", hkv, d)
+    if k.shape[0] != b or v.shape[0] != b:
+        raise ValueError("k and v must have one row per sequence")
+    _int32(slot_mapping, "slot_mapping", (b,), dev)
+    _call(dev, library().attn_decode_shared_append, *qa, k.data_ptr(), v.data_ptr(), ks, vs,
+          slot_mapping.data_ptr(), *rest)
+    return out
+
+
+def kv_pages_workspace_size(num_blocks: int, num_rows: int) -> int:
+    return _sized(library().kv_pages_workspace_size, None, num_blocks, num_rows)
+
+
+def _pool_dims(kv_cache):
+    """[..., num_blocks, block_size, num_kv_heads, head_dim] -> planes, plane
+    stride, num_blocks, block_size, row elements."""
+    import torch
+    if not isinstance(kv_cache, torch.Tensor):
+        raise TypeError("kv_cache must be a torch.Tensor")
+    if kv_cache.dtype != torch.bfloat16 or not kv_cache.is_cuda or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous bf16 CUDA tensor")
+    if kv_cache.dim() < 4:
+        raise ValueError("kv_cache must be [..., num_blocks, block_size, num_kv_heads, head_dim]")
+    nb, bs, hkv, d = kv_cache.shape[-4:]
+    plane = nb * bs * hkv * d
+    return kv_cache.numel() // max(plane, 1), plane, nb, bs, hkv * d
+
+
+def _page_rows(block_tables, context_lens, ref_counts, num_blocks, dev):
+    n = block_tables.shape[0]
+    _int32(context_lens, "context_lens", (n,), dev)
+    _int32(ref_counts, "ref_counts", (num_blocks,), dev)
+    return n, block_tables.shape[1]
+
+
+def kv_pages_fork(kv_cache, block_tables, context_lens, ref_counts, parents, workspace=None, out=None):
+    """New rows from old ones: fork, reorder, free (see include/kvpaged.h).
+    Row r of the result continues row parents[r] (-1: an empty row); an
+    unfilled last page that several rows would write to is copied in every
+    plane of ``kv_cache``.  Returns (block_tables, context_lens, ref_counts):
+    new tensors, or ``out``, three tensors that do not overlap the inputs."""
+    import torch
+    planes, stride, nb, bs, row = _pool_dims(kv_cache)
+    dev = kv_cache.device
+    _int32(block_tables, "block_tables", (None, None), dev)
+    n, mb = _page_rows(block_tables, context_lens, ref_counts, nb, dev)
+    _int32(parents, "parents", (None,), dev)
+    m = parents.shape[0]
+    if out is None:
+        out = (torch.empty((m, mb), dtype=torch.int32, device=dev),
+               torch.empty((m,), dtype=torch.int32, device=dev), torch.empty_like(ref_counts))
+    for t, name, shape in zip(out, ("out tables", "out context_lens", "out ref_counts"),
+                              ((m, mb), (m,), (nb,))):
+        _int32(t, name, shape, dev)
+    ws = _scratch(workspace, "workspace", kv_pages_workspace_size(nb, max(n, m)), dev)
+    _call(dev, library().kv_pages_fork, kv_cache.data_ptr(), planes, stride, nb, bs, row,
+          block_tables.data_ptr(), mb, context_lens.data_ptr(), n, ref_counts.data_ptr(),
+          parents.data_ptr(), m, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return tuple(out)
+
+
+def kv_pages_extend(block_tables, context_lens, ref_counts, new_tokens, block_size: int, num_slots: int,
+                    workspace=None, out=None):
+    """Room for new_tokens[r] more tokens in each row (see
+    include/kvpaged.h).  Returns (block_tables, context_lens, ref_counts,
+    slot_mapping), slot_mapping [num_slots] holding the new tokens' slots row
+    after row, then -1.  ``out``: those four tensors; the first three may be
+    the inputs themselves."""
+    import torch
+    _require(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
+    _int32(block_tables, "block_tables", (None, None), dev)
+    _require(ref_counts, "ref_counts", torch.int32, 1, dev)
+    nb = ref_counts.shape[0]
+    n, mb = _page_rows(block_tables, context_lens, ref_counts, nb, dev)
+    _int32(new_tokens, "new_tokens", (n,), dev)
+    if out is None:
+        out = (torch.empty_like(block_tables), torch.empty_like(context_lens),
+               torch.empty_like(ref_counts), torch.empty((num_slots,), dtype=torch.int32, device=dev))
+    for t, name, shape in zip(out, ("out tables", "out context_lens", "out ref_counts", "slot_mapping"),
+                              ((n, mb), (n,), (nb,), (num_slots,))):
+        _int32(t, name, shape, dev)
+    ws = _scratch(workspace, "workspace", kv_pages_workspace_size(nb, n), dev)
+    _call(dev, library().kv_pages_extend, block_tables.data_ptr(), mb, context_lens.data_ptr(), n,
+          ref_counts.data_ptr(), nb, block_size, new_tokens.data_ptr(), num_slots, out[0].data_ptr(),
+          out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), ws.data_ptr(), ws.numel())
+    return tuple(out)
+
+
+def kv_pages_compact(kv_cache, block_tables, context_lens, ref_counts, workspace=None, out=None):
+    """Moves the pages in use to the front of the pool, in every plane of
+    ``kv_cache`` (see include/kvpaged.h).  Returns (block_tables, ref_counts,
+    places), places[p] being the new id of page p (-1 if it was free): new
+    tensors, or ``out``, three tensors that do not overlap the inputs."""
+    import torch
+    planes, stride, nb, bs, row = _pool_dims(kv_cache)
+    dev = kv_cache.device
+    _int32(block_tables, "block_tables", (None, None), dev)
+    n, mb = _page_rows(block_tables, context_lens, ref_counts, nb, dev)
+    if out is None:
+        out = (torch.empty_like(block_tables), torch.empty_like(ref_counts), torch.empty_like(ref_counts))
+    for t, name, shape in zip(out, ("out tables", "out ref_counts", "places"), ((n, mb), (nb,), (nb,))):
+        _int32(t, name, shape, dev)
+    ws = _scratch(workspace, "workspace", kv_pages_workspace_size(nb, n), dev)
+    _call(dev, library().kv_pages_compact, kv_cache.data_ptr(), planes, stride, nb, bs, row,
+          block_tables.data_ptr(), mb, context_lens.data_ptr(), n, ref_counts.data_ptr(),
+          out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel())
+    return tuple(out)

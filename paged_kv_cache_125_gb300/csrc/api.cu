@@ -119,6 +119,11 @@ int device_sm_count(int* num_sms) {
   return device_info(&dev, &status, num_sms);
 }
 
+int device_handles(int** status, int* num_sms) {
+  int dev;
+  return device_info(&dev, status, num_sms);
+}
+
 }  // namespace kvp
 
 extern "C" {

@@ -1,0 +1,66 @@
+// Internal interface of the shared-prefix decode (decode_shared.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kvp_internal.h"
+
+namespace kvp {
+
+// The plan buffer of attn_shared_plan: what the attention calls of one step
+// need to know about the batch, for num_seqs = B sequences.
+struct SharedPlanHead {
+  int magic, num_seqs, group, num_kv_heads;  // the shape the plan was made for
+  int block_size, max_blocks, num_tiles, pad;
+  long long steps;   // prefix steps of 128 keys of all tiles (per kv head)
+  long long tokens;  // suffix tokens of all sequences
+};
+
+struct SharedPlan {
+  SharedPlanHead* head;
+  long long* cum_tokens;  // [B + 1] suffix tokens of the sequences before b
+  long long* cum_steps;   // [B + 1] prefix steps of the tiles before t
+  int* ctx;               // [B] context length (0: no row)
+  int* prefix;            // [B] keys read with the group, [0, prefix)
+  int* tile_of;           // [B] tile of sequence b, or -1 (prefix 0)
+  int* tile_seq;          // [B + 1] first sequence of tile t
+  int* cum_rows;          // [B + 1] sequences in the tiles before t
+  int* same;              // [B] plan kernel: leading pages shared with sequence b - 1
+  int* group_min;         // [B] plan kernel: fewest of them in a group
+  int* group_seq;         // [B] plan kernel: first sequence of a group
+};
+
+size_t shared_plan_bytes(int num_seqs);
+SharedPlan shared_plan_view(void* base, int num_seqs);
+
+cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, const int32_t* ctx,
+                               int num_seqs, int64_t num_blocks, int block_size, int group,
+                               int num_kv_heads, int min_shared_len, const SharedPlan& plan,
+                               int* status, cudaStream_t stream);
+
+size_t shared_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                              int num_sms);
+
+struct SharedCall {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  int64_t num_blocks;
+  int block_size;
+  const int32_t* block_tables;
+  int max_blocks;
+  int num_seqs, num_heads, num_kv_heads, head_dim;
+  float softmax_scale;
+  void* workspace;
+  uint16_t* out;
+  int64_t out_stride;
+};
+// app: the step's new rows, stored by the same call (or null).
+cudaError_t launch_decode_shared(const SharedCall& c, const SharedPlan& plan,
+                                 const DecodeAppend* app, int num_sms, int* status,
+                                 cudaStream_t stream);
+
+}  // namespace kvp

@@ -21,6 +21,8 @@ int check_decode_args(const char* fn, const kvp_bf16* q, int64_t q_stride_tok,
                       int num_heads, int num_kv_heads, int head_dim, const kvp_bf16* out,
                       int64_t out_stride_tok);
 int device_sm_count(int* num_sms);
+// api.cu: the current device's status word (device address) and SM count.
+int device_handles(int** status, int* num_sms);
 
 // selftest.cu: one thread waits on a barrier (arrive: after arriving on it
 // itself; else nothing arrives and the 2 ms wait expires).

@@ -1,0 +1,369 @@
+"""attn_shared_plan + attn_decode_shared (+ _append) against the fp64 oracle.
+
+The oracle attends every sequence over its own table row; the calls must give
+the same whatever pages the rows share.  Tolerance, element by element, with A
+= sum_i p_i |v_i| / sum_i p_i (the oracle's decode of the caches with |V|):
+
+  output rounded to bf16                      eps / 2 * |ref| = 2^-8 |ref|
+  weights p rounded to bf16 before P V        2^-8 A
+  scores in fp32: d = 128 products, each sum within (d + 2) 2^-24 * scale *
+  sum |q k| of the exact one (< 10 here): 8e-5, on p and on the sum l; exp2
+  within 2^-21; l and P V summed in fp32 over at most 2^13 keys a part, 2^13 *
+  2^-24 = 2^-11 each: together below                 2^-9 A
+
+so |out - ref| <= 2^-8 |ref| (1 + 2^-6) + (2^-8 + 2^-9) A."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_cache_125_gb300 as kvp
+
+from pages_reference import ceil, shared_prefixes
+from parity import assert_status_ok, u16
+
+pytestmark = pytest.mark.gpu
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+class Batch:
+    """groups: (prefix pages, [own tokens of each member]); a prefix of 0
+    pages makes a sequence of its own; own tokens 0 with prefix 0: padding."""
+
+    def __init__(self, heads, bs, groups, seed, poison=True, extra=3):
+        self.hq, self.hkv, self.d = heads
+        self.bs = bs
+        rng = np.random.default_rng(seed)
+        rows, need = [], 0
+        for prefix, own in groups:
+            shared = list(range(need, need + prefix))
+            need += prefix
+            for n in own:
+                pages = ceil(n, bs)
+                rows.append((shared + list(range(need, need + pages)), prefix * bs + n))
+                need += pages
+        self.nb = need + extra
+        ids = rng.permutation(self.nb)
+        self.b = len(rows)
+        width = max([len(r) for r, _ in rows] + [1])
+        self.tables = np.full((self.b, width), -1, np.int32)
+        for i, (r, _) in enumerate(rows):
+            self.tables[i, :len(r)] = ids[r]
+        self.lens = np.array([n for _, n in rows], np.int32)
+        self.slots = np.array([-1 if n == 0 else self.tables[i, (n - 1) // bs] * bs + (n - 1) % bs
+                               for i, n in enumerate(self.lens)], np.int32)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        shape = (self.nb, bs, self.hkv, self.d)
+        self.kc, self.vc = (torch.randn(shape, generator=g, device="cuda").to(BF16) for _ in range(2))
+        if poison:  # everything no sequence may read
+            used = np.zeros((self.nb, bs), bool)
+            for i, n in enumerate(self.lens):
+                for p in range(n):
+                    used[self.tables[i, p // bs], p % bs] = True
+            free = torch.from_numpy(~used).cuda()
+            self.kc[free] = float("nan")
+            self.vc[free] = float("nan")
+            self.vc.view(-1, self.hkv, self.d)[(~torch.from_numpy(used).view(-1)).nonzero()[::2, 0].cuda()] = float("inf")
+        self.q = torch.randn((self.b, self.hq, self.d), generator=g, device="cuda").to(BF16)
+        self.k, self.v = (torch.randn((self.b, self.hkv, self.d), generator=g, device="cuda").to(BF16)
+                          for _ in range(2))
+        self.scale = 1.0 / math.sqrt(self.d)
+
+    def dev(self, a):
+        return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+    def plan(self, min_shared=0):
+        return kvp.attn_shared_plan(self.dev(self.tables), self.dev(self.lens), self.bs, self.hq, self.hkv,
+                                    self.nb, min_shared)
+
+    def reference(self, kc=None, vc=None):
+        """-> (ref, A) of the caches as they are."""
+        k, v = u16(self.kc if kc is None else kc), u16(self.vc if vc is None else vc)
+        args = (torch.from_numpy(self.tables), torch.from_numpy(self.lens), self.hq, self.hkv, self.scale)
+        return oracle.decode(self.q.cpu(), k, v, *args), oracle.decode(self.q.cpu(), k, v & 0x7FFF, *args)
+
+    def check(self, out, ref, what=""):
+        ref, a = ref
+        got = out.float().cpu().double().numpy()
+        assert np.isfinite(got).all(), f"{what}: non-finite output"
+        tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -6) + (2.0 ** -8 + 2.0 ** -9) * np.abs(a)
+        worst = float((np.abs(got - ref) - tol).max(initial=-1.0))
+        assert worst <= 0, f"{what}: {worst} past the tolerance"
+        assert not got[self.lens == 0].any(), f"{what}: rows without context are not zero"
+
+
+def plan_prefixes(plan, b):
+    """The prefix lengths in a plan, at their place in its layout."""
+    raw = plan.cpu().numpy().tobytes()
+    head = 8 * 4 + 2 * 8
+    return np.frombuffer(raw, np.int32, b, head + 16 * (b + 1) + 4 * b).tolist()
+
+
+HEADS = [(2, 1, 64), (4, 2, 64), (16, 8, 64), (8, 1, 128), (4, 4, 128), (8, 8, 128), (16, 8, 128),
+         (32, 8, 128), (64, 8, 128)]
+SHAPES = {
+    "two": [(16, [1, 7])],
+    "one_token_each": [(8, [1, 1, 1])],
+    "alone": [(0, [1]), (0, [300]), (0, [17])],
+    "odd": [(9, [5, 40, 33]), (0, [129]), (11, [16, 17]), (0, [0]), (25, [3, 2, 1, 250])],
+    "padding": [(0, [0]), (12, [20, 50]), (0, [0, 0])],
+    "many": [(8 + i, [1 + (7 * i + 3 * j) % 90 for j in range(2 + i % 5)]) for i in range(14)],
+    "tall": [(13, [1 + (5 * i) % 37 for i in range(150)])],
+}
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "%d/%d/%d" % h)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_matches_oracle(heads, shape):
+    w = Batch(heads, 16, SHAPES[shape], seed=len(shape) + heads[0])
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(out, w.reference(), shape)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256, 512])
+def test_block_sizes(bs):
+    groups = [(ceil(400, bs), [1, bs, bs + 1, 3]), (0, [2 * bs + 5]), (ceil(1000, bs), [7, 200])]
+    for heads in ((16, 8, 128), (4, 2, 64)):
+        w = Batch(heads, bs, groups, seed=bs)
+        out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+        torch.cuda.synchronize()
+        assert_status_ok()
+        w.check(out, w.reference(), f"bs {bs}")
+
+
+@pytest.mark.parametrize("heads", [(16, 8, 128), (32, 8, 128), (4, 2, 64)], ids=lambda h: "%d/%d/%d" % h)
+def test_long_prefix_and_long_own_parts(heads):
+    w = Batch(heads, 256, [(24, [1000, 3, 700, 2000]), (3, [5000, 1])], seed=5)
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(out, w.reference(), "long")
+
+
+@pytest.mark.parametrize("heads", [(2, 1, 64), (16, 8, 128), (32, 8, 128), (64, 8, 128), (8, 1, 128)],
+                         ids=lambda h: "%d/%d/%d" % h)
+@pytest.mark.parametrize("shape", ["odd", "padding", "one_token_each", "tall"])
+def test_append_stores_and_attends(heads, shape):
+    w = Batch(heads, 16, SHAPES[shape], seed=11 + heads[0])
+    plan = w.plan()
+    kc, vc = w.kc.clone(), w.vc.clone()
+    out = kvp.attn_decode_shared_append(w.q, w.k, w.v, w.dev(w.slots), w.kc, w.vc, w.dev(w.tables), plan,
+                                        softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    kr, vr = u16(kc), u16(vc)
+    oracle.kv_store(w.k.cpu(), w.v.cpu(), torch.from_numpy(w.slots), kr, vr)
+    assert np.array_equal(u16(w.kc), kr) and np.array_equal(u16(w.vc), vr)
+    w.check(out, w.reference(), shape)
+
+
+def test_strided_rows():
+    """q, k, v and out are views into wider rows; nothing beside them is written."""
+    w = Batch((16, 8, 128), 32, [(6, [40, 9, 1]), (0, [77])], seed=3)
+    qkv = torch.randn((w.b, 16 + 8 + 8 + 2, 128), device="cuda").to(BF16)
+    qkv[:, :16], qkv[:, 16:24], qkv[:, 24:32] = w.q, w.k, w.v
+    wide = torch.full((w.b, 20, 128), 7.0, dtype=BF16, device="cuda")
+    kvp.attn_decode_shared_append(qkv[:, :16], qkv[:, 16:24], qkv[:, 24:32], w.dev(w.slots), w.kc, w.vc,
+                                  w.dev(w.tables), w.plan(), softmax_scale=w.scale, out=wide[:, 2:18])
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(wide[:, 2:18], w.reference(), "strided")
+    assert torch.all(wide[:, :2] == 7) and torch.all(wide[:, 18:] == 7)
+
+
+def test_large_and_masked_scores():
+    """Scores that grow along the sequence (the running maximum moves all the
+    time) and a key with -inf scores for every head."""
+    w = Batch((16, 8, 128), 16, [(20, [33, 50, 1])], seed=9, poison=False)
+    w.kc[int(w.tables[0, 3]), 5, :, :] = float("-inf")
+    w.q.abs_()
+    for i in range(w.tables.shape[1]):
+        for page in set(w.tables[:, i].tolist()) - {-1}:
+            w.kc[page] = (w.kc[page].float() * (0.2 + 0.35 * i)).to(BF16)
+    w.kc[int(w.tables[0, 3]), 5, :, :] = float("-inf")
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    got = out.float().cpu().double().numpy()
+    # fp64 from the definition (the scores reach some hundreds, so the fp32
+    # sums' error is taken from the values: (d + 2) 2^-24 max sum |q k| scale)
+    for b in range(w.b):
+        n = int(w.lens[b])
+        pages = torch.from_numpy(w.tables[b, :ceil(n, 16)].astype(np.int64)).cuda()
+        k = w.kc[pages].reshape(-1, 8, 128)[:n].double()
+        v = w.vc[pages].reshape(-1, 8, 128)[:n].double()
+        for h in range(16):
+            s = (k[:, h // 2] @ w.q[b, h].double()) * w.scale
+            p = torch.softmax(s, 0)
+            ref = (p @ v[:, h // 2]).cpu().numpy()
+            a = (p @ v[:, h // 2].abs()).cpu().numpy()
+            fin = torch.isfinite(s)
+            size = ((k[fin][:, h // 2].abs() @ w.q[b, h].double().abs()) * w.scale).max().item()
+            tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -6) + (2.0 ** -8 + 2.0 ** -9 + 4 * 130 * 2.0 ** -24 * size) * a
+            assert (np.abs(got[b, h] - ref) <= tol).all(), (b, h)
+
+
+def test_plan_finds_the_groups():
+    cases = [SHAPES[s] for s in ("odd", "many", "tall", "alone", "padding")]
+    cases.append([(1, [3, 4]), (64, [5, 6, 7]), (8, [1, 2])])
+    for i, groups in enumerate(cases):
+        w = Batch((16, 8, 128), 16, groups, seed=i)
+        # a page that every sequence has in common must not join the groups
+        if i == 5:
+            w.tables[:, 0] = w.tables[0, 0]
+        for min_shared in (0, 16, 176):
+            want = shared_prefixes(w.tables.tolist(), w.lens.tolist(), 16, min_shared or 128)
+            assert plan_prefixes(w.plan(min_shared), w.b) == want, (i, min_shared)
+
+
+def test_same_sequence_twice_and_whole_rows_shared():
+    """Forked rows before their first own token: identical tables and lengths."""
+    for n in (129, 160, 161, 1):
+        w = Batch((32, 8, 128), 16, [(0, [n])], seed=n)
+        w.tables, w.lens, w.b = np.repeat(w.tables, 5, 0), np.repeat(w.lens, 5), 5
+        w.q = torch.randn((5, 32, 128), device="cuda").to(BF16)
+        out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+        torch.cuda.synchronize()
+        assert_status_ok()
+        w.check(out, w.reference(), str(n))
+
+
+def test_results_do_not_change_between_calls():
+    w = Batch((32, 8, 128), 16, SHAPES["many"], seed=1)
+    plan, bt = w.plan(), w.dev(w.tables)
+    outs = [kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        o = kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan)
+    other.synchronize()
+    assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+
+
+def test_two_streams_one_plan():
+    """Calls that run side by side with workspaces of their own."""
+    w = Batch((16, 8, 128), 16, SHAPES["many"], seed=2)
+    plan, bt = w.plan(), w.dev(w.tables)
+    want = kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(kvp.attn_decode_shared_workspace_size(w.b, 16, 8, 128), dtype=torch.uint8, device="cuda")
+          for _ in streams]
+    outs = [[torch.empty_like(want) for _ in range(20)] for _ in streams]
+    for i in range(20):
+        for s, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan, workspace=ws[s], out=outs[s][i])
+    torch.cuda.synchronize()
+    assert_status_ok()
+    assert all(torch.equal(o.view(torch.int16), want.view(torch.int16)) for group in outs for o in group)
+
+
+def test_graph_replay_follows_the_tables():
+    """plan + append captured once; the replays see other tables, lengths and
+    slots, groups coming and going.  Two graphs share plan and workspace."""
+    heads, bs = (16, 8, 128), 16
+    w0 = Batch(heads, bs, [(10, [30, 31, 32, 33]), (0, [5, 6, 7, 8])], seed=0, extra=200)
+    b, width, nb = w0.b, 60, w0.nb
+    bt = torch.full((b, width), -1, dtype=I32, device="cuda")
+    ctx, slots = torch.zeros(b, dtype=I32, device="cuda"), torch.full((b,), -1, dtype=I32, device="cuda")
+    kc, vc = torch.zeros_like(w0.kc), torch.zeros_like(w0.vc)
+    q, k, v = torch.zeros_like(w0.q), torch.zeros_like(w0.k), torch.zeros_like(w0.v)
+    plan = torch.empty(kvp.attn_shared_plan_size(b, 16, 8), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kvp.attn_decode_shared_workspace_size(b, 16, 8, 128), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(2)]
+
+    def step(out):
+        kvp.attn_shared_plan(bt, ctx, bs, 16, 8, nb, plan=plan)
+        kvp.attn_decode_shared_append(q, k, v, slots, kc, vc, bt, plan, workspace=ws, out=out)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step(outs[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for out in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            step(out)
+        graphs.append(g)
+    steps = [[(10, [30, 31, 32, 33]), (0, [5, 6, 7, 8])], [(0, [9] * 8)], [(9, [1, 2]), (30, [3, 4, 5, 6, 7, 8])],
+             [(0, [0] * 8)], [(12, [100] * 8)]]
+    for i, groups in enumerate(steps):
+        w = Batch(heads, bs, groups, seed=50 + i, extra=0)
+        assert w.nb <= nb
+        kc[:w.nb], vc[:w.nb] = w.kc, w.vc
+        bt.fill_(-1)
+        bt[:, :w.tables.shape[1]] = w.dev(w.tables)
+        ctx.copy_(w.dev(w.lens))
+        slots.copy_(w.dev(w.slots))
+        q.copy_(w.q), k.copy_(w.k), v.copy_(w.v)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert_status_ok()
+        w.kc, w.vc = kc[:w.nb].clone(), vc[:w.nb].clone()
+        ref = w.reference()
+        for out in outs:
+            w.check(out, ref, f"step {i}")
+
+
+def test_empty_batch():
+    w = Batch((16, 8, 128), 16, [(0, [4])], seed=0)
+    e = torch.zeros((0, 16, 128), dtype=BF16, device="cuda")
+    bt = torch.zeros((0, 3), dtype=I32, device="cuda")
+    plan = kvp.attn_shared_plan(bt, torch.zeros(0, dtype=I32, device="cuda"), 16, 16, 8, w.nb)
+    assert kvp.attn_decode_shared(e, w.kc, w.vc, bt, plan).shape == (0, 16, 128)
+    torch.cuda.synchronize()
+    assert_status_ok()
+
+
+def test_wrong_metadata_is_reported():
+    """A plan of another shape writes nothing; a page outside the pool, a
+    length past the table and a slot that is not the last token's are
+    reported, and the other sequences are right."""
+    w = Batch((16, 8, 128), 16, [(10, [3, 4, 40]), (0, [20])], seed=8, poison=False)
+    bt, plan = w.dev(w.tables), w.plan()
+    out = torch.full_like(w.q, 3.0)
+    kvp.device_status()
+    kvp.attn_decode_shared(w.q[:3], w.kc, w.vc, bt[:3], plan, out=out[:3])
+    torch.cuda.synchronize()
+    assert kvp.device_status() == -6 and torch.all(out == 3)
+    ref = w.reference()
+    good = w.tables.copy()
+    for bad_id in (-1, w.nb, 1 << 30):
+        bad = good.copy()
+        bad[2, 11] = bad_id  # a page of sequence 2's own part
+        out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(bad), plan)
+        torch.cuda.synchronize()
+        assert kvp.device_status() == -6
+        keep = [0, 1, 3]
+        tol = 2.0 ** -8 * np.abs(ref[0]) * (1 + 2.0 ** -6) + (2.0 ** -8 + 2.0 ** -9) * ref[1]
+        err = np.abs(out.float().cpu().double().numpy() - ref[0])
+        assert (err[keep] <= tol[keep]).all()
+        bad = good.copy()
+        bad[:3, 4] = bad_id  # in the shared part
+        w2 = kvp.attn_shared_plan(w.dev(bad), w.dev(w.lens), 16, 16, 8, w.nb)
+        kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(bad), w2)
+        torch.cuda.synchronize()
+        assert kvp.device_status() == -6
+    lens = w.lens.copy()
+    lens[3] = w.tables.shape[1] * 16 + 1
+    p = kvp.attn_shared_plan(bt, w.dev(lens), 16, 16, 8, w.nb)
+    torch.cuda.synchronize()
+    assert kvp.device_status() == -6
+    slots = w.slots.copy()
+    slots[1] += 1 if slots[1] % 16 < 15 else -1
+    kvp.attn_decode_shared_append(w.q, w.k, w.v, w.dev(slots), w.kc, w.vc, bt, plan)
+    torch.cuda.synchronize()
+    assert kvp.device_status() == -6
+    slots[1] = w.nb * 16
+    kvp.attn_decode_shared_append(w.q, w.k, w.v, w.dev(slots), w.kc, w.vc, bt, plan)
+    torch.cuda.synchronize()
+    assert kvp.device_status() == -6
