@@ -53,12 +53,12 @@ int check_shared(const char* fn, const kvp::SharedCall& c, const void* plan, siz
                           "%s: q, k, v, caches, plan and out need 16-byte alignment and row strides "
                           "that are multiples of 8 elements",
                           fn);
-  if (plan_bytes < kvp::shared_plan_bytes(c.num_seqs))
-    return set_last_error(KVP_ERR_WORKSPACE, "%s: plan needs %zu bytes (got %zu)", fn,
-                          kvp::shared_plan_bytes(c.num_seqs), plan_bytes);
   int sms;
   int rc = kvp::device_sm_count(&sms);
   if (rc) return rc;
+  if (plan_bytes < kvp::shared_plan_bytes(c.num_seqs, sms))
+    return set_last_error(KVP_ERR_WORKSPACE, "%s: plan needs %zu bytes (got %zu)", fn,
+                          kvp::shared_plan_bytes(c.num_seqs, sms), plan_bytes);
   const size_t need =
       kvp::shared_workspace_bytes(c.num_seqs, c.num_heads, c.num_kv_heads, c.head_dim, sms);
   if (!c.workspace || workspace_bytes < need || !aligned16(c.workspace))
@@ -75,7 +75,7 @@ int run_shared(const char* fn, const kvp::SharedCall& c, const void* plan, size_
   rc = kvp::device_handles(&status, &sms);
   if (rc) return rc;
   const cudaError_t e =
-      kvp::launch_decode_shared(c, kvp::shared_plan_view(const_cast<void*>(plan), c.num_seqs), app,
+      kvp::launch_decode_shared(c, kvp::shared_plan_view(const_cast<void*>(plan), c.num_seqs, sms), app,
                                 sms, status, (cudaStream_t)stream);
   return e == cudaSuccess ? KVP_OK : cuda_error(e, fn);
 }
@@ -144,7 +144,9 @@ size_t attn_shared_plan_size(int num_seqs, int num_heads, int num_kv_heads) {
     set_last_error(KVP_ERR_INVALID_ARG, "attn_shared_plan_size: bad shape");
     return 0;
   }
-  return kvp::shared_plan_bytes(num_seqs);
+  int sms;
+  if (kvp::device_sm_count(&sms)) return 0;
+  return kvp::shared_plan_bytes(num_seqs, sms);
 }
 
 int attn_shared_plan(const int32_t* block_tables, int max_blocks_per_seq,
@@ -164,16 +166,18 @@ int attn_shared_plan(const int32_t* block_tables, int max_blocks_per_seq,
   if (num_seqs == 0) return KVP_OK;
   if (!block_tables || !context_lens || !plan)
     return set_last_error(KVP_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (plan_bytes < kvp::shared_plan_bytes(num_seqs) || !aligned16(plan))
-    return set_last_error(KVP_ERR_WORKSPACE, "%s: plan needs %zu bytes, 16-byte aligned (got %zu)",
-                          fn, kvp::shared_plan_bytes(num_seqs), plan_bytes);
+  if (!aligned16(plan))
+    return set_last_error(KVP_ERR_INVALID_ARG, "%s: plan needs 16-byte alignment", fn);
   int *status, sms;
   int rc = kvp::device_handles(&status, &sms);
   if (rc) return rc;
+  if (plan_bytes < kvp::shared_plan_bytes(num_seqs, sms))
+    return set_last_error(KVP_ERR_WORKSPACE, "%s: plan needs %zu bytes (got %zu)", fn,
+                          kvp::shared_plan_bytes(num_seqs, sms), plan_bytes);
   const cudaError_t e = kvp::launch_shared_plan(
       block_tables, max_blocks_per_seq, context_lens, num_seqs, num_blocks, block_size,
       num_heads / num_kv_heads, num_kv_heads, min_shared_len ? min_shared_len : kDefaultMinShared,
-      kvp::shared_plan_view(plan, num_seqs), status, (cudaStream_t)stream);
+      kvp::shared_plan_view(plan, num_seqs, sms), sms, status, (cudaStream_t)stream);
   return e == cudaSuccess ? KVP_OK : cuda_error(e, fn);
 }
 

@@ -11,7 +11,23 @@ namespace {
 
 constexpr int kPlanMagic = 0x53504c31;
 constexpr int kTileRows = 128;  // query rows of a prefix tile
-constexpr int kTileKeys = 128;  // keys of a prefix step
+constexpr int kTileKeys = 64;   // keys of a prefix step
+
+// Both split kernels cut their work, laid end to end, into one equal chunk
+// per CTA; a chunk's pieces are its segments.  Segment (item i, CTA c) has its
+// own rows of partial results: items and CTAs only ever advance together, so
+// (rows of the items before i) + c * (rows of an item) is never taken twice.
+__host__ __device__ constexpr int prefix_ctas(int sms) { return 2 * sms; }
+__host__ __device__ constexpr int own_ctas(int sms) { return sms; }
+constexpr int kLeastSteps = 2;    // prefix steps of a CTA
+// A sequence in a CTA costs about as much as 64 KiB of its stream (query,
+// page and plan look-ups, partials): in the own-part kernel's split it counts
+// that many tokens (of head_dim 128) more than it has.
+__host__ __device__ constexpr int own_gap(int num_kv_heads) { return 128 / num_kv_heads; }
+__device__ __forceinline__ long long chunk_of(long long total, int ctas, int least) {
+  const long long c = (total + ctas - 1) / ctas;
+  return c < least ? least : c;
+}
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -32,33 +48,45 @@ struct PlanArgs {
   int block_size;
   int group;         // query heads per kv head
   int num_kv_heads;
+  int gap;           // own_gap
   int min_shared;    // tokens
+  int sms;
   SharedPlan plan;
   int* status;
 };
 
-// Exclusive prefix sum over the block's threads; *total = the sum.
-template <typename T>
-__device__ T block_scan(T v, long long* warp_sums, T* total) {
+// Exclusive prefix sums of N values at once over the block's threads; total[i]
+// = the sum of v[i].  `sums` holds N x kPlanThreads / 32 sums.
+template <int N>
+__device__ void block_scan(long long (&v)[N], long long (&total)[N], long long (*sums)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T incl = v;
+  long long incl[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = (long long)incl;
-  __syncthreads();
-  const T s = (T)warp_sums[lane];
-  T ws = s;
+  for (int i = 0; i < N; ++i) {
+    incl[i] = v[i];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, ws, o);
-    if (lane >= o) ws += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += y;
+    }
   }
-  *total = __shfl_sync(0xffffffffu, ws, 31);
-  return __shfl_sync(0xffffffffu, ws - s, warp) + incl - v;
+  __syncthreads();  // the previous scan's sums have been read
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i][warp] = incl[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const long long s = sums[i][lane];
+    long long ws = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += y;
+    }
+    total[i] = __shfl_sync(0xffffffffu, ws, 31);
+    v[i] = __shfl_sync(0xffffffffu, ws - s, warp) + incl[i] - v[i];
+  }
 }
 static_assert(kPlanThreads == 1024, "block_scan needs 32 warps");
 
@@ -80,15 +108,21 @@ __device__ int shared_pages(const PlanArgs& a, int b, int prev_ctx, int ctx) {
   const int n = prev_ctx > 0 && ctx > 0 ? (min(prev_ctx, ctx) - 1) / a.block_size : 0;
   const int32_t* x = a.block_tables + (int64_t)(b - 1) * a.max_blocks;
   const int32_t* y = x + a.max_blocks;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    bool same = false;
-    if (j < n) {
-      const int e = x[j];
-      same = e == y[j] && e >= 0 && e < a.num_blocks;
+  constexpr int U = 4;  // rounds of 32 entries with their loads in flight together
+  for (int j0 = 0; j0 < n; j0 += 32 * U) {
+    int ex[U], ey[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + 32 * u + lane;
+      ex[u] = j < n ? x[j] : -1;
+      ey[u] = j < n ? y[j] : -2;
     }
-    const unsigned diff = ~__ballot_sync(0xffffffffu, same);
-    if (diff) return j0 + __ffs(diff) - 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool same = ex[u] == ey[u] && ex[u] >= 0 && ex[u] < a.num_blocks;
+      const unsigned diff = ~__ballot_sync(0xffffffffu, same);
+      if (diff) return j0 + 32 * u + __ffs(diff) - 1;
+    }
   }
   return n;
 }
@@ -99,17 +133,20 @@ __device__ int shared_pages(const PlanArgs& a, int b, int prev_ctx, int ctx) {
 // prompt, must not join groups that share much more among themselves).
 __device__ __forceinline__ bool plan_joined(const PlanArgs& a, int b, int same) {
   if (b == 0 || same == 0 || (int64_t)same * a.block_size < a.min_shared) return false;
-  const int prev = a.plan.same[b - 1];
-  const int next = b + 1 < a.num_seqs ? a.plan.same[b + 1] : 0;
+  const int prev = __ldcg(&a.plan.same[b - 1]);
+  const int next = b + 1 < a.num_seqs ? __ldcg(&a.plan.same[b + 1]) : 0;
   return 2 * (int64_t)same >= max(prev, next);
 }
 
+// One cluster.  The warps of all its CTAs compare the table rows; after a
+// cluster barrier CTA 0 forms the groups and tiles (a few prefix sums over the
+// sequences).
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArgs a) {
-  __shared__ long long warp_sums[32];
+  __shared__ long long sums[3][32];
   const SharedPlan& p = a.plan;
   const int B = a.num_seqs, bs = a.block_size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int b = warp; b < B; b += kPlanThreads / 32) {
+  for (int b = blockIdx.x + warp * gridDim.x; b < B; b += gridDim.x * (kPlanThreads / 32)) {
     const int ctx = plan_ctx(a, b);
     const int same = b > 0 ? shared_pages(a, b, plan_ctx(a, b - 1), ctx) : 0;
     if (lane == 0) {
@@ -118,68 +155,72 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
       p.group_min[b] = 0x7fffffff;
     }
   }
-  __syncthreads();
+  __threadfence();
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\t"
+      "barrier.cluster.wait.acquire;" ::
+          : "memory");
+  if (blockIdx.x) return;
   // Groups: maximal runs of joined sequences; all of a group read the pages
   // that every one of them shares.
-  int groups = 0;
+  long long groups = 0;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
-    const int same = b < B ? p.same[b] : 0;
+    const int same = b < B ? __ldcg(&p.same[b]) : 0;
     const bool joined = b < B && plan_joined(a, b, same);
-    int total;
-    const int before = block_scan(b < B && !joined ? 1 : 0, warp_sums, &total);
+    long long v[1] = {b < B && !joined ? 1 : 0}, total[1];
+    block_scan(v, total, sums);
     if (b < B) {
-      const int g = groups + before - (joined ? 1 : 0);
+      const int g = (int)(groups + v[0]) - (joined ? 1 : 0);
       p.tile_of[b] = g;
       if (joined)
         atomicMin(&p.group_min[g], same);
       else
         p.group_seq[g] = b;
     }
-    groups += total;
+    groups += total[0];
   }
   __syncthreads();
   // Tiles of 128 query rows within a group, and the prefix sums the kernels
-  // find their work by.
+  // find their work by: (tiles, sequences in tiles), steps, own tokens.
   const int tile_seqs = kTileRows / a.group;
-  int tiles = 0, rows = 0;
-  long long steps = 0, tokens = 0;
+  long long base[3] = {0, 0, 0};
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
     int ctx = 0, prefix = 0;
     bool start = false;
     if (b < B) {
-      const int g = p.tile_of[b], m = *(volatile int*)&p.group_min[g];
-      ctx = p.ctx[b];
+      const int g = p.tile_of[b], m = __ldcg(&p.group_min[g]);
+      ctx = __ldcg(&p.ctx[b]);
       prefix = m == 0x7fffffff ? 0 : m * bs;
       start = prefix > 0 && (b - p.group_seq[g]) % tile_seqs == 0;
     }
-    int total;
-    const int t = tiles + block_scan(start ? 1 : 0, warp_sums, &total) + (start ? 1 : 0) - 1;
-    tiles += total;
-    const int r = rows + block_scan(prefix > 0 ? 1 : 0, warp_sums, &total);
-    rows += total;
-    const int n = start ? (prefix + kTileKeys - 1) / kTileKeys : 0;
-    long long ltotal;
-    const long long st = steps + block_scan((long long)n, warp_sums, &ltotal);
-    steps += ltotal;
-    const long long tok = tokens + block_scan((long long)(ctx - prefix), warp_sums, &ltotal);
-    tokens += ltotal;
+    long long v[3] = {((long long)(start ? 1 : 0) << 32) | (prefix > 0 ? 1 : 0),
+                      start ? (long long)a.num_kv_heads * ((prefix + kTileKeys - 1) / kTileKeys) : 0,
+                      ctx > 0 ? a.gap + ctx - prefix : 0};
+    long long total[3];
+    block_scan(v, total, sums);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] += base[i], base[i] += total[i];
     if (b < B) {
+      const int t = (int)(v[0] >> 32) - (start ? 0 : 1);
       p.prefix[b] = prefix;
       p.tile_of[b] = prefix > 0 ? t : -1;
-      p.cum_tokens[b] = tok;
+      p.cum_tokens[b] = v[2];
       if (start) {
         p.tile_seq[t] = b;
-        p.cum_rows[t] = r;
-        p.cum_steps[t] = st;
+        p.cum_rows[t] = (int)(v[0] & 0xffffffffll);
+        p.cum_steps[t] = v[1];
       }
     }
   }
+  const int tiles = (int)(base[0] >> 32);
+  const long long pchunk = chunk_of(base[1], prefix_ctas(a.sms), kLeastSteps);
+  const long long ochunk = chunk_of(base[2], own_ctas(a.sms), 2 * a.gap);
   if (threadIdx.x == 0) {
-    p.cum_tokens[B] = tokens;
-    p.cum_rows[tiles] = rows;
-    p.cum_steps[tiles] = steps;
+    p.cum_tokens[B] = base[2];
+    p.cum_rows[tiles] = (int)(base[0] & 0xffffffffll);
+    p.cum_steps[tiles] = base[1];
     SharedPlanHead h;
     h.magic = kPlanMagic;
     h.num_seqs = B;
@@ -188,11 +229,25 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     h.block_size = bs;
     h.max_blocks = a.max_blocks;
     h.num_tiles = tiles;
+    h.sms = a.sms;
+    h.gap = a.gap;
     h.pad = 0;
-    h.steps = steps;
-    h.tokens = tokens;
+    h.prefix_chunk = pchunk;
+    h.prefix_total = base[1];
+    h.own_chunk = ochunk;
+    h.own_total = base[2];
     *p.head = h;
   }
+  __syncthreads();
+  // Where each CTA starts: the sequence (tile) whose tokens (steps) hold its
+  // first one.
+  for (int b = threadIdx.x; b < B; b += kPlanThreads)
+    for (long long c = (p.cum_tokens[b] + ochunk - 1) / ochunk; c * ochunk < p.cum_tokens[b + 1]; ++c)
+      p.cta_seq[c] = b;
+  for (int t = warp; t < tiles; t += kPlanThreads / 32)
+    for (long long c = (p.cum_steps[t] + pchunk - 1) / pchunk + lane; c * pchunk < p.cum_steps[t + 1];
+         c += 32)
+      p.cta_tile[c] = t;
 }
 
 // ------------------------------------------------------------- attention
@@ -216,7 +271,7 @@ struct SharedArgs {
   SharedPlan plan;
   float* prefix_part;  // rows of the prefix kernel's segments
   float* own_part;     // rows of the own-part kernel's segments
-  int prefix_ctas, own_ctas;
+  int sms;
   int tma_per_head;
   uint16_t* out;
   int64_t out_stride;
@@ -238,52 +293,64 @@ __device__ __forceinline__ bool plan_fits(const SharedArgs& a) {
   const SharedPlanHead& h = *a.plan.head;
   return h.magic == kPlanMagic && h.num_seqs == a.num_seqs &&
          h.group == a.num_heads / a.num_kv_heads && h.num_kv_heads == a.num_kv_heads &&
-         h.block_size == a.block_size && h.max_blocks == a.max_blocks;
+         h.block_size == a.block_size && h.max_blocks == a.max_blocks && h.sms == a.sms;
 }
-
-// Both split kernels cut their work, laid end to end, into one equal chunk
-// per CTA; a chunk's pieces are its segments.  Segment (item i, CTA c) has its
-// own rows of partial results: items and CTAs only ever advance together, so
-// (rows of the items before i) + c * (rows of an item) is never taken twice.
-__device__ __forceinline__ long long chunk_of(long long total, int ctas, int least) {
-  const long long c = (total + ctas - 1) / ctas;
-  return c < least ? least : c;
-}
-constexpr int kLeastSteps = 1;    // prefix steps of 128 keys per CTA
-constexpr int kLeastTokens = 32;  // own tokens per CTA
 
 // ------------------------------------------------- the shared prefixes
 //
 // Item: a tile t of up to 128 query rows (128 / G sequences of a group x the G
-// query heads of kv head h) against all keys of the group's prefix, taken 128
+// query heads of kv head h) against all keys of the group's prefix, taken 64
 // at a time ("step").  The items' steps, laid end to end, are split evenly
 // over the CTAs; a CTA's pieces ("segments") leave un-normalised partials.
-// Per step: S = Q K^T (tcgen05, M128 N128 K = D) -> row maxima and weights in
+// Per step: S = Q K^T (tcgen05, M128 N64 K = D) -> row maxima and weights in
 // registers -> P in tensor memory -> O += P V.  Rows of a group share the
 // same keys, so nothing but the last step's ragged end is masked.
 //
 // 192 threads: warps 0-3 softmax (thread = row), warp 4 TMA producer, warp 5
-// tensor memory and MMA issue.  One K and one V slot each: K(j + 1) loads
-// while the softmax of step j runs, V(j + 1) while S(j + 1) and its softmax
-// do.  Shared and tensor memory and registers are small enough for two CTAs
+// tensor memory and MMA issue.  S has two buffers: S(j + 1) is computed while
+// the softmax works on S(j), so the tensor core's part of a step does not stand
+// in the chain from one softmax to the next.  Shared and tensor memory and registers are small enough for two CTAs
 // per SM (which alternate on the tensor core) or for one beside a CTA of the
 // own-part kernel, whose HBM stream it overlaps.
 
+#ifndef POL_PREFIX
+#define POL_PREFIX policy_evict_last
+#endif
+#ifndef PREFIX_REGS
+#define PREFIX_REGS 112
+#endif
 constexpr int kPrefixThreads = 192;
 
-enum : int { P_QFULL, P_QEMPTY, P_KFULL, P_KEMPTY, P_VFULL, P_VEMPTY, P_SFULL, P_PFULL, P_PVDONE,
-             P_OFREE, P_DRAIN, P_BARS };
+enum : int {
+  P_KFULL = 0,   // [2]
+  P_KEMPTY = 2,  // [2]
+  P_VFULL = 4,   // [2]
+  P_VEMPTY = 6,  // [2]
+  P_SFULL = 8,   // [2]
+  P_PFULL = 10,  // [2]
+  P_QFULL = 12,
+  P_QEMPTY,
+  P_PVDONE,  // a step's PV
+  P_ODONE,   // a segment's last PV
+  P_OFREE,
+  P_DRAIN,
+  P_BARS
+};
 
 template <int D>
 struct PrefixLayout {
   static constexpr uint32_t kPanels = D / 64;
-  static constexpr uint32_t kPanelBytes = 128 * 128;
-  static constexpr uint32_t kTileBytes = 128 * D * 2;
-  static constexpr uint32_t kQ = 0, kK = kTileBytes, kV = 2 * kTileBytes;
-  static constexpr uint32_t kBar = 3 * kTileBytes;
+  static constexpr uint32_t kQPanel = kTileRows * 128;  // 128 rows x 64 columns, 128-byte swizzle
+  static constexpr uint32_t kPanel = kTileKeys * 128;   // 64 keys x 64 columns
+  static constexpr uint32_t kQBytes = kTileRows * D * 2;
+  static constexpr uint32_t kSlot = kTileKeys * D * 2;  // a step's K or V
+  static constexpr uint32_t kQ = 0, kK = kQBytes, kV = kK + 2 * kSlot;  // two slots of K and V
+  static constexpr uint32_t kBar = kV + 2 * kSlot;
   static constexpr uint32_t kAlloc = kBar + P_BARS * 8 + 16;
 };
-constexpr uint32_t kPrefixTmem = 256;  // S (P over its first half) | O
+constexpr int kMaxSub = kTileKeys / 16;    // pages of a step (the smallest page has 16 tokens)
+// Tensor memory: S of even steps | S of odd steps (P over each one's first half) | O.
+constexpr uint32_t kColO = 2 * kTileKeys, kPrefixTmem = 256;
 
 // The segments of this CTA, one after the other.
 struct PrefixSegment {
@@ -299,18 +366,18 @@ struct PrefixSegment {
     if (pos >= end) return false;
     const int Hkv = a.num_kv_heads, G = a.num_heads / Hkv;
     const long long c0 = a.plan.cum_steps[t], c1 = a.plan.cum_steps[t + 1];
-    const long long st = c1 - c0, rel = pos - Hkv * c0;
-    h = (int)(rel / st);
-    s0 = (int)(rel - h * st);
+    const int st = (int)((c1 - c0) / Hkv), rel = (int)(pos - c0);  // (at most 8 x 2^24 steps)
+    h = rel / st;
+    s0 = rel - h * st;
     const long long left = end - pos;
-    s1 = st - s0 < left ? (int)st : s0 + (int)left;
+    s1 = st - s0 < left ? st : s0 + (int)left;
     const int r0 = a.plan.cum_rows[t];
     nseq = a.plan.cum_rows[t + 1] - r0;
     seq0 = a.plan.tile_seq[t];
     prefix = a.plan.prefix[seq0];
     row0 = (long long)Hkv * G * r0 + (long long)h * nseq * G + (long long)blockIdx.x * kTileRows;
     pos += s1 - s0;
-    if (pos == Hkv * c1) ++t;
+    if (pos == c1) ++t;
     return true;
   }
 };
@@ -321,71 +388,86 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
                                 uint64_t* bars) {
   using Lay = PrefixLayout<D>;
   const int lane = threadIdx.x & 31;
-  const int G = a.num_heads / a.num_kv_heads;
   const int box = a.block_size < kTileKeys ? a.block_size : kTileKeys;
   const int nsub = kTileKeys / box;
+  const int shift = __ffs(a.block_size) - 1;  // block_size is a power of two
   const int past = (int)(a.num_blocks * a.block_size);  // a row past the pool: loads zeros
   if (lane == 0) {
     prefetch_tensormap(tmQ);
     prefetch_tensormap(tmK);
     prefetch_tensormap(tmV);
   }
-  uint32_t nq = 0, nk = 0, nv = 0;
-  bool ok = true;
+  // Other tiles read the same keys: hold on to them in L2.
+  const uint64_t keep = POL_PREFIX();
+  const int G = a.num_heads / a.num_kv_heads;
+  uint32_t n = 0, segs = 0;  // steps and segments issued; step n uses slot n & 1
+  bool ok = true, k_only = false;
   while (ok && sg.next(a)) {
-    if (nq > 0 && !mbar_wait(&bars[P_QEMPTY], (nq - 1) & 1, a.status)) break;
+    if (!mbar_wait(&bars[P_QEMPTY], (segs & 1) ^ 1u, a.status)) {
+      ok = false;
+      break;
+    }
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bars[P_QFULL], Lay::kTileBytes);
+      mbar_arrive_expect_tx(&bars[P_QFULL], Lay::kQBytes);
       for (int p = 0; p < (int)Lay::kPanels; ++p)
-        tma_load_3d(smem + Lay::kQ + p * Lay::kPanelBytes, tmQ, p * 64, sg.h * G, sg.seq0,
+        tma_load_3d(smem + Lay::kQ + p * Lay::kQPanel, tmQ, p * 64, sg.h * G, sg.seq0,
                     &bars[P_QFULL]);
     }
-    ++nq;
+    ++segs;
     const int32_t* table = a.block_tables + (int64_t)sg.seq0 * a.max_blocks;
-    for (int s = sg.s0; s < sg.s1; ++s) {
-      // Lane i looks up sub-box i of the step (at most 8).
-      int row = past;
-      const int key = s * kTileKeys + lane * box;
-      if (lane < nsub && key < sg.prefix) {
-        int phys = table[key / a.block_size];
-        if (phys < 0 || phys >= a.num_blocks) {
-          record_error(a.status, KVP_ERR_DEVICE_DATA);
-          phys = 0;  // never address a block outside the pool
+    // Lane i has the row of sub-box i & 3 of the (i / 4)-th next step.
+    int rows = past;
+    for (int s = sg.s0; s < sg.s1; ++s, ++n) {
+      const int j = (s - sg.s0) & 7;
+      if (j == 0) {
+        const int key = (s + (lane >> 2)) * kTileKeys + (lane & 3) * box;
+        rows = past;
+        if ((lane & 3) < nsub && key < sg.prefix && s + (lane >> 2) < sg.s1) {
+          int phys = table[key >> shift];
+          if (phys < 0 || phys >= a.num_blocks) {
+            record_error(a.status, KVP_ERR_DEVICE_DATA);
+            phys = 0;  // never address a block outside the pool
+          }
+          rows = (phys << shift) + (key & (a.block_size - 1));
         }
-        row = phys * a.block_size + key % a.block_size;
       }
-      int rows[8];
+      int row[kMaxSub];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rows[i] = __shfl_sync(0xffffffffu, row, i);
+      for (int i = 0; i < kMaxSub; ++i) row[i] = __shfl_sync(0xffffffffu, rows, j * 4 + i);
+      const int slot = n & 1;
+      const uint32_t par = ((n >> 1) & 1) ^ 1u;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        uint32_t& n = kv == 0 ? nk : nv;
-        const int full = kv == 0 ? P_KFULL : P_VFULL, empty = kv == 0 ? P_KEMPTY : P_VEMPTY;
-        if (n > 0 && !mbar_wait(&bars[empty], (n - 1) & 1, a.status)) {
+        const int full = (kv == 0 ? P_KFULL : P_VFULL) + slot;
+        const int empty = (kv == 0 ? P_KEMPTY : P_VEMPTY) + slot;
+        if (!mbar_wait(&bars[empty], par, a.status)) {
           ok = false;
+          k_only = kv == 1;
           break;
         }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars[full], Lay::kTileBytes);
-          uint8_t* dst = smem + (kv == 0 ? Lay::kK : Lay::kV);
+          mbar_arrive_expect_tx(&bars[full], Lay::kSlot);
+          uint8_t* dst = smem + (kv == 0 ? Lay::kK : Lay::kV) + slot * Lay::kSlot;
           const CUtensorMap* map = kv == 0 ? tmK : tmV;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < kMaxSub; ++i)
             if (i < nsub)
               for (int p = 0; p < (int)Lay::kPanels; ++p)
-                tma_load_3d(dst + p * Lay::kPanelBytes + i * box * 128, map, p * 64, sg.h, rows[i],
-                            &bars[full]);
+                tma_load_3d_hint(dst + p * Lay::kPanel + i * box * 128, map, p * 64, sg.h, row[i],
+                                 &bars[full], keep);
         }
-        ++n;
       }
       if (!ok) break;
     }
   }
-  // No copy of this CTA is in flight when it exits (after an expired wait
-  // nobody else may have waited for them).
-  if (nq) mbar_wait(&bars[P_QFULL], (nq - 1) & 1, a.status);
-  if (nk) mbar_wait(&bars[P_KFULL], (nk - 1) & 1, a.status);
-  if (nv) mbar_wait(&bars[P_VFULL], (nv - 1) & 1, a.status);
+  if (ok) return;  // the MMA thread has waited for every copy
+  // After an expired wait: no copy of this CTA is in flight when it exits.
+  // (Steps below n are complete in both; step n may have its K only.)
+  if (segs) mbar_wait(&bars[P_QFULL], (segs - 1) & 1, a.status);
+  for (int kv = 0; kv < 2; ++kv)
+    for (uint32_t i = n > 1 ? n - 2 : 0; i < n; ++i)
+      mbar_wait(&bars[(kv == 0 ? P_KFULL : P_VFULL) + (i & 1)], (i >> 1) & 1, a.status);
+  if (k_only) mbar_wait(&bars[P_KFULL + (n & 1)], (n >> 1) & 1, a.status);
 }
 
 template <int D>
@@ -395,33 +477,47 @@ __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem,
   constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kTileKeys, 0, 0);
   constexpr uint32_t idesc_o = idesc_bf16_f32(kTileRows, D, 0, 1);
   const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
-  const uint64_t dk = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
-  const uint64_t dv = smem_desc(smem_u32(smem + Lay::kV), Lay::kPanelBytes, 1024, 2);
-  const uint32_t ts = tbase, to = tbase + kTileKeys;
+  const uint64_t dk0 = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
+  const uint64_t dv0 = smem_desc(smem_u32(smem + Lay::kV), Lay::kPanel, 1024, 2);
   uint32_t n = 0, segs = 0;
-  while (sg.next(a)) {
-    if (!mbar_wait(&bars[P_QFULL], segs & 1, a.status)) goto drain;
-    for (int s = sg.s0; s < sg.s1; ++s, ++n) {
-      if (!mbar_wait(&bars[P_KFULL], n & 1, a.status)) goto drain;
-      tc_fence_after();
+  // S(n) = Q K(n)^T into buffer n & 1.  The P of step n - 2, which it
+  // overwrites, has been read: its PV was issued before.
+  auto issue_s = [&](uint32_t n, bool last) {
+    const uint32_t slot = n & 1;
+    if (!mbar_wait(&bars[P_KFULL + slot], (n >> 1) & 1, a.status)) return false;
+    tc_fence_after();
+    const uint64_t dk = dk0 + ((slot * Lay::kSlot) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * Lay::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_f16_ss(ts, dq + off, dk + off, idesc_s, kk > 0);
-      }
-      umma_commit(&bars[P_SFULL]);
-      umma_commit(&bars[P_KEMPTY]);
-      if (s + 1 == sg.s1) umma_commit(&bars[P_QEMPTY]);
-      if (!mbar_wait(&bars[P_VFULL], n & 1, a.status)) goto drain;
-      if (s == sg.s0 && segs > 0 && !mbar_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
-      if (!mbar_wait(&bars[P_PFULL], n & 1, a.status)) goto drain;
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t in = (kk & 3) * 32;
+      umma_f16_ss(tbase + slot * kTileKeys, dq + (((kk >> 2) * Lay::kQPanel + in) >> 4),
+                  dk + (((kk >> 2) * Lay::kPanel + in) >> 4), idesc_s, kk > 0);
+    }
+    umma_commit(&bars[P_SFULL + slot]);
+    umma_commit(&bars[P_KEMPTY + slot]);
+    if (last) umma_commit(&bars[P_QEMPTY]);
+    return true;
+  };
+  while (sg.next(a)) {
+    const int steps = sg.s1 - sg.s0;
+    if (!mbar_wait(&bars[P_QFULL], segs & 1, a.status)) goto drain;
+    if (!issue_s(n, steps == 1)) goto drain;
+    for (int j = 0; j < steps; ++j, ++n) {
+      // The next step's S is computed while the softmax works on this one's.
+      if (j + 1 < steps && !issue_s(n + 1, j + 2 == steps)) goto drain;
+      const uint32_t slot = n & 1, par = (n >> 1) & 1;
+      if (!mbar_wait(&bars[P_VFULL + slot], par, a.status)) goto drain;
+      if (j == 0 && segs > 0 && !mbar_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
+      if (!mbar_wait(&bars[P_PFULL + slot], par, a.status)) goto drain;
       tc_fence_after();
+      const uint64_t dv = dv0 + ((slot * Lay::kSlot) >> 4);
 #pragma unroll
       for (int kk = 0; kk < kTileKeys / 16; ++kk)
-        umma_f16_ts(to, ts + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_o,
-                    (s > sg.s0 || kk > 0) ? 1u : 0u);
-      umma_commit(&bars[P_VEMPTY]);
-      if (s + 1 == sg.s1) umma_commit(&bars[P_PVDONE]);
+        umma_f16_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
+                    idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(&bars[P_VEMPTY + slot]);
+      umma_commit(&bars[P_PVDONE]);
+      if (j + 1 == steps) umma_commit(&bars[P_ODONE]);
     }
     ++segs;
   }
@@ -439,39 +535,34 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
   const int r = threadIdx.x;  // row == TMEM lane
   const int G = a.num_heads / a.num_kv_heads;
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-  const uint32_t s_col = tbase + lane_base, o_col = s_col + kTileKeys;
+  const uint32_t t_row = tbase + lane_base, o_col = t_row + kColO;
   const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
   uint32_t n = 0, segs = 0;
   while (sg.next(a)) {
+    const bool valid = r < sg.nseq * G;
     float m = -INFINITY, l = 0.f;
     for (int s = sg.s0; s < sg.s1; ++s, ++n) {
-      if (!mbar_wait(&bars[P_SFULL], n & 1, a.status)) return;
+      if (!mbar_wait(&bars[P_SFULL + (n & 1)], (n >> 1) & 1, a.status)) return;
       tc_fence_after();
+      const uint32_t s_col = t_row + (n & 1) * kTileKeys;
       const int lim = sg.prefix - s * kTileKeys;  // columns < lim exist
-      float mx = -INFINITY;
+      uint32_t v[2][32];
+      tmem_ld32(s_col, v[0]);
+      tmem_ld32(s_col + 32, v[1]);
+      tmem_ld_wait();
+      if (lim < kTileKeys) {
 #pragma unroll
-      for (int c = 0; c < kTileKeys / 64; ++c) {
-        uint32_t v0[32], v1[32];
-        tmem_ld32(s_col + c * 64, v0);
-        tmem_ld32(s_col + c * 64 + 32, v1);
-        tmem_ld_wait();
-        if (lim >= kTileKeys) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            mx = fmaxf(mx, fmaxf(__uint_as_float(v0[i]), __uint_as_float(v1[i])));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c * 64 + i < lim) mx = fmaxf(mx, __uint_as_float(v0[i]));
-            if (c * 64 + 32 + i < lim) mx = fmaxf(mx, __uint_as_float(v1[i]));
-          }
-        }
+        for (int i = 0; i < kTileKeys; ++i)
+          if (i >= lim) v[i >> 5][i & 31] = 0xff800000u;  // -inf
       }
-      mx *= a.scale_log2;
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < kTileKeys; ++i)
+        mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[i >> 5][i & 31]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
       // The reference max m moves only when the step's max exceeds it by more
       // than 2^8; O and l keep the same stale reference, so this is exact, and
-      // P <= 2^8 is well inside bf16's range.  S(j) complete implies that PV(j
-      // - 1) is (it was issued earlier): O may be rescaled here.
+      // P <= 2^8 is well inside bf16's range.
       float alpha = 1.f;
       bool rescale = false;
       if (mx > m + 8.0f) {
@@ -479,55 +570,46 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
         alpha = fast_exp2(m - mx);  // 0 while m is -inf
         m = mx;
       }
-      if (__any_sync(0xffffffffu, rescale)) {
-        l *= alpha;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(o_col + c * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-          tmem_st32(o_col + c * 32, v);
-        }
-      }
       const float mu = m == -INFINITY ? 0.f : m;
       const float2 negm = make_float2(-mu, -mu);
       float2 sum2 = make_float2(0.f, 0.f);
+      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < kTileKeys / 64; ++c) {
-        uint32_t v[2][32], w[32];
-        tmem_ld32(s_col + c * 64, v[0]);
-        tmem_ld32(s_col + c * 64 + 32, v[1]);
-        tmem_ld_wait();
-        if (lim < kTileKeys) {
+      for (int i = 0; i < 32; ++i) {
+        const float2 x = make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
+                                     __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
+        const float2 y = __ffma2_rn(x, scale2, negm);
+        const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+        sum2 = __fadd2_rn(sum2, p);
+        w[i] = pack_bf16x2(p.x, p.y);
+      }
+      tmem_st32(s_col, w);  // P over the S columns, which this thread has read
+      if (__any_sync(0xffffffffu, rescale)) {
+        // The step before is in O.  (One phase back at most: S(n) was issued
+        // after PV(n - 2) and is complete.)
+        if (!mbar_wait(&bars[P_PVDONE], (n - 1) & 1, a.status)) return;
+        tc_fence_after();
+        l *= alpha;
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (c * 64 + i >= lim) v[i >> 5][i & 31] = 0xff800000u;  // -inf
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_col + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(o_col + c * 32, o);
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 x = make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
-                                       __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
-          const float2 y = __ffma2_rn(x, scale2, negm);
-          const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          sum2 = __fadd2_rn(sum2, p);
-          w[i] = pack_bf16x2(p.x, p.y);
-        }
-        // P over S columns that this thread has read already.
-        tmem_st32(s_col + c * 32, w);
       }
       l += sum2.x + sum2.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[P_PFULL]);
+      if (lane == 0) mbar_arrive(&bars[P_PFULL + (n & 1)]);
     }
     // The segment's partials: O, m, l of the tile's rows.
-    if (!mbar_wait(&bars[P_PVDONE], segs & 1, a.status)) return;
+    if (!mbar_wait(&bars[P_ODONE], segs & 1, a.status)) return;
     ++segs;
     tc_fence_after();
-    const bool valid = r < sg.nseq * G;
     float* row = valid ? a.prefix_part + (sg.row0 + r) * S : nullptr;
     if (valid) *reinterpret_cast<float2*>(row + D) = make_float2(m, l);
     const int qb = lane & ~3, jq = lane & 3;
@@ -559,7 +641,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPrefixThreads, 2)
+__global__ void __maxnreg__(PREFIX_REGS)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
@@ -573,23 +655,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 2)
   sg.t = 0;
   // (A plan of another shape is reported by the own-part kernel.)
   if (plan_fits(a)) {
-    const long long total = a.num_kv_heads * a.plan.head->steps;
-    const long long chunk = chunk_of(total, gridDim.x, kLeastSteps);
+    const long long total = a.plan.head->prefix_total, chunk = a.plan.head->prefix_chunk;
     sg.pos = chunk * blockIdx.x;
     sg.end = sg.pos + chunk < total ? sg.pos + chunk : total;
+    if (sg.pos < sg.end) sg.t = a.plan.cta_tile[blockIdx.x];
   }
   if (sg.pos < sg.end && !(smem_u32(smem) & 1023u)) {
-    // The tile that holds the first step: the last one that starts at or before it.
-    const int tiles = a.plan.head->num_tiles;
-    for (int t0 = 0; t0 < tiles; t0 += kPrefixThreads) {
-      const int t = t0 + (int)threadIdx.x;
-      sg.t += __syncthreads_count(t < tiles && a.num_kv_heads * a.plan.cum_steps[t] <= sg.pos);
-    }
-    --sg.t;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + P_BARS);
     if (threadIdx.x == 0) {
-      for (int i = 0; i < P_BARS; ++i) mbar_init(&bars[i], i == P_PFULL || i == P_OFREE ? 4 : 1);
+      for (int i = 0; i < P_BARS; ++i) mbar_init(&bars[i], i == P_PFULL || i == P_PFULL + 1 || i == P_OFREE ? 4 : 1);
       fence_mbar_init();
     }
     if (warp == 5) {
@@ -613,8 +688,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 2)
   } else if (sg.pos < sg.end && threadIdx.x == 0) {
     record_error(a.status, KVP_ERR_DEVICE_DATA);  // the 128-byte swizzle needs a 1 KiB aligned base
   }
-  // Launched beside the own-part kernel: do not complete before it.
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The grid, launched beside the own-part kernel, must not complete before it.
+  // One CTA waits for it, the others leave at once: their SMs take the CTAs
+  // that did not fit beside the own-part kernel at first.
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // --------------------------------------------- each sequence's own part
@@ -629,6 +707,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 2)
 // stage that ends at a sequence's last token takes that token's K / V row
 // from the new rows, and the producer warp writes them to the cache.
 
+#ifndef OWN_REGS
+#define OWN_REGS 96
+#endif
+#ifndef OWN_STAGES
+#define OWN_STAGES 4
+#endif
 constexpr int kOwnWarps = 8;  // consumer warps
 constexpr int kOwnThreads = (kOwnWarps + 1) * 32;
 constexpr int kStageRows = 64;  // tokens x kv heads of a stage
@@ -642,7 +726,7 @@ struct StageMeta {
 template <int D>
 struct OwnLayout {
   static constexpr uint32_t kHalf = kStageRows * D * 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? OWN_STAGES : 8;
   static constexpr uint32_t kMeta = 2 * kStages * kHalf;
   static constexpr uint32_t kBar = kMeta + kStages * (uint32_t)sizeof(StageMeta);
   static constexpr uint32_t kAlloc = kBar + 2 * kStages * 8;
@@ -650,24 +734,6 @@ struct OwnLayout {
 // One CTA of each kernel, or two of the prefix kernel, fit an SM (228 KiB,
 // 1 KiB of it per CTA reserved).
 static_assert(OwnLayout<128>::kAlloc + PrefixLayout<128>::kAlloc + 2048 <= 228 * 1024, "smem");
-static_assert(2 * PrefixLayout<128>::kAlloc + 2048 <= 228 * 1024, "smem");
-
-// Last index i of the non-decreasing v[0 .. n) with v[i] <= x (v[0] <= x), by
-// one warp: 32 probes a round.
-__device__ int last_at_most(const long long* v, int n, long long x) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;  // the answer is in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < hi && v[i] <= x);
-    const int k = 31 - __clz(le);  // v is sorted: lanes 0 .. k
-    const int nlo = lo + k * step;
-    hi = min(hi, nlo + step);
-    lo = nlo;
-  }
-  return lo;
-}
 
 template <int D>
 __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const CUtensorMap* tmK,
@@ -677,60 +743,108 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
   constexpr int RS = Lay::kStages;
   const int lane = threadIdx.x & 31;
   const int Hkv = a.num_kv_heads, T = kStageRows / Hkv, bs = a.block_size;
-  const long long total = a.plan.head->tokens;
-  const long long chunk = chunk_of(total, gridDim.x, kLeastTokens);
+  const int shift = __ffs(bs) - 1;  // block_size is a power of two
+  const long long total = a.plan.head->own_total, chunk = a.plan.head->own_chunk;
   long long pos = chunk * blockIdx.x;
   const long long end = pos + chunk < total ? pos + chunk : total;
-  int b = pos < end ? last_at_most(a.plan.cum_tokens, a.num_seqs, pos) : 0;
   uint8_t *ringK = smem, *ringV = smem + RS * Lay::kHalf;
+  int s = 0;
+  uint32_t ph = 0, issued = 0, issued_ph = 0;
+  bool ok = true;
+  // Read once: these keys must not push the shared prefixes out of L2.
+  const uint64_t once = policy_evict_first();
   if (lane == 0) {
     prefetch_tensormap(tmK);
     prefetch_tensormap(tmV);
-    int s = 0;
-    uint32_t ph = 0, issued = 0, issued_ph = 0;
-    bool ok = true;
-    for (; ok && pos < end; ++b) {
-      const long long c0 = a.plan.cum_tokens[b], c1 = a.plan.cum_tokens[b + 1];
-      if (c1 <= pos) continue;
-      const int start = a.plan.prefix[b], ctx = a.plan.ctx[b];
-      int t = start + (int)(pos - c0);
-      const int t1 = start + (int)((end < c1 ? end : c1) - c0);
+  }
+  if (pos < end) {
+    // Lane i knows sequence base + i; the pages of the current window of the
+    // current sequence are one per lane, and the next sequence's first window
+    // is loaded ahead.
+    int base = a.plan.cta_seq[blockIdx.x], b = base;
+    long long seq_end;
+    int ctx, own;  // context length; tokens of its own
+    auto load_seqs = [&]() {
+      const int i = base + lane;
+      const bool in = i < a.num_seqs;
+      seq_end = in ? a.plan.cum_tokens[i + 1] : 0;
+      ctx = in ? a.plan.ctx[i] : 0;
+      own = in ? ctx - a.plan.prefix[i] : 0;
+    };
+    auto load_pages = [&](int seq, int page, int last) {
+      return page + lane <= last ? a.block_tables[(int64_t)seq * a.max_blocks + page + lane] : -1;
+    };
+    load_seqs();
+    int ahead = 0, ahead_seq = -1;
+    while (ok && pos < end) {
+      if (b - base == 32) {
+        base = b;
+        load_seqs();
+      }
+      const long long c1 = __shfl_sync(0xffffffffu, seq_end, b - base);
+      const int L = __shfl_sync(0xffffffffu, ctx, b - base);
+      const long long c0 = c1 - __shfl_sync(0xffffffffu, own, b - base);  // its first token
+      if (pos < c0) pos = c0;
+      if (pos >= end) break;
+      if (c1 <= pos) {  // no tokens of its own (a padding row)
+        ++b;
+        continue;
+      }
+      int t = L - (int)(c1 - pos);
       pos = end < c1 ? end : c1;
+      const int t1 = L - (int)(c1 - pos);
+      const int last_page = (t1 - 1) >> shift;
+      int page0 = t >> shift;
+      int pages = ahead_seq == b ? ahead : load_pages(b, page0, last_page);
+      ahead_seq = -1;
+      if (b + 1 - base < 32 && b + 1 < a.num_seqs) {
+        const int L1 = __shfl_sync(0xffffffffu, ctx, b + 1 - base);
+        const int o1 = __shfl_sync(0xffffffffu, own, b + 1 - base);
+        const long long c2 = __shfl_sync(0xffffffffu, seq_end, b + 1 - base);
+        if (o1 > 0 && c2 - o1 < end) {
+          const int n1 = L1 - (int)(c2 - (end < c2 ? end : c2));
+          ahead = load_pages(b + 1, (L1 - o1) >> shift, (n1 - 1) >> shift);
+          ahead_seq = b + 1;
+        }
+      }
       bool first = true;
-      int page = -1, phys = 0;
       while (t < t1) {
-        const int bi = t / bs, off = t - bi * bs;
+        const int page = t >> shift, off = t & (bs - 1);
+        if (page - page0 == 32) {
+          page0 = page;
+          pages = load_pages(b, page0, last_page);
+        }
         int n = bs - off;
         if (n > T) n = T;
         if (n > t1 - t) n = t1 - t;
-        if (bi != page) {
-          page = bi;
-          phys = a.block_tables[(int64_t)b * a.max_blocks + bi];
-          if (phys < 0 || phys >= a.num_blocks) {
-            record_error(a.status, KVP_ERR_DEVICE_DATA);
-            phys = 0;  // never address a block outside the pool
-          }
+        int phys = __shfl_sync(0xffffffffu, pages, page - page0);
+        if (phys < 0 || phys >= a.num_blocks) {
+          if (lane == 0) record_error(a.status, KVP_ERR_DEVICE_DATA);
+          phys = 0;  // never address a block outside the pool
         }
         if (!mbar_wait(&empty[s], ph ^ 1u, a.status)) {
           ok = false;
           break;
         }
-        const bool tail = app.k_new != nullptr && t + n == ctx;
-        meta[s] = StageMeta{b, n, (first ? F_NEW : 0) | (t + n == t1 ? F_LAST : 0) | (tail ? F_TAIL : 0), 0};
-        uint8_t *dk = ringK + s * Lay::kHalf, *dv = ringV + s * Lay::kHalf;
-        mbar_arrive_expect_tx(&full[s], 2 * Lay::kHalf);
-        const int row = phys * bs + off;
-        // Rows past n (of the next page, or past the pool) are masked by the consumers.
-        if (!a.tma_per_head) {
-          tma_load_4d(dk, tmK, 0, row, 0, 0, &full[s]);
-          tma_load_4d(dv, tmV, 0, row, 0, 0, &full[s]);
-        } else {
-          for (int h = 0; h < Hkv; ++h)
-            for (int p = 0; p < D / 64; ++p) {
-              const uint32_t at = (uint32_t)((h * (D / 64) + p) * T * 128);
-              tma_load_3d(dk + at, tmK, p * 64, h, row, &full[s]);
-              tma_load_3d(dv + at, tmV, p * 64, h, row, &full[s]);
-            }
+        if (lane == 0) {
+          const bool tail = app.k_new != nullptr && t + n == L;
+          meta[s] = StageMeta{
+              b, n, (first ? F_NEW : 0) | (t + n == t1 ? F_LAST : 0) | (tail ? F_TAIL : 0), 0};
+          uint8_t *dk = ringK + s * Lay::kHalf, *dv = ringV + s * Lay::kHalf;
+          mbar_arrive_expect_tx(&full[s], 2 * Lay::kHalf);
+          const int row = (phys << shift) + off;
+          // Rows past n (of the next page, or past the pool) are masked by the consumers.
+          if (!a.tma_per_head) {
+            tma_load_4d_hint(dk, tmK, 0, row, 0, 0, &full[s], once);
+            tma_load_4d_hint(dv, tmV, 0, row, 0, 0, &full[s], once);
+          } else {
+            for (int h = 0; h < Hkv; ++h)
+              for (int p = 0; p < D / 64; ++p) {
+                const uint32_t at = (uint32_t)((h * (D / 64) + p) * T * 128);
+                tma_load_3d_hint(dk + at, tmK, p * 64, h, row, &full[s], once);
+                tma_load_3d_hint(dv + at, tmV, p * 64, h, row, &full[s], once);
+              }
+          }
         }
         issued |= 1u << s;
         issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
@@ -741,15 +855,18 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
           ph ^= 1u;
         }
       }
+      ++b;
     }
-    if (ok && mbar_wait(&empty[s], ph ^ 1u, a.status)) {
+  }
+  if (ok && mbar_wait(&empty[s], ph ^ 1u, a.status)) {
+    if (lane == 0) {
       meta[s].flags = F_DONE;
       mbar_arrive(&full[s]);
-    } else {
-      // A wait expired: let every copy this CTA issued land before the CTA exits.
-      for (int i = 0; i < RS; ++i)
-        if (issued >> i & 1u) mbar_wait(&full[i], issued_ph >> i & 1u, a.status);
     }
+  } else {
+    // A wait expired: let every copy this CTA issued land before the CTA exits.
+    for (int i = 0; i < RS; ++i)
+      if (issued >> i & 1u) mbar_wait(&full[i], issued_ph >> i & 1u, a.status);
   }
   __syncwarp();
   if (app.k_new == nullptr) return;
@@ -923,7 +1040,7 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kOwnThreads, 2)
+__global__ void __maxnreg__(OWN_REGS)
     shared_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const SharedArgs a, const SharedAppend app) {
   using Lay = OwnLayout<D>;
@@ -954,107 +1071,178 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 // ----------------------------------------------------------------- merge
 //
 // out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p over a row's partials:
-// one warp per (sequence, query head), a lane per D / 32 elements.  Launched
-// as a programmatic dependent of the prefix kernel: its plan look-ups overlap
-// the kernels before it.
+// W warps per (sequence, query head), a lane per D / 32 elements.  Launched as
+// a programmatic dependent of the prefix kernel: its plan look-ups overlap the
+// kernels before it.  Few rows (a small batch has many parts per row and too
+// few rows to fill the SMs): four warps share a row's parts.
 
 constexpr int kMergeWarps = 8;
+constexpr long long kWideMergeRows = 8192;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const SharedArgs a) {
+// x / y for the plan's work positions, which nearly always fit 32 bits.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// One row (sequence b, query head h) by W warps; `hand` passes the sums of the
+// row's warps to the first of them.
+template <int D, int W>
+__device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int lane, int warp, int wi,
+                                          int ns, long long orow, int hg, int st, long long first,
+                                          long long pchunk, long long prow, float4 (*hand)[33]) {
   constexpr int E = D / 32, S = part_stride<D>();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const bool real = row < (long long)a.num_seqs * a.num_heads && plan_fits(a);
-  int b = 0, h = 0, np = 0, ns = 0;
-  long long prow = 0, orow = 0;  // first part's row; parts of a kind are a fixed distance apart
-  const int Hkv = a.num_kv_heads, G = a.num_heads / Hkv, NS = kOwnWarps / Hkv;
-  bool some = false;
-  if (real) {
-    b = (int)(row / a.num_heads);
-    h = (int)(row - (long long)b * a.num_heads);
-    const int g = h / G;
-    some = a.plan.ctx[b] > 0;
-    if (some) {
-      const long long chunk = chunk_of(a.plan.head->tokens, a.own_ctas, kLeastTokens);
-      const long long c0 = a.plan.cum_tokens[b] / chunk, c1 = (a.plan.cum_tokens[b + 1] - 1) / chunk;
-      ns = (int)(c1 - c0 + 1) * NS;
-      orow = (b + c0) * NS * a.num_heads + h;
-      const int t = a.plan.tile_of[b];
-      if (t >= 0) {
-        const long long pchunk = chunk_of(Hkv * a.plan.head->steps, a.prefix_ctas, kLeastSteps);
-        const long long s0 = a.plan.cum_steps[t], st = a.plan.cum_steps[t + 1] - s0;
-        const long long first = Hkv * s0 + g * st;
-        const long long p0 = first / pchunk, p1 = (first + st - 1) / pchunk;
-        const int r0 = a.plan.cum_rows[t], n = a.plan.cum_rows[t + 1] - r0;
-        np = (int)(p1 - p0 + 1);
-        prow = (long long)Hkv * G * r0 + (long long)g * n * G + p0 * kTileRows +
-               (long long)(b - a.plan.tile_seq[t]) * G + h % G;
-      }
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!real) return;
-  __nv_bfloat16* out =
-      reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)b * a.out_stride + (int64_t)h * D + lane * E;
   float acc[E], M = -INFINITY, den = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (some) {
-    const int parts = np + ns;
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      // Lane k has part k0 + k: its address, m and l.
-      const int k = k0 + lane;
-      const float* mine = nullptr;
-      float mk = -INFINITY, lk = 0.f;
-      if (k < parts) {
-        mine = k < np ? a.prefix_part + (prow + (long long)k * kTileRows) * S
-                      : a.own_part + (orow + (long long)(k - np) * a.num_heads) * S;
-        const float2 ml = *reinterpret_cast<const float2*>(mine + D);
-        mk = ml.x;
-        lk = ml.y;
-      }
-      float mx = mk;
+  // Prefix parts: one per CTA that steps [first, first + st) reach; each CTA's
+  // rows start 128 rows after the one before's.
+  int np = 0;
+  if (st > 0) {
+    const long long p0 = quotient(first, pchunk);
+    np = (int)(quotient(first + st - 1, pchunk) - p0) + 1;
+    prow += p0 * kTileRows + hg;
+  }
+  const int parts = np + ns;
+  // Warp wi of the row takes parts wi, wi + W, ...; lane i has the address, m
+  // and l of the i-th of them.
+  for (int k0 = wi; k0 < parts; k0 += 32 * W) {
+    const int k = k0 + lane * W;
+    const float* mine = nullptr;
+    float mk = -INFINITY, lk = 0.f;
+    if (k < parts) {
+      mine = k < np ? a.prefix_part + (prow + (long long)k * kTileRows) * S
+                    : a.own_part + (orow + (long long)(k - np) * a.num_heads) * S;
+      const float2 ml = *reinterpret_cast<const float2*>(mine + D);
+      mk = ml.x;
+      lk = ml.y;
+    }
+    const int n = min(32, (parts - k0 + W - 1) / W);
+    // The accumulators of up to 8 parts are on their way before m and l arrive.
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float v[8][E];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float Mn = fmaxf(M, mx);
-      const float mu = Mn == -INFINITY ? 0.f : Mn;
-      const float alpha = fast_exp2(M - mu), w = fast_exp2(mk - mu);
-      M = Mn;
-      float lw = w * lk;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-      den = den * alpha + lw;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= alpha;
-      const int n = min(32, parts - k0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
+      for (int i = 0; i < 8; ++i) {
         const float* p = reinterpret_cast<const float*>(
-                             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i)) +
-                         lane * E;
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31));
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+        if (i0 + i < n) {
+          if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + lane * E);
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(p + lane * E);
+            v[i][0] = x.x, v[i][1] = x.y;
+          }
+        }
+      }
+      if (i0 == 0) {
+        float mx = mk;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float Mn = fmaxf(M, mx);
+        const float mu = Mn == -INFINITY ? 0.f : Mn;
+        const float alpha = fast_exp2(M - mu);
+        mk = fast_exp2(mk - mu);  // from here on the part's weight
+        M = Mn;
+        float lw = mk * lk;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        den = den * alpha + lw;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= alpha;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __shfl_sync(0xffffffffu, mk, (i0 + i) & 31);
+        if (i0 + i < n)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += w * v[i][e];
+      }
+    }
+  }
+  if constexpr (W > 1) {
+    // The row's warps hand their sums to the first of them.
+    float4 mine = make_float4(0.f, 0.f, 0.f, 0.f);
+    mine.x = acc[0];
+    mine.y = acc[1];
+    if constexpr (E == 4) {
+      mine.z = acc[2];
+      mine.w = acc[3];
+    }
+    hand[warp][lane] = mine;
+    if (lane == 0) hand[warp][32] = make_float4(M, den, 0.f, 0.f);
+    named_barrier_sync(1 + warp / W, W * 32);
+    if (wi == 0) {
+#pragma unroll
+      for (int j = 1; j < W; ++j) M = fmaxf(M, hand[warp + j][32].x);
+      const float mu = M == -INFINITY ? 0.f : M;
+      den = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float4 ml = hand[warp + j][32], v = hand[warp + j][lane];
+        const float w = fast_exp2(ml.x - mu);
+        den += w * ml.y;
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
         if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p);
-          acc[0] += wi * v.x;
-          acc[1] += wi * v.y;
-          acc[2] += wi * v.z;
-          acc[3] += wi * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(p);
-          acc[0] += wi * v.x;
-          acc[1] += wi * v.y;
+          acc[2] += w * v.z;
+          acc[3] += w * v.w;
         }
       }
     }
-    const float inv = 1.f / den;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= inv;
+    named_barrier_sync(1 + warp / W, W * 32);  // the buffer is free for the next row
+    if (wi != 0) return;
   }
+  const float inv = parts > 0 ? 1.f / den : 0.f;
+  __nv_bfloat16* out =
+      reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)b * a.out_stride + (int64_t)h * D + lane * E;
   if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0], acc[1]);
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+template <int D, int W>
+__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const SharedArgs a,
+                                                                        int heads) {
+  __shared__ float4 hand[W > 1 ? kMergeWarps : 1][33];  // acc of each lane; {M, den, 0, 0}
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp % W;
+  const int Hkv = a.num_kv_heads, G = a.num_heads / Hkv, NS = kOwnWarps / Hkv;
+  const int blocks = a.num_heads / heads;  // of a sequence
+  const int b = (int)(blockIdx.x / (unsigned)blocks);
+  const int h0 = (int)(blockIdx.x % (unsigned)blocks) * heads;
+  const bool fits = plan_fits(a);
+  int ns = 0;
+  long long orow = 0, prow = 0, first = 0, pchunk = 1;
+  int st = 0, rows_of_item = 0;
+  if (fits) {
+    const long long k1 = a.plan.cum_tokens[b + 1];
+    const int own = a.plan.ctx[b] - a.plan.prefix[b];
+    const int t = a.plan.tile_of[b];
+    if (own > 0) {  // every sequence with a context has tokens of its own
+      const long long chunk = a.plan.head->own_chunk;
+      const long long c0 = quotient(k1 - own, chunk), c1 = quotient(k1 - 1, chunk);
+      ns = (int)(c1 - c0 + 1) * NS;
+      orow = (b + c0) * NS * a.num_heads;
+    }
+    if (t >= 0) {
+      pchunk = a.plan.head->prefix_chunk;
+      first = a.plan.cum_steps[t];
+      st = (int)((a.plan.cum_steps[t + 1] - first) / Hkv);
+      const int r0 = a.plan.cum_rows[t];
+      rows_of_item = (a.plan.cum_rows[t + 1] - r0) * G;
+      prow = (long long)Hkv * G * r0 + (long long)(b - a.plan.tile_seq[t]) * G;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!fits) return;
+  for (int h = h0 + warp / W; h < h0 + heads; h += kMergeWarps / W)
+    merge_row<D, W>(a, b, h, lane, warp, wi, ns, orow + h, h % G, st, first + (long long)(h / G) * st,
+                    pchunk, prow + (long long)(h / G) * rows_of_item, hand);
 }
 
 // Launches a kernel, as a programmatic dependent of the stream's previous one
@@ -1062,8 +1250,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const Sh
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), unsigned grid, int threads, size_t smem, bool pdl,
                    cudaStream_t stream, Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The split kernels share SMs: without this an SM is set up with as much
+    // shared memory as the first of them needs, and the other does not fit.
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -1081,27 +1276,30 @@ template <int D, int G>
 cudaError_t launch_shared_t(const CUtensorMap& mq, const CUtensorMap& mpk, const CUtensorMap& mpv,
                             const CUtensorMap& mok, const CUtensorMap& mov, const SharedArgs& a,
                             const SharedAppend& app, cudaStream_t stream) {
-  cudaError_t e = launch(shared_own_kernel<D, G>, a.own_ctas, kOwnThreads, OwnLayout<D>::kAlloc, false,
+  cudaError_t e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, false,
                          stream, mok, mov, a, app);
   if (e != cudaSuccess) return e;
-  e = launch(shared_prefix_kernel<D>, a.prefix_ctas, kPrefixThreads, PrefixLayout<D>::kAlloc, true,
+  e = launch(shared_prefix_kernel<D>, prefix_ctas(a.sms), kPrefixThreads, PrefixLayout<D>::kAlloc, true,
              stream, mq, mpk, mpv, a);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.num_seqs * a.num_heads;
-  return launch(shared_merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
-                kMergeWarps * 32, 0, true, stream, a);
+  // Few rows: four warps a row, two rows a block; else a block per sequence
+  // and a warp per row (or as many of either as there are heads).
+  const bool wide = (long long)a.num_seqs * a.num_heads < kWideMergeRows;
+  const int heads = wide && a.num_heads > 2 ? 2 : a.num_heads;
+  return launch(wide ? shared_merge_kernel<D, 4> : shared_merge_kernel<D, 1>,
+                (unsigned)(a.num_seqs * (a.num_heads / heads)), kMergeWarps * 32, 0, true, stream, a, heads);
 }
 
 }  // namespace
 
 // ------------------------------------------------------------- host side
 
-size_t shared_plan_bytes(int num_seqs) {
+size_t shared_plan_bytes(int num_seqs, int num_sms) {
   const size_t B = (size_t)num_seqs;
-  return (sizeof(SharedPlanHead) + 16 * (B + 1) + 4 * (8 * B + 2) + 255) / 256 * 256;
+  return (sizeof(SharedPlanHead) + 16 * (B + 1) + 4 * (8 * B + 2 + 3 * num_sms) + 255) / 256 * 256;
 }
 
-SharedPlan shared_plan_view(void* base, int num_seqs) {
+SharedPlan shared_plan_view(void* base, int num_seqs, int num_sms) {
   const size_t B = (size_t)num_seqs;
   SharedPlan p;
   p.head = static_cast<SharedPlanHead*>(base);
@@ -1115,18 +1313,32 @@ SharedPlan shared_plan_view(void* base, int num_seqs) {
   p.same = p.cum_rows + B + 1;
   p.group_min = p.same + B;
   p.group_seq = p.group_min + B;
+  p.cta_seq = p.group_seq + B;
+  p.cta_tile = p.cta_seq + own_ctas(num_sms);
   return p;
 }
 
 cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, const int32_t* ctx,
                                int num_seqs, int64_t num_blocks, int block_size, int group,
                                int num_kv_heads, int min_shared_len, const SharedPlan& plan,
-                               int* status, cudaStream_t stream) {
+                               int num_sms, int* status, cudaStream_t stream) {
   const PlanArgs a{block_tables, ctx,   max_blocks,   num_seqs,       num_blocks,
-                   block_size,   group, num_kv_heads, min_shared_len, plan,
-                   status};
-  shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+                   block_size,   group, num_kv_heads, own_gap(num_kv_heads), min_shared_len, num_sms,
+                   plan,         status};
+  // A warp compares one pair of rows at a time: up to 8 CTAs (a portable cluster).
+  int ctas = 1;
+  while (ctas < 8 && ctas * (kPlanThreads / 32) < num_seqs) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
 }
 
 // Rows of partial results: see chunk_of.
@@ -1139,8 +1351,8 @@ static size_t own_rows(int num_seqs, int num_heads, int num_kv_heads, int ctas) 
 
 size_t shared_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                               int num_sms) {
-  const size_t rows = prefix_rows(num_seqs, num_heads, 2 * num_sms) +
-                      own_rows(num_seqs, num_heads, num_kv_heads, num_sms);
+  const size_t rows = prefix_rows(num_seqs, num_heads, prefix_ctas(num_sms)) +
+                      own_rows(num_seqs, num_heads, num_kv_heads, own_ctas(num_sms));
   return rows * (head_dim + 4) * sizeof(float);
 }
 
@@ -1160,10 +1372,9 @@ cudaError_t launch_decode_shared(const SharedCall& c, const SharedPlan& plan,
   a.num_kv_heads = Hkv;
   a.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   a.plan = plan;
-  a.prefix_ctas = 2 * num_sms;
-  a.own_ctas = num_sms;
+  a.sms = num_sms;
   a.prefix_part = static_cast<float*>(c.workspace);
-  a.own_part = a.prefix_part + prefix_rows(c.num_seqs, c.num_heads, a.prefix_ctas) * (D + 4);
+  a.own_part = a.prefix_part + prefix_rows(c.num_seqs, c.num_heads, prefix_ctas(num_sms)) * (D + 4);
   a.out = c.out;
   a.out_stride = c.out_stride;
   a.status = status;

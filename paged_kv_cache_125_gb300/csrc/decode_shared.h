@@ -13,15 +13,21 @@ namespace kvp {
 // need to know about the batch, for num_seqs = B sequences.
 struct SharedPlanHead {
   int magic, num_seqs, group, num_kv_heads;  // the shape the plan was made for
-  int block_size, max_blocks, num_tiles, pad;
-  long long steps;   // prefix steps of 128 keys of all tiles (per kv head)
-  long long tokens;  // suffix tokens of all sequences
+  int block_size, max_blocks, num_tiles;
+  int sms;                 // SMs of the device it was made on
+  int gap, pad;            // positions before each sequence's own tokens (see own_gap)
+  long long prefix_chunk;  // steps per CTA of the prefix kernel, of prefix_total
+  long long prefix_total;
+  long long own_chunk;     // positions per CTA of the own-part kernel, of own_total
+  long long own_total;
 };
 
 struct SharedPlan {
   SharedPlanHead* head;
-  long long* cum_tokens;  // [B + 1] suffix tokens of the sequences before b
-  long long* cum_steps;   // [B + 1] prefix steps of the tiles before t
+  long long* cum_tokens;  // [B + 1] positions (gap + own tokens) of the sequences before b
+  long long* cum_steps;   // [B + 1] prefix steps of the tiles before t, all kv heads
+  int* cta_seq;           // [sms] sequence that own-part CTA c starts in
+  int* cta_tile;          // [2 * sms] tile that prefix CTA c starts in
   int* ctx;               // [B] context length (0: no row)
   int* prefix;            // [B] keys read with the group, [0, prefix)
   int* tile_of;           // [B] tile of sequence b, or -1 (prefix 0)
@@ -32,13 +38,13 @@ struct SharedPlan {
   int* group_seq;         // [B] plan kernel: first sequence of a group
 };
 
-size_t shared_plan_bytes(int num_seqs);
-SharedPlan shared_plan_view(void* base, int num_seqs);
+size_t shared_plan_bytes(int num_seqs, int num_sms);
+SharedPlan shared_plan_view(void* base, int num_seqs, int num_sms);
 
 cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, const int32_t* ctx,
                                int num_seqs, int64_t num_blocks, int block_size, int group,
                                int num_kv_heads, int min_shared_len, const SharedPlan& plan,
-                               int* status, cudaStream_t stream);
+                               int num_sms, int* status, cudaStream_t stream);
 
 size_t shared_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                               int num_sms);

@@ -97,7 +97,7 @@ class Batch:
 def plan_prefixes(plan, b):
     """The prefix lengths in a plan, at their place in its layout."""
     raw = plan.cpu().numpy().tobytes()
-    head = 8 * 4 + 2 * 8
+    head = 10 * 4 + 4 * 8
     return np.frombuffer(raw, np.int32, b, head + 16 * (b + 1) + 4 * b).tolist()
 
 
@@ -322,6 +322,22 @@ def test_empty_batch():
     assert kvp.attn_decode_shared(e, w.kc, w.vc, bt, plan).shape == (0, 16, 128)
     torch.cuda.synchronize()
     assert_status_ok()
+
+
+def test_buffers_that_are_too_small_are_refused():
+    w = Batch((16, 8, 128), 16, [(10, [3, 4])], seed=8)
+    bt, plan = w.dev(w.tables), w.plan()
+    need = kvp.attn_shared_plan_size(2, 16, 8)
+    assert need < kvp.attn_shared_plan_size(512, 16, 8) and kvp.attn_shared_plan_size(0, 16, 8) > 0
+    small = torch.empty(need - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(kvp.KvpError, match="plan needs %d bytes" % need):
+        kvp.attn_shared_plan(bt, w.dev(w.lens), 16, 16, 8, w.nb, plan=small)
+    with pytest.raises(kvp.KvpError, match="plan needs %d bytes" % need):
+        kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, small)
+    need = kvp.attn_decode_shared_workspace_size(2, 16, 8, 128)
+    small = torch.empty(need - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(kvp.KvpError, match="workspace needs %d bytes" % need):
+        kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan, workspace=small)
 
 
 def test_wrong_metadata_is_reported():

@@ -37,14 +37,10 @@ def test_plan_validation(lib):
     assert _plan(lib, mb=1 << 20, bs=4096) == UNSUPPORTED and "capacity" in _err(lib)
     for name in ("bt", "ctx", "plan"):
         assert _plan(lib, **{name: None}) == INVALID and "null" in _err(lib)
-    need = kvp.attn_shared_plan_size(4, 16, 8)
-    assert _plan(lib, n=need - 1) == WORKSPACE and str(need) in _err(lib)
-    assert _plan(lib, plan=MIS) == WORKSPACE and "16-byte" in _err(lib)
+    assert _plan(lib, plan=MIS) == INVALID and "16-byte" in _err(lib)
 
 
 def test_sizes(lib):
-    assert kvp.attn_shared_plan_size(0, 16, 8) > 0
-    assert kvp.attn_shared_plan_size(512, 16, 8) > kvp.attn_shared_plan_size(4, 16, 8)
     assert kvp.kv_pages_workspace_size(1000, 10) > kvp.kv_pages_workspace_size(100, 10)
     for args in ((-1, 16, 8), (1 << 20, 16, 8), (4, 24, 8)):
         with pytest.raises(kvp.KvpError, match="bad shape"):
@@ -86,7 +82,6 @@ def test_decode_validation(lib, append):
         assert _decode(lib, append, **{n: MIS}) == INVALID and "16-byte" in _err(lib), n
     for n in ["qs", "os"] + (["ks", "vs"] if append else []):
         assert _decode(lib, append, **{n: 16 * 128 + 4}) == INVALID and "multiples" in _err(lib), n
-    assert _decode(lib, append, pn=64) == WORKSPACE and "plan needs" in _err(lib)
 
 
 def _pages(lib, op, **kw):
