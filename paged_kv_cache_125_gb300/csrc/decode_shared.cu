@@ -2,6 +2,7 @@
 // sequences share leading pages.
 #include "decode_shared.h"
 
+#include <atomic>
 #include <type_traits>
 
 #include "kvp_device.cuh"
@@ -131,18 +132,20 @@ __device__ int shared_pages(const PlanArgs& a, int b, int prev_ctx, int ctx) {
 // enough of them, and not less than half of what either neighbour shares
 // (a page or two that all requests have in common, e.g. a short system
 // prompt, must not join groups that share much more among themselves).
-__device__ __forceinline__ bool plan_joined(const PlanArgs& a, int b, int same) {
+__device__ __forceinline__ bool plan_joined(const PlanArgs& a, int b, int prev, int same, int next) {
   if (b == 0 || same == 0 || (int64_t)same * a.block_size < a.min_shared) return false;
-  const int prev = __ldcg(&a.plan.same[b - 1]);
-  const int next = b + 1 < a.num_seqs ? __ldcg(&a.plan.same[b + 1]) : 0;
   return 2 * (int64_t)same >= max(prev, next);
 }
 
 // One cluster.  The warps of all its CTAs compare the table rows; after a
-// cluster barrier CTA 0 forms the groups and tiles (a few prefix sums over the
-// sequences).
+// cluster barrier CTA 0 forms the groups and tiles by prefix sums over the
+// sequences, 1024 at a time.  The first 1024 sequences' shared-page counts and
+// groups stay in shared memory (later ones go through the plan buffer): the
+// kernel is a chain of small dependent steps, and each round trip to L2 that
+// it does without is 0.7 us of a step's latency.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArgs a) {
   __shared__ long long sums[3][32];
+  __shared__ int s_same[kPlanThreads + 2], s_min[kPlanThreads], s_seq[kPlanThreads];
   const SharedPlan& p = a.plan;
   const int B = a.num_seqs, bs = a.block_size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -152,7 +155,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     if (lane == 0) {
       p.ctx[b] = ctx;
       p.same[b] = same;
-      p.group_min[b] = 0x7fffffff;
     }
   }
   __threadfence();
@@ -161,43 +163,60 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
       "barrier.cluster.wait.acquire;" ::
           : "memory");
   if (blockIdx.x) return;
+
   // Groups: maximal runs of joined sequences; all of a group read the pages
   // that every one of them shares.
+  const bool small = B <= kPlanThreads;
+  int* group_min = small ? s_min : p.group_min;
+  int* group_seq = small ? s_seq : p.group_seq;
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) group_min[b] = 0x7fffffff;
+  int my_ctx = 0, my_group = 0;  // of sequence threadIdx.x
   long long groups = 0;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
-    const int same = b < B ? __ldcg(&p.same[b]) : 0;
-    const bool joined = b < B && plan_joined(a, b, same);
+    // (s_same[i]: sequence b0 - 1 + i)
+    s_same[threadIdx.x + 1] = b < B ? __ldcg(&p.same[b]) : 0;
+    if (threadIdx.x == 0) s_same[0] = b > 0 ? __ldcg(&p.same[b - 1]) : 0;
+    if (threadIdx.x == 1) s_same[kPlanThreads + 1] = b0 + kPlanThreads < B ? __ldcg(&p.same[b0 + kPlanThreads]) : 0;
+    if (b0 == 0 && b < B) my_ctx = __ldcg(&p.ctx[b]);
+    __syncthreads();
+    const int same = s_same[threadIdx.x + 1];
+    const bool joined =
+        b < B && plan_joined(a, b, s_same[threadIdx.x], same, s_same[threadIdx.x + 2]);
     long long v[1] = {b < B && !joined ? 1 : 0}, total[1];
     block_scan(v, total, sums);
     if (b < B) {
       const int g = (int)(groups + v[0]) - (joined ? 1 : 0);
-      p.tile_of[b] = g;
+      if (b0 == 0) my_group = g;
+      if (!small) p.tile_of[b] = g;
       if (joined)
-        atomicMin(&p.group_min[g], same);
+        atomicMin(&group_min[g], same);
       else
-        p.group_seq[g] = b;
+        group_seq[g] = b;
     }
     groups += total[0];
+    __syncthreads();
   }
-  __syncthreads();
+
   // Tiles of 128 query rows within a group, and the prefix sums the kernels
-  // find their work by: (tiles, sequences in tiles), steps, own tokens.
+  // find their work by: (tiles, sequences in tiles), steps, own positions.
   const int tile_seqs = kTileRows / a.group;
   long long base[3] = {0, 0, 0};
+  long long my_step = 0, my_pos = 0;  // sums before sequence threadIdx.x,
+  int my_steps = 0, my_len = 0, my_tile = -1;  // and what it adds to them
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
     int ctx = 0, prefix = 0;
     bool start = false;
     if (b < B) {
-      const int g = p.tile_of[b], m = __ldcg(&p.group_min[g]);
-      ctx = __ldcg(&p.ctx[b]);
+      const int g = small ? my_group : p.tile_of[b], m = *(volatile int*)&group_min[g];
+      ctx = small ? my_ctx : __ldcg(&p.ctx[b]);
       prefix = m == 0x7fffffff ? 0 : m * bs;
-      start = prefix > 0 && (b - p.group_seq[g]) % tile_seqs == 0;
+      start = prefix > 0 && (b - *(volatile int*)&group_seq[g]) % tile_seqs == 0;
     }
-    long long v[3] = {((long long)(start ? 1 : 0) << 32) | (prefix > 0 ? 1 : 0),
-                      start ? (long long)a.num_kv_heads * ((prefix + kTileKeys - 1) / kTileKeys) : 0,
-                      ctx > 0 ? a.gap + ctx - prefix : 0};
+    const int steps = start ? a.num_kv_heads * ((prefix + kTileKeys - 1) / kTileKeys) : 0;
+    const int len = ctx > 0 ? a.gap + ctx - prefix : 0;
+    long long v[3] = {((long long)(start ? 1 : 0) << 32) | (prefix > 0 ? 1 : 0), steps, len};
     long long total[3];
     block_scan(v, total, sums);
 #pragma unroll
@@ -211,6 +230,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
         p.tile_seq[t] = b;
         p.cum_rows[t] = (int)(v[0] & 0xffffffffll);
         p.cum_steps[t] = v[1];
+      }
+      if (b0 == 0) {
+        my_step = v[1];
+        my_pos = v[2];
+        my_steps = steps;
+        my_len = len;
+        my_tile = t;
       }
     }
   }
@@ -238,16 +264,35 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     h.own_total = base[2];
     *p.head = h;
   }
-  __syncthreads();
-  // Where each CTA starts: the sequence (tile) whose tokens (steps) hold its
-  // first one.
-  for (int b = threadIdx.x; b < B; b += kPlanThreads)
-    for (long long c = (p.cum_tokens[b] + ochunk - 1) / ochunk; c * ochunk < p.cum_tokens[b + 1]; ++c)
+  // Where each CTA starts: the sequence (tile) whose positions (steps) hold
+  // its first one.
+  if (!small) __syncthreads();  // the sums written above
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    if (!small) {
+      my_len = my_steps = 0;
+      if (b < B) {
+        my_pos = p.cum_tokens[b];
+        my_len = (int)(p.cum_tokens[b + 1] - my_pos);
+      }
+      my_tile = b;
+      if (b < tiles) {
+        my_step = p.cum_steps[b];
+        my_steps = (int)(p.cum_steps[b + 1] - my_step);
+      }
+    }
+    for (long long c = (my_pos + ochunk - 1) / ochunk; c * ochunk < my_pos + my_len; ++c)
       p.cta_seq[c] = b;
-  for (int t = warp; t < tiles; t += kPlanThreads / 32)
-    for (long long c = (p.cum_steps[t] + pchunk - 1) / pchunk + lane; c * pchunk < p.cum_steps[t + 1];
-         c += 32)
-      p.cta_tile[c] = t;
+    // A tile may hold many CTAs' starts: the warp's lanes take them together.
+    unsigned with = __ballot_sync(0xffffffffu, my_steps > 0);
+    while (with) {
+      const int i = __ffs(with) - 1;
+      with &= with - 1;
+      const long long st = __shfl_sync(0xffffffffu, my_step, i);
+      const int n = __shfl_sync(0xffffffffu, my_steps, i), t = __shfl_sync(0xffffffffu, my_tile, i);
+      for (long long c = (st + pchunk - 1) / pchunk + lane; c * pchunk < st + n; c += 32) p.cta_tile[c] = t;
+    }
+  }
 }
 
 // ------------------------------------------------------------- attention
@@ -1073,11 +1118,9 @@ __global__ void __maxnreg__(OWN_REGS)
 // out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p over a row's partials:
 // W warps per (sequence, query head), a lane per D / 32 elements.  Launched as
 // a programmatic dependent of the prefix kernel: its plan look-ups overlap the
-// kernels before it.  Few rows (a small batch has many parts per row and too
-// few rows to fill the SMs): four warps share a row's parts.
+// kernels before it.
 
 constexpr int kMergeWarps = 8;
-constexpr long long kWideMergeRows = 8192;
 
 // x / y for the plan's work positions, which nearly always fit 32 bits.
 __device__ __forceinline__ long long quotient(long long x, long long y) {
@@ -1091,6 +1134,7 @@ __device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int
                                           int ns, long long orow, int hg, int st, long long first,
                                           long long pchunk, long long prow, float4 (*hand)[33]) {
   constexpr int E = D / 32, S = part_stride<D>();
+  constexpr int U = 4;  // parts whose loads are in flight together
   float acc[E], M = -INFINITY, den = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1103,62 +1147,48 @@ __device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int
     prow += p0 * kTileRows + hg;
   }
   const int parts = np + ns;
-  // Warp wi of the row takes parts wi, wi + W, ...; lane i has the address, m
-  // and l of the i-th of them.
-  for (int k0 = wi; k0 < parts; k0 += 32 * W) {
-    const int k = k0 + lane * W;
-    const float* mine = nullptr;
-    float mk = -INFINITY, lk = 0.f;
-    if (k < parts) {
-      mine = k < np ? a.prefix_part + (prow + (long long)k * kTileRows) * S
-                    : a.own_part + (orow + (long long)(k - np) * a.num_heads) * S;
-      const float2 ml = *reinterpret_cast<const float2*>(mine + D);
-      mk = ml.x;
-      lk = ml.y;
-    }
-    const int n = min(32, (parts - k0 + W - 1) / W);
-    // The accumulators of up to 8 parts are on their way before m and l arrive.
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float v[8][E];
+  const float* pp = a.prefix_part + prow * S;
+  const float* op = a.own_part + orow * S;
+  const long long ostep = (long long)a.num_heads * S;
+  // Warp wi of the row takes parts wi, wi + W, ...; every lane has their m and l.
+  for (int k0 = wi; k0 < parts; k0 += U * W) {
+    float v[U][E], mk[U], lk[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* p = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (i0 + i) & 31));
+    for (int i = 0; i < U; ++i) {
+      const int k = k0 + i * W;
+      mk[i] = -INFINITY;
+      lk[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-        if (i0 + i < n) {
-          if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p + lane * E);
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(p + lane * E);
-            v[i][0] = x.x, v[i][1] = x.y;
-          }
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      if (k < parts) {
+        const float* p = k < np ? pp + (long long)k * kTileRows * S : op + (k - np) * ostep;
+        const float2 ml = *reinterpret_cast<const float2*>(p + D);
+        mk[i] = ml.x;
+        lk[i] = ml.y;
+        if constexpr (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p + lane * E);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(p + lane * E);
+          v[i][0] = x.x, v[i][1] = x.y;
         }
       }
-      if (i0 == 0) {
-        float mx = mk;
+    }
+    float Mn = M;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float Mn = fmaxf(M, mx);
-        const float mu = Mn == -INFINITY ? 0.f : Mn;
-        const float alpha = fast_exp2(M - mu);
-        mk = fast_exp2(mk - mu);  // from here on the part's weight
-        M = Mn;
-        float lw = mk * lk;
+    for (int i = 0; i < U; ++i) Mn = fmaxf(Mn, mk[i]);
+    const float mu = Mn == -INFINITY ? 0.f : Mn;
+    const float alpha = fast_exp2(M - mu);
+    M = Mn;
+    den *= alpha;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-        den = den * alpha + lw;
+    for (int e = 0; e < E; ++e) acc[e] *= alpha;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= alpha;
-      }
+    for (int i = 0; i < U; ++i) {
+      const float w = fast_exp2(mk[i] - mu);
+      den += w * lk[i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = __shfl_sync(0xffffffffu, mk, (i0 + i) & 31);
-        if (i0 + i < n)
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += w * v[i][e];
-      }
+      for (int e = 0; e < E; ++e) acc[e] += w * v[i][e];
     }
   }
   if constexpr (W > 1) {
@@ -1207,7 +1237,7 @@ __device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int
 }
 
 template <int D, int W>
-__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const SharedArgs a,
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const SharedArgs a,
                                                                         int heads) {
   __shared__ float4 hand[W > 1 ? kMergeWarps : 1][33];  // acc of each lane; {M, den, 0, 0}
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp % W;
@@ -1245,20 +1275,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const Sh
                     pchunk, prow + (long long)(h / G) * rows_of_item, hand);
 }
 
+// Sets a split kernel up for its dynamic shared memory, once per device.  The
+// split kernels share SMs: without the carve-out an SM is set up with as much
+// shared memory as the first of them needs, and the other does not fit.
+template <typename... Params>
+cudaError_t allow_smem(void (*kernel)(Params...), size_t smem, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);  // (device_info takes devices 0 .. 63)
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Launches a kernel, as a programmatic dependent of the stream's previous one
 // when pdl is set.
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), unsigned grid, int threads, size_t smem, bool pdl,
                    cudaStream_t stream, Args... args) {
-  if (smem) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    // The split kernels share SMs: without this an SM is set up with as much
-    // shared memory as the first of them needs, and the other does not fit.
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -1276,18 +1315,25 @@ template <int D, int G>
 cudaError_t launch_shared_t(const CUtensorMap& mq, const CUtensorMap& mpk, const CUtensorMap& mpv,
                             const CUtensorMap& mok, const CUtensorMap& mov, const SharedArgs& a,
                             const SharedAppend& app, cudaStream_t stream) {
-  cudaError_t e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, false,
+  static std::atomic<uint64_t> own_set, prefix_set;
+  cudaError_t e = allow_smem(shared_own_kernel<D, G>, OwnLayout<D>::kAlloc, &own_set);
+  if (e == cudaSuccess) e = allow_smem(shared_prefix_kernel<D>, PrefixLayout<D>::kAlloc, &prefix_set);
+  if (e != cudaSuccess) return e;
+  e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, false,
                          stream, mok, mov, a, app);
   if (e != cudaSuccess) return e;
   e = launch(shared_prefix_kernel<D>, prefix_ctas(a.sms), kPrefixThreads, PrefixLayout<D>::kAlloc, true,
              stream, mq, mpk, mpv, a);
   if (e != cudaSuccess) return e;
-  // Few rows: four warps a row, two rows a block; else a block per sequence
-  // and a warp per row (or as many of either as there are heads).
-  const bool wide = (long long)a.num_seqs * a.num_heads < kWideMergeRows;
-  const int heads = wide && a.num_heads > 2 ? 2 : a.num_heads;
-  return launch(wide ? shared_merge_kernel<D, 4> : shared_merge_kernel<D, 1>,
-                (unsigned)(a.num_seqs * (a.num_heads / heads)), kMergeWarps * 32, 0, true, stream, a, heads);
+  // Few rows: several warps share a row's parts.  A block takes as many heads
+  // of a sequence as leave up to four blocks per SM, all resident at once.
+  const long long rows = (long long)a.num_seqs * a.num_heads, warps = 4ll * a.sms * kMergeWarps;
+  const int W = rows * 4 <= warps ? 4 : rows * 2 <= warps ? 2 : 1;
+  int heads = kMergeWarps / W < a.num_heads ? kMergeWarps / W : a.num_heads;
+  while (heads < a.num_heads && rows / heads > 4 * a.sms) heads *= 2;
+  const unsigned grid = (unsigned)(rows / heads);
+  auto merge = W == 4 ? shared_merge_kernel<D, 4> : W == 2 ? shared_merge_kernel<D, 2> : shared_merge_kernel<D, 1>;
+  return launch(merge, grid, kMergeWarps * 32, 0, true, stream, a, heads);
 }
 
 }  // namespace
