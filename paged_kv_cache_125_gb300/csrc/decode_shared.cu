@@ -103,29 +103,42 @@ __device__ __forceinline__ int plan_ctx(const PlanArgs& a, int b) {
 
 // Leading pages that rows b - 1 and b of the table share, by one warp.  Only
 // pages before each sequence's last token count, so that every sequence keeps
-// at least one token of its own.
-__device__ int shared_pages(const PlanArgs& a, int b, int prev_ctx, int ctx) {
+// at least one token of its own.  *ctx = sequence b's context length.
+__device__ int shared_pages(const PlanArgs& a, int b, int* ctx) {
   const int lane = threadIdx.x & 31;
-  const int n = prev_ctx > 0 && ctx > 0 ? (min(prev_ctx, ctx) - 1) / a.block_size : 0;
-  const int32_t* x = a.block_tables + (int64_t)(b - 1) * a.max_blocks;
-  const int32_t* y = x + a.max_blocks;
+  const int32_t* y = a.block_tables + (int64_t)b * a.max_blocks;
+  const int32_t* x = b > 0 ? y - a.max_blocks : y;
   constexpr int U = 4;  // rounds of 32 entries with their loads in flight together
-  for (int j0 = 0; j0 < n; j0 += 32 * U) {
-    int ex[U], ey[U];
+  int ex[U], ey[U];
+  auto load = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + 32 * u + lane;
-      ex[u] = j < n ? x[j] : -1;
-      ey[u] = j < n ? y[j] : -2;
+      ex[u] = j < a.max_blocks ? x[j] : -1;
+      ey[u] = j < a.max_blocks ? y[j] : -2;
     }
+  };
+  load(0);  // beside the lengths that say how many of them count
+  const int prev = b > 0 ? plan_ctx(a, b - 1) : 0;
+  *ctx = plan_ctx(a, b);
+  const int n = prev > 0 && *ctx > 0 ? (min(prev, *ctx) - 1) / a.block_size : 0;
+  for (int j0 = 0; j0 < n; j0 += 32 * U) {
+    if (j0) load(j0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool same = ex[u] == ey[u] && ex[u] >= 0 && ex[u] < a.num_blocks;
+      const bool same = j0 + 32 * u + lane < n && ex[u] == ey[u] && ex[u] >= 0 && ex[u] < a.num_blocks;
       const unsigned diff = ~__ballot_sync(0xffffffffu, same);
       if (diff) return j0 + 32 * u + __ffs(diff) - 1;
     }
   }
   return n;
+}
+
+// Stores v in CTA 0's copy of a shared variable of the cluster.
+__device__ __forceinline__ void store_cta0(int* p, int v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // Sequence b reads its first pages together with sequence b - 1: it shares
@@ -145,19 +158,32 @@ __device__ __forceinline__ bool plan_joined(const PlanArgs& a, int b, int prev, 
 // it does without is 0.7 us of a step's latency.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArgs a) {
   __shared__ long long sums[3][32];
-  __shared__ int s_same[kPlanThreads + 2], s_min[kPlanThreads], s_seq[kPlanThreads];
+  __shared__ int s_same[kPlanThreads + 2], s_min[kPlanThreads + 1], s_seq[kPlanThreads + 1],
+      s_ctx[kPlanThreads];
+  __shared__ long long s_tokens[kPlanThreads + 1], s_steps[kPlanThreads + 1];
   const SharedPlan& p = a.plan;
   const int B = a.num_seqs, bs = a.block_size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool small = B <= kPlanThreads;
+  // Every CTA of the cluster runs before one writes to another's shared memory.
+  asm volatile(
+      "barrier.cluster.arrive.relaxed;\n\t"
+      "barrier.cluster.wait;" ::
+          : "memory");
   for (int b = blockIdx.x + warp * gridDim.x; b < B; b += gridDim.x * (kPlanThreads / 32)) {
-    const int ctx = plan_ctx(a, b);
-    const int same = b > 0 ? shared_pages(a, b, plan_ctx(a, b - 1), ctx) : 0;
+    int ctx;
+    const int same = shared_pages(a, b, &ctx);
     if (lane == 0) {
       p.ctx[b] = ctx;
-      p.same[b] = same;
+      if (small) {
+        store_cta0(&s_same[b + 1], same);
+        store_cta0(&s_ctx[b], ctx);
+      } else {
+        p.same[b] = same;
+      }
     }
   }
-  __threadfence();
+  if (!small) __threadfence();
   asm volatile(
       "barrier.cluster.arrive.release;\n\t"
       "barrier.cluster.wait.acquire;" ::
@@ -166,7 +192,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
 
   // Groups: maximal runs of joined sequences; all of a group read the pages
   // that every one of them shares.
-  const bool small = B <= kPlanThreads;
   int* group_min = small ? s_min : p.group_min;
   int* group_seq = small ? s_seq : p.group_seq;
   for (int b = threadIdx.x; b < B; b += kPlanThreads) group_min[b] = 0x7fffffff;
@@ -174,15 +199,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
   long long groups = 0;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
-    // (s_same[i]: sequence b0 - 1 + i)
-    s_same[threadIdx.x + 1] = b < B ? __ldcg(&p.same[b]) : 0;
-    if (threadIdx.x == 0) s_same[0] = b > 0 ? __ldcg(&p.same[b - 1]) : 0;
-    if (threadIdx.x == 1) s_same[kPlanThreads + 1] = b0 + kPlanThreads < B ? __ldcg(&p.same[b0 + kPlanThreads]) : 0;
-    if (b0 == 0 && b < B) my_ctx = __ldcg(&p.ctx[b]);
+    // s_same[i]: sequence b0 - 1 + i
+    if (!small) {
+      s_same[threadIdx.x + 1] = b < B ? __ldcg(&p.same[b]) : 0;
+      if (threadIdx.x == 0) s_same[0] = b > 0 ? __ldcg(&p.same[b - 1]) : 0;
+      if (threadIdx.x == 1)
+        s_same[kPlanThreads + 1] = b0 + kPlanThreads < B ? __ldcg(&p.same[b0 + kPlanThreads]) : 0;
+    } else if (b < B) {
+      my_ctx = s_ctx[b];
+    }
     __syncthreads();
     const int same = s_same[threadIdx.x + 1];
-    const bool joined =
-        b < B && plan_joined(a, b, s_same[threadIdx.x], same, s_same[threadIdx.x + 2]);
+    const bool joined = b < B && plan_joined(a, b, b > 0 ? s_same[threadIdx.x] : 0, same,
+                                             b + 1 < B ? s_same[threadIdx.x + 2] : 0);
     long long v[1] = {b < B && !joined ? 1 : 0}, total[1];
     block_scan(v, total, sums);
     if (b < B) {
@@ -202,8 +231,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
   // find their work by: (tiles, sequences in tiles), steps, own positions.
   const int tile_seqs = kTileRows / a.group;
   long long base[3] = {0, 0, 0};
-  long long my_step = 0, my_pos = 0;  // sums before sequence threadIdx.x,
-  int my_steps = 0, my_len = 0, my_tile = -1;  // and what it adds to them
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
     int ctx = 0, prefix = 0;
@@ -223,20 +250,23 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     for (int i = 0; i < 3; ++i) v[i] += base[i], base[i] += total[i];
     if (b < B) {
       const int t = (int)(v[0] >> 32) - (start ? 0 : 1);
+      const int r = (int)(v[0] & 0xffffffffll);
       p.prefix[b] = prefix;
       p.tile_of[b] = prefix > 0 ? t : -1;
       p.cum_tokens[b] = v[2];
       if (start) {
         p.tile_seq[t] = b;
-        p.cum_rows[t] = (int)(v[0] & 0xffffffffll);
+        p.cum_rows[t] = r;
         p.cum_steps[t] = v[1];
       }
-      if (b0 == 0) {
-        my_step = v[1];
-        my_pos = v[2];
-        my_steps = steps;
-        my_len = len;
-        my_tile = t;
+      if (small) {  // for the starts below, in arrays that the groups are done with
+        s_same[b] = prefix;
+        s_tokens[b] = v[2];
+        if (start) {
+          s_seq[t] = b;
+          s_min[t] = r;
+          s_steps[t] = v[1];
+        }
       }
     }
   }
@@ -264,33 +294,37 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     h.own_total = base[2];
     *p.head = h;
   }
-  // Where each CTA starts: the sequence (tile) whose positions (steps) hold
-  // its first one.
-  if (!small) __syncthreads();  // the sums written above
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + (int)threadIdx.x;
-    if (!small) {
-      my_len = my_steps = 0;
-      if (b < B) {
-        my_pos = p.cum_tokens[b];
-        my_len = (int)(p.cum_tokens[b + 1] - my_pos);
-      }
-      my_tile = b;
-      if (b < tiles) {
-        my_step = p.cum_steps[b];
-        my_steps = (int)(p.cum_steps[b + 1] - my_step);
-      }
+  if (threadIdx.x == 0 && small) {
+    s_tokens[B] = base[2];
+    s_min[tiles] = (int)(base[0] & 0xffffffffll);
+    s_steps[tiles] = base[1];
+  }
+  __syncthreads();
+  // Where each CTA starts: the last sequence (tile) whose positions (steps)
+  // begin at or before its first one.
+  const long long *tokens = small ? s_tokens : p.cum_tokens, *tsteps = small ? s_steps : p.cum_steps;
+  const int *prefixes = small ? s_same : p.prefix, *ctxs = small ? s_ctx : p.ctx;
+  const int *tile_seq = small ? s_seq : p.tile_seq, *tile_rows = small ? s_min : p.cum_rows;
+  for (int i = threadIdx.x; i < own_ctas(a.sms) + prefix_ctas(a.sms); i += kPlanThreads) {
+    const bool own = i < own_ctas(a.sms);
+    const int c = own ? i : i - own_ctas(a.sms);
+    const long long x = c * (own ? ochunk : pchunk);
+    if (x >= (own ? base[2] : base[1])) continue;
+    const long long* v = own ? tokens : tsteps;
+    int lo = 0, hi = own ? B : tiles;  // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (v[mid] <= x)
+        lo = mid;
+      else
+        hi = mid;
     }
-    for (long long c = (my_pos + ochunk - 1) / ochunk; c * ochunk < my_pos + my_len; ++c)
-      p.cta_seq[c] = b;
-    // A tile may hold many CTAs' starts: the warp's lanes take them together.
-    unsigned with = __ballot_sync(0xffffffffu, my_steps > 0);
-    while (with) {
-      const int i = __ffs(with) - 1;
-      with &= with - 1;
-      const long long st = __shfl_sync(0xffffffffu, my_step, i);
-      const int n = __shfl_sync(0xffffffffu, my_steps, i), t = __shfl_sync(0xffffffffu, my_tile, i);
-      for (long long c = (st + pchunk - 1) / pchunk + lane; c * pchunk < st + n; c += 32) p.cta_tile[c] = t;
+    if (own) {
+      p.own_start[c] = SharedOwnStart{lo, ctxs[lo], ctxs[lo] - prefixes[lo], 0, v[lo + 1], 0};
+    } else {
+      const int seq0 = tile_seq[lo];
+      p.prefix_start[c] = SharedPrefixStart{
+          lo, seq0, tile_rows[lo + 1] - tile_rows[lo], prefixes[seq0], v[lo], v[lo + 1]};
     }
   }
 }
@@ -400,29 +434,42 @@ constexpr uint32_t kColO = 2 * kTileKeys, kPrefixTmem = 256;
 // The segments of this CTA, one after the other.
 struct PrefixSegment {
   long long pos, end;  // flat steps left
-  int t;               // current tile
+  // the current tile
+  int t;
+  int seq0, nseq;      // its sequences
+  int prefix;          // its keys
+  long long c0, c1;    // its steps of the flat order
   // the segment
   int h, s0, s1;       // kv head, steps [s0, s1) of the item
-  int seq0, nseq;      // the tile's sequences
-  int prefix;          // its keys
-  long long row0;      // first row of partials
+  long long row0;      // first row of partials, after those of the tiles before
+
+  __device__ void begin(const SharedPrefixStart& s) {
+    t = s.tile;
+    seq0 = s.seq0;
+    nseq = s.nseq;
+    prefix = s.prefix;
+    c0 = s.step0;
+    c1 = s.step1;
+  }
 
   __device__ bool next(const SharedArgs& a) {
     if (pos >= end) return false;
     const int Hkv = a.num_kv_heads, G = a.num_heads / Hkv;
-    const long long c0 = a.plan.cum_steps[t], c1 = a.plan.cum_steps[t + 1];
-    const int st = (int)((c1 - c0) / Hkv), rel = (int)(pos - c0);  // (at most 8 x 2^24 steps)
+    if (pos == c1) {
+      ++t;
+      seq0 = a.plan.tile_seq[t];
+      nseq = a.plan.cum_rows[t + 1] - a.plan.cum_rows[t];
+      prefix = a.plan.prefix[seq0];
+      c0 = c1;
+      c1 = a.plan.cum_steps[t + 1];
+    }
+    const int st = (int)(c1 - c0) / Hkv, rel = (int)(pos - c0);  // (at most 8 x 2^24 steps)
     h = rel / st;
     s0 = rel - h * st;
     const long long left = end - pos;
     s1 = st - s0 < left ? st : s0 + (int)left;
-    const int r0 = a.plan.cum_rows[t];
-    nseq = a.plan.cum_rows[t + 1] - r0;
-    seq0 = a.plan.tile_seq[t];
-    prefix = a.plan.prefix[seq0];
-    row0 = (long long)Hkv * G * r0 + (long long)h * nseq * G + (long long)blockIdx.x * kTileRows;
+    row0 = (long long)h * nseq * G + (long long)blockIdx.x * kTileRows;
     pos += s1 - s0;
-    if (pos == c1) ++t;
     return true;
   }
 };
@@ -585,6 +632,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
   uint32_t n = 0, segs = 0;
   while (sg.next(a)) {
     const bool valid = r < sg.nseq * G;
+    const long long row0 = (long long)a.num_heads * a.plan.cum_rows[sg.t] + sg.row0;
     float m = -INFINITY, l = 0.f;
     for (int s = sg.s0; s < sg.s1; ++s, ++n) {
       if (!mbar_wait(&bars[P_SFULL + (n & 1)], (n >> 1) & 1, a.status)) return;
@@ -655,7 +703,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
     if (!mbar_wait(&bars[P_ODONE], segs & 1, a.status)) return;
     ++segs;
     tc_fence_after();
-    float* row = valid ? a.prefix_part + (sg.row0 + r) * S : nullptr;
+    float* row = valid ? a.prefix_part + (row0 + r) * S : nullptr;
     if (valid) *reinterpret_cast<float2*>(row + D) = make_float2(m, l);
     const int qb = lane & ~3, jq = lane & 3;
     float* qrow[4];
@@ -697,13 +745,13 @@ __global__ void __maxnreg__(PREFIX_REGS)
   PrefixSegment sg;
   sg.pos = 0;
   sg.end = 0;
-  sg.t = 0;
   // (A plan of another shape is reported by the own-part kernel.)
+  const SharedPrefixStart start = a.plan.prefix_start[blockIdx.x];
   if (plan_fits(a)) {
     const long long total = a.plan.head->prefix_total, chunk = a.plan.head->prefix_chunk;
     sg.pos = chunk * blockIdx.x;
     sg.end = sg.pos + chunk < total ? sg.pos + chunk : total;
-    if (sg.pos < sg.end) sg.t = a.plan.cta_tile[blockIdx.x];
+    sg.begin(start);
   }
   if (sg.pos < sg.end && !(smem_u32(smem) & 1023u)) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
@@ -790,6 +838,7 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
   const int Hkv = a.num_kv_heads, T = kStageRows / Hkv, bs = a.block_size;
   const int shift = __ffs(bs) - 1;  // block_size is a power of two
   const long long total = a.plan.head->own_total, chunk = a.plan.head->own_chunk;
+  const SharedOwnStart start = a.plan.own_start[blockIdx.x];
   long long pos = chunk * blockIdx.x;
   const long long end = pos + chunk < total ? pos + chunk : total;
   uint8_t *ringK = smem, *ringV = smem + RS * Lay::kHalf;
@@ -806,7 +855,7 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
     // Lane i knows sequence base + i; the pages of the current window of the
     // current sequence are one per lane, and the next sequence's first window
     // is loaded ahead.
-    int base = a.plan.cta_seq[blockIdx.x], b = base;
+    int base = start.seq, b = base;
     long long seq_end;
     int ctx, own;  // context length; tokens of its own
     auto load_seqs = [&]() {
@@ -819,8 +868,17 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
     auto load_pages = [&](int seq, int page, int last) {
       return page + lane <= last ? a.block_tables[(int64_t)seq * a.max_blocks + page + lane] : -1;
     };
+    // The first sequence comes with the start record; its first pages are under
+    // way before the look-ups of the others.
+    int ahead, ahead_seq = b;
+    {
+      const long long c0 = start.seq_end - start.own, p0 = pos > c0 ? pos : c0;
+      const long long p1 = end < start.seq_end ? end : start.seq_end;
+      ahead = p0 < p1 ? load_pages(b, (start.ctx - (int)(start.seq_end - p0)) >> shift,
+                                   (start.ctx - (int)(start.seq_end - p1) - 1) >> shift)
+                      : -1;
+    }
     load_seqs();
-    int ahead = 0, ahead_seq = -1;
     while (ok && pos < end) {
       if (b - base == 32) {
         base = b;
@@ -951,7 +1009,7 @@ __device__ __forceinline__ uint32_t stage_off(uint32_t region, int T, int row, i
 
 template <int D, int G>
 __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8_t* smem,
-                             const StageMeta* meta, uint64_t* full, uint64_t* empty) {
+                             const StageMeta* meta, uint64_t* full, uint64_t* empty, int first_seq) {
   using Lay = OwnLayout<D>;
   constexpr int RS = Lay::kStages;
   constexpr int P = D / 64, NQ = D / 8, KS = D / 16, S = part_stride<D>();
@@ -970,18 +1028,24 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
   float m = -INFINITY, l = 0.f;
   int s = 0;
   uint32_t ph = 0;
+  int qseq = -1;  // the sequence whose query qa holds
+  auto load_q = [&](int b) {
+    qseq = b;
+    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q + (int64_t)b * a.q_stride +
+                                                             (int64_t)(head0 + r) * D);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      qa[ks][0] = srow ? qrow[ks * 8 + c] : 0u;
+      qa[ks][1] = srow ? qrow[ks * 8 + 4 + c] : 0u;
+    }
+  };
+  if (first_seq >= 0) load_q(first_seq);  // while the first keys are on their way
   while (true) {
     if (!mbar_wait(&full[s], ph, a.status)) return;
     const StageMeta md = meta[s];
     if (md.flags & F_DONE) break;
     if (md.flags & F_NEW) {
-      const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q + (int64_t)md.b * a.q_stride +
-                                                               (int64_t)(head0 + r) * D);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        qa[ks][0] = srow ? qrow[ks * 8 + c] : 0u;
-        qa[ks][1] = srow ? qrow[ks * 8 + 4 + c] : 0u;
-      }
+      if (md.b != qseq) load_q(md.b);
 #pragma unroll
       for (int i = 0; i < KS; ++i) ot[i][0] = ot[i][1] = ot[i][2] = ot[i][3] = 0.f;
       m = -INFINITY;
@@ -1110,7 +1174,10 @@ __global__ void __maxnreg__(OWN_REGS)
   if ((threadIdx.x >> 5) == kOwnWarps)
     own_producer<D>(a, app, &tmK, &tmV, smem, meta, full, empty);
   else
-    own_consumer<D, G>(a, app, smem, meta, full, empty);
+    own_consumer<D, G>(a, app, smem, meta, full, empty,
+                       a.plan.head->own_chunk * blockIdx.x < a.plan.head->own_total
+                           ? a.plan.own_start[blockIdx.x].seq
+                           : -1);
 }
 
 // ----------------------------------------------------------------- merge
@@ -1342,14 +1409,18 @@ cudaError_t launch_shared_t(const CUtensorMap& mq, const CUtensorMap& mpk, const
 
 size_t shared_plan_bytes(int num_seqs, int num_sms) {
   const size_t B = (size_t)num_seqs;
-  return (sizeof(SharedPlanHead) + 16 * (B + 1) + 4 * (8 * B + 2 + 3 * num_sms) + 255) / 256 * 256;
+  return (sizeof(SharedPlanHead) + own_ctas(num_sms) * sizeof(SharedOwnStart) +
+          prefix_ctas(num_sms) * sizeof(SharedPrefixStart) + 16 * (B + 1) + 4 * (8 * B + 2) + 255) /
+         256 * 256;
 }
 
 SharedPlan shared_plan_view(void* base, int num_seqs, int num_sms) {
   const size_t B = (size_t)num_seqs;
   SharedPlan p;
   p.head = static_cast<SharedPlanHead*>(base);
-  p.cum_tokens = reinterpret_cast<long long*>(p.head + 1);
+  p.own_start = reinterpret_cast<SharedOwnStart*>(p.head + 1);
+  p.prefix_start = reinterpret_cast<SharedPrefixStart*>(p.own_start + own_ctas(num_sms));
+  p.cum_tokens = reinterpret_cast<long long*>(p.prefix_start + prefix_ctas(num_sms));
   p.cum_steps = p.cum_tokens + B + 1;
   p.ctx = reinterpret_cast<int*>(p.cum_steps + B + 1);
   p.prefix = p.ctx + B;
@@ -1359,8 +1430,6 @@ SharedPlan shared_plan_view(void* base, int num_seqs, int num_sms) {
   p.same = p.cum_rows + B + 1;
   p.group_min = p.same + B;
   p.group_seq = p.group_min + B;
-  p.cta_seq = p.group_seq + B;
-  p.cta_tile = p.cta_seq + own_ctas(num_sms);
   return p;
 }
 

@@ -20,14 +20,27 @@ struct SharedPlanHead {
   long long prefix_total;
   long long own_chunk;     // positions per CTA of the own-part kernel, of own_total
   long long own_total;
+  long long pad2;
+};
+static_assert(sizeof(SharedPlanHead) == 80, "the records after it are 16-byte aligned");
+
+// What a CTA needs to begin, in one load.
+struct alignas(16) SharedOwnStart {
+  int seq, ctx, own, pad;  // the sequence that holds its first position; its lengths
+  long long seq_end;       // cum_tokens[seq + 1]
+  long long pad2;
+};
+struct alignas(16) SharedPrefixStart {
+  int tile, seq0, nseq, prefix;  // the tile that holds its first step
+  long long step0, step1;        // cum_steps[tile], cum_steps[tile + 1]
 };
 
 struct SharedPlan {
   SharedPlanHead* head;
   long long* cum_tokens;  // [B + 1] positions (gap + own tokens) of the sequences before b
   long long* cum_steps;   // [B + 1] prefix steps of the tiles before t, all kv heads
-  int* cta_seq;           // [sms] sequence that own-part CTA c starts in
-  int* cta_tile;          // [2 * sms] tile that prefix CTA c starts in
+  SharedOwnStart* own_start;        // [sms] where own-part CTA c starts
+  SharedPrefixStart* prefix_start;  // [2 * sms] where prefix CTA c starts
   int* ctx;               // [B] context length (0: no row)
   int* prefix;            // [B] keys read with the group, [0, prefix)
   int* tile_of;           // [B] tile of sequence b, or -1 (prefix 0)

@@ -45,6 +45,20 @@ struct Team {
 
 __device__ __forceinline__ int ld_cg(const int* p) { return __ldcg(p); }
 
+// How the team's threads walk table rows: 1 .. 32 lanes of a warp per row, as
+// many as the row has entries for.
+struct RowWalk {
+  int lanes, lane, first, step;
+  __device__ RowWalk(int max_blocks, int rank, int size) {
+    lanes = 32;
+    while (lanes > 1 && lanes / 2 >= max_blocks) lanes /= 2;
+    lane = threadIdx.x & (lanes - 1);
+    const int per_cta = kPlanThreads / lanes;
+    first = rank + (int)threadIdx.x / lanes * size;
+    step = per_cta * size;
+  }
+};
+
 // Exclusive prefix sum of v over the block's threads; *total = the sum.
 // `warp_sums` holds kPlanThreads / 32 sums.
 template <typename T>
@@ -73,7 +87,7 @@ __device__ T block_scan(T v, long long* warp_sums, T* total) {
 static_assert(kPlanThreads == 1024, "block_scan needs 32 warps");
 
 __device__ __forceinline__ int row_pages(int len, int block_size) {
-  return (int)(((int64_t)len + block_size - 1) / block_size);
+  return (int)(((unsigned)len + (unsigned)block_size - 1u) / (unsigned)block_size);
 }
 
 // context_lens[r] if it fits its table row, else 0 (recorded): such a row has
@@ -87,46 +101,85 @@ __device__ __forceinline__ int row_len(const PagesArgs& a, int r) {
   return c;
 }
 
-// This CTA's segment of the pages, and the rank of its first counted page:
-// counts the pages of the segment that `pick` accepts, publishes the count in
-// the workspace, and sums those of the CTAs before it.
+// This CTA's segment of the pages.  A thread looks at four consecutive pages
+// at a time (segments start at multiples of four).
 struct Segment {
   int64_t begin, end;
   int64_t base, total;  // counted pages before the segment / in the pool
 };
+constexpr int kPagesPerThread = 4;
+constexpr int kPagesPerRound = kPlanThreads * kPagesPerThread;
 
-template <typename Pick>
-__device__ Segment count_pages(const PagesArgs& a, const Team& t, long long* warp_sums, Pick pick) {
+__device__ __forceinline__ Segment segment_of(const PagesArgs& a, const Team& t) {
   Segment s;
-  const int64_t per = (a.num_blocks + t.size - 1) / t.size;
+  const int64_t per = ((a.num_blocks + t.size - 1) / t.size + 3) / 4 * 4;
   s.begin = min(per * t.rank, a.num_blocks);
   s.end = min(s.begin + per, a.num_blocks);
-  int mine = 0;
-  for (int64_t p = s.begin + threadIdx.x; p < s.end; p += kPlanThreads) mine += pick(p) ? 1 : 0;
+  s.base = s.total = 0;
+  return s;
+}
+
+// Entries p .. p + 3 of an array of the pages (those past the end read as
+// `past`); one load where the array allows it.
+__device__ __forceinline__ int4 load_pages(const int* v, int64_t p, int64_t end, int past) {
+  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(v) & 15u) == 0)
+    return __ldcg(reinterpret_cast<const int4*>(v + p));
+  int4 r;
+  r.x = p < end ? __ldcg(v + p) : past;
+  r.y = p + 1 < end ? __ldcg(v + p + 1) : past;
+  r.z = p + 2 < end ? __ldcg(v + p + 2) : past;
+  r.w = p + 3 < end ? __ldcg(v + p + 3) : past;
+  return r;
+}
+__device__ __forceinline__ void store_pages(int* v, int64_t p, int64_t end, const int4& x) {
+  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(v) & 15u) == 0) {
+    *reinterpret_cast<int4*>(v + p) = x;
+    return;
+  }
+  if (p < end) v[p] = x.x;
+  if (p + 1 < end) v[p + 1] = x.y;
+  if (p + 2 < end) v[p + 2] = x.z;
+  if (p + 3 < end) v[p + 3] = x.w;
+}
+
+// Publishes this CTA's count and sums those of the CTAs before it (a team
+// barrier).
+__device__ void rank_segment(const PagesArgs& a, const Team& t, long long* warp_sums, int mine,
+                             Segment* s) {
   int total;
   block_scan(mine, warp_sums, &total);
   if (threadIdx.x == 0) a.ws.team_counts[t.rank] = total;
   t.sync();
-  s.base = s.total = 0;
+  s->base = s->total = 0;
   for (int i = 0; i < t.size; ++i) {
     const int c = ld_cg(&a.ws.team_counts[i]);
-    if (i < t.rank) s.base += c;
-    s.total += c;
+    if (i < t.rank) s->base += c;
+    s->total += c;
   }
-  return s;
 }
 
-// Calls use(page, rank) for every page of the segment that `pick` accepts, in
-// order, with its rank among the pool's; stops after rank limit - 1.
-template <typename Pick, typename Use>
-__device__ void for_pages(const Segment& s, int64_t limit, long long* warp_sums, Pick pick, Use use) {
+__device__ __forceinline__ int zeros(const int4& x) {
+  return (x.x == 0) + (x.y == 0) + (x.z == 0) + (x.w == 0);
+}
+
+// Calls use(page, rank) for the free pages (counts[p] == 0) of the segment in
+// order, with their ranks among the pool's; stops after rank limit - 1.
+template <typename Use>
+__device__ void for_free_pages(const int* counts, const Segment& s, int64_t limit,
+                               long long* warp_sums, Use use) {
   int64_t base = s.base;
-  for (int64_t p0 = s.begin; p0 < s.end && base < limit; p0 += kPlanThreads) {
-    const int64_t p = p0 + threadIdx.x;
-    const bool ok = p < s.end && pick(p);
+  for (int64_t p0 = s.begin; p0 < s.end && base < limit; p0 += kPagesPerRound) {
+    const int64_t p = p0 + threadIdx.x * kPagesPerThread;
+    const int4 c = p < s.end ? load_pages(counts, p, s.end, 1) : make_int4(1, 1, 1, 1);
     int total;
-    const int64_t k = base + block_scan(ok ? 1 : 0, warp_sums, &total);
-    if (ok && k < limit) use(p, k);
+    int64_t k = base + block_scan(zeros(c), warp_sums, &total);
+    const int v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v[i] == 0) {
+        if (k < limit) use(p + i, k);
+        ++k;
+      }
     base += total;
   }
 }
@@ -138,27 +191,30 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
   const Team t;
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
+  const RowWalk rows(a.max_blocks, t.rank, t.size);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  for (int64_t p = t.thread(); p < a.num_blocks; p += t.threads()) {
-    a.out_counts[p] = a.ref_counts[p];
-    a.ws.page[p] = kIntMax;  // lowest new row whose unfilled last page this is
+  Segment s = segment_of(a, t);
+  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound) {
+    store_pages(a.out_counts, p, s.end, load_pages(a.ref_counts, p, s.end, 0));
+    // ws.page: the lowest new row whose unfilled last page this is
+    store_pages(a.ws.page, p, s.end, make_int4(kIntMax, kIntMax, kIntMax, kIntMax));
   }
   t.sync();
 
   // Every old row lets go of its pages; every new row takes its parent's,
   // except an unfilled last page, which goes to one new row (below).
-  for (int64_t i = t.thread(); i < (int64_t)a.num_rows * mb; i += t.threads()) {
-    const int r = (int)(i / mb), j = (int)(i % mb);
-    if (j >= row_pages(row_len(a, r), bs)) continue;
-    const int e = a.block_tables[i];
-    if (e < 0 || e >= a.num_blocks)
-      record_error(a.status, KVP_ERR_DEVICE_DATA);
-    else
-      atomicAdd(&a.out_counts[e], -1);
+  for (int r = rows.first; r < a.num_rows; r += rows.step) {
+    const int n = row_pages(row_len(a, r), bs);
+    for (int j = rows.lane; j < n; j += rows.lanes) {
+      const int e = a.block_tables[r * mb + j];
+      if (e < 0 || e >= a.num_blocks)
+        record_error(a.status, KVP_ERR_DEVICE_DATA);
+      else
+        atomicAdd(&a.out_counts[e], -1);
+    }
   }
-  for (int64_t i = t.thread(); i < (int64_t)a.num_out * mb; i += t.threads()) {
-    const int r = (int)(i / mb), j = (int)(i % mb);
+  for (int r = rows.first; r < a.num_out; r += rows.step) {
     int p = a.parents[r];
     if (p < -1 || p >= a.num_rows) {
       record_error(a.status, KVP_ERR_DEVICE_DATA);
@@ -166,15 +222,17 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
     }
     const int len = p >= 0 ? row_len(a, p) : 0;
     const int n = row_pages(len, bs);
-    if (j == 0) a.out_lens[r] = len;
-    int e = j < n ? a.block_tables[(int64_t)p * mb + j] : -1;
-    if (e >= a.num_blocks || e < 0) e = -1;  // recorded above, with the parent's row
-    a.out_tables[i] = e;
-    if (e < 0) continue;
-    if (j == n - 1 && len % bs)
-      atomicMin(&a.ws.page[e], r);
-    else
-      atomicAdd(&a.out_counts[e], 1);
+    if (rows.lane == 0) a.out_lens[r] = len;
+    for (int j = rows.lane; j < a.max_blocks; j += rows.lanes) {
+      int e = j < n ? a.block_tables[p * mb + j] : -1;
+      if (e >= a.num_blocks || e < 0) e = -1;  // recorded above, with the parent's row
+      a.out_tables[r * mb + j] = e;
+      if (e < 0) continue;
+      if (j == n - 1 && len % bs)
+        atomicMin(&a.ws.page[e], r);
+      else
+        atomicAdd(&a.out_counts[e], 1);
+    }
   }
   t.sync();
 
@@ -204,9 +262,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
   }
   t.sync();
   const int copies = ld_cg(&a.ws.head->copies);
-  auto is_free = [&](int64_t p) { return ld_cg(&a.out_counts[p]) == 0; };
-  const Segment s = count_pages(a, t, warp_sums, is_free);
-  for_pages(s, copies, warp_sums, is_free, [&](int64_t p, int64_t k) {
+  int mine = 0;
+  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound)
+    mine += zeros(load_pages(a.out_counts, p, s.end, 1));
+  rank_segment(a, t, warp_sums, mine, &s);
+  for_free_pages(a.out_counts, s, copies, warp_sums, [&](int64_t p, int64_t k) {
     const int r = ld_cg(&a.ws.row[k]);
     const int len = ld_cg(&a.out_lens[r]);
     int* entry = &a.out_tables[r * mb + row_pages(len, bs) - 1];
@@ -236,26 +296,29 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
 
 // ---------------------------------------------------------------- extend
 
-// The number of entries of the non-decreasing v[0 .. n) that are <= x.
-__device__ __forceinline__ int upper_bound(const int* v, int n, int64_t x) {
+// Last index i with v[i] <= x of the non-decreasing v[0 .. n), v[0] <= x.
+__device__ __forceinline__ int last_at_most(const int* v, int n, int64_t x) {
   int lo = 0, hi = n;
-  while (lo < hi) {
+  while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((int64_t)ld_cg(&v[mid]) <= x)
-      lo = mid + 1;
+    if ((int64_t)v[mid] <= x)
+      lo = mid;
     else
       hi = mid;
   }
   return lo;
 }
 
+constexpr int kRowsInSmem = 2048;
+
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesArgs a) {
   __shared__ long long warp_sums[32];
+  __shared__ int s_page0[kRowsInSmem], s_token0[kRowsInSmem];
   const Team t;
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
 
-  // Rows: pages needed and new tokens, with their prefix sums over the rows.
+  // The rows, by CTA 0: pages needed and new tokens, and their prefix sums.
   if (t.rank == 0) {
     long long pages = 0, tokens = 0;
     for (int r0 = 0; r0 < a.num_rows; r0 += kPlanThreads) {
@@ -264,9 +327,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
       int add = 0, len = 0;
       bool bad = false;
       if (r < a.num_rows) {
+        add = a.new_tokens[r];
         len = row_len(a, r);
         bad = len != a.context_lens[r];
-        add = a.new_tokens[r];
         if (add < 0 || (int64_t)len + add > mb * bs) {  // does not fit the row: takes no slots
           bad = true;
           add = 0;
@@ -287,12 +350,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
       pages += total;
       const long long token0 = tokens + block_scan(asked, warp_sums, &total);
       tokens += total;
-      if (r < a.num_rows) {
-        a.ws.row[r] = (int)min(page0, (long long)kIntMax);  // past every page and slot
-        a.ws.row2[r] = (int)min(token0, (long long)kIntMax);
-        a.ws.row3[r] = len;
-        a.ws.row4[r] = add;
-      }
+      if (r < a.num_rows)
+        a.ws.grow[r] = RowGrowth{(int)min(page0, (long long)kIntMax),
+                                 (int)min(token0, (long long)kIntMax), len, add};
     }
     if (threadIdx.x == 0) {
       a.ws.head->copies = (int)min(pages, (long long)kIntMax);
@@ -300,50 +360,79 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
       if (tokens > a.num_slots) record_error(a.status, KVP_ERR_DEVICE_DATA);
     }
   }
-  auto is_free = [&](int64_t p) { return ld_cg(&a.ref_counts[p]) == 0; };
-  const Segment s = count_pages(a, t, warp_sums, is_free);  // (a team barrier)
-  const int pages = ld_cg(&a.ws.head->copies);
-
-  // The tables as they were; the new entries follow below.
-  for (int64_t i = t.thread(); i < a.num_rows * mb; i += t.threads()) {
-    const int r = (int)(i / mb), j = (int)(i % mb);
-    const int len = ld_cg(&a.ws.row3[r]);
-    const int had = row_pages(len, bs), add = ld_cg(&a.ws.row4[r]);
-    const int has = row_pages(len + add, bs);
-    const bool fits = (int64_t)ld_cg(&a.ws.row[r]) + (has - had) <= s.total;
-    if (j < had)
-      a.out_tables[i] = a.block_tables[i];
-    else if (j >= has || !fits)
-      a.out_tables[i] = -1;
-    if (j == 0) {
-      if (!fits && has > had) record_error(a.status, KVP_ERR_DEVICE_DATA);
-      a.out_lens[r] = !fits && has > had ? len : len + add;
+  // Meanwhile the others: the tables as they were (new pages follow below).
+  const int copiers = t.size > 1 ? t.size - 1 : 1, me = t.size > 1 ? t.rank - 1 : 0;
+  if (me >= 0) {
+    const RowWalk rows(a.max_blocks, me, copiers);
+    const bool in_place = a.out_tables == a.block_tables;
+    for (int r = rows.first; r < a.num_rows; r += rows.step) {
+      const int had = row_pages(row_len(a, r), bs);
+      const int32_t* from = a.block_tables + r * mb;
+      int32_t* to = a.out_tables + r * mb;
+      int j = rows.lane;
+      if (in_place) j += had / rows.lanes * rows.lanes;
+#pragma unroll 4
+      for (; j < a.max_blocks; j += rows.lanes)
+        if (j >= had)
+          to[j] = -1;
+        else if (!in_place)
+          to[j] = from[j];
     }
   }
-  // Free page of rank k goes to the row whose pages start at or before k.
-  if (a.out_counts != a.ref_counts)
-    for (int64_t p = s.begin + threadIdx.x; p < s.end; p += kPlanThreads)
-      a.out_counts[p] = a.ref_counts[p];
-  __syncthreads();
-  for_pages(s, pages, warp_sums, is_free, [&](int64_t p, int64_t k) {
-    const int r = upper_bound(a.ws.row, a.num_rows, k) - 1;
-    const int len = ld_cg(&a.ws.row3[r]), add = ld_cg(&a.ws.row4[r]), page0 = ld_cg(&a.ws.row[r]);
-    const int had = row_pages(len, bs), need = row_pages(len + add, bs) - had;
-    if (page0 + need > s.total) return;  // not enough pages left for the whole row
-    a.out_tables[r * mb + had + (k - page0)] = (int)p;
-    a.out_counts[p] = 1;
-  });
-  t.sync();
+  // The counts as they were, and the free pages among them.
+  Segment s = segment_of(a, t);
+  int mine = 0;
+  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound) {
+    const int4 c = load_pages(a.ref_counts, p, s.end, 1);
+    mine += zeros(c);
+    if (a.out_counts != a.ref_counts) store_pages(a.out_counts, p, s.end, c);
+  }
+  rank_segment(a, t, warp_sums, mine, &s);  // (a team barrier)
 
+  // The rows' prefix sums, to search in: in shared memory, or (too many rows)
+  // packed in the workspace, by every CTA for itself, all writing the same.
+  const bool small = a.num_rows <= kRowsInSmem;
+  int* page0 = small ? s_page0 : a.ws.row;
+  int* token0 = small ? s_token0 : a.ws.row2;
+  for (int r = threadIdx.x; r < a.num_rows; r += kPlanThreads) {
+    const int2 g = __ldcg(reinterpret_cast<const int2*>(&a.ws.grow[r]));
+    page0[r] = g.x;
+    token0[r] = g.y;
+  }
+  __syncthreads();
+  // Free page of rank k goes to the last row whose pages start at or before k.
+  const int pages = ld_cg(&a.ws.head->copies);
+  if (pages > 0) {
+    for_free_pages(a.ref_counts, s, pages, warp_sums, [&](int64_t p, int64_t k) {
+      const int r = last_at_most(page0, a.num_rows, k);
+      const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));  // page0, token0, len, add
+      const int had = row_pages(g.z, bs), need = row_pages(g.z + g.w, bs) - had;
+      if (g.x + need > s.total) return;  // not enough pages left for the whole row
+      a.out_tables[r * mb + had + (k - g.x)] = (int)p;
+      a.out_counts[p] = 1;
+    });
+    t.sync();
+  }
+
+  // Whether the pool had the pages that a row needs.
+  auto served = [&](const int4& g) {
+    const int need = row_pages(g.z + g.w, bs) - row_pages(g.z, bs);
+    return need == 0 || (int64_t)g.x + need <= s.total;
+  };
+  for (int64_t r = t.thread(); r < a.num_rows; r += t.threads()) {
+    const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));
+    if (!served(g)) record_error(a.status, KVP_ERR_DEVICE_DATA);
+    a.out_lens[r] = served(g) ? g.z + g.w : g.z;
+  }
   const int tokens = ld_cg(&a.ws.head->tokens);
   for (int64_t i = t.thread(); i < a.num_slots; i += t.threads()) {
     int slot = -1;
     if (i < tokens) {
-      const int r = upper_bound(a.ws.row2, a.num_rows, i) - 1;
-      const int len = ld_cg(&a.ws.row3[r]);
-      const int64_t pos = len + (i - ld_cg(&a.ws.row2[r]));
-      if (pos < ld_cg(&a.out_lens[r]))
-        slot = ld_cg(&a.out_tables[r * mb + pos / bs]) * bs + (int)(pos % bs);
+      const int r = last_at_most(token0, a.num_rows, i);
+      const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));
+      const int pos = g.z + (int)(i - g.y);
+      if (served(g) && pos < g.z + g.w)
+        slot = ld_cg(&a.out_tables[r * mb + pos / bs]) * bs + pos % bs;
     }
     a.slot_mapping[i] = slot;
   }
@@ -355,22 +444,33 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesA
   __shared__ long long warp_sums[32];
   const Team t;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto is_live = [&](int64_t p) { return a.ref_counts[p] > 0; };
-  const Segment s = count_pages(a, t, warp_sums, is_live);
+  Segment s = segment_of(a, t);
+  auto live4 = [](const int4& c) { return (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0); };
+  int mine = 0;
+  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound)
+    mine += live4(load_pages(a.ref_counts, p, s.end, 0));
+  rank_segment(a, t, warp_sums, mine, &s);
   const int64_t live = s.total;  // pages [0, live) hold everything afterwards
 
   // Live pages before each page; free page p < live is hole p - before(p).
   int64_t base = s.base;
-  for (int64_t p0 = s.begin; p0 < s.end; p0 += kPlanThreads) {
-    const int64_t p = p0 + threadIdx.x;
-    const bool ok = p < s.end && is_live(p);
+  for (int64_t p0 = s.begin; p0 < s.end; p0 += kPagesPerRound) {
+    const int64_t p = p0 + threadIdx.x * kPagesPerThread;
+    const int4 c = p < s.end ? load_pages(a.ref_counts, p, s.end, 0) : make_int4(0, 0, 0, 0);
     int total;
-    const int64_t before = base + block_scan(ok ? 1 : 0, warp_sums, &total);
-    if (p < s.end) {
-      a.ws.page[p] = (int)before;
-      if (!ok && p < live) a.ws.page2[p - before] = (int)p;
-    }
+    int before = (int)base + block_scan(live4(c), warp_sums, &total);
     base += total;
+    const int v[4] = {c.x, c.y, c.z, c.w};
+    int o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = before;
+      if (v[i] > 0)
+        ++before;
+      else if (p + i < s.end && p + i < live)
+        a.ws.page2[p + i - before] = (int)(p + i);
+    }
+    if (p < s.end) store_pages(a.ws.page, p, s.end, make_int4(o[0], o[1], o[2], o[3]));
   }
   t.sync();
   const int64_t staying = live < a.num_blocks ? ld_cg(&a.ws.page[live]) : live;
@@ -391,15 +491,18 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesA
     a.places[p] = place;
   }
   t.sync();
-  for (int64_t i = t.thread(); i < (int64_t)a.num_rows * a.max_blocks; i += t.threads()) {
-    const int r = (int)(i / a.max_blocks), j = (int)(i % a.max_blocks);
-    int e = -1;
-    if (j < row_pages(row_len(a, r), a.block_size)) {
-      const int old = a.block_tables[i];
-      if (old >= 0 && old < a.num_blocks) e = ld_cg(&a.places[old]);
-      if (e < 0) record_error(a.status, KVP_ERR_DEVICE_DATA);  // a row's page is outside or free
+  const RowWalk rows(a.max_blocks, t.rank, t.size);
+  for (int r = rows.first; r < a.num_rows; r += rows.step) {
+    const int n = row_pages(row_len(a, r), a.block_size);
+    for (int j = rows.lane; j < a.max_blocks; j += rows.lanes) {
+      int e = -1;
+      if (j < n) {
+        const int old = a.block_tables[(int64_t)r * a.max_blocks + j];
+        if (old >= 0 && old < a.num_blocks) e = ld_cg(&a.places[old]);
+        if (e < 0) record_error(a.status, KVP_ERR_DEVICE_DATA);  // a row's page is outside or free
+      }
+      a.out_tables[(int64_t)r * a.max_blocks + j] = e;
     }
-    a.out_tables[i] = e;
   }
 }
 
@@ -486,14 +589,14 @@ cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int cluster
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// CTAs of the plan: one per 4096 elements of its largest array.
+// CTAs of the plan: enough to see its largest array in one round.
 int team_size(const PagesArgs& a) {
   const int64_t rows = a.num_rows > a.num_out ? a.num_rows : a.num_out;
   int64_t n = rows * a.max_blocks;
   if (a.num_blocks > n) n = a.num_blocks;
   if (a.num_slots > n) n = a.num_slots;
   int size = 1;
-  while (size < kMaxTeam && size * 4096 < n) size *= 2;
+  while (size < kMaxTeam && (int64_t)size * kPlanThreads < n) size *= 2;
   return size;
 }
 
@@ -512,22 +615,24 @@ cudaError_t launch_copies(const PagesArgs& a, const PagesCache& c, int num_sms, 
 
 size_t pages_workspace_bytes(int64_t num_blocks, int64_t rows) {
   const int64_t pairs = num_blocks > rows ? num_blocks : rows;
-  return 256 + (size_t)pairs * sizeof(PagePair) + (size_t)(2 * num_blocks + 4 * rows) * sizeof(int);
+  const int64_t pages = (num_blocks + 3) / 4 * 4;
+  return 256 + (size_t)pairs * sizeof(PagePair) + (size_t)rows * (sizeof(RowGrowth) + 2 * sizeof(int)) +
+         (size_t)(2 * pages) * sizeof(int);
 }
 
 PagesWorkspace pages_workspace(void* base, int64_t num_blocks, int64_t rows) {
   PagesWorkspace w;
   uint8_t* p = static_cast<uint8_t*>(base);
   const int64_t pairs = num_blocks > rows ? num_blocks : rows;
+  const int64_t pages = (num_blocks + 3) / 4 * 4;
   w.head = reinterpret_cast<PagesHead*>(p);
   w.team_counts = reinterpret_cast<int*>(p + 64);
   w.pairs = reinterpret_cast<PagePair*>(p + 256);
-  w.page = reinterpret_cast<int*>(w.pairs + pairs);
-  w.page2 = w.page + num_blocks;
-  w.row = w.page2 + num_blocks;
+  w.grow = reinterpret_cast<RowGrowth*>(w.pairs + pairs);
+  w.page = reinterpret_cast<int*>(w.grow + rows);
+  w.page2 = w.page + pages;
+  w.row = w.page2 + pages;
   w.row2 = w.row + rows;
-  w.row3 = w.row2 + rows;
-  w.row4 = w.row3 + rows;
   return w;
 }
 

@@ -17,12 +17,19 @@ struct PagePair {
   int src, dst, tokens, pad;
 };
 
+// What a row asks of kv_pages_extend.
+struct alignas(16) RowGrowth {
+  int page0, token0;  // new pages / asked tokens of the rows before it
+  int len, add;       // its length; the tokens it can take (if the pool has the pages)
+};
+
 struct PagesWorkspace {
   PagesHead* head;
   int* team_counts;         // one count per CTA of the plan kernel
   PagePair* pairs;          // [max(num_blocks, rows)]
+  RowGrowth* grow;          // [rows]
   int *page, *page2;        // [num_blocks]
-  int *row, *row2, *row3, *row4;  // [rows]
+  int *row, *row2;          // [rows]
 };
 
 struct PagesArgs {

@@ -97,7 +97,8 @@ class Batch:
 def plan_prefixes(plan, b):
     """The prefix lengths in a plan, at their place in its layout."""
     raw = plan.cpu().numpy().tobytes()
-    head = 10 * 4 + 4 * 8
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    head = 80 + 32 * sms + 32 * 2 * sms  # and where each CTA starts
     return np.frombuffer(raw, np.int32, b, head + 16 * (b + 1) + 4 * b).tolist()
 
 
