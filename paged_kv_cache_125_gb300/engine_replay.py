@@ -42,8 +42,10 @@ class ReplayStep:
 class EngineReplay:
     def __init__(self, requests, num_layers: int, num_heads: int, num_kv_heads: int, head_dim: int,
                  block_size: int, num_blocks: int, max_num_seqs: int, max_num_batched_tokens: int,
-                 device, stream=None):
-        """``requests``: (prompt token ids, max_tokens) pairs, submitted in order."""
+                 device, stream=None, shared_prefix: bool = False):
+        """``requests``: (prompt token ids, max_tokens) pairs, submitted in order.
+        ``shared_prefix``: decode steps read the blocks that neighbouring
+        sequences share (prefix-cache hits) once for all of them."""
         self.device = torch.device(device)
         self.num_layers, self.num_heads, self.num_kv_heads = num_layers, num_heads, num_kv_heads
         self.head_dim, self.block_size = head_dim, block_size
@@ -56,7 +58,8 @@ class EngineReplay:
         max_blocks = max((len(t) + o + block_size - 1) // block_size for t, o in requests)
         self.graphs = LayeredDecodeGraphs([(self.kv[0, l], self.kv[1, l]) for l in range(num_layers)],
                                           num_heads, max_blocks, max_bs=max_num_seqs,
-                                          softmax_scale=self.scale, stream=stream)
+                                          softmax_scale=self.scale, stream=stream,
+                                          shared_prefix=shared_prefix)
 
     def done(self) -> bool:
         return self.sched.is_finished()

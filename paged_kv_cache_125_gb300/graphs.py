@@ -17,10 +17,17 @@ each bucket's graph reads its own compact views of it, so a step's metadata,
 padding rows included, arrives in ONE host-to-device copy of a packed pinned
 buffer (``run_packed``).  q, k and v are not part of it: in an engine the
 model's projections write them into the graph's fixed buffers.
+
+With ``shared_prefix`` a graph begins with ``attn_shared_plan`` over the step's
+block tables and its layers run ``attn_decode_shared_append``: sequences of the
+step that are neighbours and map their first blocks to the same physical ones
+(prefix-cache hits, forked sequences) have those blocks read once for all of
+them.  The outputs are the same up to rounding.
 """
 from __future__ import annotations
 
-from . import attn_decode_paged_append, attn_decode_workspace_size
+from . import (attn_decode_paged_append, attn_decode_shared_append, attn_decode_shared_workspace_size,
+               attn_decode_workspace_size, attn_shared_plan, attn_shared_plan_size)
 
 
 def default_buckets(max_bs: int) -> list[int]:
@@ -108,6 +115,37 @@ class _PackedMeta:
         return pb
 
 
+class _DecodeCalls:
+    """The library calls of a decode step: its plan (shared_prefix) and one
+    attention call per layer, with the scratch that they need."""
+
+    def _init_calls(self, max_bs: int, shared_prefix: bool, num_blocks: int, dev) -> None:
+        import torch
+        self.shared_prefix, self.num_blocks = shared_prefix, num_blocks
+        hq, hkv, d, bs = self.num_heads, self.num_kv_heads, self.head_dim, self.block_size
+        self.plan = None
+        if shared_prefix:
+            ws = attn_decode_shared_workspace_size(max_bs, hq, hkv, d, dev)
+            self.plan = torch.empty((attn_shared_plan_size(max_bs, hq, hkv, dev),), dtype=torch.uint8,
+                                    device=dev)
+        else:
+            ws = attn_decode_workspace_size(max_bs, hq, d, self.capacity, bs)
+        self.workspace = torch.empty((max(ws, 1),), dtype=torch.uint8, device=dev)
+
+    def _plan_step(self, bt, ctx) -> None:
+        if self.shared_prefix:
+            attn_shared_plan(bt, ctx, self.block_size, self.num_heads, self.num_kv_heads,
+                             self.num_blocks, plan=self.plan)
+
+    def _attend(self, q, k, v, slots, kc, vc, bt, ctx, out) -> None:
+        if self.shared_prefix:
+            attn_decode_shared_append(q, k, v, slots, kc, vc, bt, self.plan, softmax_scale=self.scale,
+                                      workspace=self.workspace, out=out)
+        else:
+            attn_decode_paged_append(q, k, v, slots, kc, vc, bt, ctx, self.capacity,
+                                     softmax_scale=self.scale, workspace=self.workspace, out=out)
+
+
 def bucket_for(buckets: list[int], b: int) -> int:
     """Smallest bucket >= b."""
     for x in buckets:
@@ -116,7 +154,7 @@ def bucket_for(buckets: list[int], b: int) -> int:
     raise ValueError(f"batch of {b} exceeds the largest bucket {buckets[-1]}")
 
 
-class DecodeGraphs(_PackedMeta):
+class DecodeGraphs(_PackedMeta, _DecodeCalls):
     """Captured store + decode graphs for one layer's cache.
 
     ``k_cache`` / ``v_cache``: [num_blocks, block_size, num_kv_heads, head_dim]
@@ -125,7 +163,7 @@ class DecodeGraphs(_PackedMeta):
 
     def __init__(self, k_cache, v_cache, num_heads: int, max_blocks_per_seq: int,
                  max_bs: int = 512, buckets: list[int] | None = None,
-                 softmax_scale: float | None = None, stream=None):
+                 softmax_scale: float | None = None, stream=None, shared_prefix: bool = False):
         import torch
         self.k_cache, self.v_cache = k_cache, v_cache
         nb, bs, hkv, d = k_cache.shape
@@ -143,8 +181,7 @@ class DecodeGraphs(_PackedMeta):
         self.v = torch.zeros((max_bs, hkv, d), dtype=bf16, device=dev)
         self._init_meta(max_bs, max_blocks_per_seq, dev)
         self.out = torch.zeros((max_bs, num_heads, d), dtype=bf16, device=dev)
-        ws_bytes = attn_decode_workspace_size(max_bs, num_heads, d, self.capacity, bs)
-        self.workspace = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+        self._init_calls(max_bs, shared_prefix, nb, dev)
         self.stream = stream or torch.cuda.Stream(dev)
         self.graphs = {}
         for b in self.buckets:
@@ -152,9 +189,9 @@ class DecodeGraphs(_PackedMeta):
 
     def _step(self, b: int) -> None:
         slots, ctx, bt = self.meta_views(b)
-        attn_decode_paged_append(self.q[:b], self.k[:b], self.v[:b], slots, self.k_cache,
-                                 self.v_cache, bt, ctx, self.capacity, softmax_scale=self.scale,
-                                 workspace=self.workspace, out=self.out[:b])
+        self._plan_step(bt, ctx)
+        self._attend(self.q[:b], self.k[:b], self.v[:b], slots, self.k_cache, self.v_cache, bt, ctx,
+                     self.out[:b])
 
     def _capture(self, b: int):
         import torch
@@ -198,7 +235,7 @@ class DecodeGraphs(_PackedMeta):
         return self.out[:b]
 
 
-class LayeredDecodeGraphs(_PackedMeta):
+class LayeredDecodeGraphs(_PackedMeta, _DecodeCalls):
     """The decode step of a whole model as one graph per bucket: every layer's
     ``attn_decode_paged_append`` in one capture, the way the pages' engine
     captures its model forward for decode ("nano-vLLM-1", ModelRunner
@@ -212,7 +249,8 @@ class LayeredDecodeGraphs(_PackedMeta):
     other on one stream, so they share one workspace."""
 
     def __init__(self, kv_layers, num_heads: int, max_blocks_per_seq: int, max_bs: int = 512,
-                 buckets: list[int] | None = None, softmax_scale: float | None = None, stream=None):
+                 buckets: list[int] | None = None, softmax_scale: float | None = None, stream=None,
+                 shared_prefix: bool = False):
         import torch
         self.kv_layers = list(kv_layers)
         nb, bs, hkv, d = self.kv_layers[0][0].shape
@@ -231,18 +269,16 @@ class LayeredDecodeGraphs(_PackedMeta):
         self.v = torch.zeros((n_layers, max_bs, hkv, d), dtype=bf16, device=dev)
         self.out = torch.zeros((n_layers, max_bs, num_heads, d), dtype=bf16, device=dev)
         self._init_meta(max_bs, max_blocks_per_seq, dev)
-        ws_bytes = attn_decode_workspace_size(max_bs, num_heads, d, self.capacity, bs)
-        self.workspace = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+        self._init_calls(max_bs, shared_prefix, nb, dev)
         self.stream = stream or torch.cuda.Stream(dev)
         self.graphs = {b: self._capture(b) for b in self.buckets}
 
     def _step(self, b: int) -> None:
         slots, ctx, bt = self.meta_views(b)
+        self._plan_step(bt, ctx)
         for layer, (kc, vc) in enumerate(self.kv_layers):
-            attn_decode_paged_append(self.q[layer, :b], self.k[layer, :b], self.v[layer, :b],
-                                     slots, kc, vc, bt, ctx, self.capacity,
-                                     softmax_scale=self.scale, workspace=self.workspace,
-                                     out=self.out[layer, :b])
+            self._attend(self.q[layer, :b], self.k[layer, :b], self.v[layer, :b], slots, kc, vc, bt, ctx,
+                         self.out[layer, :b])
 
     def _capture(self, b: int):
         import torch
