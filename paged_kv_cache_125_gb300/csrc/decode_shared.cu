@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
       "barrier.cluster.wait.acquire;" ::
           : "memory");
   if (blockIdx.x) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Groups: maximal runs of joined sequences; all of a group read the pages
   // that every one of them shares.
@@ -847,10 +848,6 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
   bool ok = true;
   // Read once: these keys must not push the shared prefixes out of L2.
   const uint64_t once = policy_evict_first();
-  if (lane == 0) {
-    prefetch_tensormap(tmK);
-    prefetch_tensormap(tmV);
-  }
   if (pos < end) {
     // Lane i knows sequence base + i; the pages of the current window of the
     // current sequence are one per lane, and the next sequence's first window
@@ -1157,18 +1154,23 @@ __global__ void __maxnreg__(OWN_REGS)
   StageMeta* meta = reinterpret_cast<StageMeta*>(smem + Lay::kMeta);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
   uint64_t* empty = full + Lay::kStages;
-  // The prefix kernel may start beside this one.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!plan_fits(a) || (smem_u32(smem) & 1023u)) {
-    if (threadIdx.x == 0) record_error(a.status, KVP_ERR_DEVICE_DATA);
-    return;
-  }
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
     for (int i = 0; i < Lay::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kOwnWarps);
     }
     fence_mbar_init();
+  }
+  // The call's first kernel: everything before it on the stream is complete
+  // from here on.  Only then may the prefix kernel start beside it, so that
+  // kernel can rely on the same.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!plan_fits(a) || (smem_u32(smem) & 1023u)) {
+    if (threadIdx.x == 0) record_error(a.status, KVP_ERR_DEVICE_DATA);
+    return;
   }
   __syncthreads();
   if ((threadIdx.x >> 5) == kOwnWarps)
@@ -1336,6 +1338,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (The next call's first kernel may get ready now; it waits for this grid.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!fits) return;
   for (int h = h0 + warp / W; h < h0 + heads; h += kMergeWarps / W)
     merge_row<D, W>(a, b, h, lane, warp, wi, ns, orow + h, h % G, st, first + (long long)(h / G) * st,
@@ -1386,7 +1390,7 @@ cudaError_t launch_shared_t(const CUtensorMap& mq, const CUtensorMap& mpk, const
   cudaError_t e = allow_smem(shared_own_kernel<D, G>, OwnLayout<D>::kAlloc, &own_set);
   if (e == cudaSuccess) e = allow_smem(shared_prefix_kernel<D>, PrefixLayout<D>::kAlloc, &prefix_set);
   if (e != cudaSuccess) return e;
-  e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, false,
+  e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, true,
                          stream, mok, mov, a, app);
   if (e != cudaSuccess) return e;
   e = launch(shared_prefix_kernel<D>, prefix_ctas(a.sms), kPrefixThreads, PrefixLayout<D>::kAlloc, true,
