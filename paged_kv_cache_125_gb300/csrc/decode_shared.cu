@@ -393,13 +393,10 @@ __device__ __forceinline__ bool plan_fits(const SharedArgs& a) {
 // per SM (which alternate on the tensor core) or for one beside a CTA of the
 // own-part kernel, whose HBM stream it overlaps.
 
-#ifndef POL_PREFIX
-#define POL_PREFIX policy_evict_last
-#endif
-#ifndef PREFIX_REGS
-#define PREFIX_REGS 112
-#endif
 constexpr int kPrefixThreads = 192;
+// Two warps of this kernel and three of the own-part kernel must fit one SM
+// sub-partition's 16384 registers: 32 * (2 * 112 + 3 * 96).
+constexpr int kPrefixRegs = 112;
 
 enum : int {
   P_KFULL = 0,   // [2]
@@ -491,7 +488,7 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
     prefetch_tensormap(tmV);
   }
   // Other tiles read the same keys: hold on to them in L2.
-  const uint64_t keep = POL_PREFIX();
+  const uint64_t keep = policy_evict_last();
   const int G = a.num_heads / a.num_kv_heads;
   uint32_t n = 0, segs = 0;  // steps and segments issued; step n uses slot n & 1
   bool ok = true, k_only = false;
@@ -735,7 +732,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
 }
 
 template <int D>
-__global__ void __maxnreg__(PREFIX_REGS)
+__global__ void __maxnreg__(kPrefixRegs)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
@@ -801,14 +798,10 @@ __global__ void __maxnreg__(PREFIX_REGS)
 // stage that ends at a sequence's last token takes that token's K / V row
 // from the new rows, and the producer warp writes them to the cache.
 
-#ifndef OWN_REGS
-#define OWN_REGS 96
-#endif
-#ifndef OWN_STAGES
-#define OWN_STAGES 4
-#endif
 constexpr int kOwnWarps = 8;  // consumer warps
 constexpr int kOwnThreads = (kOwnWarps + 1) * 32;
+constexpr int kOwnRegs = 96;
+static_assert(32 * (2 * kPrefixRegs + 3 * kOwnRegs) <= 16384, "registers of a sub-partition");
 constexpr int kStageRows = 64;  // tokens x kv heads of a stage
 
 enum : int { F_NEW = 1, F_LAST = 2, F_DONE = 4, F_TAIL = 8 };
@@ -820,7 +813,7 @@ struct StageMeta {
 template <int D>
 struct OwnLayout {
   static constexpr uint32_t kHalf = kStageRows * D * 2;
-  static constexpr int kStages = D == 128 ? OWN_STAGES : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kMeta = 2 * kStages * kHalf;
   static constexpr uint32_t kBar = kMeta + kStages * (uint32_t)sizeof(StageMeta);
   static constexpr uint32_t kAlloc = kBar + 2 * kStages * 8;
@@ -1146,7 +1139,7 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
 }
 
 template <int D, int G>
-__global__ void __maxnreg__(OWN_REGS)
+__global__ void __maxnreg__(kOwnRegs)
     shared_own_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const SharedArgs a, const SharedAppend app) {
   using Lay = OwnLayout<D>;

@@ -221,6 +221,49 @@ def test_plan_finds_the_groups():
             assert plan_prefixes(w.plan(min_shared), w.b) == want, (i, min_shared)
 
 
+def test_more_sequences_than_one_round_of_the_plan():
+    """Over 1024 sequences, groups across the rounds' borders among them."""
+    groups = [(9, [1 + i % 5 for i in range(700)])] + [(0, [3 + i % 40]) for i in range(200)]
+    groups += [(8 + i % 7, [1 + (3 * j + i) % 30 for j in range(2 + i % 6)]) for i in range(120)]
+    groups += [(20, [2] * 650), (0, [0] * 5)]
+    w = Batch((4, 2, 64), 16, groups, seed=4)
+    assert w.b > 1900
+    plan = w.plan()
+    assert plan_prefixes(plan, w.b) == shared_prefixes(w.tables.tolist(), w.lens.tolist(), 16)
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), plan, softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(out, w.reference(), "many sequences")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_tables(seed):
+    """Any tables: pages shared by neighbours, by others, at other places, the
+    same page twice in a row, and rows in any order."""
+    rng = np.random.default_rng(1000 + seed)
+    heads = HEADS[seed % len(HEADS)]
+    bs = int(rng.choice([16, 32, 64, 256]))
+    w = Batch(heads, bs, [(0, [1])], seed=seed, poison=False, extra=int(rng.integers(4, 60)))
+    b, width = int(rng.integers(1, 90)), int(rng.integers(1, 40))
+    tables = rng.integers(0, w.nb, (b, width))
+    for i in range(1, b):  # leading pages of an earlier row, mostly of the one before
+        if rng.random() < 0.7:
+            j = i - 1 if rng.random() < 0.8 else int(rng.integers(0, i))
+            n = int(rng.integers(0, width + 1)) if rng.random() < 0.5 else width
+            tables[i, :n] = tables[j, :n]
+    lens = rng.integers(0, width * bs + 1, b)
+    lens[rng.random(b) < 0.5] = width * bs - int(rng.integers(0, bs))
+    w.b, w.tables, w.lens = b, tables.astype(np.int32), lens.astype(np.int32)
+    w.q = torch.randn((b, heads[0], heads[2]), device="cuda").to(BF16)
+    min_shared = int(rng.choice([0, 1, 64, 300]))
+    plan = w.plan(min_shared)
+    assert plan_prefixes(plan, b) == shared_prefixes(w.tables.tolist(), lens.tolist(), bs, min_shared or 128)
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), plan, softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(out, w.reference(), str(seed))
+
+
 def test_same_sequence_twice_and_whole_rows_shared():
     """Forked rows before their first own token: identical tables and lengths."""
     for n in (129, 160, 161, 1):
