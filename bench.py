@@ -74,11 +74,11 @@ TRAFFIC = {
     # prefill, tensor-core decode, merge) from one ncu --metrics capture, summed
     "mixed": {"file": ["paged_kv_cache_125_gb300/csrc/api.cu", "paged_kv_cache_125_gb300/csrc/prefill.cu",
                        "paged_kv_cache_125_gb300/csrc/decode.cu", "paged_kv_cache_125_gb300/csrc/kv_store.cu"],
-              "sha256": ["67530d107bbd4d9366bf0e741036ab01295e5defadb3a6051ddf6a63b3bea151",
+              "sha256": ["873800b68240450d90e2b0c87b252cddda1e7b9541fb66907ed09a822049787b",
                          "87f871db8ebb10db8884dfb6f61e8fbd782b1ab78e6e3c724783916fafdec3e9",
                          "07f434c766015d559ae0affb2f61e9797e9003a251cbb795c3e28b4c04ea3955",
                          "3de4572fdae061866219311055c3a52252d20b51b0cd3367ae6c4c0e416b6024"],
-              "bytes": 1280745472},
+              "bytes": 1280774144},
     # kv_copy_blocks on the 64-pair, 56-plane call, one ncu --metrics capture
     "copy_blocks": {"file": "paged_kv_cache_125_gb300/csrc/copy_blocks.cu",
                     "sha256": "4257c5bb2346e1bde3299c7f093b29e7939976617646de065c32796c7035dea2",

@@ -687,6 +687,39 @@ __global__ void __launch_bounds__((kBaseWarps + 1) * 32, 1)
 // rescaled only when a head's max grows by more than 2^8 (exact: O and l keep
 // the same stale reference, and P <= 2^8 fits bf16).
 
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                        uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                          uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+
+// d += a b: m16n8k16, bf16 inputs, fp32 accumulate (rows 8..15 of a are zero).
+__device__ __forceinline__ void mma_k16(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+}
+
+// d += a b: m16n8k8, bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // Byte offset of 16-byte chunk q of token row `row` in a stage half.
 __device__ __forceinline__ uint32_t chunk_off(uint32_t region, int T, int row, int q) {
   return region + (uint32_t)(((q >> 3) * T + row) * 128 + (((q & 7) ^ (row & 7)) << 4));
@@ -1086,6 +1119,47 @@ cudaError_t launch_decode_t(const DecodeArgs& a, const AppendArgs& app, int ctas
                             (const int*)a.split_seq, ctas, a.num_heads, a.out, a.out_stride);
 }
 
+// Tensor maps of one layer's K and V caches for the tensor-core path.  The
+// stage box is {64 columns, T tokens, D / 64 panels, Hkv heads} over a 4-D
+// view (column, token row, panel, head) of the [rows, Hkv, D] cache, which
+// lands a stage as [head][panel][token][64] in one copy per half; if the
+// driver does not take that view, a 3-D map (column, head, row) with a box
+// {64, 1, T} per (head, panel) gives the same layout.
+bool decode_maps(const DecodeArgs& a, int D, CUtensorMap* mk, CUtensorMap* mv, int* per_head) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const int Hkv = a.num_kv_heads, T = kTokensAllHeads / Hkv;
+  const cuuint64_t rows = (cuuint64_t)a.num_blocks * a.block_size;
+  {
+    cuuint64_t dims[4] = {64, rows, (cuuint64_t)(D / 64), (cuuint64_t)Hkv};
+    cuuint64_t strides[3] = {(cuuint64_t)Hkv * D * 2, 128, (cuuint64_t)D * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)T, (cuuint32_t)(D / 64), (cuuint32_t)Hkv};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    bool ok = true;
+    for (int i = 0; i < 2 && ok; ++i)
+      ok = enc(i == 0 ? mk : mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               const_cast<uint16_t*>(i == 0 ? a.k_cache : a.v_cache), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    if (ok) {
+      *per_head = 0;
+      return true;
+    }
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)T};
+  cuuint32_t es[3] = {1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (enc(i == 0 ? mk : mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<uint16_t*>(i == 0 ? a.k_cache : a.v_cache), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  *per_head = 1;
+  return true;
+}
+
 cudaError_t launch_merge(const DecodeArgs& a, int D, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, a.num_heads);
@@ -1108,9 +1182,7 @@ template <int D, int G>
 cudaError_t launch_decode_mma_t(DecodeArgs a, const AppendArgs& app, int ctas, cudaStream_t stream,
                                 bool pdl) {
   CUtensorMap mk, mv;
-  if (!stage_tensor_maps(a.k_cache, a.v_cache, a.num_blocks * (int64_t)a.block_size, a.num_kv_heads, D,
-                         kTokensAllHeads / a.num_kv_heads, &mk, &mv, &a.tma_per_head))
-    return cudaErrorInvalidValue;
+  if (!decode_maps(a, D, &mk, &mv, &a.tma_per_head)) return cudaErrorInvalidValue;
   const size_t smem = decode_mma_smem_bytes<D, G>(mma_ring_stages<D, G>());
   cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<D, G>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1139,46 +1211,6 @@ cudaError_t launch_decode_any(const DecodeArgs& a, const AppendArgs& app, int ct
 }
 
 }  // namespace
-
-// Tensor maps of one layer's K and V caches for the tensor-core path.  The
-// stage box is {64 columns, T tokens, D / 64 panels, Hkv heads} over a 4-D
-// view (column, token row, panel, head) of the [rows, Hkv, D] cache, which
-// lands a stage as [head][panel][token][64] in one copy per half; if the
-// driver does not take that view, a 3-D map (column, head, row) with a box
-// {64, 1, T} per (head, panel) gives the same layout.
-bool stage_tensor_maps(const uint16_t* k_cache, const uint16_t* v_cache, int64_t rows, int Hkv,
-                       int D, int T, CUtensorMap* mk, CUtensorMap* mv, int* per_head) {
-  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-  if (!enc) return false;
-  {
-    cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64), (cuuint64_t)Hkv};
-    cuuint64_t strides[3] = {(cuuint64_t)Hkv * D * 2, 128, (cuuint64_t)D * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)T, (cuuint32_t)(D / 64), (cuuint32_t)Hkv};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    bool ok = true;
-    for (int i = 0; i < 2 && ok; ++i)
-      ok = enc(i == 0 ? mk : mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-               const_cast<uint16_t*>(i == 0 ? k_cache : v_cache), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    if (ok) {
-      *per_head = 0;
-      return true;
-    }
-  }
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)T};
-  cuuint32_t es[3] = {1, 1, 1};
-  for (int i = 0; i < 2; ++i)
-    if (enc(i == 0 ? mk : mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<uint16_t*>(i == 0 ? k_cache : v_cache), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  *per_head = 1;
-  return true;
-}
 
 bool decode_supported(int num_heads, int num_kv_heads, int head_dim) {
   if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return false;

@@ -5,7 +5,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "kvp_device.cuh"
+#include "kvp_warp.cuh"
 
 namespace kvp {
 namespace {
@@ -352,7 +352,6 @@ struct SharedArgs {
   float* prefix_part;  // rows of the prefix kernel's segments
   float* own_part;     // rows of the own-part kernel's segments
   int sms;
-  int tma_per_head;
   uint16_t* out;
   int64_t out_stride;
   int* status;
@@ -927,17 +926,8 @@ __device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const
           mbar_arrive_expect_tx(&full[s], 2 * Lay::kHalf);
           const int row = (phys << shift) + off;
           // Rows past n (of the next page, or past the pool) are masked by the consumers.
-          if (!a.tma_per_head) {
-            tma_load_4d_hint(dk, tmK, 0, row, 0, 0, &full[s], once);
-            tma_load_4d_hint(dv, tmV, 0, row, 0, 0, &full[s], once);
-          } else {
-            for (int h = 0; h < Hkv; ++h)
-              for (int p = 0; p < D / 64; ++p) {
-                const uint32_t at = (uint32_t)((h * (D / 64) + p) * T * 128);
-                tma_load_3d_hint(dk + at, tmK, p * 64, h, row, &full[s], once);
-                tma_load_3d_hint(dv + at, tmV, p * 64, h, row, &full[s], once);
-              }
-          }
+          tma_load_4d_hint(dk, tmK, 0, row, 0, 0, &full[s], once);
+          tma_load_4d_hint(dv, tmV, 0, row, 0, 0, &full[s], once);
         }
         issued |= 1u << s;
         issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
@@ -1498,8 +1488,8 @@ cudaError_t launch_decode_shared(const SharedCall& c, const SharedPlan& plan,
   if (!rows_tensor_map(&mq, c.q, c.num_seqs, c.num_heads, D, c.q_stride, G, kTileRows / G) ||
       !rows_tensor_map(&mpk, c.k_cache, rows, Hkv, D, (int64_t)Hkv * D, 1, box) ||
       !rows_tensor_map(&mpv, c.v_cache, rows, Hkv, D, (int64_t)Hkv * D, 1, box) ||
-      !stage_tensor_maps(c.k_cache, c.v_cache, rows, Hkv, D, kStageRows / Hkv, &mok, &mov,
-                         &a.tma_per_head))
+      !stage_tensor_map(&mok, c.k_cache, rows, Hkv, D, kStageRows / Hkv) ||
+      !stage_tensor_map(&mov, c.v_cache, rows, Hkv, D, kStageRows / Hkv))
     return cudaErrorInvalidValue;
   auto run = [&](auto d, auto g) {
     return launch_shared_t<decltype(d)::value, decltype(g)::value>(mq, mpk, mpv, mok, mov, a, ap, stream);

@@ -2,7 +2,6 @@
 // translation units of libkvpaged.  Not installed; not part of the ABI.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -91,16 +90,6 @@ cudaError_t launch_decode(const uint16_t* q, int64_t q_stride, const uint16_t* k
 // prefill.cu: cuTensorMapEncodeTiled (a PFN_cuTensorMapEncodeTiled_v12000), or
 // null if the driver does not provide it.
 void* tensor_map_encoder();
-// prefill.cu: 3-D map over [rows, heads, D] bf16 (row stride in elements),
-// 128-byte swizzle, box {64, box_heads, box_rows}.
-bool rows_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int D,
-                     int64_t row_stride, int box_heads, int box_rows);
-// decode.cu: maps of one layer's K and V caches ([rows, Hkv, D]) that land a
-// stage of T token rows as [head][64-column panel][token][64] with the
-// 128-byte swizzle, in one box ({64, T, D / 64, Hkv}; *per_head 0) or one per
-// (head, panel) ({64, 1, T}; *per_head 1).
-bool stage_tensor_maps(const uint16_t* k_cache, const uint16_t* v_cache, int64_t rows, int Hkv,
-                       int D, int T, CUtensorMap* mk, CUtensorMap* mv, int* per_head);
 bool prefill_supported(int num_heads, int num_kv_heads, int head_dim, int block_size);
 // New rows of attn_prefill_varlen_append, stored by a kv_store launch just
 // before the prefill: row t of k / v (row stride `stride`) is the key /

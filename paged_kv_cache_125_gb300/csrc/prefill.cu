@@ -365,6 +365,32 @@ __device__ __forceinline__ bool ring_item(const Sched* sc, uint64_t* bars, int k
   return it.b >= 0;
 }
 
+// Transpose of a 4 x 4 matrix of 16-byte chunks held by the 4 lanes of a
+// quad: on entry lane j holds chunks 0..3 of its row in w[0..3]; on exit lane
+// j holds chunk j of rows 0..3 of the quad.  Two butterfly stages; in each, a
+// chunk moves to the partner lane when one bit of its chunk index differs
+// from the same bit of the lane index.
+__device__ __forceinline__ void quad_transpose16(uint32_t (&w)[4][4], int lane) {
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1) {
+    const bool hi = (lane & m) != 0;
+#pragma unroll
+    for (int k0 = 0; k0 < 4; ++k0) {
+      if (k0 & m) continue;
+      const int k1 = k0 | m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t send = hi ? w[k0][i] : w[k1][i];
+        const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, m);
+        if (hi)
+          w[k0][i] = recv;
+        else
+          w[k1][i] = recv;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1005,11 +1031,6 @@ cudaError_t launch_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorM
 }  // namespace
 
 void* tensor_map_encoder() { return get_encoder() ? reinterpret_cast<void*>(g_encode) : nullptr; }
-
-bool rows_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int heads, int D,
-                     int64_t row_stride, int box_heads, int box_rows) {
-  return get_encoder() && make_map(m, base, rows, heads, D, row_stride, box_heads, box_rows);
-}
 
 bool prefill_supported(int num_heads, int num_kv_heads, int head_dim, int block_size) {
   if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return false;
