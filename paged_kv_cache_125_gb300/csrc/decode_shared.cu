@@ -1,5 +1,40 @@
-// attn_shared_plan / attn_decode_shared: paged decode of a batch whose
+// attn_shared_plan / attn_decode_shared(_append): paged decode of a batch whose
 // sequences share leading pages.
+//
+// Sources: "【nano-vllm 学习】04 - 自顶向下的引擎调度层源码学习2", section
+// "场景优化1：Parallel Memory Shared" (sequences of one prompt map their prompt
+// blocks to the same physical blocks), and the prefix cache of "nano-vLLM-1",
+// BlockManager "3. 核心方法一：分配 (allocate)"; the attention is that of
+// attn_decode_paged.
+//
+// With the keys of sequence b cut into a part that its group shares and a part
+// of its own, softmax(q K^T) V is put together from partial results (m = the
+// largest scaled score, l = sum 2^(s - m), acc = sum 2^(s - m) v, all fp32):
+//     M = max_p m_p,  out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.
+// So a group's shared keys can be read once, as a matrix product with all the
+// queries of the group, which turns the part that is read B times by
+// attn_decode_paged from HBM-bound into tensor-core work.
+//
+// Four kernels: the plan (once per step: groups, tiles, where each CTA starts),
+// and per layer the own parts (HBM-bound), the prefixes (tcgen05) and the
+// merge.  The two in the middle are sized to share every SM (shared memory
+// 131 + 99 of 228 KB, registers, 256 tensor-memory columns), one CTA each: the
+// tensor core works on the prefixes under the stream of the own parts, whatever
+// their proportion, with nothing to choose on the host.  The grids depend on
+// the SM count alone, so a captured call serves any batch of its size.
+//
+// Measured on one GB300 (device time of plan + call, its bytes read once):
+//   512 sequences, 32/8/128, 8192 keys shared, 64 .. 1000 own    234 us
+//     (own parts alone 162 us = 6.7 TB/s, prefixes alone 73 us = 940 TFLOP/s;
+//      together 211: the two meet at the tensor pipe, which the warp MMAs of
+//      the own parts use too, and in L2; 20 merge and plan)
+//   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           47 us
+//   16 sequences, 64/8/128, 32768 shared, up to 64 own             48 us
+//   against attn_decode_paged on such tables, 16/8/128: 64 sequences with 2048
+//   shared and 100 .. 600 own 30 against 98 us, with 8192 39 against 320.
+// Break-even of the default min_shared_len (128 tokens; shared against not):
+// groups of 4 x 16 27.9 / 29.3 us, one group of 64 27.0 / 29.2; groups of two
+// pay from 2048 tokens on only (1024: 37 / 35 us, 8192: 114 / 165).
 #include "decode_shared.h"
 
 #include <atomic>
@@ -20,7 +55,10 @@ constexpr int kTileKeys = 64;   // keys of a prefix step
 // (rows of the items before i) + c * (rows of an item) is never taken twice.
 __host__ __device__ constexpr int prefix_ctas(int sms) { return 2 * sms; }
 __host__ __device__ constexpr int own_ctas(int sms) { return sms; }
-constexpr int kLeastSteps = 2;    // prefix steps of a CTA
+// Prefix steps of a CTA: each CTA that touches an item adds a part to its rows'
+// merge, but a chain of steps is latency (8 sequences behind 1024 tokens, four
+// layers: 51.7 / 50.1 / 53.1 / 66.7 us with at least 1 / 2 / 4 / 8).
+constexpr int kLeastSteps = 2;
 // A sequence in a CTA costs about as much as 64 KiB of its stream (query,
 // page and plan look-ups, partials): in the own-part kernel's split it counts
 // that many tokens (of head_dim 128) more than it has.
@@ -37,8 +75,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // ------------------------------------------------------------------ plan
-
-constexpr int kPlanThreads = 1024;
 
 struct PlanArgs {
   const int32_t* block_tables;
@@ -57,8 +93,8 @@ struct PlanArgs {
 };
 
 // Exclusive prefix sums of N values at once over the block's threads; total[i]
-// = the sum of v[i].  `sums` holds N x kPlanThreads / 32 sums.
-template <int N>
+// = the sum of v[i].  `sums` holds the warps' sums.
+template <int T, int N>
 __device__ void block_scan(long long (&v)[N], long long (&total)[N], long long (*sums)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl[N];
@@ -78,7 +114,7 @@ __device__ void block_scan(long long (&v)[N], long long (&total)[N], long long (
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const long long s = sums[i][lane];
+    const long long s = lane < T / 32 ? sums[i][lane] : 0;
     long long ws = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -89,8 +125,6 @@ __device__ void block_scan(long long (&v)[N], long long (&total)[N], long long (
     v[i] = __shfl_sync(0xffffffffu, ws - s, warp) + incl[i] - v[i];
   }
 }
-static_assert(kPlanThreads == 1024, "block_scan needs 32 warps");
-
 __device__ __forceinline__ int plan_ctx(const PlanArgs& a, int b) {
   const int c = a.context_lens[b];
   const int64_t cap = (int64_t)a.max_blocks * a.block_size;
@@ -152,25 +186,26 @@ __device__ __forceinline__ bool plan_joined(const PlanArgs& a, int b, int prev, 
 
 // One cluster.  The warps of all its CTAs compare the table rows; after a
 // cluster barrier CTA 0 forms the groups and tiles by prefix sums over the
-// sequences, 1024 at a time.  The first 1024 sequences' shared-page counts and
-// groups stay in shared memory (later ones go through the plan buffer): the
+// sequences, T at a time.  Up to T sequences' shared-page counts and groups
+// stay in shared memory (of more, they go through the plan buffer): the
 // kernel is a chain of small dependent steps, and each round trip to L2 that
 // it does without is 0.7 us of a step's latency.
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArgs a) {
+template <int T>
+__global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
   __shared__ long long sums[3][32];
-  __shared__ int s_same[kPlanThreads + 2], s_min[kPlanThreads + 1], s_seq[kPlanThreads + 1],
-      s_ctx[kPlanThreads];
-  __shared__ long long s_tokens[kPlanThreads + 1], s_steps[kPlanThreads + 1];
+  __shared__ int s_same[T + 2], s_min[T + 1], s_seq[T + 1],
+      s_ctx[T];
+  __shared__ long long s_tokens[T + 1], s_steps[T + 1];
   const SharedPlan& p = a.plan;
   const int B = a.num_seqs, bs = a.block_size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool small = B <= kPlanThreads;
+  const bool small = B <= T;
   // Every CTA of the cluster runs before one writes to another's shared memory.
   asm volatile(
       "barrier.cluster.arrive.relaxed;\n\t"
       "barrier.cluster.wait;" ::
           : "memory");
-  for (int b = blockIdx.x + warp * gridDim.x; b < B; b += gridDim.x * (kPlanThreads / 32)) {
+  for (int b = blockIdx.x + warp * gridDim.x; b < B; b += gridDim.x * (T / 32)) {
     int ctx;
     const int same = shared_pages(a, b, &ctx);
     if (lane == 0) {
@@ -195,17 +230,17 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
   // that every one of them shares.
   int* group_min = small ? s_min : p.group_min;
   int* group_seq = small ? s_seq : p.group_seq;
-  for (int b = threadIdx.x; b < B; b += kPlanThreads) group_min[b] = 0x7fffffff;
+  for (int b = threadIdx.x; b < B; b += T) group_min[b] = 0x7fffffff;
   int my_ctx = 0, my_group = 0;  // of sequence threadIdx.x
   long long groups = 0;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += T) {
     const int b = b0 + (int)threadIdx.x;
     // s_same[i]: sequence b0 - 1 + i
     if (!small) {
       s_same[threadIdx.x + 1] = b < B ? __ldcg(&p.same[b]) : 0;
       if (threadIdx.x == 0) s_same[0] = b > 0 ? __ldcg(&p.same[b - 1]) : 0;
       if (threadIdx.x == 1)
-        s_same[kPlanThreads + 1] = b0 + kPlanThreads < B ? __ldcg(&p.same[b0 + kPlanThreads]) : 0;
+        s_same[T + 1] = b0 + T < B ? __ldcg(&p.same[b0 + T]) : 0;
     } else if (b < B) {
       my_ctx = s_ctx[b];
     }
@@ -214,7 +249,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     const bool joined = b < B && plan_joined(a, b, b > 0 ? s_same[threadIdx.x] : 0, same,
                                              b + 1 < B ? s_same[threadIdx.x + 2] : 0);
     long long v[1] = {b < B && !joined ? 1 : 0}, total[1];
-    block_scan(v, total, sums);
+    block_scan<T>(v, total, sums);
     if (b < B) {
       const int g = (int)(groups + v[0]) - (joined ? 1 : 0);
       if (b0 == 0) my_group = g;
@@ -232,7 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
   // find their work by: (tiles, sequences in tiles), steps, own positions.
   const int tile_seqs = kTileRows / a.group;
   long long base[3] = {0, 0, 0};
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += T) {
     const int b = b0 + (int)threadIdx.x;
     int ctx = 0, prefix = 0;
     bool start = false;
@@ -246,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
     const int len = ctx > 0 ? a.gap + ctx - prefix : 0;
     long long v[3] = {((long long)(start ? 1 : 0) << 32) | (prefix > 0 ? 1 : 0), steps, len};
     long long total[3];
-    block_scan(v, total, sums);
+    block_scan<T>(v, total, sums);
 #pragma unroll
     for (int i = 0; i < 3; ++i) v[i] += base[i], base[i] += total[i];
     if (b < B) {
@@ -306,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const PlanArg
   const long long *tokens = small ? s_tokens : p.cum_tokens, *tsteps = small ? s_steps : p.cum_steps;
   const int *prefixes = small ? s_same : p.prefix, *ctxs = small ? s_ctx : p.ctx;
   const int *tile_seq = small ? s_seq : p.tile_seq, *tile_rows = small ? s_min : p.cum_rows;
-  for (int i = threadIdx.x; i < own_ctas(a.sms) + prefix_ctas(a.sms); i += kPlanThreads) {
+  for (int i = threadIdx.x; i < own_ctas(a.sms) + prefix_ctas(a.sms); i += T) {
     const bool own = i < own_ctas(a.sms);
     const int c = own ? i : i - own_ctas(a.sms);
     const long long x = c * (own ? ochunk : pchunk);
@@ -388,9 +423,12 @@ __device__ __forceinline__ bool plan_fits(const SharedArgs& a) {
 // 192 threads: warps 0-3 softmax (thread = row), warp 4 TMA producer, warp 5
 // tensor memory and MMA issue.  S has two buffers: S(j + 1) is computed while
 // the softmax works on S(j), so the tensor core's part of a step does not stand
-// in the chain from one softmax to the next.  Shared and tensor memory and registers are small enough for two CTAs
-// per SM (which alternate on the tensor core) or for one beside a CTA of the
-// own-part kernel, whose HBM stream it overlaps.
+// in the chain from one softmax to the next (one buffer: 128 us instead of 73
+// for 512 x 32 rows over 8192 keys).  What bounds it is that chain (barrier,
+// tensor-memory load, maximum, exponentials, store, barrier; the tensor pipe is
+// active 45% of the time with two CTAs on an SM, issue slots 34%).  A step of
+// 128 keys would need 384 columns of tensor memory.  K and V are read once per
+// tile from L2 (552 MB for those rows; 38 MB from HBM).
 
 constexpr int kPrefixThreads = 192;
 // Two warps of this kernel and three of the own-part kernel must fit one SM
@@ -796,6 +834,11 @@ __global__ void __maxnreg__(kPrefixRegs)
 // query head and consumer warp of its kv head.  With the fused store, the
 // stage that ends at a sequence's last token takes that token's K / V row
 // from the new rows, and the producer warp writes them to the cache.
+//
+// HBM-bound: alone it reads 1.09 GB in 162 us and 2.06 GB in 290 us (6.7 and
+// 7.1 TB/s), every byte once.  Four 32 KiB stages beside a prefix CTA's 99 KB
+// (three: 2% slower).  The loads are marked evict-first: they are read once and
+// would push the prefixes out of L2 (own parts of 512 sequences 171 us without).
 
 constexpr int kOwnWarps = 8;  // consumer warps
 constexpr int kOwnThreads = (kOwnWarps + 1) * 32;
@@ -1170,7 +1213,8 @@ __global__ void __maxnreg__(kOwnRegs)
 // out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p over a row's partials:
 // W warps per (sequence, query head), a lane per D / 32 elements.  Launched as
 // a programmatic dependent of the prefix kernel: its plan look-ups overlap the
-// kernels before it.
+// kernels before it.  Bound by latency: a few parts of 528 bytes a row, from
+// L2; 12 us for 16384 rows, 4 us for 1024.
 
 constexpr int kMergeWarps = 8;
 
@@ -1427,12 +1471,17 @@ cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, cons
   const PlanArgs a{block_tables, ctx,   max_blocks,   num_seqs,       num_blocks,
                    block_size,   group, num_kv_heads, own_gap(num_kv_heads), min_shared_len, num_sms,
                    plan,         status};
-  // A warp compares one pair of rows at a time: up to 8 CTAs (a portable cluster).
+  // A warp compares one pair of rows at a time: up to 8 CTAs (a portable
+  // cluster).  Few sequences: smaller CTAs, whose barriers cost less (64
+  // sequences 5.1 us with 256 threads, 6.9 with 1024), as long as there are
+  // warps enough (138: 8.1 us with 256 threads, 6.9 with 512, 7.4 with 1024;
+  // 512: 9.5 us with 512, 8.9 with 1024).
+  const int threads = num_seqs <= 128 ? 256 : num_seqs <= 256 ? 512 : 1024;
   int ctas = 1;
-  while (ctas < 8 && ctas * (kPlanThreads / 32) < num_seqs) ctas *= 2;
+  while (ctas < 8 && ctas * (threads / 32) < num_seqs) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1440,7 +1489,11 @@ cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, cons
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg,
+                            threads == 256   ? shared_plan_kernel<256>
+                            : threads == 512 ? shared_plan_kernel<512>
+                                             : shared_plan_kernel<1024>,
+                            a);
 }
 
 // Rows of partial results: see chunk_of.
