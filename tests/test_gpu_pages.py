@@ -226,6 +226,54 @@ def test_compact_all_live_all_free_and_wrong_pages():
         assert np.array_equal(raw(cache), want)
 
 
+def test_moves_across_2_32_bytes():
+    """Copies from the end of a pool of 12.6 GB to its start, in both planes."""
+    nb, bs = 12000, 256
+    cache = torch.empty((2, nb, bs, 8, 128), dtype=BF16, device="cuda")
+    tables = [[nb - 1, nb - 2, 5, nb // 2], [nb - 7, -1, -1, -1]]
+    lens, counts = [4 * bs - 3, 100], [0] * nb
+    for p in tables[0] + tables[1][:1]:
+        counts[p] = 1
+        cache[:, p] = bits((2, bs, 8, 128), p)
+    t, c, places, moves, bad = ref.compact(tables, lens, counts, bs)
+    want = {d: raw(cache[:, s]).copy() for s, d in moves}
+    kvp.device_status()
+    ot, oc, op = kvp.kv_pages_compact(cache, dev(tables), dev(lens), dev(counts))
+    check_status(bad)
+    assert (ot.tolist(), oc.tolist(), op.tolist()) == (t, c, places) and len(moves) == 5
+    for d, w in want.items():
+        assert np.array_equal(raw(cache[:, d]), w), d
+    parents = [0, 0, 1, 1]
+    t2, l2, c2, copies, bad = ref.fork(t, lens, c, parents, bs)
+    ot2, ol2, oc2 = kvp.kv_pages_fork(cache, ot, dev(lens), oc, dev(parents))
+    check_status(bad)
+    assert (ot2.tolist(), ol2.tolist(), oc2.tolist()) == (t2, l2, c2) and len(copies) == 2
+    for s, d, n in copies:
+        assert torch.equal(cache[:, d, :n].view(torch.int16), cache[:, s, :n].view(torch.int16))
+
+
+def test_more_rows_than_fit_in_shared_memory():
+    """Over 2048 rows: the searches of kv_pages_extend go through the workspace."""
+    p = Pool(9000, 16, 2600, 4, seed=3)
+    new = [int(p.rng.integers(0, min(64 - x, 20) + 1)) for x in p.lens]
+    total = sum(new)
+    t, l, c, s, bad = ref.extend(p.tables, p.lens, p.counts, new, 16, total)
+    kvp.device_status()
+    ot, ol, oc, slots = kvp.kv_pages_extend(*p.args(), dev(new), 16, total)
+    check_status(bad)
+    assert ol.tolist() == l and slots.tolist() == s and oc.tolist() == c and ot.tolist() == t
+    parents = p.rng.integers(-1, 2600, 3000).tolist()
+    cache = bits((1, 9000, 16, 1, 64), 4)
+    want = raw(cache).copy()
+    t2, l2, c2, copies, bad = ref.fork(t, l, c, parents, 16)
+    for a, b, n in copies:
+        want[:, b, :n] = want[:, a, :n]
+    ot, ol, oc = kvp.kv_pages_fork(cache, ot, ol, oc, dev(parents))
+    check_status(bad)
+    assert (ot.tolist(), ol.tolist(), oc.tolist()) == (t2, l2, c2)
+    assert np.array_equal(raw(cache), want)
+
+
 def test_empty_tables():
     cache = bits((2, 6, 16, 1, 64), 3)
     before = raw(cache).copy()

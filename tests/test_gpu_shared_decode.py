@@ -358,6 +358,35 @@ def test_graph_replay_follows_the_tables():
             w.check(out, ref, f"step {i}")
 
 
+def test_pages_past_2_31_elements():
+    """A cache of 3.1e9 elements, the batch's pages at its far end."""
+    w = Batch((16, 8, 128), 256, [(3, [100, 300]), (0, [513])], seed=6)
+    nb = 12000
+    ids = np.arange(nb - w.nb, nb)
+    kc, vc = (torch.empty((nb, 256, 8, 128), dtype=BF16, device="cuda") for _ in range(2))
+    kc[nb - w.nb:], vc[nb - w.nb:] = w.kc, w.vc
+    tables = np.where(w.tables >= 0, ids[w.tables], -1).astype(np.int32)
+    slots = np.array([ids[s // 256] * 256 + s % 256 for s in w.slots], np.int32)
+    plan = kvp.attn_shared_plan(w.dev(tables), w.dev(w.lens), 256, 16, 8, nb)
+    out = kvp.attn_decode_shared_append(w.q, w.k, w.v, w.dev(slots), kc, vc, w.dev(tables), plan)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    kr, vr = u16(w.kc), u16(w.vc)
+    oracle.kv_store(w.k.cpu(), w.v.cpu(), torch.from_numpy(w.slots), kr, vr)
+    assert np.array_equal(u16(kc[nb - w.nb:]), kr) and np.array_equal(u16(vc[nb - w.nb:]), vr)
+    w.check(out, w.reference(kc[nb - w.nb:], vc[nb - w.nb:]))
+
+
+def test_out_may_be_q():
+    w = Batch((32, 8, 128), 16, SHAPES["odd"], seed=21)
+    ref = w.reference()
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), out=w.q)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    assert out.data_ptr() == w.q.data_ptr()
+    w.check(out, ref, "in place")
+
+
 def test_empty_batch():
     w = Batch((16, 8, 128), 16, [(0, [4])], seed=0)
     e = torch.zeros((0, 16, 128), dtype=BF16, device="cuda")
