@@ -427,9 +427,10 @@ int attn_decode_paged_noalloc(const kvp_bf16 *q, int64_t q_stride_tok, const kvp
  *                    records KVP_ERR_DEVICE_DATA
  *   min_shared_len   tokens (0: the library's default, 128)
  *   plan             device buffer of at least attn_shared_plan_size() bytes,
+ *                    (a number of the shape and the current device),
  *                    16-byte aligned.  It holds the step's context lengths
- *                    too: one plan serves every layer of the step, and the
- *                    next step needs a new one.
+ *                    too: one plan serves every layer of the step on this
+ *                    device, and the next step needs a new one.
  * Supported: num_heads / num_kv_heads in {1, 2, 4, 8}, num_kv_heads in
  * {1, 2, 4, 8}; block_size 16 * 2^k (16..4096); num_seqs < 2^20.
  * num_seqs == 0 is a no-op.

@@ -38,6 +38,8 @@
 #include "decode_shared.h"
 
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 #include <type_traits>
 
 #include "kvp_warp.cuh"
@@ -383,6 +385,8 @@ struct SharedArgs {
   int max_blocks;
   int num_seqs, num_heads, num_kv_heads;
   float scale_log2;
+  float prefix_scale_log2;  // its magnitude, for the prefix kernel: never 0
+  uint32_t prefix_negate;   // and its sign, as the negate-A bit of an MMA
   SharedPlan plan;
   float* prefix_part;  // rows of the prefix kernel's segments
   float* own_part;     // rows of the own-part kernel's segments
@@ -601,7 +605,7 @@ template <int D>
 __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem, uint64_t* bars,
                            uint32_t tbase) {
   using Lay = PrefixLayout<D>;
-  constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kTileKeys, 0, 0);
+  const uint32_t idesc_s = idesc_bf16_f32(kTileRows, kTileKeys, 0, 0) | a.prefix_negate;
   constexpr uint32_t idesc_o = idesc_bf16_f32(kTileRows, D, 0, 1);
   const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
   const uint64_t dk0 = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
@@ -663,7 +667,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
   const int G = a.num_heads / a.num_kv_heads;
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
   const uint32_t t_row = tbase + lane_base, o_col = t_row + kColO;
-  const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+  const float2 scale2 = make_float2(a.prefix_scale_log2, a.prefix_scale_log2);
   uint32_t n = 0, segs = 0;
   while (sg.next(a)) {
     const bool valid = r < sg.nseq * G;
@@ -687,7 +691,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
 #pragma unroll
       for (int i = 0; i < kTileKeys; ++i)
         mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[i >> 5][i & 31]));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.prefix_scale_log2;
       // The reference max m moves only when the step's max exceeds it by more
       // than 2^8; O and l keep the same stale reference, so this is exact, and
       // P <= 2^8 is well inside bf16's range.
@@ -1526,6 +1530,12 @@ cudaError_t launch_decode_shared(const SharedCall& c, const SharedPlan& plan,
   a.num_heads = c.num_heads;
   a.num_kv_heads = Hkv;
   a.scale_log2 = c.softmax_scale * 1.4426950408889634f;
+  // The prefix kernel takes the maximum of a row before it scales it and masks
+  // with -inf, so its scale is positive: the sign goes to the matrix product
+  // (bit 13 of an instruction descriptor negates A), and 0 becomes a magnitude
+  // at which all scores below 10^32 are 0 to 2^-19.
+  a.prefix_scale_log2 = std::fmax(std::fabs(a.scale_log2), FLT_MIN);
+  a.prefix_negate = a.scale_log2 < 0.f ? 1u << 13 : 0u;
   a.plan = plan;
   a.sms = num_sms;
   a.prefix_part = static_cast<float*>(c.workspace);

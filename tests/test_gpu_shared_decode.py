@@ -208,6 +208,18 @@ def test_large_and_masked_scores():
             assert (np.abs(got[b, h] - ref) <= tol).all(), (b, h)
 
 
+@pytest.mark.parametrize("times", [-1.0, 0.0, 0.02, -1e-20, 1e-44])
+def test_any_scale(times):
+    """softmax_scale is any finite number, 0 (the values' mean) and negative
+    ones too; prefixes that end inside a step of the prefix kernel."""
+    w = Batch((16, 8, 128), 16, SHAPES["odd"], seed=22)
+    w.scale *= times
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    w.check(out, w.reference(), str(times))
+
+
 def test_plan_finds_the_groups():
     cases = [SHAPES[s] for s in ("odd", "many", "tall", "alone", "padding")]
     cases.append([(1, [3, 4]), (64, [5, 6, 7]), (8, [1, 2])])
