@@ -460,118 +460,84 @@ def attn_mixed_step(q, k, v, slot_mapping, cu_seqlens_q, cu_seqlens_k, max_seqle
 
 
 # The calls below run once per layer or step from Python, next to kernels of a
-# few microseconds, so their checks are written to cost little when all is
-# well: one comparison of everything at once per tensor, and the checks that
-# name the fault only where that fails.
+# few microseconds.  Their arguments are checked and marshalled by an extension
+# module (csrc/python/calls.cpp), which makes the call when all is well and
+# otherwise returns None: then the checks here name the fault.
 
-class _Torch:
-    """What these calls need of torch, looked up once."""
-
-    def __init__(self):
-        import torch
-        self.torch = torch
-        self.i32, self.u8, self.bf16 = torch.int32, torch.uint8, torch.bfloat16
-        self.empty, self.empty_like = torch.empty, torch.empty_like
-        self.current_device = torch.cuda.current_device
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_CALLS = None
 
 
-_TORCH = None
-_SIZES = {}
-
-
-def _torch():
-    global _TORCH
-    if _TORCH is None:
-        library()
-        _TORCH = _Torch()
-    return _TORCH
+def _calls():
+    """The extension module, built with the library."""
+    global _CALLS
+    lib = library()
+    with _LIB_LOCK:
+        if _CALLS is None:
+            import importlib.machinery
+            import importlib.util
+            from . import _build
+            path = _build.calls_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"the extension module is not built ({path}); run "
+                                   "`python -m paged_kv_cache_125_gb300._build` first")
+            loader = importlib.machinery.ExtensionFileLoader("_kvpaged_calls", path)
+            spec = importlib.util.spec_from_file_location("_kvpaged_calls", path, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            module.set_check(_check)
+            _CALLS = module
+    return _CALLS
 
 
 def _call(idx, fn, *args):
     """fn(*args, stream) on device idx, the tensors', and its current stream."""
-    T = _torch()
-    if idx == T.current_device():
-        rc = fn(*args, T.stream(idx))
-    else:
-        with T.torch.cuda.device(idx):
-            rc = fn(*args, T.stream(idx))
-    if rc:
-        _check(rc)
+    import torch
+    with torch.cuda.device(idx):
+        _check(fn(*args, torch.cuda.current_stream(idx).cuda_stream))
 
 
-def _sized(name, idx, *args) -> int:
-    """A size query of the library on device idx (None: the current one,
-    whichever it is); a size depends on its arguments and the device alone."""
-    T = _torch()
-    n = _SIZES.get((name, idx, args))
-    if n is None:
-        with T.torch.cuda.device(idx) if idx is not None else contextlib.nullcontext():
-            n = int(getattr(library(), name)(*args))
-        if n == 0:
-            _check(-1)
-        if idx is not None:
-            _SIZES[name, idx, args] = n
+def _sized(name, device, *args) -> int:
+    """A size query of the library on a device (None: the current one)."""
+    import torch
+    fn = getattr(library(), name)
+    with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
+        n = int(fn(*args))
+    if n == 0:
+        _check(-1)
     return n
 
 
-def _int32(t, name, shape, idx):
-    """An int32 tensor of that shape (None: any size), contiguous, on device idx."""
-    T = _torch()
-    if (isinstance(t, T.torch.Tensor) and t.dtype is T.i32 and t.get_device() == idx and
-            t.is_contiguous()):
-        have = t.shape
-        if have == shape or (len(have) == len(shape) and
-                             all(w is None or w == n for n, w in zip(have, shape))):
-            return
-    _require(t, name, T.i32, len(shape))
-    _require(t, name, T.i32, len(shape), T.torch.device("cuda", idx))
-    want = ", ".join("*" if w is None else str(w) for w in shape)
-    raise ValueError(f"{name} must be contiguous [{want}], got {tuple(t.shape)}")
+def _int32(t, name, shape, dev):
+    """An int32 tensor of that shape (None: any size), contiguous, on dev."""
+    import torch
+    _require(t, name, torch.int32, len(shape), dev)
+    if not t.is_contiguous() or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must be contiguous [{want}], got {tuple(t.shape)}")
 
 
-def _scratch(t, name, nbytes, idx):
+def _scratch(t, name, nbytes, dev):
     """The caller's buffer, or a new one."""
-    T = _torch()
+    import torch
     if t is None:
-        return T.empty(nbytes, dtype=T.u8, device=idx)
-    if not (isinstance(t, T.torch.Tensor) and t.dtype is T.u8 and t.get_device() == idx and
-            t.is_contiguous()):
-        _require(t, name, T.u8, 1)
-        _require(t, name, T.u8, 1, T.torch.device("cuda", idx))
+        return torch.empty(nbytes(), dtype=torch.uint8, device=dev)
+    _require(t, name, torch.uint8, 1, dev)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _heads_rows(t, name, shape, idx):
+def _heads_rows(t, name, shape, dev):
     """bf16 rows [rows, heads, head_dim], heads and head_dim contiguous -> row stride."""
-    T = _torch()
-    if isinstance(t, T.torch.Tensor) and t.dtype is T.bf16 and t.get_device() == idx and t.shape == shape:
-        s0, s1, s2 = t.stride()
-        if s2 == 1 and s1 == shape[2]:
-            return s0
-    _require(t, name, T.bf16, 3)
-    _require(t, name, T.bf16, 3, T.torch.device("cuda", idx))
+    import torch
+    _require(t, name, torch.bfloat16, 3, dev)
     if t.shape[0] != shape[0]:
         raise ValueError(f"{name} must have one row per sequence")
     return _rows(t, name, shape[1], shape[2])
 
 
-def _cuda_index(t, name, dtype, ndim):
-    _require(t, name, dtype, ndim)
-    return t.get_device()
-
-
 def attn_shared_plan_size(num_seqs: int, num_heads: int, num_kv_heads: int, device=None) -> int:
-    return _sized("attn_shared_plan_size", _device_index(device), num_seqs, num_heads, num_kv_heads)
-
-
-def _device_index(device):
-    """None, an index or a torch device -> an index (None: the current device)."""
-    if device is None or isinstance(device, int):
-        return device
-    return _torch().torch.device(device).index
+    return _sized("attn_shared_plan_size", device, num_seqs, num_heads, num_kv_heads)
 
 
 def attn_shared_plan(block_tables, context_lens, block_size: int, num_heads: int, num_kv_heads: int,
@@ -580,57 +546,25 @@ def attn_shared_plan(block_tables, context_lens, block_size: int, num_heads: int
     share (see include/kvpaged.h) and returns the plan, a uint8 device tensor
     that attn_decode_shared / attn_decode_shared_append of every layer of this
     step take.  ``plan``: a buffer to fill (attn_shared_plan_size bytes)."""
-    T = _torch()
-    idx = _cuda_index(block_tables, "block_tables", T.i32, 2)
+    done = (_CALLS or _calls()).attn_shared_plan(block_tables, context_lens, block_size, num_heads,
+                                                 num_kv_heads, num_blocks, min_shared_len, plan)
+    if done is not None:
+        return done
+    import torch
+    _require(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
     b, width = block_tables.shape
-    _int32(block_tables, "block_tables", (b, width), idx)
-    _int32(context_lens, "context_lens", (b,), idx)
-    plan = _scratch(plan, "plan", _sized("attn_shared_plan_size", idx, b, num_heads, num_kv_heads)
-                    if plan is None else 0, idx)
-    _call(idx, _LIB.attn_shared_plan, block_tables.data_ptr(), width, context_lens.data_ptr(), b,
+    _int32(block_tables, "block_tables", (b, width), dev)
+    _int32(context_lens, "context_lens", (b,), dev)
+    plan = _scratch(plan, "plan", lambda: attn_shared_plan_size(b, num_heads, num_kv_heads, dev), dev)
+    _call(dev.index, library().attn_shared_plan, block_tables.data_ptr(), width, context_lens.data_ptr(), b,
           num_blocks, block_size, num_heads, num_kv_heads, min_shared_len, plan.data_ptr(), plan.numel())
     return plan
 
 
 def attn_decode_shared_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
                                       device=None) -> int:
-    return _sized("attn_decode_shared_workspace_size", _device_index(device), num_seqs, num_heads,
-                  num_kv_heads, head_dim)
-
-
-def _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale, workspace, out):
-    """Checks what attn_decode_shared and its append form have in common;
-    -> (device index, shape of q, kv heads, out, (q, stride), (caches .. out))."""
-    T = _torch()
-    same = k_cache.shape == v_cache.shape if isinstance(v_cache, T.torch.Tensor) and \
-        isinstance(k_cache, T.torch.Tensor) else False
-    if not (same and k_cache.dtype is T.bf16 and v_cache.dtype is T.bf16 and k_cache.dim() == 4 and
-            k_cache.get_device() == v_cache.get_device() >= 0 and k_cache.is_contiguous() and
-            v_cache.is_contiguous()):
-        _cache_dims(k_cache, v_cache)
-    idx = k_cache.get_device()
-    nb, bs, hkv, d = k_cache.shape
-    _cuda_index(q, "q", T.bf16, 3)
-    shape = q.shape
-    b, hq, _ = shape
-    if shape[2] != d:
-        raise ValueError("head_dim of q and caches differ")
-    qs = _heads_rows(q, "q", shape, idx)
-    _int32(block_tables, "block_tables", (b, None), idx)
-    if out is None:
-        out = T.empty(shape, dtype=T.bf16, device=idx)
-    os_ = _heads_rows(out, "out", shape, idx)
-    if plan is None:
-        raise TypeError("plan must be a torch.Tensor")
-    plan = _scratch(plan, "plan", 0, idx)
-    workspace = _scratch(workspace, "workspace",
-                         _sized("attn_decode_shared_workspace_size", idx, b, hq, hkv, d)
-                         if workspace is None else 0, idx)
-    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
-    return (idx, shape, hkv, out, (q.data_ptr(), qs),
-            (k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, block_tables.data_ptr(),
-             block_tables.shape[1], plan.data_ptr(), plan.numel(), b, hq, hkv, d, scale,
-             workspace.data_ptr(), workspace.numel(), out.data_ptr(), os_))
+    return _sized("attn_decode_shared_workspace_size", device, num_seqs, num_heads, num_kv_heads, head_dim)
 
 
 def attn_decode_shared(q, k_cache, v_cache, block_tables, plan, softmax_scale: float | None = None,
@@ -638,10 +572,12 @@ def attn_decode_shared(q, k_cache, v_cache, block_tables, plan, softmax_scale: f
     """attn_decode_paged over a batch planned by attn_shared_plan (which has
     the context lengths): the pages that a group of neighbouring sequences
     share are read once for the group."""
-    idx, _, _, out, qa, rest = _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale,
-                                            workspace, out)
-    _call(idx, _LIB.attn_decode_shared, *qa, *rest)
-    return out
+    done = (_CALLS or _calls()).attn_decode_shared(q, None, None, None, k_cache, v_cache, block_tables, plan,
+                                                   softmax_scale, workspace, out)
+    if done is not None:
+        return done
+    return _decode_shared(q, None, None, None, k_cache, v_cache, block_tables, plan, softmax_scale, workspace,
+                          out)
 
 
 def attn_decode_shared_append(q, k, v, slot_mapping, k_cache, v_cache, block_tables, plan,
@@ -649,12 +585,45 @@ def attn_decode_shared_append(q, k, v, slot_mapping, k_cache, v_cache, block_tab
     """kv_store(k, v, slot_mapping, k_cache, v_cache) followed by
     attn_decode_shared, in one call (see include/kvpaged.h).  Row b of k / v
     is sequence b's new token, stored at slot_mapping[b]."""
-    idx, shape, hkv, out, qa, rest = _shared_args(q, k_cache, v_cache, block_tables, plan, softmax_scale,
-                                                  workspace, out)
-    new = (shape[0], hkv, shape[2])
-    ks, vs = _heads_rows(k, "k", new, idx), _heads_rows(v, "v", new, idx)
-    _int32(slot_mapping, "slot_mapping", (shape[0],), idx)
-    _call(idx, _LIB.attn_decode_shared_append, *qa, k.data_ptr(), v.data_ptr(), ks, vs,
+    if k is None:
+        raise TypeError("k must be a torch.Tensor")
+    done = (_CALLS or _calls()).attn_decode_shared(q, k, v, slot_mapping, k_cache, v_cache, block_tables, plan,
+                                                   softmax_scale, workspace, out)
+    if done is not None:
+        return done
+    return _decode_shared(q, k, v, slot_mapping, k_cache, v_cache, block_tables, plan, softmax_scale, workspace,
+                          out)
+
+
+def _decode_shared(q, k, v, slot_mapping, k_cache, v_cache, block_tables, plan, softmax_scale, workspace, out):
+    import torch
+    nb, bs, hkv, d = _cache_dims(k_cache, v_cache)
+    dev = k_cache.device
+    _require(q, "q", torch.bfloat16, 3, dev)
+    b, hq, _ = q.shape
+    if q.shape[2] != d:
+        raise ValueError("head_dim of q and caches differ")
+    qs = _heads_rows(q, "q", q.shape, dev)
+    _int32(block_tables, "block_tables", (b, None), dev)
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=dev)
+    os_ = _heads_rows(out, "out", q.shape, dev)
+    if plan is None:
+        raise TypeError("plan must be a torch.Tensor")
+    plan = _scratch(plan, "plan", None, dev)
+    workspace = _scratch(workspace, "workspace",
+                         lambda: attn_decode_shared_workspace_size(b, hq, hkv, d, dev), dev)
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    rest = (k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, block_tables.data_ptr(), block_tables.shape[1],
+            plan.data_ptr(), plan.numel(), b, hq, hkv, d, scale, workspace.data_ptr(), workspace.numel(),
+            out.data_ptr(), os_)
+    if k is None:
+        _call(dev.index, library().attn_decode_shared, q.data_ptr(), qs, *rest)
+        return out
+    new = (b, hkv, d)
+    ks, vs = _heads_rows(k, "k", new, dev), _heads_rows(v, "v", new, dev)
+    _int32(slot_mapping, "slot_mapping", (b,), dev)
+    _call(dev.index, library().attn_decode_shared_append, q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, vs,
           slot_mapping.data_ptr(), *rest)
     return out
 
@@ -664,29 +633,29 @@ def kv_pages_workspace_size(num_blocks: int, num_rows: int) -> int:
 
 
 def _pool_dims(kv_cache):
-    """[..., num_blocks, block_size, num_kv_heads, head_dim] -> device index,
+    """[..., num_blocks, block_size, num_kv_heads, head_dim] -> device,
     planes, plane stride, num_blocks, block_size, row elements."""
-    T = _torch()
-    if not isinstance(kv_cache, T.torch.Tensor):
+    import torch
+    if not isinstance(kv_cache, torch.Tensor):
         raise TypeError("kv_cache must be a torch.Tensor")
-    if kv_cache.dtype is not T.bf16 or not kv_cache.is_cuda or not kv_cache.is_contiguous():
+    if kv_cache.dtype is not torch.bfloat16 or not kv_cache.is_cuda or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous bf16 CUDA tensor")
     if kv_cache.dim() < 4:
         raise ValueError("kv_cache must be [..., num_blocks, block_size, num_kv_heads, head_dim]")
     nb, bs, hkv, d = kv_cache.shape[-4:]
     plane = nb * bs * hkv * d
-    return kv_cache.get_device(), kv_cache.numel() // max(plane, 1), plane, nb, bs, hkv * d
+    return kv_cache.device, kv_cache.numel() // max(plane, 1), plane, nb, bs, hkv * d
 
 
-def _outputs(out, names, shapes, idx):
+def _outputs(out, names, shapes, dev):
     """The caller's output tensors, checked, or new ones."""
-    T = _torch()
+    import torch
     if out is None:
-        return tuple(T.empty(s, dtype=T.i32, device=idx) for s in shapes)
+        return tuple(torch.empty(s, dtype=torch.int32, device=dev) for s in shapes)
     if len(out) != len(shapes):
         raise ValueError(f"out must be {len(shapes)} tensors")
     for t, name, shape in zip(out, names, shapes):
-        _int32(t, name, shape, idx)
+        _int32(t, name, shape, dev)
     return tuple(out)
 
 
@@ -696,17 +665,20 @@ def kv_pages_fork(kv_cache, block_tables, context_lens, ref_counts, parents, wor
     unfilled last page that several rows would write to is copied in every
     plane of ``kv_cache``.  Returns (block_tables, context_lens, ref_counts):
     new tensors, or ``out``, three tensors that do not overlap the inputs."""
-    idx, planes, stride, nb, bs, row = _pool_dims(kv_cache)
-    _int32(block_tables, "block_tables", (None, None), idx)
+    done = (_CALLS or _calls()).kv_pages_fork(kv_cache, block_tables, context_lens, ref_counts, parents,
+                                              workspace, out)
+    if done is not None:
+        return done
+    dev, planes, stride, nb, bs, row = _pool_dims(kv_cache)
+    _int32(block_tables, "block_tables", (None, None), dev)
     n, mb = block_tables.shape
-    _int32(context_lens, "context_lens", (n,), idx)
-    _int32(ref_counts, "ref_counts", (nb,), idx)
-    _int32(parents, "parents", (None,), idx)
+    _int32(context_lens, "context_lens", (n,), dev)
+    _int32(ref_counts, "ref_counts", (nb,), dev)
+    _int32(parents, "parents", (None,), dev)
     m = parents.shape[0]
-    out = _outputs(out, ("out tables", "out context_lens", "out ref_counts"), ((m, mb), (m,), (nb,)), idx)
-    need = _sized("kv_pages_workspace_size", idx, nb, max(n, m)) if workspace is None else 0
-    ws = _scratch(workspace, "workspace", need, idx)
-    _call(idx, _LIB.kv_pages_fork, kv_cache.data_ptr(), planes, stride, nb, bs, row,
+    out = _outputs(out, ("out tables", "out context_lens", "out ref_counts"), ((m, mb), (m,), (nb,)), dev)
+    ws = _scratch(workspace, "workspace", lambda: kv_pages_workspace_size(nb, max(n, m)), dev)
+    _call(dev.index, library().kv_pages_fork, kv_cache.data_ptr(), planes, stride, nb, bs, row,
           block_tables.data_ptr(), mb, context_lens.data_ptr(), n, ref_counts.data_ptr(),
           parents.data_ptr(), m, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
           ws.data_ptr(), ws.numel())
@@ -720,19 +692,23 @@ def kv_pages_extend(block_tables, context_lens, ref_counts, new_tokens, block_si
     slot_mapping), slot_mapping [num_slots] holding the new tokens' slots row
     after row, then -1.  ``out``: those four tensors; the first three may be
     the inputs themselves."""
-    T = _torch()
-    idx = _cuda_index(block_tables, "block_tables", T.i32, 2)
+    done = (_CALLS or _calls()).kv_pages_extend(block_tables, context_lens, ref_counts, new_tokens, block_size,
+                                                num_slots, workspace, out)
+    if done is not None:
+        return done
+    import torch
+    _require(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.device
     n, mb = block_tables.shape
-    _int32(block_tables, "block_tables", (n, mb), idx)
-    _int32(context_lens, "context_lens", (n,), idx)
-    _int32(ref_counts, "ref_counts", (None,), idx)
-    _int32(new_tokens, "new_tokens", (n,), idx)
+    _int32(block_tables, "block_tables", (n, mb), dev)
+    _int32(context_lens, "context_lens", (n,), dev)
+    _int32(ref_counts, "ref_counts", (None,), dev)
+    _int32(new_tokens, "new_tokens", (n,), dev)
     nb = ref_counts.shape[0]
     out = _outputs(out, ("out tables", "out context_lens", "out ref_counts", "slot_mapping"),
-                   ((n, mb), (n,), (nb,), (num_slots,)), idx)
-    need = _sized("kv_pages_workspace_size", idx, nb, n) if workspace is None else 0
-    ws = _scratch(workspace, "workspace", need, idx)
-    _call(idx, _LIB.kv_pages_extend, block_tables.data_ptr(), mb, context_lens.data_ptr(), n,
+                   ((n, mb), (n,), (nb,), (num_slots,)), dev)
+    ws = _scratch(workspace, "workspace", lambda: kv_pages_workspace_size(nb, n), dev)
+    _call(dev.index, library().kv_pages_extend, block_tables.data_ptr(), mb, context_lens.data_ptr(), n,
           ref_counts.data_ptr(), nb, block_size, new_tokens.data_ptr(), num_slots, out[0].data_ptr(),
           out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), ws.data_ptr(), ws.numel())
     return out
@@ -743,15 +719,17 @@ def kv_pages_compact(kv_cache, block_tables, context_lens, ref_counts, workspace
     ``kv_cache`` (see include/kvpaged.h).  Returns (block_tables, ref_counts,
     places), places[p] being the new id of page p (-1 if it was free): new
     tensors, or ``out``, three tensors that do not overlap the inputs."""
-    idx, planes, stride, nb, bs, row = _pool_dims(kv_cache)
-    _int32(block_tables, "block_tables", (None, None), idx)
+    done = (_CALLS or _calls()).kv_pages_compact(kv_cache, block_tables, context_lens, ref_counts, workspace, out)
+    if done is not None:
+        return done
+    dev, planes, stride, nb, bs, row = _pool_dims(kv_cache)
+    _int32(block_tables, "block_tables", (None, None), dev)
     n, mb = block_tables.shape
-    _int32(context_lens, "context_lens", (n,), idx)
-    _int32(ref_counts, "ref_counts", (nb,), idx)
-    out = _outputs(out, ("out tables", "out ref_counts", "places"), ((n, mb), (nb,), (nb,)), idx)
-    need = _sized("kv_pages_workspace_size", idx, nb, n) if workspace is None else 0
-    ws = _scratch(workspace, "workspace", need, idx)
-    _call(idx, _LIB.kv_pages_compact, kv_cache.data_ptr(), planes, stride, nb, bs, row,
+    _int32(context_lens, "context_lens", (n,), dev)
+    _int32(ref_counts, "ref_counts", (nb,), dev)
+    out = _outputs(out, ("out tables", "out ref_counts", "places"), ((n, mb), (nb,), (nb,)), dev)
+    ws = _scratch(workspace, "workspace", lambda: kv_pages_workspace_size(nb, n), dev)
+    _call(dev.index, library().kv_pages_compact, kv_cache.data_ptr(), planes, stride, nb, bs, row,
           block_tables.data_ptr(), mb, context_lens.data_ptr(), n, ref_counts.data_ptr(),
           out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel())
     return out

@@ -291,6 +291,36 @@ def test_empty_tables():
     check_status(False)
 
 
+def test_arguments_of_the_wrong_kind_are_named():
+    p = Pool(60, 16, 5, 6, seed=3)
+    bt, lens, counts = p.args()
+    cache, par = bits((2, 60, 16, 1, 64), 3), dev([0, 1])
+    i32 = dict(dtype=I32, device="cuda")
+    for error, match, call in (
+            (ValueError, "ref_counts", lambda: kvp.kv_pages_fork(cache, bt, lens, counts[:-1], par)),
+            (TypeError, "parents", lambda: kvp.kv_pages_fork(cache, bt, lens, counts, par.long())),
+            (TypeError, "parents", lambda: kvp.kv_pages_fork(cache, bt, lens, counts, [0, 1])),
+            (ValueError, "kv_cache", lambda: kvp.kv_pages_fork(cache[0, 0], bt, lens, counts, par)),
+            (ValueError, "kv_cache", lambda: kvp.kv_pages_fork(cache.transpose(0, 1), bt, lens, counts, par)),
+            (ValueError, "3 tensors", lambda: kvp.kv_pages_fork(cache, bt, lens, counts, par, out=(bt, lens))),
+            (ValueError, "out tables", lambda: kvp.kv_pages_fork(
+                cache, bt, lens, counts, par, out=(bt.clone(), lens.clone(), counts.clone()))),
+            (kvp.KvpError, "overlaps an input", lambda: kvp.kv_pages_fork(
+                cache, bt, lens, counts, dev(range(5)), out=(bt, lens.clone(), counts.clone()))),
+            (kvp.KvpError, "workspace needs", lambda: kvp.kv_pages_fork(
+                cache, bt, lens, counts, par, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
+            (ValueError, "context_lens", lambda: kvp.kv_pages_extend(bt, lens[:-1], counts, lens, 16, 4)),
+            (ValueError, "new_tokens", lambda: kvp.kv_pages_extend(bt, lens, counts, lens.cpu(), 16, 4)),
+            (ValueError, "slot_mapping", lambda: kvp.kv_pages_extend(
+                bt, lens, counts, dev([0] * 5), 16, 4, out=[bt, lens, counts, torch.empty(3, **i32)])),
+            (ValueError, "block_tables", lambda: kvp.kv_pages_compact(cache, bt.t().contiguous().t(), lens, counts)),
+            (ValueError, "places", lambda: kvp.kv_pages_compact(
+                cache, bt, lens, counts, out=(bt.clone(), counts.clone(), par)))):
+        with pytest.raises(error, match=match):
+            call()
+    check_status(False)
+
+
 def test_results_do_not_depend_on_order():
     p = Pool(5000, 16, 300, 40, seed=1)
     parents = dev(p.rng.integers(0, 300, 300))

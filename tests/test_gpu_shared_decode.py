@@ -425,6 +425,37 @@ def test_buffers_that_are_too_small_are_refused():
         kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan, workspace=small)
 
 
+def test_arguments_of_the_wrong_kind_are_named():
+    w = Batch((16, 8, 128), 16, [(10, [3, 4])], seed=8)
+    bt, lens, slots, plan = w.dev(w.tables), w.dev(w.lens), w.dev(w.slots), w.plan()
+    ok = dict(q=w.q, k=w.k, v=w.v, slot_mapping=slots, k_cache=w.kc, v_cache=w.vc, block_tables=bt, plan=plan)
+    wide = torch.empty((2, 16, 130), dtype=BF16, device="cuda")
+    cases = [(TypeError, "q must be", dict(q=w.q.float())), (ValueError, "head_dim", dict(q=w.q[..., :64])),
+             (ValueError, "contiguous", dict(q=wide[..., :128])),
+             (ValueError, "k must have one row", dict(k=w.k[:1])), (ValueError, "v must be a CUDA", dict(v=w.v.cpu())),
+             (TypeError, "k must be", dict(k=None)), (TypeError, "v must be", dict(v=None)),
+             (ValueError, "slot_mapping", dict(slot_mapping=slots[:1])),
+             (TypeError, "slot_mapping", dict(slot_mapping=slots.long())),
+             (ValueError, "block_tables", dict(block_tables=bt.t().contiguous().t())),
+             (TypeError, "plan", dict(plan=None)), (TypeError, "plan", dict(plan=plan.float())),
+             (ValueError, "out", dict(out=torch.empty((2, 16, 64), dtype=BF16, device="cuda"))),
+             (ValueError, "v_cache|caches", dict(v_cache=w.vc[:-1])),
+             (TypeError, "workspace", dict(workspace=torch.empty(9, device="cuda")))]
+    for error, match, change in cases:
+        with pytest.raises(error, match=match):
+            kvp.attn_decode_shared_append(**{**ok, **change})
+    for error, match, args in ((ValueError, "context_lens", (bt, lens[:1])), (TypeError, "context_lens", (bt, lens.long())),
+                               (ValueError, "block_tables", (bt[0], lens)), (TypeError, "block_tables", (None, lens))):
+        with pytest.raises(error, match=match):
+            kvp.attn_shared_plan(*args, 16, 16, 8, w.nb)
+    # numbers of other types are taken as they are elsewhere
+    a = kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan, softmax_scale=1)
+    b = kvp.attn_decode_shared(w.q, w.kc, w.vc, bt, plan, softmax_scale=1.0)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    assert torch.equal(a, b)
+
+
 def test_wrong_metadata_is_reported():
     """A plan of another shape writes nothing; a page outside the pool, a
     length past the table and a slot that is not the last token's are
