@@ -315,7 +315,7 @@ int kv_pages_extend(const int32_t* block_tables, int max_blocks_per_seq,
   int sms;
   rc = kvp::device_handles(&a.status, &sms);
   if (rc) return rc;
-  const cudaError_t e = kvp::launch_pages_extend(a, (cudaStream_t)stream);
+  const cudaError_t e = kvp::launch_pages_extend(a, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? KVP_OK : cuda_error(e, fn);
 }
 

@@ -16,15 +16,18 @@
 // take minima, so results do not depend on the order of execution.
 //
 // The plans are chains of dependent look-ups, bound by latency: a beam step of
-// 256 rows 13 us, a token for each of 512 rows over 150,000 pages 25 us, the
-// plan of a compaction 7 us.  The copies are bound by HBM (see below).
+// 256 rows 12 us, a token for each of 512 rows over 150,000 pages 12 us (25 with
+// a barrier pair and a load per round of 4096 pages, and the team keeping the
+// table rows), the plan of a compaction of 1024 pages 9 us, of a few rows or
+// pages 6 to 9.  The copies are bound by HBM (see below).
 #include "kvp_device.cuh"
 #include "pages.h"
 
 namespace kvp {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // of a plan CTA, at most
+constexpr int kFewThreads = 256;    // where there is little to do (kRounds warps at least)
 constexpr int kIntMax = 0x7fffffff;
 constexpr int kMaxTeam = 8;  // CTAs of a plan cluster (the portable limit)
 
@@ -37,14 +40,13 @@ struct Team {
   }
   // Barrier over every thread of the team; orders their global memory accesses.
   __device__ void sync() const {
-    __threadfence();
     asm volatile(
         "barrier.cluster.arrive.release;\n\t"
         "barrier.cluster.wait.acquire;" ::
             : "memory");
   }
-  __device__ int64_t thread() const { return (int64_t)rank * kPlanThreads + threadIdx.x; }
-  __device__ int64_t threads() const { return (int64_t)size * kPlanThreads; }
+  __device__ int64_t thread() const { return (int64_t)rank * blockDim.x + threadIdx.x; }
+  __device__ int64_t threads() const { return (int64_t)size * blockDim.x; }
 };
 
 __device__ __forceinline__ int ld_cg(const int* p) { return __ldcg(p); }
@@ -57,38 +59,46 @@ struct RowWalk {
     lanes = 32;
     while (lanes > 1 && lanes / 2 >= max_blocks) lanes /= 2;
     lane = threadIdx.x & (lanes - 1);
-    const int per_cta = kPlanThreads / lanes;
+    const int per_cta = (int)blockDim.x / lanes;
     first = rank + (int)threadIdx.x / lanes * size;
     step = per_cta * size;
   }
 };
 
-// Exclusive prefix sum of v over the block's threads; *total = the sum.
-// `warp_sums` holds kPlanThreads / 32 sums.
-template <typename T>
-__device__ T block_scan(T v, long long* warp_sums, T* total) {
+// Exclusive prefix sums of N values at once over the block's threads; total[i] =
+// the sum of v[i].  `sums` holds the warps' sums.
+template <typename T, int N>
+__device__ __forceinline__ void block_scan(T (&v)[N], T (&total)[N], long long (*sums)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T incl = v;
+  T incl[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+  for (int i = 0; i < N; ++i) {
+    incl[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += y;
+    }
   }
   __syncthreads();
-  if (lane == 31) warp_sums[warp] = (long long)incl;
-  __syncthreads();
-  const T s = (T)warp_sums[lane];  // kPlanThreads / 32 == 32 sums
-  T ws = s;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, ws, o);
-    if (lane >= o) ws += y;
+  for (int i = 0; i < N; ++i)
+    if (lane == 31) sums[i][warp] = (long long)incl[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const T s = lane < (int)blockDim.x / 32 ? (T)sums[i][lane] : T(0);
+    T ws = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += y;
+    }
+    total[i] = __shfl_sync(0xffffffffu, ws, 31);
+    v[i] = __shfl_sync(0xffffffffu, ws - s, warp) + incl[i] - v[i];
   }
-  *total = __shfl_sync(0xffffffffu, ws, 31);
-  const T before = __shfl_sync(0xffffffffu, ws - s, warp);
-  return before + incl - v;
 }
-static_assert(kPlanThreads == 1024, "block_scan needs 32 warps");
+static_assert(kPlanThreads <= 1024, "block_scan takes 32 warps");
 
 __device__ __forceinline__ int row_pages(int len, int block_size) {
   return (int)(((unsigned)len + (unsigned)block_size - 1u) / (unsigned)block_size);
@@ -105,14 +115,20 @@ __device__ __forceinline__ int row_len(const PagesArgs& a, int r) {
   return c;
 }
 
-// This CTA's segment of the pages.  A thread looks at four consecutive pages
-// at a time (segments start at multiples of four).
+// The pages of a kind (free, in use) are numbered from the lowest on.  Each CTA
+// of the team has a segment of the pool, which it takes in spans of 8 rounds; in
+// a round a thread looks at four consecutive pages (segments start at multiples
+// of four).  The marks of a whole span are kept in registers, four bits a round,
+// and ranked by one scan over packed byte counts, so that a pool of 260,000 pages
+// is read once and ranked with three barriers in each CTA.
 struct Segment {
   int64_t begin, end;
-  int64_t base, total;  // counted pages before the segment / in the pool
+  int64_t base, total;  // marked pages before the segment / in the pool
 };
-constexpr int kPagesPerThread = 4;
-constexpr int kPagesPerRound = kPlanThreads * kPagesPerThread;
+constexpr int kRounds = 8;
+static_assert(kFewThreads / 32 >= kRounds, "a warp ranks the marks of a round");
+__device__ __forceinline__ int pages_per_round() { return (int)blockDim.x * 4; }
+__device__ __forceinline__ int pages_per_span() { return (int)blockDim.x * 4 * kRounds; }
 
 __device__ __forceinline__ Segment segment_of(const PagesArgs& a, const Team& t) {
   Segment s;
@@ -123,11 +139,12 @@ __device__ __forceinline__ Segment segment_of(const PagesArgs& a, const Team& t)
   return s;
 }
 
+__device__ __forceinline__ bool quads(const void* v) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0; }
+
 // Entries p .. p + 3 of an array of the pages (those past the end read as
 // `past`); one load where the array allows it.
 __device__ __forceinline__ int4 load_pages(const int* v, int64_t p, int64_t end, int past) {
-  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(v) & 15u) == 0)
-    return __ldcg(reinterpret_cast<const int4*>(v + p));
+  if (p + 4 <= end && quads(v)) return __ldcg(reinterpret_cast<const int4*>(v + p));
   int4 r;
   r.x = p < end ? __ldcg(v + p) : past;
   r.y = p + 1 < end ? __ldcg(v + p + 1) : past;
@@ -136,7 +153,7 @@ __device__ __forceinline__ int4 load_pages(const int* v, int64_t p, int64_t end,
   return r;
 }
 __device__ __forceinline__ void store_pages(int* v, int64_t p, int64_t end, const int4& x) {
-  if (p + 4 <= end && (reinterpret_cast<uintptr_t>(v) & 15u) == 0) {
+  if (p + 4 <= end && quads(v)) {
     *reinterpret_cast<int4*>(v + p) = x;
     return;
   }
@@ -146,13 +163,112 @@ __device__ __forceinline__ void store_pages(int* v, int64_t p, int64_t end, cons
   if (p + 3 < end) v[p + 3] = x.w;
 }
 
-// Publishes this CTA's count and sums those of the CTAs before it (a team
-// barrier).
-__device__ void rank_segment(const PagesArgs& a, const Team& t, long long* warp_sums, int mine,
-                             Segment* s) {
-  int total;
-  block_scan(mine, warp_sums, &total);
-  if (threadIdx.x == 0) a.ws.team_counts[t.rank] = total;
+// The page of entry 0 that a thread looks at in round i of a span.
+__device__ __forceinline__ int64_t page_of(int64_t p0, int i) {
+  return p0 + i * pages_per_round() + (int)threadIdx.x * 4;
+}
+
+// Rounds of the span at p0.
+__device__ __forceinline__ int rounds_of(int64_t p0, int64_t end) {
+  return (int)(((int)min(end - p0, (int64_t)pages_per_span()) + pages_per_round() - 1) / (unsigned)pages_per_round());
+}
+
+struct RankScratch {
+  uint2 warp[32];           // marks of each warp: a byte per even / odd round
+  int before[kRounds][32];  // marks of a round in the warps before
+  int round[kRounds];       // marks of a round
+};
+
+struct Marks {
+  unsigned bits;       // four a round
+  unsigned even, odd;  // marks of the lanes before, a byte per even / odd round
+};
+
+__device__ __forceinline__ int span_total(const RankScratch& s) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) n += s.round[i];
+  return n;
+}
+
+// Marks the pages p of the span at p0 with flag(v[p]) (false for `past`) and
+// ranks them; copies v to `copy` (null: does not).
+template <typename Flag>
+__device__ __forceinline__ Marks mark_span(const int* v, int64_t p0, int64_t end, int past, RankScratch& s,
+                                           Flag flag, int* copy = nullptr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rounds = rounds_of(p0, end);
+  Marks m{0, 0, 0};
+  auto take = [&](const int4& c, int i) {
+    const unsigned b = (unsigned)flag(c.x) | (unsigned)flag(c.y) << 1 | (unsigned)flag(c.z) << 2 |
+                       (unsigned)flag(c.w) << 3;
+    m.bits |= b << (4 * i);
+    if (copy && page_of(p0, i) < end) store_pages(copy, page_of(p0, i), end, c);
+  };
+  if (quads(v) && end % 4 == 0) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < rounds; i0 += 4) {
+      int4 c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t p = page_of(p0, i0 + i);
+        c[i] = p < end ? __ldcg(reinterpret_cast<const int4*>(v + p)) : make_int4(past, past, past, past);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) take(c[i], i0 + i);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < rounds; ++i) take(load_pages(v, page_of(p0, i), end, past), i);
+  }
+  unsigned n = m.bits - (m.bits >> 1 & 0x55555555u);
+  n = (n & 0x33333333u) + (n >> 2 & 0x33333333u);  // marks of each round, 4 bits
+  const unsigned even = n & 0x0f0f0f0fu, odd = n >> 4 & 0x0f0f0f0fu;
+  m.even = even, m.odd = odd;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {  // (a warp has at most 128 marks a round)
+    const unsigned e = __shfl_up_sync(0xffffffffu, m.even, o), d = __shfl_up_sync(0xffffffffu, m.odd, o);
+    if (lane >= o) m.even += e, m.odd += d;
+  }
+  __syncthreads();  // the span before has been used
+  if (lane == 31) s.warp[warp] = make_uint2(m.even, m.odd);
+  m.even -= even, m.odd -= odd;
+  __syncthreads();
+  if (warp < kRounds) {
+    const uint2 w = lane < (int)blockDim.x / 32 ? s.warp[lane] : make_uint2(0, 0);
+    const int mine = ((warp & 1 ? w.y : w.x) >> (warp / 2 * 8)) & 255;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    s.before[warp][lane] = incl - mine;
+    if (lane == 31) s.round[warp] = incl;
+  }
+  __syncthreads();
+  return m;
+}
+
+// Marked pages of round i before this thread's four.
+__device__ __forceinline__ int rank_in_round(const Marks& m, const RankScratch& s, int i) {
+  return s.before[i][threadIdx.x >> 5] + (((i & 1 ? m.odd : m.even) >> (i / 2 * 8)) & 255);
+}
+
+// Marks the team's pages: their number in the pool and before each segment, and
+// the marks of this CTA's span (of the last one, if there are several).  (A
+// team barrier.)
+template <typename Flag>
+__device__ __forceinline__ Marks mark_segment(const PagesArgs& a, const Team& t, const int* v, int past,
+                                              RankScratch& scratch, Segment* s, Flag flag,
+                                              int* copy = nullptr) {
+  Marks m{0, 0, 0};
+  int mine = 0;
+  for (int64_t p0 = s->begin; p0 < s->end; p0 += pages_per_span()) {
+    m = mark_span(v, p0, s->end, past, scratch, flag, copy);
+    mine += span_total(scratch);
+  }
+  if (threadIdx.x == 0) a.ws.team_counts[t.rank] = mine;
   t.sync();
   s->base = s->total = 0;
   for (int i = 0; i < t.size; ++i) {
@@ -160,38 +276,53 @@ __device__ void rank_segment(const PagesArgs& a, const Team& t, long long* warp_
     if (i < t.rank) s->base += c;
     s->total += c;
   }
+  return m;
 }
 
-__device__ __forceinline__ int zeros(const int4& x) {
-  return (x.x == 0) + (x.y == 0) + (x.z == 0) + (x.w == 0);
+template <typename Flag>
+__device__ __noinline__ Marks mark_again(const int* v, int64_t p0, int64_t end, int past, RankScratch& s,
+                                         Flag flag) {
+  return mark_span(v, p0, end, past, s, flag);
 }
 
-// Calls use(page, rank) for the free pages (counts[p] == 0) of the segment in
-// order, with their ranks among the pool's; stops after rank limit - 1.
-template <typename Use>
-__device__ void for_free_pages(const int* counts, const Segment& s, int64_t limit,
-                               long long* warp_sums, Use use) {
-  int64_t base = s.base;
-  for (int64_t p0 = s.begin; p0 < s.end && base < limit; p0 += kPagesPerRound) {
-    const int64_t p = p0 + threadIdx.x * kPagesPerThread;
-    const int4 c = p < s.end ? load_pages(counts, p, s.end, 1) : make_int4(1, 1, 1, 1);
-    int total;
-    int64_t k = base + block_scan(zeros(c), warp_sums, &total);
-    const int v[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (v[i] == 0) {
-        if (k < limit) use(p + i, k);
-        ++k;
-      }
-    base += total;
+// Calls use(p0, m, rank) for each span of the segment, with its first page, its
+// marks and the marked pages of the pool before it.  m: of mark_segment.
+template <typename Flag, typename Use>
+__device__ __forceinline__ void for_spans(const int* v, int past, RankScratch& scratch, const Segment& s,
+                                          Marks m, int64_t limit, Flag flag, Use use) {
+  int64_t rank = s.base;
+  for (int64_t p0 = s.begin; p0 < s.end && rank < limit; p0 += pages_per_span()) {
+    if (s.end - s.begin > pages_per_span()) m = mark_again(v, p0, s.end, past, scratch, flag);
+    use(p0, m, rank);
+    rank += span_total(scratch);
   }
+}
+
+__device__ __forceinline__ bool is_free(int count) { return count == 0; }
+
+// Calls use(page, four, rank) for the free pages of the segment with ranks <
+// limit, four at a time: free page number rank is page + i of the lowest bit i of
+// `four`, and so on.
+template <typename Use>
+__device__ __forceinline__ void for_free_pages(const int* counts, RankScratch& scratch, const Segment& s,
+                                               const Marks& marks, int64_t limit, Use use) {
+  for_spans(counts, 1, scratch, s, marks, limit, is_free, [&](int64_t p0, const Marks& m, int64_t rank) {
+#pragma unroll 1
+    for (int i = 0; i < rounds_of(p0, s.end) && rank < limit; ++i) {
+      const int64_t k = rank + rank_in_round(m, scratch, i);
+      unsigned four = m.bits >> (4 * i) & 15u;
+      while (four && k + __popc(four) > limit) four &= 0x7fffffffu >> __clz(four);  // without its highest
+      if (four) use(page_of(p0, i), four, k);
+      rank += scratch.round[i];
+    }
+  });
 }
 
 // ------------------------------------------------------------------ fork
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs a) {
-  __shared__ long long warp_sums[32];
+  __shared__ long long warp_sums[1][32];
+  __shared__ RankScratch scratch;
   const Team t;
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
@@ -199,7 +330,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Segment s = segment_of(a, t);
-  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound) {
+#pragma unroll 4
+  for (int64_t p = s.begin + threadIdx.x * 4; p < s.end; p += pages_per_round()) {
     store_pages(a.out_counts, p, s.end, load_pages(a.ref_counts, p, s.end, 0));
     // ws.page: the lowest new row whose unfilled last page this is
     store_pages(a.ws.page, p, s.end, make_int4(kIntMax, kIntMax, kIntMax, kIntMax));
@@ -232,51 +364,50 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
       if (e >= a.num_blocks || e < 0) e = -1;  // recorded above, with the parent's row
       a.out_tables[r * mb + j] = e;
       if (e < 0) continue;
-      if (j == n - 1 && len % bs)
-        atomicMin(&a.ws.page[e], r);
-      else
+      // (one of the rows on an unfilled page is its holder, whichever it is)
+      if (j != n - 1 || len % bs == 0 || atomicMin(&a.ws.page[e], r) == kIntMax)
         atomicAdd(&a.out_counts[e], 1);
     }
   }
   t.sync();
 
-  // The lowest new row on an unfilled page keeps it; the others, in row
-  // order, get copies.
+  // The lowest new row on an unfilled page keeps it; the others, in row order,
+  // get copies.  Copy k is noted as {page, its place in the row, tokens, row}.
   if (t.rank == 0) {
     int copies = 0;
-    for (int r0 = 0; r0 < a.num_out; r0 += kPlanThreads) {
+    for (int r0 = 0; r0 < a.num_out; r0 += blockDim.x) {
       const int r = r0 + (int)threadIdx.x;
-      bool copy = false;
+      int len = 0, e = -1;
       if (r < a.num_out) {
-        const int len = ld_cg(&a.out_lens[r]);
-        if (len % bs) {
-          const int e = ld_cg(&a.out_tables[r * mb + row_pages(len, bs) - 1]);
-          if (e >= 0) {
-            copy = ld_cg(&a.ws.page[e]) != r;
-            if (!copy) atomicAdd(&a.out_counts[e], 1);
-          }
-        }
+        len = ld_cg(&a.out_lens[r]);
+        if (len % bs) e = ld_cg(&a.out_tables[r * mb + row_pages(len, bs) - 1]);
       }
-      int total;
-      const int k = copies + block_scan(copy ? 1 : 0, warp_sums, &total);
-      if (copy) a.ws.row[k] = r;
-      copies += total;
+      const bool copy = e >= 0 && ld_cg(&a.ws.page[e]) != r;
+      int k[1] = {copy ? 1 : 0}, total[1];
+      block_scan(k, total, warp_sums);
+      if (copy) a.ws.pairs[copies + k[0]] = PagePair{e, row_pages(len, bs) - 1, len % bs, r};
+      copies += total[0];
     }
     if (threadIdx.x == 0) a.ws.head->copies = copies;
   }
-  t.sync();
+  const Marks marks = mark_segment(a, t, a.out_counts, 1, scratch, &s, is_free);
   const int copies = ld_cg(&a.ws.head->copies);
-  int mine = 0;
-  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound)
-    mine += zeros(load_pages(a.out_counts, p, s.end, 1));
-  rank_segment(a, t, warp_sums, mine, &s);
-  for_free_pages(a.out_counts, s, copies, warp_sums, [&](int64_t p, int64_t k) {
-    const int r = ld_cg(&a.ws.row[k]);
-    const int len = ld_cg(&a.out_lens[r]);
-    int* entry = &a.out_tables[r * mb + row_pages(len, bs) - 1];
-    a.ws.pairs[k] = PagePair{ld_cg(entry), (int)p, len % bs, 0};
-    *entry = (int)p;
-    a.out_counts[p] = 1;
+  auto noted = [&](int64_t k) { return __ldcg(reinterpret_cast<const int4*>(&a.ws.pairs[k])); };
+  for_free_pages(a.out_counts, scratch, s, marks, copies, [&](int64_t p0, unsigned four, int64_t k) {
+    const int n = __popc(four);
+    int4 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) c[i] = noted(k + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) {
+        const int p = (int)p0 + __ffs(four) - 1;
+        four &= four - 1;
+        a.out_tables[c[i].w * mb + c[i].y] = p;
+        a.out_counts[p] = 1;
+        a.ws.pairs[k + i] = PagePair{c[i].x, p, c[i].z, 0};
+      }
   });
   if (s.total >= copies) return;
   // The pool ran out: rows past the last free page are dropped.
@@ -285,27 +416,25 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
   record_error(a.status, KVP_ERR_DEVICE_DATA);
   if (threadIdx.x == 0) a.ws.head->copies = (int)s.total;
   for (int64_t k = s.total; k < copies; ++k) {
-    const int r = ld_cg(&a.ws.row[k]);
-    const int n = row_pages(ld_cg(&a.out_lens[r]), bs);
-    for (int j = threadIdx.x; j < n; j += kPlanThreads) {
-      const int e = ld_cg(&a.out_tables[r * mb + j]);
-      if (j < n - 1 && e >= 0) atomicAdd(&a.out_counts[e], -1);
-      a.out_tables[r * mb + j] = -1;
+    const int4 c = noted(k);
+    for (int j = threadIdx.x; j <= c.y; j += blockDim.x) {
+      const int e = ld_cg(&a.out_tables[c.w * mb + j]);
+      if (j < c.y && e >= 0) atomicAdd(&a.out_counts[e], -1);
+      a.out_tables[c.w * mb + j] = -1;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) a.out_lens[r] = 0;
-    __syncthreads();
+    if (threadIdx.x == 0) a.out_lens[c.w] = 0;
   }
 }
 
 // ---------------------------------------------------------------- extend
 
-// Last index i with v[i] <= x of the non-decreasing v[0 .. n), v[0] <= x.
-__device__ __forceinline__ int last_at_most(const int* v, int n, int64_t x) {
+// Last row i with rows[i].*first <= x, of n >= 1 rows in which it never falls
+// and starts at 0.
+__device__ __forceinline__ int last_at_most(const RowGrowth* rows, int n, int RowGrowth::*first, int64_t x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((int64_t)v[mid] <= x)
+    if ((int64_t)(rows[mid].*first) <= x)
       lo = mid;
     else
       hi = mid;
@@ -315,19 +444,59 @@ __device__ __forceinline__ int last_at_most(const int* v, int n, int64_t x) {
 
 constexpr int kRowsInSmem = 2048;
 
+// Pages that a row of length len asks for (0: its new length does not fit).
+__device__ __forceinline__ int asked_pages(const PagesArgs& a, int r, int len) {
+  const int add = a.new_tokens[r];
+  if (add < 0 || (int64_t)len + add > (int64_t)a.max_blocks * a.block_size) return 0;
+  return row_pages(len + add, a.block_size) - row_pages(len, a.block_size);
+}
+
+// The table rows as they were, by CTA `me` of `n`: all entries but those of the
+// pages that a row asks for, which the team writes.
+__device__ void keep_rows(const PagesArgs& a, int me, int n) {
+  const int64_t mb = a.max_blocks;
+  if (a.out_tables == a.block_tables) {
+    const RowWalk rows(a.max_blocks, me, n);
+    for (int r = rows.first; r < a.num_rows; r += rows.step) {
+      const int len = row_len(a, r), from = row_pages(len, a.block_size) + asked_pages(a, r, len);
+      for (int j = from + rows.lane; j < a.max_blocks; j += rows.lanes) a.out_tables[r * mb + j] = -1;
+    }
+    return;
+  }
+  const int64_t entries = a.num_rows * mb, step = (int64_t)n * blockDim.x;
+#pragma unroll 4
+  for (int64_t i = (int64_t)me * blockDim.x + threadIdx.x; i < entries; i += step) {
+    const int r = (int)(entries <= kIntMax ? (unsigned)i / (unsigned)a.max_blocks : i / mb);
+    const int j = (int)(i - r * mb);
+    const int len = row_len(a, r), had = row_pages(len, a.block_size);
+    if (j < had)
+      a.out_tables[i] = a.block_tables[i];
+    else if (j >= had + asked_pages(a, r, len))
+      a.out_tables[i] = -1;
+  }
+}
+
+// The first cluster is the team; CTAs behind it, if there are any, keep the
+// table rows.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesArgs a) {
-  __shared__ long long warp_sums[32];
-  __shared__ int s_page0[kRowsInSmem], s_token0[kRowsInSmem];
+  __shared__ long long warp_sums[2][32];
+  __shared__ RowGrowth s_grow[kRowsInSmem];
+  __shared__ RankScratch scratch;
   const Team t;
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
+  const int keepers = (int)gridDim.x - t.size;
+  if ((int)blockIdx.x >= t.size) {
+    keep_rows(a, (int)blockIdx.x - t.size, keepers);
+    return;
+  }
 
   // The rows, by CTA 0: pages needed and new tokens, and their prefix sums.
   if (t.rank == 0) {
     long long pages = 0, tokens = 0;
-    for (int r0 = 0; r0 < a.num_rows; r0 += kPlanThreads) {
+    for (int r0 = 0; r0 < a.num_rows; r0 += blockDim.x) {
       const int r = r0 + (int)threadIdx.x;
-      long long need = 0, asked = 0;
+      long long v[2] = {0, 0}, total[2];  // pages needed, tokens asked for
       int add = 0, len = 0;
       bool bad = false;
       if (r < a.num_rows) {
@@ -338,7 +507,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
           bad = true;
           add = 0;
         }
-        asked = add;
+        v[1] = add;
         if (!bad && add > 0 && len % bs) {  // the new tokens start in the last page: no one else's
           const int e = a.block_tables[r * mb + row_pages(len, bs) - 1];
           bad = e < 0 || e >= a.num_blocks || a.ref_counts[e] > 1;
@@ -347,16 +516,14 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
           record_error(a.status, KVP_ERR_DEVICE_DATA);
           add = 0;
         }
-        need = row_pages(len + add, bs) - row_pages(len, bs);
+        v[0] = row_pages(len + add, bs) - row_pages(len, bs);
       }
-      long long total;
-      const long long page0 = pages + block_scan(need, warp_sums, &total);
-      pages += total;
-      const long long token0 = tokens + block_scan(asked, warp_sums, &total);
-      tokens += total;
+      block_scan(v, total, warp_sums);
       if (r < a.num_rows)
-        a.ws.grow[r] = RowGrowth{(int)min(page0, (long long)kIntMax),
-                                 (int)min(token0, (long long)kIntMax), len, add};
+        a.ws.grow[r] = RowGrowth{(int)min(pages + v[0], (long long)kIntMax),
+                                 (int)min(tokens + v[1], (long long)kIntMax), len, add};
+      pages += total[0];
+      tokens += total[1];
     }
     if (threadIdx.x == 0) {
       a.ws.head->copies = (int)min(pages, (long long)kIntMax);
@@ -364,78 +531,58 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
       if (tokens > a.num_slots) record_error(a.status, KVP_ERR_DEVICE_DATA);
     }
   }
-  // Meanwhile the others: the tables as they were (new pages follow below).
-  const int copiers = t.size > 1 ? t.size - 1 : 1, me = t.size > 1 ? t.rank - 1 : 0;
-  if (me >= 0) {
-    const RowWalk rows(a.max_blocks, me, copiers);
-    const bool in_place = a.out_tables == a.block_tables;
-    for (int r = rows.first; r < a.num_rows; r += rows.step) {
-      const int had = row_pages(row_len(a, r), bs);
-      const int32_t* from = a.block_tables + r * mb;
-      int32_t* to = a.out_tables + r * mb;
-      int j = rows.lane;
-      if (in_place) j += had / rows.lanes * rows.lanes;
-#pragma unroll 4
-      for (; j < a.max_blocks; j += rows.lanes)
-        if (j >= had)
-          to[j] = -1;
-        else if (!in_place)
-          to[j] = from[j];
-    }
-  }
+  // Meanwhile the others: the tables as they were.
+  if (keepers == 0 && (t.rank > 0 || t.size == 1))
+    keep_rows(a, t.size > 1 ? t.rank - 1 : 0, t.size > 1 ? t.size - 1 : 1);
   // The counts as they were, and the free pages among them.
   Segment s = segment_of(a, t);
-  int mine = 0;
-  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound) {
-    const int4 c = load_pages(a.ref_counts, p, s.end, 1);
-    mine += zeros(c);
-    if (a.out_counts != a.ref_counts) store_pages(a.out_counts, p, s.end, c);
-  }
-  rank_segment(a, t, warp_sums, mine, &s);  // (a team barrier)
+  const Marks marks = mark_segment(a, t, a.ref_counts, 1, scratch, &s, is_free,
+                                   a.out_counts != a.ref_counts ? a.out_counts : nullptr);
 
-  // The rows' prefix sums, to search in: in shared memory, or (too many rows)
-  // packed in the workspace, by every CTA for itself, all writing the same.
-  const bool small = a.num_rows <= kRowsInSmem;
-  int* page0 = small ? s_page0 : a.ws.row;
-  int* token0 = small ? s_token0 : a.ws.row2;
-  for (int r = threadIdx.x; r < a.num_rows; r += kPlanThreads) {
-    const int2 g = __ldcg(reinterpret_cast<const int2*>(&a.ws.grow[r]));
-    page0[r] = g.x;
-    token0[r] = g.y;
-  }
+  // The rows, to search in: in shared memory unless there are too many.
+  if (a.num_rows <= kRowsInSmem)
+    for (int r = threadIdx.x; r < a.num_rows; r += blockDim.x)
+      *reinterpret_cast<int4*>(&s_grow[r]) = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));
+  const RowGrowth* grow = a.num_rows <= kRowsInSmem ? s_grow : a.ws.grow;
   __syncthreads();
+  // Whether the pool had the pages that a row needs.
+  auto served = [&](const RowGrowth& g) {
+    const int need = row_pages(g.len + g.add, bs) - row_pages(g.len, bs);
+    return need == 0 || (int64_t)g.page0 + need <= s.total;
+  };
   // Free page of rank k goes to the last row whose pages start at or before k.
-  const int pages = ld_cg(&a.ws.head->copies);
+  const int pages = ld_cg(&a.ws.head->copies), tokens = ld_cg(&a.ws.head->tokens);
   if (pages > 0) {
-    for_free_pages(a.ref_counts, s, pages, warp_sums, [&](int64_t p, int64_t k) {
-      const int r = last_at_most(page0, a.num_rows, k);
-      const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));  // page0, token0, len, add
-      const int had = row_pages(g.z, bs), need = row_pages(g.z + g.w, bs) - had;
-      if (g.x + need > s.total) return;  // not enough pages left for the whole row
-      a.out_tables[r * mb + had + (k - g.x)] = (int)p;
-      a.out_counts[p] = 1;
+    for_free_pages(a.ref_counts, scratch, s, marks, pages, [&](int64_t p0, unsigned four, int64_t k) {
+      for (; four; four &= four - 1, ++k) {
+        const int r = last_at_most(grow, a.num_rows, &RowGrowth::page0, k);
+        const RowGrowth g = grow[r];
+        if (!served(g)) return;  // not enough pages left for the whole row
+        const int64_t p = p0 + __ffs(four) - 1;
+        a.out_tables[r * mb + row_pages(g.len, bs) + (k - g.page0)] = (int)p;
+        a.out_counts[p] = 1;
+      }
     });
     t.sync();
   }
 
-  // Whether the pool had the pages that a row needs.
-  auto served = [&](const int4& g) {
-    const int need = row_pages(g.z + g.w, bs) - row_pages(g.z, bs);
-    return need == 0 || (int64_t)g.x + need <= s.total;
-  };
   for (int64_t r = t.thread(); r < a.num_rows; r += t.threads()) {
-    const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));
-    if (!served(g)) record_error(a.status, KVP_ERR_DEVICE_DATA);
-    a.out_lens[r] = served(g) ? g.z + g.w : g.z;
+    const RowGrowth g = grow[r];
+    const bool ok = served(g);
+    if (!ok) record_error(a.status, KVP_ERR_DEVICE_DATA);
+    a.out_lens[r] = ok ? g.len + g.add : g.len;
+    if (!ok || g.add == 0) {  // entries that no page came for
+      const int had = row_pages(g.len, bs), asked = asked_pages(a, (int)r, g.len);
+      for (int j = had; j < had + asked; ++j) a.out_tables[r * mb + j] = -1;
+    }
   }
-  const int tokens = ld_cg(&a.ws.head->tokens);
   for (int64_t i = t.thread(); i < a.num_slots; i += t.threads()) {
     int slot = -1;
     if (i < tokens) {
-      const int r = last_at_most(token0, a.num_rows, i);
-      const int4 g = __ldcg(reinterpret_cast<const int4*>(&a.ws.grow[r]));
-      const int pos = g.z + (int)(i - g.y);
-      if (served(g) && pos < g.z + g.w)
+      const int r = last_at_most(grow, a.num_rows, &RowGrowth::token0, i);
+      const RowGrowth g = grow[r];
+      const int pos = g.len + (int)(i - g.token0);
+      if (served(g) && pos < g.len + g.add)
         slot = ld_cg(&a.out_tables[r * mb + pos / bs]) * bs + pos % bs;
     }
     a.slot_mapping[i] = slot;
@@ -445,55 +592,63 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
 // --------------------------------------------------------------- compact
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesArgs a) {
-  __shared__ long long warp_sums[32];
+  __shared__ RankScratch scratch;
   const Team t;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Segment s = segment_of(a, t);
-  auto live4 = [](const int4& c) { return (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0); };
-  int mine = 0;
-  for (int64_t p = s.begin + threadIdx.x * kPagesPerThread; p < s.end; p += kPagesPerRound)
-    mine += live4(load_pages(a.ref_counts, p, s.end, 0));
-  rank_segment(a, t, warp_sums, mine, &s);
+  auto in_use = [](int count) { return count > 0; };
+  const Marks marks = mark_segment(a, t, a.ref_counts, 0, scratch, &s, in_use);
   const int64_t live = s.total;  // pages [0, live) hold everything afterwards
 
-  // Live pages before each page; free page p < live is hole p - before(p).
-  int64_t base = s.base;
-  for (int64_t p0 = s.begin; p0 < s.end; p0 += kPagesPerRound) {
-    const int64_t p = p0 + threadIdx.x * kPagesPerThread;
-    const int4 c = p < s.end ? load_pages(a.ref_counts, p, s.end, 0) : make_int4(0, 0, 0, 0);
-    int total;
-    int before = (int)base + block_scan(live4(c), warp_sums, &total);
-    base += total;
-    const int v[4] = {c.x, c.y, c.z, c.w};
-    int o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = before;
-      if (v[i] > 0)
-        ++before;
-      else if (p + i < s.end && p + i < live)
-        a.ws.page2[p + i - before] = (int)(p + i);
+  // Free page p < live is hole p - (pages in use before it); and how many of
+  // the pages in use stay.
+  if (t.rank == 0 && threadIdx.x == 0 && live == a.num_blocks) a.ws.head->copies = 0;
+  for_spans(a.ref_counts, 0, scratch, s, marks, kIntMax, in_use, [&](int64_t p0, const Marks& m, int64_t rank) {
+#pragma unroll 1
+    for (int i = 0; i < rounds_of(p0, s.end) && p0 + i * pages_per_round() <= live; ++i) {
+      int64_t k = rank + rank_in_round(m, scratch, i);
+      const unsigned four = m.bits >> (4 * i) & 15u;
+      for (int j = 0; j < 4; ++j) {
+        const int64_t p = page_of(p0, i) + j;
+        if (p >= s.end) break;
+        if (p == live) a.ws.head->copies = (int)(live - k);
+        if (four >> j & 1)
+          ++k;
+        else if (p < live)
+          a.ws.page[p - k] = (int)p;
+      }
+      rank += scratch.round[i];
     }
-    if (p < s.end) store_pages(a.ws.page, p, s.end, make_int4(o[0], o[1], o[2], o[3]));
-  }
+  });
   t.sync();
-  const int64_t staying = live < a.num_blocks ? ld_cg(&a.ws.page[live]) : live;
-  if (t.thread() == 0) a.ws.head->copies = (int)(live - staying);
-  for (int64_t p = t.thread(); p < a.num_blocks; p += t.threads()) {
-    const int c = a.ref_counts[p];
-    int place = -1;
-    if (c > 0 && p >= live) {  // the k-th live page above moves into the k-th hole below
-      const int64_t k = ld_cg(&a.ws.page[p]) - staying;
-      place = ld_cg(&a.ws.page2[k]);
-      a.ws.pairs[k] = PagePair{(int)p, place, a.block_size, 0};
-      a.out_counts[place] = c;
-    } else if (c > 0) {
-      place = (int)p;
-      a.out_counts[p] = c;
+  const int64_t staying = live - ld_cg(&a.ws.head->copies);
+  for_spans(a.ref_counts, 0, scratch, s, marks, kIntMax, in_use, [&](int64_t p0, const Marks& m, int64_t rank) {
+#pragma unroll 1
+    for (int i = 0; i < rounds_of(p0, s.end); ++i) {
+      const int64_t p = page_of(p0, i);
+      if (p < s.end) {
+        int64_t k = rank + rank_in_round(m, scratch, i);
+        const int4 c4 = load_pages(a.ref_counts, p, s.end, 0);
+        const int c[4] = {c4.x, c4.y, c4.z, c4.w};
+        int place[4];
+        int64_t at[4];  // the k-th page in use above moves into the k-th hole below
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          at[j] = c[j] > 0 && p + j >= live ? k - staying : -1;
+          place[j] = at[j] >= 0 ? ld_cg(&a.ws.page[at[j]]) : c[j] > 0 ? (int)(p + j) : -1;
+          k += c[j] > 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (at[j] >= 0) a.ws.pairs[at[j]] = PagePair{(int)(p + j), place[j], a.block_size, 0};
+          if (c[j] > 0) a.out_counts[place[j]] = c[j];
+          if (p + j >= live && p + j < s.end) a.out_counts[p + j] = 0;
+        }
+        store_pages(a.places, p, s.end, make_int4(place[0], place[1], place[2], place[3]));
+      }
+      rank += scratch.round[i];
     }
-    if (p >= live) a.out_counts[p] = 0;
-    a.places[p] = place;
-  }
+  });
   t.sync();
   const RowWalk rows(a.max_blocks, t.rank, t.size);
   for (int r = rows.first; r < a.num_rows; r += rows.step) {
@@ -662,15 +817,23 @@ cudaError_t launch(void (*kernel)(Params...), int grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// CTAs of the plan: enough to see its largest array in one round.
-int team_size(const PagesArgs& a) {
+// The plan's launch: enough threads to see its largest array in one round, the
+// pages four at a time.
+struct TeamShape {
+  int size, threads;
+};
+TeamShape team_shape(const PagesArgs& a) {
   const int64_t rows = a.num_rows > a.num_out ? a.num_rows : a.num_out;
   int64_t n = rows * a.max_blocks;
-  if (a.num_blocks > n) n = a.num_blocks;
+  if (a.num_blocks / 4 > n) n = a.num_blocks / 4;
   if (a.num_slots > n) n = a.num_slots;
+  // (256 threads up to 512 of them: 8.0 against 9.7 us for a token for each of 8
+  // rows, 11.1 against 11.5 for a compaction of 400 pages; up to 1024 the latter
+  // of 1000 pages takes 15.9 against 13.7.)
+  if (n <= 2 * kFewThreads) return {1, kFewThreads};
   int size = 1;
   while (size < kMaxTeam && (int64_t)size * kPlanThreads < n) size *= 2;
-  return size;
+  return {size, kPlanThreads};
 }
 
 cudaError_t launch_copies(const PagesArgs& a, const PagesCache& c, int num_sms, cudaStream_t stream) {
@@ -696,8 +859,8 @@ cudaError_t launch_copies(const PagesArgs& a, const PagesCache& c, int num_sms, 
 size_t pages_workspace_bytes(int64_t num_blocks, int64_t rows) {
   const int64_t pairs = num_blocks > rows ? num_blocks : rows;
   const int64_t pages = (num_blocks + 3) / 4 * 4;
-  return 256 + (size_t)pairs * sizeof(PagePair) + (size_t)rows * (sizeof(RowGrowth) + 2 * sizeof(int)) +
-         (size_t)(2 * pages) * sizeof(int);
+  return 256 + (size_t)pairs * sizeof(PagePair) + (size_t)rows * sizeof(RowGrowth) +
+         (size_t)pages * sizeof(int);
 }
 
 PagesWorkspace pages_workspace(void* base, int64_t num_blocks, int64_t rows) {
@@ -710,28 +873,34 @@ PagesWorkspace pages_workspace(void* base, int64_t num_blocks, int64_t rows) {
   w.pairs = reinterpret_cast<PagePair*>(p + 256);
   w.grow = reinterpret_cast<RowGrowth*>(w.pairs + pairs);
   w.page = reinterpret_cast<int*>(w.grow + rows);
-  w.page2 = w.page + pages;
-  w.row = w.page2 + pages;
-  w.row2 = w.row + rows;
   return w;
 }
 
 cudaError_t launch_pages_fork(const PagesArgs& a, const PagesCache& c, int num_sms,
                               cudaStream_t stream) {
-  const int size = team_size(a);
-  cudaError_t e = launch(fork_plan_kernel, size, kPlanThreads, 0, size, false, stream, a);
+  const TeamShape t = team_shape(a);
+  cudaError_t e = launch(fork_plan_kernel, t.size, t.threads, 0, t.size, false, stream, a);
   return e != cudaSuccess ? e : launch_copies(a, c, num_sms, stream);
 }
 
-cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream) {
-  const int size = team_size(a);
-  return launch(extend_plan_kernel, size, kPlanThreads, 0, size, false, stream, a);
+cudaError_t launch_pages_extend(const PagesArgs& a, int num_sms, cudaStream_t stream) {
+  const TeamShape t = team_shape(a);
+  // CTAs that keep the table rows, two entries a thread.  In place there is
+  // little to keep, and the lengths must be read before the team writes them.
+  const int64_t entries = (int64_t)a.num_rows * a.max_blocks;
+  int keepers = 0;
+  if (t.size == kMaxTeam && a.out_tables != a.block_tables && a.out_lens != a.context_lens) {
+    const int64_t cluster = 2ll * t.threads * t.size;
+    const int64_t want = (entries + cluster - 1) / cluster, room = num_sms / t.size - 1;
+    keepers = t.size * (int)(want < room ? want : room);
+  }
+  return launch(extend_plan_kernel, t.size + keepers, t.threads, 0, t.size, false, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PagesArgs& a, const PagesCache& c, int num_sms,
                                  cudaStream_t stream) {
-  const int size = team_size(a);
-  cudaError_t e = launch(compact_plan_kernel, size, kPlanThreads, 0, size, false, stream, a);
+  const TeamShape t = team_shape(a);
+  cudaError_t e = launch(compact_plan_kernel, t.size, t.threads, 0, t.size, false, stream, a);
   return e != cudaSuccess ? e : launch_copies(a, c, num_sms, stream);
 }
 

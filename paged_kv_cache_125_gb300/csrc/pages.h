@@ -28,8 +28,7 @@ struct PagesWorkspace {
   int* team_counts;         // one count per CTA of the plan kernel
   PagePair* pairs;          // [max(num_blocks, rows)]
   RowGrowth* grow;          // [rows]
-  int *page, *page2;        // [num_blocks]
-  int *row, *row2;          // [rows]
+  int* page;                // [num_blocks]
 };
 
 struct PagesArgs {
@@ -62,7 +61,7 @@ size_t pages_workspace_bytes(int64_t num_blocks, int64_t rows);
 PagesWorkspace pages_workspace(void* base, int64_t num_blocks, int64_t rows);
 cudaError_t launch_pages_fork(const PagesArgs& a, const PagesCache& c, int num_sms,
                               cudaStream_t stream);
-cudaError_t launch_pages_extend(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_extend(const PagesArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesArgs& a, const PagesCache& c, int num_sms,
                                  cudaStream_t stream);
 

@@ -65,7 +65,7 @@ class Pool:
 
 
 POOLS = [(12, 16, 3, 3), (40, 16, 7, 5), (200, 1, 9, 20), (300, 32, 40, 9), (700, 7, 90, 13), (5000, 16, 300, 40),
-         (9000, 256, 1100, 8)]
+         (9000, 256, 1100, 8), (600001, 2, 70, 3001)]
 
 
 def check_status(bad):
