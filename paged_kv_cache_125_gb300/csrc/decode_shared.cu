@@ -61,6 +61,15 @@ __host__ __device__ constexpr int own_ctas(int sms) { return sms; }
 // merge, but a chain of steps is latency (8 sequences behind 1024 tokens, four
 // layers: 51.7 / 50.1 / 53.1 / 66.7 us with at least 1 / 2 / 4 / 8).
 constexpr int kLeastSteps = 2;
+// An SM holds one prefix CTA beside its own-part CTA; the second one begins when
+// either has ended.  So the first gets as many steps more as it can do beside the
+// own part: kLeadSteps for the latency of that kernel, and one per kLeadOwn tokens
+// x kv heads of its share.  Equal chunks / these (us): 16 sequences behind 4096
+// tokens 23.1 / 19.8, 128 behind 8192 49.7 / 46.8, 64 behind 32768 with 500 ..
+// 2500 own 101.8 / 97.8.  (kLeadSteps 0, 4, 6: 128 behind 8192 49.7, 48.1, 49.1;
+// kLeadOwn 64 as 128, 256 loses 9 us of the last.)
+constexpr int kLeadSteps = 2;
+constexpr int kLeadOwn = 128;
 // A sequence in a CTA costs about as much as 64 KiB of its stream (query,
 // page and plan look-ups, partials): in the own-part kernel's split it counts
 // that many tokens (of head_dim 128) more than it has.
@@ -68,6 +77,39 @@ __host__ __device__ constexpr int own_gap(int num_kv_heads) { return 128 / num_k
 __device__ __forceinline__ long long chunk_of(long long total, int ctas, int least) {
   const long long c = (total + ctas - 1) / ctas;
   return c < least ? least : c;
+}
+
+// x / y for the plan's work positions, which nearly always fit 32 bits.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// Where the prefix CTAs' chunks begin: an SM takes one of the first wave beside
+// its own-part CTA and one of the second when either has ended.
+struct PrefixSplit {
+  int wave;  // CTAs of the first wave
+  long long first, second;
+  __device__ explicit PrefixSplit(const SharedPlanHead& h)
+      : wave(h.sms), first(h.prefix_chunk), second(h.prefix_chunk2) {}
+  __device__ PrefixSplit(int sms, long long a, long long b) : wave(sms), first(a), second(b) {}
+  __device__ long long begin(int cta) const {
+    return cta < wave ? cta * first : wave * first + (cta - wave) * second;
+  }
+  __device__ long long end(int cta) const { return begin(cta) + (cta < wave ? first : second); }
+  // The CTA of step x.
+  __device__ long long cta(long long x) const {
+    const long long y = x - wave * first;
+    return y < 0 ? quotient(x, first) : wave + quotient(y, second);
+  }
+};
+
+__device__ __forceinline__ PrefixSplit split_prefixes(long long total, long long own, int sms) {
+  const long long per_sm = (total + sms - 1) / sms, lead = kLeadSteps + own / kLeadOwn;
+  long long first = (per_sm + lead + 1) / 2;
+  if (first > per_sm) first = per_sm;
+  if (first < kLeastSteps) first = kLeastSteps;
+  const long long rest = total - first * sms;
+  return PrefixSplit(sms, first, chunk_of(rest > 0 ? rest : 0, sms, kLeastSteps));
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -309,8 +351,8 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
     }
   }
   const int tiles = (int)(base[0] >> 32);
-  const long long pchunk = chunk_of(base[1], prefix_ctas(a.sms), kLeastSteps);
   const long long ochunk = chunk_of(base[2], own_ctas(a.sms), 2 * a.gap);
+  const PrefixSplit split = split_prefixes(base[1], ochunk * a.num_kv_heads, a.sms);
   if (threadIdx.x == 0) {
     p.cum_tokens[B] = base[2];
     p.cum_rows[tiles] = (int)(base[0] & 0xffffffffll);
@@ -326,7 +368,8 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
     h.sms = a.sms;
     h.gap = a.gap;
     h.pad = 0;
-    h.prefix_chunk = pchunk;
+    h.prefix_chunk = split.first;
+    h.prefix_chunk2 = split.second;
     h.prefix_total = base[1];
     h.own_chunk = ochunk;
     h.own_total = base[2];
@@ -346,7 +389,7 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
   for (int i = threadIdx.x; i < own_ctas(a.sms) + prefix_ctas(a.sms); i += T) {
     const bool own = i < own_ctas(a.sms);
     const int c = own ? i : i - own_ctas(a.sms);
-    const long long x = c * (own ? ochunk : pchunk);
+    const long long x = own ? c * ochunk : split.begin(c);
     if (x >= (own ? base[2] : base[1])) continue;
     const long long* v = own ? tokens : tsteps;
     int lo = 0, hi = own ? B : tiles;  // the answer is in [lo, hi)
@@ -787,9 +830,9 @@ __global__ void __maxnreg__(kPrefixRegs)
   // (A plan of another shape is reported by the own-part kernel.)
   const SharedPrefixStart start = a.plan.prefix_start[blockIdx.x];
   if (plan_fits(a)) {
-    const long long total = a.plan.head->prefix_total, chunk = a.plan.head->prefix_chunk;
-    sg.pos = chunk * blockIdx.x;
-    sg.end = sg.pos + chunk < total ? sg.pos + chunk : total;
+    const PrefixSplit split(*a.plan.head);
+    sg.pos = split.begin(blockIdx.x);
+    sg.end = min(split.end(blockIdx.x), a.plan.head->prefix_total);
     sg.begin(start);
   }
   if (sg.pos < sg.end && !(smem_u32(smem) & 1023u)) {
@@ -1222,17 +1265,12 @@ __global__ void __maxnreg__(kOwnRegs)
 
 constexpr int kMergeWarps = 8;
 
-// x / y for the plan's work positions, which nearly always fit 32 bits.
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
 // One row (sequence b, query head h) by W warps; `hand` passes the sums of the
 // row's warps to the first of them.
 template <int D, int W>
 __device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int lane, int warp, int wi,
                                           int ns, long long orow, int hg, int st, long long first,
-                                          long long pchunk, long long prow, float4 (*hand)[33]) {
+                                          const PrefixSplit& split, long long prow, float4 (*hand)[33]) {
   constexpr int E = D / 32, S = part_stride<D>();
   constexpr int U = 4;  // parts whose loads are in flight together
   float acc[E], M = -INFINITY, den = 0.f;
@@ -1242,8 +1280,8 @@ __device__ __forceinline__ void merge_row(const SharedArgs& a, int b, int h, int
   // rows start 128 rows after the one before's.
   int np = 0;
   if (st > 0) {
-    const long long p0 = quotient(first, pchunk);
-    np = (int)(quotient(first + st - 1, pchunk) - p0) + 1;
+    const long long p0 = split.cta(first);
+    np = (int)(split.cta(first + st - 1) - p0) + 1;
     prow += p0 * kTileRows + hg;
   }
   const int parts = np + ns;
@@ -1347,7 +1385,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
   const int h0 = (int)(blockIdx.x % (unsigned)blocks) * heads;
   const bool fits = plan_fits(a);
   int ns = 0;
-  long long orow = 0, prow = 0, first = 0, pchunk = 1;
+  long long orow = 0, prow = 0, first = 0;
+  PrefixSplit split(1, 1, 1);
   int st = 0, rows_of_item = 0;
   if (fits) {
     const long long k1 = a.plan.cum_tokens[b + 1];
@@ -1360,7 +1399,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
       orow = (b + c0) * NS * a.num_heads;
     }
     if (t >= 0) {
-      pchunk = a.plan.head->prefix_chunk;
+      split = PrefixSplit(*a.plan.head);
       first = a.plan.cum_steps[t];
       st = (int)((a.plan.cum_steps[t + 1] - first) / Hkv);
       const int r0 = a.plan.cum_rows[t];
@@ -1374,7 +1413,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
   if (!fits) return;
   for (int h = h0 + warp / W; h < h0 + heads; h += kMergeWarps / W)
     merge_row<D, W>(a, b, h, lane, warp, wi, ns, orow + h, h % G, st, first + (long long)(h / G) * st,
-                    pchunk, prow + (long long)(h / G) * rows_of_item, hand);
+                    split, prow + (long long)(h / G) * rows_of_item, hand);
 }
 
 // Sets a split kernel up for its dynamic shared memory, once per device.  The

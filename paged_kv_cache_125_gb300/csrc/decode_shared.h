@@ -16,11 +16,11 @@ struct SharedPlanHead {
   int block_size, max_blocks, num_tiles;
   int sms;                 // SMs of the device it was made on
   int gap, pad;            // positions before each sequence's own tokens (see own_gap)
-  long long prefix_chunk;  // steps per CTA of the prefix kernel, of prefix_total
+  long long prefix_chunk;  // steps of a prefix CTA of the first wave, of prefix_total
   long long prefix_total;
   long long own_chunk;     // positions per CTA of the own-part kernel, of own_total
   long long own_total;
-  long long pad2;
+  long long prefix_chunk2;  // steps of a prefix CTA of the second wave
 };
 static_assert(sizeof(SharedPlanHead) == 80, "the records after it are 16-byte aligned");
 
