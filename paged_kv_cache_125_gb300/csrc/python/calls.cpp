@@ -251,7 +251,7 @@ Pool pool_of(Args& a, int i) {
 template <int N>
 struct Outputs {
   at::Tensor t[N];
-  PyObject* theirs = nullptr;  // the caller's
+  bool theirs = false;  // the caller's
 
   bool take(Args& a, PyObject* given_out, std::initializer_list<int64_t> (&shapes)[N]) {
     if (given_out == Py_None) return a.ok;
@@ -265,22 +265,20 @@ struct Outputs {
       if (!x) return a.ok = false;
       t[i] = *x;
     }
-    theirs = given_out;
-    return true;
+    return theirs = true;
   }
   void make(std::initializer_list<int64_t> (&shapes)[N], int idx) {
     if (theirs) return;
     for (int i = 0; i < N; ++i) t[i] = fresh(at::IntArrayRef(shapes[i].begin(), shapes[i].size()), at::kInt, idx);
   }
+  // (Wrapping a tensor of the caller's gives the caller's own object.)
   PyObject* result() {
     PyObject* r = PyTuple_New(N);
-    if (!r) return nullptr;
-    PyObject** items = theirs ? PySequence_Fast_ITEMS(theirs) : nullptr;
-    for (int i = 0; i < N; ++i) {
-      PyObject* x = theirs ? given(items[i]) : THPVariable_Wrap(t[i]);
+    for (int i = 0; r && i < N; ++i) {
+      PyObject* x = THPVariable_Wrap(t[i]);
       if (!x) {
-        Py_DECREF(r);
-        return nullptr;
+        Py_CLEAR(r);
+        break;
       }
       PyTuple_SET_ITEM(r, i, x);
     }

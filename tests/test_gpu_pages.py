@@ -321,6 +321,19 @@ def test_arguments_of_the_wrong_kind_are_named():
     check_status(False)
 
 
+def test_given_outputs_are_returned():
+    p = Pool(60, 16, 5, 6, seed=4)
+    bt, lens, counts = p.args()
+    out = [torch.empty((2, 6), dtype=I32, device="cuda"), torch.empty(2, dtype=I32, device="cuda"), counts.clone()]
+    got = kvp.kv_pages_fork(bits((2, 60, 16, 1, 64), 3), bt, lens, counts, dev([3, 3]), out=out)
+    assert isinstance(got, tuple) and all(a is b for a, b in zip(got, out))
+    out = [bt, lens, counts, torch.empty(9, dtype=I32, device="cuda")]
+    got = kvp.kv_pages_extend(bt, lens, counts, dev([1] * 5), 16, 9, out=out)
+    assert isinstance(got, tuple) and all(a is b for a, b in zip(got, out))
+    torch.cuda.synchronize()
+    kvp.device_status()  # (whether the rows fit is not this test's matter)
+
+
 def test_results_do_not_depend_on_order():
     p = Pool(5000, 16, 300, 40, seed=1)
     parents = dev(p.rng.integers(0, 300, 300))
