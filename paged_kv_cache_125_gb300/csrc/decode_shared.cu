@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
   const int B = a.num_seqs, bs = a.block_size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool small = B <= T;
+  // (Launched in the shadow of the kernel before.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // Every CTA of the cluster runs before one writes to another's shared memory.
   asm volatile(
       "barrier.cluster.arrive.relaxed;\n\t"
@@ -1528,12 +1530,14 @@ cudaError_t launch_shared_plan(const int32_t* block_tables, int max_blocks, cons
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg,
                             threads == 256   ? shared_plan_kernel<256>
                             : threads == 512 ? shared_plan_kernel<512>

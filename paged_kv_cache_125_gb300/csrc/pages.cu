@@ -318,6 +318,13 @@ __device__ __forceinline__ void for_free_pages(const int* counts, RankScratch& s
   });
 }
 
+// A plan is launched in the shadow of the kernel before it on the stream, and
+// lets the copies, which wait for it, get ready.
+__device__ __forceinline__ void plan_begins() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ fork
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs a) {
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
   const RowWalk rows(a.max_blocks, t.rank, t.size);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  plan_begins();
 
   Segment s = segment_of(a, t);
 #pragma unroll 4
@@ -485,6 +492,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
   const Team t;
   const int bs = a.block_size;
   const int64_t mb = a.max_blocks;
+  plan_begins();
   const int keepers = (int)gridDim.x - t.size;
   if ((int)blockIdx.x >= t.size) {
     keep_rows(a, (int)blockIdx.x - t.size, keepers);
@@ -594,7 +602,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesArgs a) {
   __shared__ RankScratch scratch;
   const Team t;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  plan_begins();
   Segment s = segment_of(a, t);
   auto in_use = [](int count) { return count > 0; };
   const Marks marks = mark_segment(a, t, a.ref_counts, 0, scratch, &s, in_use);
@@ -879,7 +887,7 @@ PagesWorkspace pages_workspace(void* base, int64_t num_blocks, int64_t rows) {
 cudaError_t launch_pages_fork(const PagesArgs& a, const PagesCache& c, int num_sms,
                               cudaStream_t stream) {
   const TeamShape t = team_shape(a);
-  cudaError_t e = launch(fork_plan_kernel, t.size, t.threads, 0, t.size, false, stream, a);
+  cudaError_t e = launch(fork_plan_kernel, t.size, t.threads, 0, t.size, true, stream, a);
   return e != cudaSuccess ? e : launch_copies(a, c, num_sms, stream);
 }
 
@@ -894,13 +902,13 @@ cudaError_t launch_pages_extend(const PagesArgs& a, int num_sms, cudaStream_t st
     const int64_t want = (entries + cluster - 1) / cluster, room = num_sms / t.size - 1;
     keepers = t.size * (int)(want < room ? want : room);
   }
-  return launch(extend_plan_kernel, t.size + keepers, t.threads, 0, t.size, false, stream, a);
+  return launch(extend_plan_kernel, t.size + keepers, t.threads, 0, t.size, true, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PagesArgs& a, const PagesCache& c, int num_sms,
                                  cudaStream_t stream) {
   const TeamShape t = team_shape(a);
-  cudaError_t e = launch(compact_plan_kernel, t.size, t.threads, 0, t.size, false, stream, a);
+  cudaError_t e = launch(compact_plan_kernel, t.size, t.threads, 0, t.size, true, stream, a);
   return e != cudaSuccess ? e : launch_copies(a, c, num_sms, stream);
 }
 
