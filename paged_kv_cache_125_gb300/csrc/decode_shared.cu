@@ -455,10 +455,12 @@ struct SharedAppend {
 
 // True if the plan was made for this call's batch and shape.
 __device__ __forceinline__ bool plan_fits(const SharedArgs& a) {
-  const SharedPlanHead& h = *a.plan.head;
-  return h.magic == kPlanMagic && h.num_seqs == a.num_seqs &&
-         h.group == a.num_heads / a.num_kv_heads && h.num_kv_heads == a.num_kv_heads &&
-         h.block_size == a.block_size && h.max_blocks == a.max_blocks && h.sms == a.sms;
+  // The head's first eight fields: magic, num_seqs, group, num_kv_heads;
+  // block_size, max_blocks, num_tiles, sms.
+  const int4* h = reinterpret_cast<const int4*>(a.plan.head);
+  const int4 x = h[0], y = h[1];
+  return (x.x == kPlanMagic) & (x.y == a.num_seqs) & (x.z == a.num_heads / a.num_kv_heads) &
+         (x.w == a.num_kv_heads) & (y.x == a.block_size) & (y.y == a.max_blocks) & (y.w == a.sms);
 }
 
 // ------------------------------------------------- the shared prefixes
@@ -916,18 +918,15 @@ struct OwnLayout {
 static_assert(OwnLayout<128>::kAlloc + PrefixLayout<128>::kAlloc + 2048 <= 228 * 1024, "smem");
 
 template <int D>
-__device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const CUtensorMap* tmK,
-                             const CUtensorMap* tmV, uint8_t* smem, StageMeta* meta,
-                             uint64_t* full, uint64_t* empty) {
+__device__ void own_producer(const SharedArgs& a, const SharedAppend& app, const SharedOwnStart& start,
+                             long long pos, const long long end, const CUtensorMap* tmK,
+                             const CUtensorMap* tmV, uint8_t* smem, StageMeta* meta, uint64_t* full,
+                             uint64_t* empty) {
   using Lay = OwnLayout<D>;
   constexpr int RS = Lay::kStages;
   const int lane = threadIdx.x & 31;
   const int Hkv = a.num_kv_heads, T = kStageRows / Hkv, bs = a.block_size;
   const int shift = __ffs(bs) - 1;  // block_size is a power of two
-  const long long total = a.plan.head->own_total, chunk = a.plan.head->own_chunk;
-  const SharedOwnStart start = a.plan.own_start[blockIdx.x];
-  long long pos = chunk * blockIdx.x;
-  const long long end = pos + chunk < total ? pos + chunk : total;
   uint8_t *ringK = smem, *ringV = smem + RS * Lay::kHalf;
   int s = 0;
   uint32_t ph = 0, issued = 0, issued_ph = 0;
@@ -1245,18 +1244,19 @@ __global__ void __maxnreg__(kOwnRegs)
   // kernel can rely on the same.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (One round trip for all of these, and for the head that plan_fits looks at.)
+  const SharedOwnStart start = a.plan.own_start[blockIdx.x];
+  const long long chunk = a.plan.head->own_chunk, total = a.plan.head->own_total;
   if (!plan_fits(a) || (smem_u32(smem) & 1023u)) {
     if (threadIdx.x == 0) record_error(a.status, KVP_ERR_DEVICE_DATA);
     return;
   }
   __syncthreads();
+  const long long pos = chunk * blockIdx.x, end = min(pos + chunk, total);
   if ((threadIdx.x >> 5) == kOwnWarps)
-    own_producer<D>(a, app, &tmK, &tmV, smem, meta, full, empty);
+    own_producer<D>(a, app, start, pos, end, &tmK, &tmV, smem, meta, full, empty);
   else
-    own_consumer<D, G>(a, app, smem, meta, full, empty,
-                       a.plan.head->own_chunk * blockIdx.x < a.plan.head->own_total
-                           ? a.plan.own_start[blockIdx.x].seq
-                           : -1);
+    own_consumer<D, G>(a, app, smem, meta, full, empty, pos < end ? start.seq : -1);
 }
 
 // ----------------------------------------------------------------- merge
