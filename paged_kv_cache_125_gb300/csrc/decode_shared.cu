@@ -833,8 +833,14 @@ __global__ void __maxnreg__(kPrefixRegs)
   PrefixSegment sg;
   sg.pos = 0;
   sg.end = 0;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + P_BARS);
   // (A plan of another shape is reported by the own-part kernel.)
   const SharedPrefixStart start = a.plan.prefix_start[blockIdx.x];
+  if (threadIdx.x == 4 * 32) {
+    for (int i = 0; i < P_BARS; ++i) mbar_init(&bars[i], i == P_PFULL || i == P_PFULL + 1 || i == P_OFREE ? 4 : 1);
+    fence_mbar_init();
+  }
   if (plan_fits(a)) {
     const PrefixSplit split(*a.plan.head);
     sg.pos = split.begin(blockIdx.x);
@@ -842,26 +848,27 @@ __global__ void __maxnreg__(kPrefixRegs)
     sg.begin(start);
   }
   if (sg.pos < sg.end && !(smem_u32(smem) & 1023u)) {
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + P_BARS);
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < P_BARS; ++i) mbar_init(&bars[i], i == P_PFULL || i == P_PFULL + 1 || i == P_OFREE ? 4 : 1);
-      fence_mbar_init();
-    }
-    if (warp == 5) {
-      tmem_alloc(tmem_slot, kPrefixTmem);
-      tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tbase = *tmem_slot;
-    if (warp == 4)
+    uint32_t tbase = 0;
+    if (warp == 4) {
+      // The producer has set the barriers up itself and needs no tensor memory:
+      // its first loads are under way before the others have theirs.
+      __syncwarp();
+      asm volatile("bar.arrive 1, %0;" ::"n"(kPrefixThreads) : "memory");
       prefix_producer<D>(a, sg, &tmQ, &tmK, &tmV, smem, bars);
-    else if (warp < 4)
-      prefix_softmax<D>(a, sg, bars, tbase);
-    else if ((threadIdx.x & 31) == 0)
-      prefix_mma<D>(a, sg, smem, bars, tbase);
+    } else {
+      if (warp == 5) {
+        tmem_alloc(tmem_slot, kPrefixTmem);
+        tmem_relinquish();
+      }
+      tc_fence_before();
+      named_barrier_sync(1, kPrefixThreads);
+      tc_fence_after();
+      tbase = *tmem_slot;
+      if (warp < 4)
+        prefix_softmax<D>(a, sg, bars, tbase);
+      else if ((threadIdx.x & 31) == 0)
+        prefix_mma<D>(a, sg, smem, bars, tbase);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
