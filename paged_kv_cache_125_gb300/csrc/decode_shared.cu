@@ -72,10 +72,12 @@ constexpr int kLeastSteps = 2;
 // kLeadOwn 64 as 128, 256 loses 9 us of the last.)
 constexpr int kLeadSteps = 2;
 constexpr int kLeadOwn = 128;
-// A sequence in a CTA costs about as much as 64 KiB of its stream (query,
-// page and plan look-ups, partials): in the own-part kernel's split it counts
-// that many tokens (of head_dim 128) more than it has.
-__host__ __device__ constexpr int own_gap(int num_kv_heads) { return 128 / num_kv_heads; }
+// A sequence in a CTA costs about as much as two or three stages of its stream
+// (query, page and plan look-ups, partials): in the own-part kernel's split it
+// counts three stages of tokens more than it has (16 prompts x 8 samples 63.1 us
+// with two, 62.3 with three, 62.5 with four).  A CTA takes as much at least (one
+// document for 16 sequences: 44.5 us, 45.3 with twice that).
+__host__ __device__ constexpr int own_gap(int num_kv_heads) { return 3 * 64 / num_kv_heads; }
 __device__ __forceinline__ long long chunk_of(long long total, int ctas, int least) {
   const long long c = (total + ctas - 1) / ctas;
   return c < least ? least : c;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const PlanArgs a) {
     }
   }
   const int tiles = (int)(base[0] >> 32);
-  const long long ochunk = chunk_of(base[2], own_ctas(a.sms), 2 * a.gap);
+  const long long ochunk = chunk_of(base[2], own_ctas(a.sms), a.gap);
   const PrefixSplit split = split_prefixes(base[1], ochunk * a.num_kv_heads, a.sms);
   if (threadIdx.x == 0) {
     p.cum_tokens[B] = base[2];
