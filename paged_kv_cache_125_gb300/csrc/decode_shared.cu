@@ -24,14 +24,14 @@
 // the SM count alone, so a captured call serves any batch of its size.
 //
 // Measured on one GB300 (device time of plan + call, its bytes read once):
-//   512 sequences, 32/8/128, 8192 keys shared, 64 .. 1000 own    232 us
+//   512 sequences, 32/8/128, 8192 keys shared, 64 .. 1000 own    231 us
 //     (own parts alone 162 us = 6.7 TB/s, prefixes alone 73 us = 940 TFLOP/s;
-//      together 211: the prefixes are through after 122, and the own parts run
+//      together 208: the prefixes are through after 122, and the own parts run
 //      at 60% until then, which is not one resource's doing: without the MMAs
 //      of the prefixes 18 us less, without those of the own parts 16, with the
 //      own parts' bytes from L2 19; 20 merge and plan)
-//   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           47 us
-//   16 sequences, 64/8/128, 32768 shared, up to 64 own             47 us
+//   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           46 us
+//   16 sequences, 64/8/128, 32768 shared, up to 64 own             45 us
 //   against attn_decode_paged on such tables, 16/8/128: 64 sequences with 2048
 //   shared and 100 .. 600 own 30 against 98 us, with 8192 39 against 320.
 // Break-even of the default min_shared_len (128 tokens; shared against not):
