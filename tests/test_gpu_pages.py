@@ -334,6 +334,41 @@ def test_given_outputs_are_returned():
     kvp.device_status()  # (whether the rows fit is not this test's matter)
 
 
+def test_work_of_another_stream_is_waited_for():
+    """The inputs are written late on one stream; the calls run on another one
+    that waits for it, behind a kernel of its own."""
+    p = Pool(700, 16, 60, 9, seed=8)
+    real, parents, new = p.args(), dev(p.rng.integers(-1, 60, 50)), dev(p.rng.integers(0, 3, 60))
+    cache = bits((1, 700, 16, 1, 64), 5)
+    image = raw(cache).copy()
+
+    def ops(a):
+        return (*kvp.kv_pages_fork(cache, *a, parents), *kvp.kv_pages_extend(*a, new, 16, 180),
+                *kvp.kv_pages_compact(cache, *a), kvp.attn_shared_plan(a[0], a[1], 16, 2, 1, 700))
+
+    want = [x.clone() for x in ops(real)]
+    after = raw(cache).copy()
+    kvp.device_status()  # (rows that cannot grow are not this test's matter)
+    for _ in range(3):
+        cache.copy_(torch.from_numpy(image).cuda().view(BF16))
+        a = [torch.zeros_like(x) for x in real]
+        torch.cuda.synchronize()
+        writer, reader = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.stream(writer):
+            torch.cuda._sleep(4_000_000)
+            for x, y in zip(a, real):
+                x.copy_(y)
+        with torch.cuda.stream(reader):
+            torch.zeros(1000, device="cuda").add_(1)
+            reader.wait_stream(writer)
+            got = ops(a)
+        torch.cuda.synchronize()
+        kvp.device_status()
+        assert all(torch.equal(x, y) for x, y in zip(got[:-1], want[:-1]))
+        assert torch.equal(got[-1][:80], want[-1][:80])  # the plan's head, its totals among it
+        assert np.array_equal(raw(cache), after)
+
+
 def test_results_do_not_depend_on_order():
     p = Pool(5000, 16, 300, 40, seed=1)
     parents = dev(p.rng.integers(0, 300, 300))
