@@ -521,6 +521,10 @@ constexpr int kMaxSub = kTileKeys / 16;    // pages of a step (the smallest page
 // Tensor memory: S of even steps | S of odd steps (P over each one's first half) | O.
 constexpr uint32_t kColO = 2 * kTileKeys, kPrefixTmem = 256;
 
+// Steps of the next unit, of `left` in the segment: an even step and the one
+// after it have their S in one matrix product of 128 keys, which reads Q once.
+__device__ __forceinline__ int unit_of(uint32_t n, int left) { return !(n & 1) && left > 1 ? 2 : 1; }
+
 // The segments of this CTA, one after the other.
 struct PrefixSegment {
   long long pos, end;  // flat steps left
@@ -582,8 +586,9 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
   // Other tiles read the same keys: hold on to them in L2.
   const uint64_t keep = policy_evict_last();
   const int G = a.num_heads / a.num_kv_heads;
-  uint32_t n = 0, segs = 0;  // steps and segments issued; step n uses slot n & 1
-  bool ok = true, k_only = false;
+  uint32_t n = 0, segs = 0;    // steps and segments begun; step n uses slot n & 1
+  uint32_t issued[2] = {0, 0};  // loads of K, of V
+  bool ok = true;
   while (ok && sg.next(a)) {
     if (!mbar_wait(&bars[P_QEMPTY], (segs & 1) ^ 1u, a.status)) {
       ok = false;
@@ -597,14 +602,15 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
     }
     ++segs;
     const int32_t* table = a.block_tables + (int64_t)sg.seq0 * a.max_blocks;
-    // Lane i has the row of sub-box i & 3 of the (i / 4)-th next step.
-    int rows = past;
-    for (int s = sg.s0; s < sg.s1; ++s, ++n) {
-      const int j = (s - sg.s0) & 7;
-      if (j == 0) {
-        const int key = (s + (lane >> 2)) * kTileKeys + (lane & 3) * box;
+    // Lane i has the row of sub-box i & 3 of the (i / 4)-th of 8 steps from w on.
+    int rows = past, w = sg.s0 - 8;
+    for (int s = sg.s0; ok && s < sg.s1;) {
+      const int unit = unit_of(n, sg.s1 - s);
+      if (s + unit > w + 8) {
+        w = s;
+        const int key = (w + (lane >> 2)) * kTileKeys + (lane & 3) * box;
         rows = past;
-        if ((lane & 3) < nsub && key < sg.prefix && s + (lane >> 2) < sg.s1) {
+        if ((lane & 3) < nsub && key < sg.prefix && w + (lane >> 2) < sg.s1) {
           int phys = table[key >> shift];
           if (phys < 0 || phys >= a.num_blocks) {
             record_error(a.status, KVP_ERR_DEVICE_DATA);
@@ -613,93 +619,93 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
           rows = (phys << shift) + (key & (a.block_size - 1));
         }
       }
-      int row[kMaxSub];
-#pragma unroll
-      for (int i = 0; i < kMaxSub; ++i) row[i] = __shfl_sync(0xffffffffu, rows, j * 4 + i);
-      const int slot = n & 1;
-      const uint32_t par = ((n >> 1) & 1) ^ 1u;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll 1
+      for (int i = 0; ok && i < 2 * unit; ++i) {  // K of the unit's steps, then V
+        const int kv = i >= unit, u = i - kv * unit;
+        const uint32_t slot = (n + u) & 1, par = ((n + u) >> 1 & 1) ^ 1u;
         const int full = (kv == 0 ? P_KFULL : P_VFULL) + slot;
         const int empty = (kv == 0 ? P_KEMPTY : P_VEMPTY) + slot;
+        int row[kMaxSub];
+#pragma unroll
+        for (int k = 0; k < kMaxSub; ++k) row[k] = __shfl_sync(0xffffffffu, rows, (s + u - w) * 4 + k);
         if (!mbar_wait(&bars[empty], par, a.status)) {
           ok = false;
-          k_only = kv == 1;
           break;
         }
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars[full], Lay::kSlot);
-          uint8_t* dst = smem + (kv == 0 ? Lay::kK : Lay::kV) + slot * Lay::kSlot;
+          uint8_t* dst = smem + (kv == 0 ? Lay::kK + slot * Lay::kPanel : Lay::kV + slot * Lay::kSlot);
+          const uint32_t panel = kv == 0 ? 2 * Lay::kPanel : Lay::kPanel;
           const CUtensorMap* map = kv == 0 ? tmK : tmV;
 #pragma unroll
-          for (int i = 0; i < kMaxSub; ++i)
-            if (i < nsub)
+          for (int k = 0; k < kMaxSub; ++k)
+            if (k < nsub)
               for (int p = 0; p < (int)Lay::kPanels; ++p)
-                tma_load_3d_hint(dst + p * Lay::kPanel + i * box * 128, map, p * 64, sg.h, row[i],
-                                 &bars[full], keep);
+                tma_load_3d_hint(dst + p * panel + k * box * 128, map, p * 64, sg.h, row[k], &bars[full],
+                                 keep);
         }
+        ++issued[kv];
       }
-      if (!ok) break;
+      s += unit;
+      n += unit;
     }
   }
   if (ok) return;  // the MMA thread has waited for every copy
   // After an expired wait: no copy of this CTA is in flight when it exits.
-  // (Steps below n are complete in both; step n may have its K only.)
   if (segs) mbar_wait(&bars[P_QFULL], (segs - 1) & 1, a.status);
   for (int kv = 0; kv < 2; ++kv)
-    for (uint32_t i = n > 1 ? n - 2 : 0; i < n; ++i)
+    for (uint32_t i = issued[kv] > 2 ? issued[kv] - 2 : 0; i < issued[kv]; ++i)
       mbar_wait(&bars[(kv == 0 ? P_KFULL : P_VFULL) + (i & 1)], (i >> 1) & 1, a.status);
-  if (k_only) mbar_wait(&bars[P_KFULL + (n & 1)], (n >> 1) & 1, a.status);
 }
 
 template <int D>
 __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem, uint64_t* bars,
                            uint32_t tbase) {
   using Lay = PrefixLayout<D>;
-  const uint32_t idesc_s = idesc_bf16_f32(kTileRows, kTileKeys, 0, 0) | a.prefix_negate;
+  const uint32_t idesc_s1 = idesc_bf16_f32(kTileRows, kTileKeys, 0, 0) | a.prefix_negate;
+  const uint32_t idesc_s2 = idesc_bf16_f32(kTileRows, 2 * kTileKeys, 0, 0) | a.prefix_negate;
   constexpr uint32_t idesc_o = idesc_bf16_f32(kTileRows, D, 0, 1);
   const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
   const uint64_t dk0 = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
   const uint64_t dv0 = smem_desc(smem_u32(smem + Lay::kV), Lay::kPanel, 1024, 2);
   uint32_t n = 0, segs = 0;
-  // S(n) = Q K(n)^T into buffer n & 1.  The P of step n - 2, which it
-  // overwrites, has been read: its PV was issued before.
-  auto issue_s = [&](uint32_t n, bool last) {
-    const uint32_t slot = n & 1;
-    if (!mbar_wait(&bars[P_KFULL + slot], (n >> 1) & 1, a.status)) return false;
-    tc_fence_after();
-    const uint64_t dk = dk0 + ((slot * Lay::kSlot) >> 4);
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t in = (kk & 3) * 32;
-      umma_f16_ss(tbase + slot * kTileKeys, dq + (((kk >> 2) * Lay::kQPanel + in) >> 4),
-                  dk + (((kk >> 2) * Lay::kPanel + in) >> 4), idesc_s, kk > 0);
-    }
-    umma_commit(&bars[P_SFULL + slot]);
-    umma_commit(&bars[P_KEMPTY + slot]);
-    if (last) umma_commit(&bars[P_QEMPTY]);
-    return true;
-  };
   while (sg.next(a)) {
     const int steps = sg.s1 - sg.s0;
     if (!mbar_wait(&bars[P_QFULL], segs & 1, a.status)) goto drain;
-    if (!issue_s(n, steps == 1)) goto drain;
-    for (int j = 0; j < steps; ++j, ++n) {
-      // The next step's S is computed while the softmax works on this one's.
-      if (j + 1 < steps && !issue_s(n + 1, j + 2 == steps)) goto drain;
-      const uint32_t slot = n & 1, par = (n >> 1) & 1;
-      if (!mbar_wait(&bars[P_VFULL + slot], par, a.status)) goto drain;
-      if (j == 0 && segs > 0 && !mbar_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
-      if (!mbar_wait(&bars[P_PFULL + slot], par, a.status)) goto drain;
+    for (int j = 0; j < steps;) {
+      // S = Q K^T of the unit.  The P that it overwrites have been read: their
+      // PV were issued before.
+      const int unit = unit_of(n, steps - j);
+      for (int u = 0; u < unit; ++u)
+        if (!mbar_wait(&bars[P_KFULL + ((n + u) & 1)], ((n + u) >> 1) & 1, a.status)) goto drain;
       tc_fence_after();
-      const uint64_t dv = dv0 + ((slot * Lay::kSlot) >> 4);
+      const uint64_t dk = dk0 + (((n & 1) * Lay::kPanel) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < kTileKeys / 16; ++kk)
-        umma_f16_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
-                    idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-      umma_commit(&bars[P_VEMPTY + slot]);
-      umma_commit(&bars[P_PVDONE]);
-      if (j + 1 == steps) umma_commit(&bars[P_ODONE]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t in = (kk & 3) * 32;
+        umma_f16_ss(tbase + (n & 1) * kTileKeys, dq + (((kk >> 2) * Lay::kQPanel + in) >> 4),
+                    dk + (((kk >> 2) * 2 * Lay::kPanel + in) >> 4), unit == 2 ? idesc_s2 : idesc_s1, kk > 0);
+      }
+      for (int u = 0; u < unit; ++u) {
+        umma_commit(&bars[P_SFULL + ((n + u) & 1)]);
+        umma_commit(&bars[P_KEMPTY + ((n + u) & 1)]);
+      }
+      if (j + unit == steps) umma_commit(&bars[P_QEMPTY]);
+      for (int u = 0; u < unit; ++u, ++j, ++n) {
+        const uint32_t slot = n & 1, par = (n >> 1) & 1;
+        if (!mbar_wait(&bars[P_VFULL + slot], par, a.status)) goto drain;
+        if (j == 0 && segs > 0 && !mbar_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
+        if (!mbar_wait(&bars[P_PFULL + slot], par, a.status)) goto drain;
+        tc_fence_after();
+        const uint64_t dv = dv0 + ((slot * Lay::kSlot) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          umma_f16_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
+                      idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&bars[P_VEMPTY + slot]);
+        umma_commit(&bars[P_PVDONE]);
+        if (j + 1 == steps) umma_commit(&bars[P_ODONE]);
+      }
     }
     ++segs;
   }
