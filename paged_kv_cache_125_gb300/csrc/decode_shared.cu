@@ -658,6 +658,45 @@ __device__ void prefix_producer(const SharedArgs& a, PrefixSegment sg, const CUt
       mbar_wait(&bars[(kv == 0 ? P_KFULL : P_VFULL) + (i & 1)], (i >> 1) & 1, a.status);
 }
 
+// MMAs and commits of a converged warp, by one of its lanes (the same each time).
+// A lane that runs alone has its operands in vector registers and moves each to
+// the uniform ones that these instructions take: 70 cycles an MMA.
+__device__ __forceinline__ void warp_umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void warp_umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// A bounded wait with one outcome for the warp, which stays converged.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+__device__ __forceinline__ void warp_umma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int D>
 __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem, uint64_t* bars,
                            uint32_t tbase) {
@@ -671,48 +710,48 @@ __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem,
   uint32_t n = 0, segs = 0;
   while (sg.next(a)) {
     const int steps = sg.s1 - sg.s0;
-    if (!mbar_wait(&bars[P_QFULL], segs & 1, a.status)) goto drain;
+    if (!warp_wait(&bars[P_QFULL], segs & 1, a.status)) goto drain;
     for (int j = 0; j < steps;) {
       // S = Q K^T of the unit.  The P that it overwrites have been read: their
       // PV were issued before.
       const int unit = unit_of(n, steps - j);
       for (int u = 0; u < unit; ++u)
-        if (!mbar_wait(&bars[P_KFULL + ((n + u) & 1)], ((n + u) >> 1) & 1, a.status)) goto drain;
+        if (!warp_wait(&bars[P_KFULL + ((n + u) & 1)], ((n + u) >> 1) & 1, a.status)) goto drain;
       tc_fence_after();
       const uint64_t dk = dk0 + (((n & 1) * Lay::kPanel) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t in = (kk & 3) * 32;
-        umma_f16_ss(tbase + (n & 1) * kTileKeys, dq + (((kk >> 2) * Lay::kQPanel + in) >> 4),
+        warp_umma_ss(tbase + (n & 1) * kTileKeys, dq + (((kk >> 2) * Lay::kQPanel + in) >> 4),
                     dk + (((kk >> 2) * 2 * Lay::kPanel + in) >> 4), unit == 2 ? idesc_s2 : idesc_s1, kk > 0);
       }
       for (int u = 0; u < unit; ++u) {
-        umma_commit(&bars[P_SFULL + ((n + u) & 1)]);
-        umma_commit(&bars[P_KEMPTY + ((n + u) & 1)]);
+        warp_umma_commit(&bars[P_SFULL + ((n + u) & 1)]);
+        warp_umma_commit(&bars[P_KEMPTY + ((n + u) & 1)]);
       }
-      if (j + unit == steps) umma_commit(&bars[P_QEMPTY]);
+      if (j + unit == steps) warp_umma_commit(&bars[P_QEMPTY]);
       for (int u = 0; u < unit; ++u, ++j, ++n) {
         const uint32_t slot = n & 1, par = (n >> 1) & 1;
-        if (!mbar_wait(&bars[P_VFULL + slot], par, a.status)) goto drain;
-        if (j == 0 && segs > 0 && !mbar_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
-        if (!mbar_wait(&bars[P_PFULL + slot], par, a.status)) goto drain;
+        if (!warp_wait(&bars[P_VFULL + slot], par, a.status)) goto drain;
+        if (j == 0 && segs > 0 && !warp_wait(&bars[P_OFREE], (segs - 1) & 1, a.status)) goto drain;
+        if (!warp_wait(&bars[P_PFULL + slot], par, a.status)) goto drain;
         tc_fence_after();
         const uint64_t dv = dv0 + ((slot * Lay::kSlot) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          umma_f16_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
+          warp_umma_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
                       idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&bars[P_VEMPTY + slot]);
-        umma_commit(&bars[P_PVDONE]);
-        if (j + 1 == steps) umma_commit(&bars[P_ODONE]);
+        warp_umma_commit(&bars[P_VEMPTY + slot]);
+        warp_umma_commit(&bars[P_PVDONE]);
+        if (j + 1 == steps) warp_umma_commit(&bars[P_ODONE]);
       }
     }
     ++segs;
   }
 drain:
   // Every MMA this thread issued has completed before the CTA tears down.
-  umma_commit(&bars[P_DRAIN]);
-  mbar_wait(&bars[P_DRAIN], 0, a.status);
+  warp_umma_commit(&bars[P_DRAIN]);
+  warp_wait(&bars[P_DRAIN], 0, a.status);
 }
 
 template <int D>
@@ -874,7 +913,7 @@ __global__ void __maxnreg__(kPrefixRegs)
       tbase = *tmem_slot;
       if (warp < 4)
         prefix_softmax<D>(a, sg, bars, tbase);
-      else if ((threadIdx.x & 31) == 0)
+      else
         prefix_mma<D>(a, sg, smem, bars, tbase);
     }
     tc_fence_before();
