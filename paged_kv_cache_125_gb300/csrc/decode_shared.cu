@@ -24,14 +24,14 @@
 // the SM count alone, so a captured call serves any batch of its size.
 //
 // Measured on one GB300 (device time of plan + call, its bytes read once):
-//   512 sequences, 32/8/128, 8192 keys shared, 64 .. 1000 own    231 us
-//     (own parts alone 162 us = 6.7 TB/s, prefixes alone 73 us = 940 TFLOP/s;
-//      together 208: the prefixes are through after 122, and the own parts run
-//      at 60% until then, which is not one resource's doing: without the MMAs
-//      of the prefixes 18 us less, without those of the own parts 16, with the
-//      own parts' bytes from L2 19; 20 merge and plan)
+//   512 sequences, 32/8/128, 8192 keys shared, 64 .. 1000 own    216 us
+//     (own parts alone 162 us = 6.7 TB/s, prefixes alone 64 us = 1080 TFLOP/s;
+//      together 192: the prefixes are through after 113, and the own parts run
+//      at 70% until then, which is not one resource's doing: neither without the
+//      MMAs of either, nor with the bytes of either from L2 or halved, does it
+//      come near 162; 20 merge and plan)
 //   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           46 us
-//   16 sequences, 64/8/128, 32768 shared, up to 64 own             45 us
+//   16 sequences, 64/8/128, 32768 shared, up to 64 own             44 us
 //   against attn_decode_paged on such tables, 16/8/128: 64 sequences with 2048
 //   shared and 100 .. 600 own 30 against 98 us, with 8192 39 against 320.
 // Break-even of the default min_shared_len (128 tokens; shared against not):
@@ -469,21 +469,23 @@ __device__ __forceinline__ bool plan_fits(const SharedArgs& a) {
 //
 // Item: a tile t of up to 128 query rows (128 / G sequences of a group x the G
 // query heads of kv head h) against all keys of the group's prefix, taken 64
-// at a time ("step").  The items' steps, laid end to end, are split evenly
-// over the CTAs; a CTA's pieces ("segments") leave un-normalised partials.
-// Per step: S = Q K^T (tcgen05, M128 N64 K = D) -> row maxima and weights in
+// at a time ("step").  The items' steps, laid end to end, are split over the
+// CTAs; a CTA's pieces ("segments") leave un-normalised partials.
+// Per step: S = Q K^T (tcgen05, M128, K = D) -> row maxima and weights in
 // registers -> P in tensor memory -> O += P V.  Rows of a group share the
 // same keys, so nothing but the last step's ragged end is masked.
 //
 // 192 threads: warps 0-3 softmax (thread = row), warp 4 TMA producer, warp 5
-// tensor memory and MMA issue.  S has two buffers: S(j + 1) is computed while
-// the softmax works on S(j), so the tensor core's part of a step does not stand
-// in the chain from one softmax to the next (one buffer: 128 us instead of 73
-// for 512 x 32 rows over 8192 keys).  What bounds it is that chain (barrier,
-// tensor-memory load, maximum, exponentials, store, barrier; the tensor pipe is
-// active 45% of the time with two CTAs on an SM, issue slots 34%).  A step of
-// 128 keys would need 384 columns of tensor memory.  K and V are read once per
-// tile from L2 (552 MB for those rows; 38 MB from HBM).
+// tensor memory and MMA issue.  S of two steps is one product (N 128), so that Q
+// is read from shared memory half as often: alone the kernel takes the same, but
+// the own parts beside it gain (231 to 216 us for 512 sequences).  The softmax of
+// the second step runs on while the first one's PV is issued.
+// 512 x 32 rows over 8192 keys: 64 us, 1080 TFLOP/s (128 with one S of 64 keys and
+// the MMAs issued by a lane alone).  What bounds it is the chain of a step, 1960
+// cycles: softmax 690 (552 of them arithmetic), PV and S of the next steps 1000,
+// half of it issue; the tensor pipe is active 51% of the time with two CTAs on an
+// SM, issue slots 38%.  K and V are read once per tile from L2 (552 MB for those
+// rows; 39 MB from HBM).
 
 constexpr int kPrefixThreads = 192;
 // Two warps of this kernel and three of the own-part kernel must fit one SM
