@@ -1321,7 +1321,7 @@ __global__ void __maxnreg__(kOwnRegs)
 // W warps per (sequence, query head), a lane per D / 32 elements.  Launched as
 // a programmatic dependent of the prefix kernel: its plan look-ups overlap the
 // kernels before it.  Bound by latency: a few parts of 528 bytes a row, from
-// L2; 12 us for 16384 rows, 4 us for 1024.
+// L2; 10 us for 16384 rows, 4 us for 1024.
 
 constexpr int kMergeWarps = 8;
 
