@@ -484,7 +484,7 @@ __device__ void keep_rows(const PagesArgs& a, int me, int n) {
 }
 
 // The first cluster is the team; CTAs behind it, if there are any, keep the
-// table rows.
+// table rows.  Nothing orders the two, so the team reads no entry that they write.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesArgs a) {
   __shared__ long long warp_sums[2][32];
   __shared__ RowGrowth s_grow[kRowsInSmem];
@@ -590,8 +590,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const PagesAr
       const int r = last_at_most(grow, a.num_rows, &RowGrowth::token0, i);
       const RowGrowth g = grow[r];
       const int pos = g.len + (int)(i - g.token0);
+      // A page that the row had comes from the input: keep_rows may be CTAs of
+      // other clusters, which no barrier of the team orders.  (In place too: the
+      // entries that a row had are never written.)
       if (served(g) && pos < g.len + g.add)
-        slot = ld_cg(&a.out_tables[r * mb + pos / bs]) * bs + pos % bs;
+        slot = (pos / bs < row_pages(g.len, bs) ? a.block_tables[r * mb + pos / bs]
+                                                : ld_cg(&a.out_tables[r * mb + pos / bs])) * bs + pos % bs;
     }
     a.slot_mapping[i] = slot;
   }

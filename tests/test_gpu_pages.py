@@ -252,6 +252,47 @@ def test_moves_across_2_32_bytes():
         assert torch.equal(cache[:, d, :n].view(torch.int16), cache[:, s, :n].view(torch.int16))
 
 
+@pytest.mark.parametrize("kind", ["one", "ragged"])
+def test_extend_beside_other_work(kind):
+    """Rows with unfilled last pages in a table so large that CTAs beside the
+    team keep it, into outputs that hold other pages' ids, while matrix
+    products of a second stream have SMs: the slots of a page that the row had
+    must not wait for its entry in the new table."""
+    bs, rows, width = 16, 512, 500
+    rng = np.random.default_rng(7)
+    lens = [int(x) // bs * bs + int(rng.integers(1, bs)) for x in rng.integers(128, (width - 4) * bs, rows)]
+    held = sum(ref.ceil(n, bs) for n in lens)
+    nb = held + 3 * rows
+    ids, at, tables, counts = rng.permutation(nb).tolist(), 0, [], [0] * nb
+    for n in lens:
+        row, at = ids[at:at + ref.ceil(n, bs)], at + ref.ceil(n, bs)
+        tables.append(row + [-1] * (width - len(row)))
+        for p in row:
+            counts[p] = 1
+    new = [1] * rows if kind == "one" else rng.integers(0, 2 * bs, rows).tolist()
+    total = sum(new)
+    t, l, c, s, bad = ref.extend(tables, lens, counts, new, bs, total)
+    assert not bad
+    args, new = (dev(tables), dev(lens), dev(counts)), dev(new)
+    want = [dev(x) for x in (t, l, c, s)]
+    outs = [[torch.empty_like(x) for x in want] for _ in range(8)]
+    side, m = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda").to(BF16)
+    kvp.device_status()
+    for i in range(12):
+        for out in outs:
+            for x in out:
+                x.fill_((i * 977 + 5) % nb)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(6):
+                torch.matmul(m, m)
+        for out in outs:
+            kvp.kv_pages_extend(*args, new, bs, total, out=out)
+        check_status(False)
+        for out in outs:
+            assert all(torch.equal(x, y) for x, y in zip(out, want)), i
+
+
 def test_more_rows_than_fit_in_shared_memory():
     """Over 2048 rows: the searches of kv_pages_extend go through the workspace."""
     p = Pool(9000, 16, 2600, 4, seed=3)
