@@ -22,6 +22,7 @@ import ctypes
 import math
 import os
 import threading
+import warnings
 
 __all__ = ["kv_store", "kv_copy_blocks", "attn_prefill_varlen", "attn_prefill_varlen_append",
            "attn_mixed_step",
@@ -462,31 +463,46 @@ def attn_mixed_step(q, k, v, slot_mapping, cu_seqlens_q, cu_seqlens_k, max_seqle
 # The calls below run once per layer or step from Python, next to kernels of a
 # few microseconds.  Their arguments are checked and marshalled by an extension
 # module (csrc/python/calls.cpp), which makes the call when all is well and
-# otherwise returns None: then the checks here name the fault.
+# otherwise returns None: then the checks here name the fault.  Where there is no
+# extension module for the installed torch, the code here makes every call itself.
 
 _CALLS = None
 
 
+class _NoCalls:
+    """Stands for the extension module where there is none: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _calls():
-    """The extension module, built with the library."""
+    """The extension module, built with the library, or what stands for it."""
     global _CALLS
-    lib = library()
+    library()
     with _LIB_LOCK:
         if _CALLS is None:
-            import importlib.machinery
-            import importlib.util
-            from . import _build
-            path = _build.calls_path()
-            if not os.path.exists(path):
-                raise RuntimeError(f"the extension module is not built ({path}); run "
-                                   "`python -m paged_kv_cache_125_gb300._build` first")
-            loader = importlib.machinery.ExtensionFileLoader("_kvpaged_calls", path)
-            spec = importlib.util.spec_from_file_location("_kvpaged_calls", path, loader=loader)
-            module = importlib.util.module_from_spec(spec)
-            loader.exec_module(module)
-            module.set_check(_check)
-            _CALLS = module
+            _CALLS = _load_calls() or _NoCalls()
     return _CALLS
+
+
+def _load_calls():
+    import importlib.machinery
+    import importlib.util
+    from . import _build
+    path = _build.calls_path()
+    if not os.path.exists(path):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_kvpaged_calls", path)
+    spec = importlib.util.spec_from_file_location("_kvpaged_calls", path, loader=loader)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"the extension module does not load, its calls go through ctypes: {e}")
+        return None
+    module.set_check(_check)
+    return module
 
 
 def _call(idx, fn, *args):

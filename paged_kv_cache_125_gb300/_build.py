@@ -7,7 +7,9 @@ source or header is newer than the library.
 
 The extension module (csrc/python/calls.cpp) is host code against the C++
 headers of the installed torch, compiled with g++ next to the nvcc jobs; its
-file name carries that torch's version.
+file name carries that torch's version.  The library needs none of these: without
+torch there is no extension module to build, and where it cannot be built a
+warning says why and the Python binding makes the same calls through ctypes.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import re
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -54,8 +57,12 @@ def _stale() -> bool:
                   + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__], LIB)
 
 
-def _calls_stale() -> bool:
-    return _newer([CALLS_SRC, os.path.join(INCLUDE, "kvpaged.h"), __file__], calls_path())
+def _calls_stale(force: bool = False) -> bool:
+    try:
+        out = calls_path()
+    except ImportError:
+        return False  # no torch: nothing to bind to
+    return force or _newer([CALLS_SRC, os.path.join(INCLUDE, "kvpaged.h"), __file__], out)
 
 
 def _run(cmd, what: str):
@@ -87,10 +94,15 @@ def _link_calls(obj: str):
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT, exist_ok=True)
     with ThreadPoolExecutor(max_workers=1) as ex:
-        calls = ex.submit(_compile_calls) if force or _calls_stale() else None
+        calls = ex.submit(_compile_calls) if _calls_stale(force) else None
         _build_library(force, verbose, extra_flags)
         if calls is not None:
-            _link_calls(calls.result())
+            try:
+                _link_calls(calls.result())
+            except (RuntimeError, OSError, ImportError) as e:
+                if os.path.exists(calls_path()):  # of an older header: its calls may not match the library's
+                    os.remove(calls_path())
+                warnings.warn(f"the extension module was not built, its calls go through ctypes: {e}")
     return LIB
 
 
