@@ -50,7 +50,11 @@
  * - Head mapping (GQA): query head h reads kv head h / (num_heads /
  *   num_kv_heads).
  * - Arithmetic: bf16 inputs, fp32 accumulation, softmax in fp32 (base-2
- *   exponentials with log2(e) folded into the scale), bf16 outputs.
+ *   exponentials with log2(e) folded into the scale), bf16 outputs.  For the
+ *   product with V, weights are rounded to bf16 where it runs on tensor cores
+ *   (prefill; decode of four and eight query heads per kv head); decode of one
+ *   and two heads has them in fp32, shared decode as two bf16 numbers (within
+ *   2^-15).
  */
 #ifndef KVPAGED_H
 #define KVPAGED_H
@@ -418,8 +422,9 @@ int attn_decode_paged_noalloc(const kvp_bf16 *q, int64_t q_stride_tok, const kvp
  * run of neighbours that share at least min_shared_len tokens (and at least
  * half of what the next pair on either side shares); its prefix is what all
  * of its members share.  Sharing is found by comparing block ids, so the
- * attention's result is that of attn_decode_paged for any tables; batches
- * gain when sequences with a common prefix are neighbours.
+ * attention's result is that of attn_decode_paged for any tables, up to the
+ * order of fp32 sums and the weights' rounding (see Arithmetic); batches gain
+ * when sequences with a common prefix are neighbours.
  *
  *   block_tables     [num_seqs, max_blocks_per_seq] int32
  *   context_lens     [num_seqs] int32 (0: padding row); a length outside

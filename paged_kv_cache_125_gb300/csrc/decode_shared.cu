@@ -116,6 +116,19 @@ __device__ __forceinline__ PrefixSplit split_prefixes(long long total, long long
   return PrefixSplit(sms, first, chunk_of(rest > 0 ? rest : 0, sms, kLeastSteps));
 }
 
+// The weights are rounded to bf16 for the matrix products with V.  With one or two
+// query heads per kv head, where attn_decode_paged has them in fp32, they go in as two
+// bf16 numbers, the second being what the first leaves out (split_bf16x2: within 2^-15).
+// Against 64 bits, 2-norm, 16/8/128, 16 sequences of 1000 to 1200 keys, shared or not:
+// 0.00166, as a result rounded once and as attn_decode_paged (32/8/128 0.0023, both).
+// In the own parts that takes no more products (see own_consumer); the prefixes have
+// twice those with V: 512 sequences of 16/8/128 behind 8192 tokens 67.7 against 59.5 us
+// with one number, with own parts of 64 .. 1000 tokens 201 against 190, 64 behind 2048
+// with 100 .. 1500 48.7 against 47.9.  (A barrier of its own for the second number, so
+// that its arithmetic runs under the first product: 104 us, registers spill.)
+// With four or eight heads one number, as in attn_decode_paged.
+__host__ __device__ constexpr bool fine_weights(int group) { return group <= 2; }
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -699,7 +712,7 @@ __device__ __forceinline__ void warp_umma_commit(uint64_t* bar) {
       : "memory");
 }
 
-template <int D>
+template <int D, bool kFine>
 __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem, uint64_t* bars,
                            uint32_t tbase) {
   using Lay = PrefixLayout<D>;
@@ -740,9 +753,9 @@ __device__ void prefix_mma(const SharedArgs& a, PrefixSegment sg, uint8_t* smem,
         tc_fence_after();
         const uint64_t dv = dv0 + ((slot * Lay::kSlot) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          warp_umma_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8, dv + ((kk * 16 * 128) >> 4),
-                      idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < (kFine ? 2 : 1) * kTileKeys / 16; ++kk)  // P, then its rest
+          warp_umma_ts(tbase + kColO, tbase + slot * kTileKeys + kk * 8,
+                       dv + ((kk % (kTileKeys / 16) * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         warp_umma_commit(&bars[P_VEMPTY + slot]);
         warp_umma_commit(&bars[P_PVDONE]);
         if (j + 1 == steps) warp_umma_commit(&bars[P_ODONE]);
@@ -756,7 +769,7 @@ drain:
   warp_wait(&bars[P_DRAIN], 0, a.status);
 }
 
-template <int D>
+template <int D, bool kFine>
 __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* bars,
                                uint32_t tbase) {
   constexpr int S = part_stride<D>();
@@ -803,17 +816,32 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
       const float mu = m == -INFINITY ? 0.f : m;
       const float2 negm = make_float2(-mu, -mu);
       float2 sum2 = make_float2(0.f, 0.f);
-      uint32_t w[32];
+      // P over the S columns, which this thread has read: in bf16, and (kFine)
+      // what that leaves of each weight in the slot's other half.
+      constexpr int kHalf = kTileKeys / 2, W = kFine ? kHalf / 4 : kHalf;  // columns of a store
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 x = make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
-                                     __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
-        const float2 y = __ffma2_rn(x, scale2, negm);
-        const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-        sum2 = __fadd2_rn(sum2, p);
-        w[i] = pack_bf16x2(p.x, p.y);
+      for (int c = 0; c < kHalf; c += W) {
+        uint32_t w[W], rest[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int i = c + j;
+          const float2 x = make_float2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
+                                       __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
+          const float2 y = __ffma2_rn(x, scale2, negm);
+          const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          sum2 = __fadd2_rn(sum2, p);
+          if constexpr (kFine)
+            split_bf16x2(p.x, p.y, w[j], rest[j]);
+          else
+            w[j] = pack_bf16x2(p.x, p.y);
+        }
+        if constexpr (kFine) {
+          tmem_st8(s_col + c, w);
+          tmem_st8(s_col + kHalf + c, rest);
+        } else {
+          tmem_st32(s_col + c, w);
+        }
       }
-      tmem_st32(s_col, w);  // P over the S columns, which this thread has read
       if (__any_sync(0xffffffffu, rescale)) {
         // The step before is in O.  (One phase back at most: S(n) was issued
         // after PV(n - 2) and is complete.)
@@ -870,7 +898,7 @@ __device__ void prefix_softmax(const SharedArgs& a, PrefixSegment sg, uint64_t* 
   }
 }
 
-template <int D>
+template <int D, bool kFine>
 __global__ void __maxnreg__(kPrefixRegs)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -914,9 +942,9 @@ __global__ void __maxnreg__(kPrefixRegs)
       tc_fence_after();
       tbase = *tmem_slot;
       if (warp < 4)
-        prefix_softmax<D>(a, sg, bars, tbase);
+        prefix_softmax<D, kFine>(a, sg, bars, tbase);
       else
-        prefix_mma<D>(a, sg, smem, bars, tbase);
+        prefix_mma<D, kFine>(a, sg, smem, bars, tbase);
     }
     tc_fence_before();
     __syncthreads();
@@ -1147,7 +1175,12 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
   const int g = warp % Hkv, sub = warp / Hkv;
   const int head0 = g * G;
   const int r = lane >> 2, c = lane & 3;
-  const bool srow = r < G;  // this thread's S row is a real head
+  // S row r is that of head r.  With fine weights rows 4 .. 7 are the heads of rows
+  // 0 .. 3 again (there is room: at most two), and the product with V takes the weights
+  // in the former and what bf16 leaves of them in the latter, as columns of one MMA.
+  constexpr bool kTwice = fine_weights(G);
+  const int head = kTwice ? r & 3 : r;
+  const bool srow = head < G;  // this thread's S row is a real head
   const uint32_t region = (uint32_t)(g * P * T * 128);
   const int mrow = sub * 8 + (lane & 7), msel = lane >> 3;
   const uint32_t kbase = smem_u32(smem), vbase = kbase + RS * Lay::kHalf;
@@ -1161,7 +1194,7 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
   auto load_q = [&](int b) {
     qseq = b;
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q + (int64_t)b * a.q_stride +
-                                                             (int64_t)(head0 + r) * D);
+                                                             (int64_t)(head0 + head) * D);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       qa[ks][0] = srow ? qrow[ks * 8 + c] : 0u;
@@ -1236,7 +1269,14 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
       const float mu = m == -INFINITY ? 0.f : m;
       const float p0 = fast_exp2(x0 - mu), p1 = fast_exp2(x1 - mu);
       l += p0 + p1;
-      const uint32_t pb = pack_bf16x2(p0, p1);
+      uint32_t pb;
+      if constexpr (kTwice) {
+        uint32_t rest;
+        split_bf16x2(p0, p1, pb, rest);
+        if (r >= 4) pb = rest;
+      } else {
+        pb = pack_bf16x2(p0, p1);
+      }
       // V rows past the warp's tokens may hold anything: zero them.
       const uint32_t keep = 2 * c >= nt ? 0u : (2 * c + 1 >= nt ? 0x0000ffffu : 0xffffffffu);
 #pragma unroll
@@ -1256,6 +1296,12 @@ __device__ void own_consumer(const SharedArgs& a, const SharedAppend& app, uint8
     }
     if (!(md.flags & F_LAST)) continue;
     // The segment's partials: heads 2c, 2c + 1 of each thread.
+    if constexpr (kTwice) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ot[i][x] += __shfl_xor_sync(0xffffffffu, ot[i][x], 2);
+    }
     float lt = l;
     lt += __shfl_xor_sync(0xffffffffu, lt, 1);
     lt += __shfl_xor_sync(0xffffffffu, lt, 2);
@@ -1517,13 +1563,14 @@ cudaError_t launch_shared_t(const CUtensorMap& mq, const CUtensorMap& mpk, const
                             const CUtensorMap& mok, const CUtensorMap& mov, const SharedArgs& a,
                             const SharedAppend& app, cudaStream_t stream) {
   static std::atomic<uint64_t> own_set, prefix_set;
+  const auto prefix_kernel = shared_prefix_kernel<D, fine_weights(G)>;
   cudaError_t e = allow_smem(shared_own_kernel<D, G>, OwnLayout<D>::kAlloc, &own_set);
-  if (e == cudaSuccess) e = allow_smem(shared_prefix_kernel<D>, PrefixLayout<D>::kAlloc, &prefix_set);
+  if (e == cudaSuccess) e = allow_smem(prefix_kernel, PrefixLayout<D>::kAlloc, &prefix_set);
   if (e != cudaSuccess) return e;
   e = launch(shared_own_kernel<D, G>, own_ctas(a.sms), kOwnThreads, OwnLayout<D>::kAlloc, true,
                          stream, mok, mov, a, app);
   if (e != cudaSuccess) return e;
-  e = launch(shared_prefix_kernel<D>, prefix_ctas(a.sms), kPrefixThreads, PrefixLayout<D>::kAlloc, true,
+  e = launch(prefix_kernel, prefix_ctas(a.sms), kPrefixThreads, PrefixLayout<D>::kAlloc, true,
              stream, mq, mpk, mpv, a);
   if (e != cudaSuccess) return e;
   // Few rows: several warps share a row's parts.  A block takes as many heads

@@ -42,6 +42,19 @@ __device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(b0));
 }
 
+// x and y >= 0 as two bf16 numbers each: `hi` is x (1 - 2^-8) rounded, so always
+// below x, and `rest` what it leaves out, between 2^-16 x and 2^-7 x (exact before
+// it is rounded, by 2^-15 x at most).  Both have x's sign: a product with an
+// infinity keeps it, where a rest of 0 or below would make a NaN.
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& rest) {
+  const float2 v = make_float2(x, y);
+  const float2 low = __fmul2_rn(v, make_float2(0.99609375f, 0.99609375f));
+  hi = pack_bf16x2(low.x, low.y);
+  const float2 h = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+  const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), v);
+  rest = pack_bf16x2(r.x, r.y);
+}
+
 // Transpose of a 4 x 4 matrix of 16-byte chunks held by the 4 lanes of a
 // quad: on entry lane j holds chunks 0..3 of its row in w[0..3]; on exit lane
 // j holds chunk j of rows 0..3 of the quad.  Two butterfly stages; in each, a

@@ -162,6 +162,53 @@ def test_append_stores_and_attends(heads, shape):
     w.check(out, w.reference(), shape)
 
 
+@pytest.mark.parametrize("heads", [h for h in HEADS if h[0] <= 2 * h[1]], ids=lambda h: "%d/%d/%d" % h)
+@pytest.mark.parametrize("shape", ["shared", "alone"])
+def test_weights_are_held_to_15_bits(shape, heads):
+    """Where attn_decode_paged has its weights in fp32 (one and two query heads
+    per kv head), a weight is two bf16 numbers, off by 2^-15 at most.  Few keys,
+    so that a rounding to one bf16 would show.  Against the tolerance above, with A as there:
+
+      output                                      2^-8 |ref| (1 + 2^-6)
+      weights                                     2^-15 A = 3.1e-5 A
+      scores: d = 128 products, each sum within (d + 2) 2^-23 * scale * sum |q k|
+      (< 10 here), if its additions cut off instead of rounding: 1.55e-4, on p and
+      on the sum l                                3.1e-4 A
+      exponents of at most 32 in fp32, exp2       5e-6 A, twice
+      l and P V over at most 512 keys             512 (2^-24 + 2^-23) A = 9.2e-5 A
+
+    together below 2^-11 A."""
+    groups = {"shared": [(1 + i % 7, [1 + (3 * i + j) % 5 for j in range(2 + i % 4)]) for i in range(24)],
+              "alone": [(0, [1 + (5 * i) % 60]) for i in range(70)]}[shape]
+    w = Batch(heads, 16, groups, seed=31 + heads[0])
+    plan = w.plan(16)
+    assert any(plan_prefixes(plan, w.b)) == (shape == "shared")
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), plan, softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    ref, a = w.reference()
+    tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -6) + 2.0 ** -11 * np.abs(a)
+    over = np.abs(out.float().cpu().double().numpy() - ref) - tol
+    assert over.max() <= 0, f"{(over > 0).mean():.2%} past the tolerance"
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "%d/%d/%d" % h)
+def test_infinite_values(heads):
+    """An infinity in V at a key that is read is one in the output (weights are
+    above 0), in the shared part, in a part of its own and in a single token's."""
+    w = Batch(heads, 16, [(9, [20, 3, 1]), (0, [1]), (0, [40])], seed=17, poison=False)
+    for b, pos, col, sign in ((0, 30, 2, 1), (0, 143, 5, -1), (1, 144, 7, 1), (3, 0, 9, -1), (4, 25, 11, 1)):
+        w.vc[int(w.tables[b, pos // 16]), pos % 16, :, col] = sign * float("inf")
+    out = kvp.attn_decode_shared(w.q, w.kc, w.vc, w.dev(w.tables), w.plan(), softmax_scale=w.scale)
+    torch.cuda.synchronize()
+    assert_status_ok()
+    want = {2: [1, 1, 1, 0, 0], 5: [-1, -1, -1, 0, 0], 7: [0, 1, 0, 0, 0], 9: [0, 0, 0, -1, 0], 11: [0, 0, 0, 0, 1]}
+    for col in range(w.d):
+        for b, sign in enumerate(want.get(col, [0] * 5)):
+            x = out[b, :, col].float()
+            assert torch.all(x == sign * float("inf")) if sign else torch.isfinite(x).all(), (b, col)
+
+
 def test_strided_rows():
     """q, k, v and out are views into wider rows; nothing beside them is written."""
     w = Batch((16, 8, 128), 32, [(6, [40, 9, 1]), (0, [77])], seed=3)
