@@ -423,14 +423,20 @@ int attn_decode_paged_noalloc(const kvp_bf16 *q, int64_t q_stride_tok, const kvp
  * half of what the next pair on either side shares); its prefix is what all
  * of its members share.  Sharing is found by comparing block ids, so the
  * attention's result is that of attn_decode_paged for any tables, up to the
- * order of fp32 sums and the weights' rounding (see Arithmetic); batches gain
- * when sequences with a common prefix are neighbours.
+ * order of fp32 sums and the weights' rounding (see Arithmetic).
+ * What is gained depends on the rows' order and on one level: sequences that
+ * share but are no neighbours are read each for itself (put them next to one
+ * another), and where groups have a shorter prefix in common (a system prompt
+ * that is at least half of what a group shares) the batch can become one group
+ * with that prefix alone.  A min_shared_len above the common prompt keeps the
+ * groups apart.
  *
  *   block_tables     [num_seqs, max_blocks_per_seq] int32
  *   context_lens     [num_seqs] int32 (0: padding row); a length outside
  *                    [0, max_blocks_per_seq * block_size] is clamped and
  *                    records KVP_ERR_DEVICE_DATA
- *   min_shared_len   tokens (0: the library's default, 128)
+ *   min_shared_len   tokens (0: the library's default, 128, which suits groups
+ *                    of four and more; pairs gain from 512 to 1024 on)
  *   plan             device buffer of at least attn_shared_plan_size() bytes,
  *                    (a number of the shape and the current device),
  *                    16-byte aligned.  It holds the step's context lengths

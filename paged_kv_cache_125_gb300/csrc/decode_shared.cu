@@ -30,13 +30,18 @@
 //      at 70% until then, which is not one resource's doing: neither without the
 //      MMAs of either, nor with the bytes of either from L2 or halved, does it
 //      come near 162; 20 merge and plan)
-//   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           46 us
+//   64 sequences, 16/8/128, 2048 shared, 100 .. 1500 own           46.5 us
 //   16 sequences, 64/8/128, 32768 shared, up to 64 own             44 us
 //   against attn_decode_paged on such tables, 16/8/128: 64 sequences with 2048
-//   shared and 100 .. 600 own 30 against 98 us, with 8192 39 against 320.
-// Break-even of the default min_shared_len (128 tokens; shared against not):
-// groups of 4 x 16 27.9 / 29.3 us, one group of 64 27.0 / 29.2; groups of two
-// pay from 2048 tokens on only (1024: 37 / 35 us, 8192: 114 / 165).
+//   shared and 100 .. 600 own 33 against 100 us, with 8192 35 against 323; on tables
+//   that share nothing: 64 sequences of 100 .. 1500 46 against 45, 128 of 500 .. 4000
+//   178 against 182, 512 of 64 .. 1000 (32/8/128) 177 against 195.
+// Break-even of the default min_shared_len (128 tokens; groups joined / not, 16/8/128,
+// 64 sequences of 100 .. 600 own tokens, +-1 us): 4 groups of 16 28.8 / 30.6 us, one of
+// 64 28.7 / 30.8.  Groups of four gain from 256 tokens on (32 groups: 46.6 / 53.4; 128
+// tokens 46.2 / 47.1), of two from 512 to 1024 (32 groups: 512 tokens 41.7 / 42.2, 1024
+// 54.7 / 57.9, 8192 188 / 311); below, pairs lose up to 2 us, with few tokens of their
+// own 4 (100 pairs with up to 64: 128 tokens 41.4 / 32.8, 512 61.5 / 72.5).
 #include "decode_shared.h"
 
 #include <atomic>
@@ -973,7 +978,9 @@ __global__ void __maxnreg__(kPrefixRegs)
 // from the new rows, and the producer warp writes them to the cache.
 //
 // HBM-bound: alone it reads 1.09 GB in 162 us and 2.06 GB in 290 us (6.7 and
-// 7.1 TB/s), every byte once.  Four 32 KiB stages beside a prefix CTA's 99 KB
+// 7.1 TB/s), every byte once where a page has 64 / Hkv tokens or more; of smaller
+// pages (16 or 32 tokens with one kv head, 16 with two) a copy brings what lies behind
+// the page too, masked: two or four times the bytes.  Four 32 KiB stages beside a prefix CTA's 99 KB
 // (three: 2% slower).  The loads are marked evict-first: they are read once and
 // would push the prefixes out of L2 (own parts of 512 sequences 171 us without).
 

@@ -22,9 +22,10 @@ With ``shared_prefix`` a graph begins with ``attn_shared_plan`` over the step's
 block tables and its layers run ``attn_decode_shared_append``: sequences of the
 step that are neighbours and map their first blocks to the same physical ones
 (prefix-cache hits, forked sequences) have those blocks read once for all of
-them.  The outputs are the same up to the order of fp32 sums and, with one or two
-query heads per kv head, to weights within 2^-15 (two bf16 numbers); with four or
-eight both have their weights in bf16.
+them; the caller puts rows that share next to one another.  The outputs are the
+same up to the order of fp32 sums and, with one or two query heads per kv head,
+to weights within 2^-15 (two bf16 numbers); with four or eight both have their
+weights in bf16.
 """
 from __future__ import annotations
 
