@@ -538,7 +538,8 @@ struct PrefixLayout {
   static constexpr uint32_t kAlloc = kBar + P_BARS * 8 + 16;
 };
 constexpr int kMaxSub = kTileKeys / 16;    // pages of a step (the smallest page has 16 tokens)
-// Tensor memory: S of even steps | S of odd steps (P over each one's first half) | O.
+// Tensor memory: S of even steps | S of odd steps (P over each one's first half, what
+// bf16 leaves of it over the second) | O.
 constexpr uint32_t kColO = 2 * kTileKeys, kPrefixTmem = 256;
 
 // Steps of the next unit, of `left` in the segment: an even step and the one
