@@ -17,6 +17,11 @@
  *   kv_pages_fork, kv_pages_extend, kv_pages_compact
  *                        block tables, reference counts and pages handled on
  *                        the device: fork / reorder / free, grow, compact
+ *   attn_rope_freqs, attn_rope
+ *                        rotary positions of the step's query and key rows
+ *   kv_quant_store, kv_quant_store_rope, kv_quant_load, attn_decode_quant
+ *                        the paged cache in 8 bits with a scale for each block
+ *                        of tokens and kv head: written, read back, decoded over
  *
  * Sources: "nano-vLLM-1" (Senjl's Digital Garden), ModelRunner sections
  * "3. KV cache 分配", "4. prefill 输入打包", "5. deocde 输入打包" and BlockManager
@@ -600,6 +605,175 @@ int kv_pages_compact(kvp_bf16 *cache, int64_t num_planes, int64_t plane_stride, 
                      const int32_t *ref_counts, int32_t *out_tables, int32_t *out_ref_counts,
                      int32_t *places, void *workspace, size_t workspace_bytes,
                      kvp_stream_t stream);
+
+/*
+ * Rotary positions.  "Nano vLLM 解读（5）：解析 ModelRunner", prepare_prefill and
+ * prepare_decode (positions of the step's tokens, for the model's rotary
+ * embedding): the step before the attention calls.
+ *
+ * Pair i of a head's first rotary_dim numbers is turned by the angle
+ * position * w_i, w_i = base^(-2i / rotary_dim), stretched for contexts longer
+ * than those a model was trained on:
+ */
+enum {
+  KVP_ROPE_NONE = 0,
+  KVP_ROPE_LINEAR = 1,    /* w_i / factor */
+  KVP_ROPE_NTK = 2,       /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+  KVP_ROPE_YARN = 3,      /* w_i and w_i / factor, blended over the pairs: w_i up to the pair that turns `high`
+                           * times over original_len tokens (rounded down), w_i / factor from the one that turns
+                           * `low` times on (rounded up); cosines and sines times 0.1 ln(factor) + 1 */
+  KVP_ROPE_WAVELENGTH = 4 /* w_i and w_i / factor, blended over the pairs' turns t in original_len tokens: w_i
+                           * from t = high on, w_i / factor up to t = low, by (t - low) / (high - low) between */
+};
+
+/*
+ * attn_rope_freqs - the pairs' angles, computed on the host in 64 bits.
+ *   rotary_dim  even, 2 .. 1024
+ *   factor      >= 1; original_len >= 1 and 0 < low < high for the last two kinds
+ *   freqs       HOST array of rotary_dim / 2: pair i's angle per position, in
+ *               turns, as a fraction of 2^64.  The calls below take a device
+ *               copy of it.
+ *   magnitude   HOST: what cosines and sines are multiplied by
+ * Needs no GPU.  An angle of position p is off by p * 2^-53 of itself per turn
+ * at most, so positions up to 2^31 lose nothing that bf16 rows hold.
+ */
+int attn_rope_freqs(int rotary_dim, double base, int scaling, double factor, double original_len, double low,
+                    double high, uint64_t *freqs, float *magnitude);
+
+/*
+ * attn_rope - rotary positions of a step's query and key rows, in one launch.
+ *
+ * (x, y) of pair i become (x cos - y sin, y cos + x sin), where the pair is
+ * numbers i and i + rotary_dim / 2 of a head (interleaved == 0) or 2i and
+ * 2i + 1 (interleaved != 0).  Numbers from rotary_dim on are passed on.  fp32
+ * arithmetic, rounded once to bf16.
+ *
+ *   q, k        [num_tokens, num_heads or num_kv_heads, head_dim] bf16 (num_heads
+ *               or num_kv_heads 0: none, pointers unused)
+ *   positions   [num_tokens] int64, any value
+ *   freqs       [rotary_dim / 2] uint64, device
+ *   q_out,k_out the same shapes; either may be its input itself (in place, same
+ *               stride), otherwise outputs overlap no input
+ * Any head_dim up to 1024, stride and alignment; 16-byte accesses are used where
+ * rows are 16-byte aligned with strides and head_dim in multiples of 8 and
+ * rotary_dim is a multiple of 16 (8 if interleaved).
+ */
+int attn_rope(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k, int64_t k_stride_tok,
+              const int64_t *positions, int64_t num_tokens, const uint64_t *freqs, int rotary_dim, int interleaved,
+              float magnitude, int num_heads, int num_kv_heads, int head_dim, kvp_bf16 *q_out,
+              int64_t q_out_stride_tok, kvp_bf16 *k_out, int64_t k_out_stride_tok, kvp_stream_t stream);
+
+/*
+ * The cache in 8 bits.  One layer's cache is four arrays:
+ *   k_cache, v_cache    [num_blocks, block_size, num_kv_heads, head_dim] codes
+ *   k_scales, v_scales  [num_blocks, block_size / scale_tokens, num_kv_heads] fp32
+ * all contiguous and 16-byte aligned.  The number at (slot, head, e) is its
+ * code times the scale of the scale_tokens tokens around the slot and the head.
+ * Half the bytes of a bf16 cache (and 4 / (scale_tokens * head_dim) more for the
+ * scales); e4m3 keeps 4 significant bits of each number whatever its size, int8
+ * steps of 1/127 of a block's largest number to twice that.
+ *   scale_tokens  a power of two up to 256 that divides block_size
+ * Supported: head_dim in {64, 128}; a pool of fewer than 2^31 slots.
+ * A page is copied, moved or freed like one of a bf16 cache: kv_copy_blocks and
+ * the page calls take the code arrays as 16-bit numbers of half the head_dim;
+ * kv_copy_blocks takes the scale arrays likewise.
+ */
+enum {
+  KVP_E4M3 = 0, /* 8-bit floats: 4 exponent bits, 3 of mantissa, up to 448 */
+  KVP_INT8 = 1  /* whole numbers -127 .. 127 */
+};
+
+/*
+ * kv_quant_store - kv_store into an 8-bit cache.
+ *
+ * Rows of the call whose slots lie in one block of scale_tokens tokens and
+ * follow one another (slots s, s + 1, ...; the rows neighbours) are a run.  Its
+ * scale is the least power of two, 2^-64 or more, with which no number of the
+ * run exceeds the largest code; a run that does not begin its block (offset 0)
+ * takes the block's present scale where that is larger.  Where a block's scale
+ * grows, the codes of its other tokens are rounded anew at the new scale
+ * (a present scale that is not above 0 leaves them zero).  A run at offset 0
+ * begins the block: other tokens' codes stay as they are and mean nothing until
+ * they are stored.  Codes are rounded to nearest, ties to even.  Infinities and
+ * NaN do not count for the scale; infinities become the largest code, NaN is
+ * kept in e4m3 and becomes 0 in int8.
+ *
+ *   k, v            [num_tokens, num_kv_heads, head_dim] bf16, 16-byte aligned,
+ *                   row strides in multiples of 8 elements
+ *   slot_mapping    [num_tokens] int32; negative: writes nothing.  Slots must be
+ *                   distinct, and those of one block must form one run (a
+ *                   sequence's new tokens do): otherwise that block's contents
+ *                   are undefined.  A slot >= num_blocks * block_size is skipped
+ *                   and records KVP_ERR_DEVICE_DATA.
+ */
+int kv_quant_store(const kvp_bf16 *k, const kvp_bf16 *v, int64_t k_stride_tok, int64_t v_stride_tok,
+                   const int32_t *slot_mapping, int64_t num_tokens, void *k_cache, void *v_cache, float *k_scales,
+                   float *v_scales, int format, int64_t num_blocks, int block_size, int scale_tokens,
+                   int num_kv_heads, int head_dim, kvp_stream_t stream);
+
+/*
+ * kv_quant_store_rope - attn_rope of q and k, and kv_quant_store of the rotated
+ * k and of v, in one launch.  The rotated keys are quantised from fp32, without
+ * a rounding to bf16 between.  Arguments as in those calls; num_heads 0: no q.
+ * Rows with a negative slot have their q rotated too.
+ */
+int kv_quant_store_rope(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k, const kvp_bf16 *v,
+                        int64_t k_stride_tok, int64_t v_stride_tok, const int64_t *positions,
+                        const int32_t *slot_mapping, int64_t num_tokens, const uint64_t *freqs, int rotary_dim,
+                        int interleaved, float magnitude, int num_heads, kvp_bf16 *q_out,
+                        int64_t q_out_stride_tok, void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                        int format, int64_t num_blocks, int block_size, int scale_tokens, int num_kv_heads,
+                        int head_dim, kvp_stream_t stream);
+
+/*
+ * kv_quant_load - sequences of an 8-bit cache as bf16 rows.
+ *
+ * Token p < context_lens[b] of sequence b, found through block_tables as in
+ * attn_decode_paged, becomes row starts[b] + p of k and v: code times scale,
+ * rounded once.  Rows that no token goes to stay as they are.  With starts in
+ * multiples of 16 the rows are pages of a bf16 cache with block_size 16, which
+ * attn_prefill_varlen reads through a block table (page starts[b] / 16 + i is
+ * entry i of row b): the prefill of a prefix hit over an 8-bit cache.
+ *
+ *   starts            [num_seqs] int32
+ *   max_context_len   upper bound of context_lens (work is sized by it; a longer
+ *                     sequence is read all the same)
+ *   num_rows          rows of k and v: a token whose row is not in 0 ..
+ *                     num_rows - 1 is skipped and records KVP_ERR_DEVICE_DATA, as
+ *                     are tokens of a page id outside the pool
+ *   k, v              [num_rows, num_kv_heads, head_dim] bf16, 16-byte aligned,
+ *                     row strides in multiples of 8 elements
+ * At most 65535 sequences.
+ */
+int kv_quant_load(const void *k_cache, const void *v_cache, const float *k_scales, const float *v_scales,
+                  int format, int64_t num_blocks, int block_size, int scale_tokens, const int32_t *block_tables,
+                  int max_blocks_per_seq, const int32_t *context_lens, const int32_t *starts, int num_seqs,
+                  int max_context_len, int num_kv_heads, int head_dim, int64_t num_rows, kvp_bf16 *k,
+                  int64_t k_stride_tok, kvp_bf16 *v, int64_t v_stride_tok, kvp_stream_t stream);
+
+/* Bytes of device workspace attn_decode_quant needs for this shape on the
+ * current device (0 on error; see kvp_last_error). */
+size_t attn_decode_quant_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                        int max_context_len);
+
+/*
+ * attn_decode_quant - attn_decode_paged over an 8-bit cache:
+ *     out[b, h] = sum_{p < context_lens[b]} softmax_p(q[b, h] . k_p * scale) v_p
+ * with k_p, v_p the codes times their scales.
+ *
+ * Arguments as attn_decode_paged, with the cache's arrays and a workspace of
+ * attn_decode_quant_workspace_size() bytes.  Scales of tokens within a context
+ * are finite and not negative (kv_quant_store's are); codes and scales beyond a
+ * context may be anything.
+ * Supported: num_kv_heads in {1, 2, 4, 8}; num_heads / num_kv_heads in
+ * {1, 2, 4, 8}.
+ */
+int attn_decode_quant(const kvp_bf16 *q, int64_t q_stride_tok, const void *k_cache, const void *v_cache,
+                      const float *k_scales, const float *v_scales, int format, int64_t num_blocks, int block_size,
+                      int scale_tokens, const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens, int num_seqs, int max_context_len, int num_heads,
+                      int num_kv_heads, int head_dim, float softmax_scale, void *workspace, size_t workspace_bytes,
+                      kvp_bf16 *out, int64_t out_stride_tok, kvp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,8 @@ PyTorch fallback: if the library cannot be loaded, every call raises.
     attn_decode_paged(q, k_cache, v_cache, block_tables, context_lens, max_context_len, ...)
     attn_shared_plan(block_tables, context_lens, ...) + attn_decode_shared(q, ..., plan)
     kv_pages_fork / kv_pages_extend / kv_pages_compact(..., block_tables, context_lens, ref_counts, ...)
+    attn_rope_freqs(rotary_dim, ...) + attn_rope(q, k, positions, freqs, magnitude, interleaved)
+    kv_quant_store / kv_quant_store_rope / kv_quant_load / attn_decode_quant(..., k_cache, v_cache, k_scales, v_scales, ...)
 """
 from __future__ import annotations
 
@@ -31,6 +33,8 @@ __all__ = ["kv_store", "kv_copy_blocks", "attn_prefill_varlen", "attn_prefill_va
            "attn_shared_plan", "attn_shared_plan_size", "attn_decode_shared",
            "attn_decode_shared_append", "attn_decode_shared_workspace_size",
            "kv_pages_fork", "kv_pages_extend", "kv_pages_compact", "kv_pages_workspace_size",
+           "attn_rope_freqs", "attn_rope", "kv_quant_store", "kv_quant_store_rope", "kv_quant_load",
+           "attn_decode_quant", "attn_decode_quant_workspace_size",
            "device_status", "selftest_wait", "library", "library_path", "KvpError"]
 
 _LIB_LOCK = threading.Lock()
@@ -42,6 +46,7 @@ ERROR_NAMES = {-1: "KVP_ERR_INVALID_ARG", -2: "KVP_ERR_UNSUPPORTED", -3: "KVP_ER
 
 # Every symbol include/kvpaged.h declares, with its ctypes signature.
 _P, _I64, _I32, _F32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_F64 = ctypes.c_double
 SIGNATURES = {
     "kvp_last_error": (ctypes.c_char_p, []),
     "kvp_version": (_I32, []),
@@ -79,6 +84,18 @@ SIGNATURES = {
                                _P]),
     "kv_pages_compact": (_I32, [_P, _I64, _I64, _I64, _I32, _I64, _P, _I32, _P, _I32, _P, _P, _P, _P,
                                 _P, _SZ, _P]),
+    "attn_rope_freqs": (_I32, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P, _P]),
+    "attn_rope": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _F32, _I32, _I32, _I32, _P, _I64, _P,
+                         _I64, _P]),
+    "kv_quant_store": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32,
+                              _P]),
+    "kv_quant_store_rope": (_I32, [_P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _I32, _F32, _I32, _P,
+                                   _I64, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P]),
+    "kv_quant_load": (_I32, [_P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                             _I64, _P, _I64, _P, _I64, _P]),
+    "attn_decode_quant_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "attn_decode_quant": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _I32, _P, _I32, _I32, _I32,
+                                 _I32, _I32, _F32, _P, _SZ, _P, _I64, _P]),
 }
 
 
@@ -748,4 +765,225 @@ def kv_pages_compact(kv_cache, block_tables, context_lens, ref_counts, workspace
     _call(dev.index, library().kv_pages_compact, kv_cache.data_ptr(), planes, stride, nb, bs, row,
           block_tables.data_ptr(), mb, context_lens.data_ptr(), n, ref_counts.data_ptr(),
           out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+# ----------------------------------------------- rotary positions, the 8-bit cache
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+_ROPE_TURNS = {"yarn": (1.0, 32.0), "wavelength": (1.0, 4.0)}
+
+
+def attn_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                    original_len: float = 0, low: float | None = None, high: float | None = None, device="cuda"):
+    """The angles per position of a model's rotary pairs, for attn_rope and
+    kv_quant_store_rope: ``(freqs, magnitude)``, an int64 tensor of
+    rotary_dim / 2 on ``device`` and a number.  ``scaling`` stretches them
+    for contexts longer than ``original_len`` by ``factor`` ("linear", "ntk",
+    "yarn", "wavelength"; see include/kvpaged.h); ``low`` / ``high`` are the
+    turns over original_len between which the last two blend (by default 1
+    and 32, 1 and 4)."""
+    import torch
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_ROPE_SCALINGS)}, got {scaling!r}")
+    turns = _ROPE_TURNS.get(scaling, (0.0, 0.0))
+    low, high = (turns[0] if low is None else low), (turns[1] if high is None else high)
+    freqs = (ctypes.c_uint64 * max(1, int(rotary_dim) // 2))()
+    magnitude = ctypes.c_float()
+    _check(library().attn_rope_freqs(int(rotary_dim), float(base), _ROPE_SCALINGS[scaling], float(factor),
+                                     float(original_len), float(low), float(high), freqs,
+                                     ctypes.byref(magnitude)))
+    return torch.tensor(list(freqs), dtype=torch.int64, device=device), magnitude.value
+
+
+def _rows_of(t, name, n, dev):
+    """bf16 rows [n, heads, head_dim], heads and head_dim contiguous -> row stride."""
+    import torch
+    _require(t, name, torch.bfloat16, 3, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} rows, got shape {tuple(t.shape)}")
+    return _rows(t, name, t.shape[1], t.shape[2])
+
+
+def _rope_tensors(positions, freqs, n, dev):
+    import torch
+    for t, name in ((positions, "positions"), (freqs, "freqs")):
+        _require(t, name, torch.int64, 1, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if positions.shape[0] != n:
+        raise ValueError("positions must have one entry per row")
+
+
+def attn_rope(q, k, positions, freqs, magnitude: float = 1.0, interleaved: bool = False, out=None):
+    """Rotary positions of a step's query and key rows (see include/kvpaged.h).
+    ``freqs`` and ``magnitude`` are attn_rope_freqs's; ``k`` may be None.
+    Returns (q, k): new tensors, or ``out``, two tensors, which may be q and
+    k themselves."""
+    done = (_CALLS or _calls()).attn_rope(q, k, positions, freqs, magnitude, interleaved, out)
+    if done is not None:
+        return done
+    import torch
+    _require(q, "q", torch.bfloat16, 3)
+    dev, (n, hq, d) = q.device, q.shape
+    qs = _rows_of(q, "q", n, dev)
+    hkv, ks = 0, 0
+    if k is not None:
+        ks = _rows_of(k, "k", n, dev)
+        hkv = k.shape[1]
+        if k.shape[2] != d:
+            raise ValueError("head_dim of q and k differ")
+    _rope_tensors(positions, freqs, n, dev)
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=dev),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev))
+    q_out, k_out = out
+    qos = _rows_of(q_out, "out q", n, dev)
+    if q_out.shape != q.shape:
+        raise ValueError("out q must have q's shape")
+    kos = 0
+    if k is not None:
+        kos = _rows_of(k_out, "out k", n, dev)
+        if k_out.shape != k.shape:
+            raise ValueError("out k must have k's shape")
+    _call(dev.index, library().attn_rope, q.data_ptr(), qs, None if k is None else k.data_ptr(), ks,
+          positions.data_ptr(), n, freqs.data_ptr(), 2 * freqs.shape[0], int(interleaved), float(magnitude), hq, hkv,
+          d, q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos)
+    return q_out, (None if k is None else k_out)
+
+
+def _quant_cache(k_cache, v_cache, k_scales, v_scales):
+    """The arrays of an 8-bit cache -> device, shape, format, scale_tokens."""
+    import torch
+    formats = {torch.float8_e4m3fn: 0, torch.int8: 1}
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    if k_cache.dtype not in formats:
+        raise TypeError(f"k_cache must be float8_e4m3fn or int8, got {k_cache.dtype}")
+    _require(k_cache, "k_cache", k_cache.dtype, 4)
+    dev = k_cache.device
+    _require(v_cache, "v_cache", k_cache.dtype, 4, dev)
+    if k_cache.shape != v_cache.shape or not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("k_cache / v_cache must be contiguous [num_blocks, block_size, kv_heads, head_dim]")
+    nb, bs, hkv, d = k_cache.shape
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _require(t, name, torch.float32, 3, dev)
+        if t.shape != k_scales.shape or t.shape[0] != nb or t.shape[2] != hkv or not t.is_contiguous() or \
+                t.shape[1] == 0 or bs % t.shape[1]:
+            raise ValueError(f"{name} must be contiguous [num_blocks, block_size / scale_tokens, kv_heads], got "
+                             f"{tuple(t.shape)}")
+    return dev, (nb, bs, hkv, d), formats[k_cache.dtype], bs // k_scales.shape[1]
+
+
+def _pointers(*tensors):
+    return tuple(t.data_ptr() for t in tensors)
+
+
+def kv_quant_store(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales) -> None:
+    """kv_store into an 8-bit cache (float8_e4m3fn or int8 codes, and for each
+    block of tokens and kv head an fp32 scale; see include/kvpaged.h)."""
+    if (_CALLS or _calls()).kv_quant_store(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales) is not None:
+        return
+    dev, (nb, bs, hkv, d), form, tokens = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _int32(slot_mapping, "slot_mapping", (None,), dev)
+    n = slot_mapping.shape[0]
+    new = (n, hkv, d)
+    ks, vs = _heads_rows(k, "k", new, dev), _heads_rows(v, "v", new, dev)
+    _call(dev.index, library().kv_quant_store, k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), n,
+          *_pointers(k_cache, v_cache, k_scales, v_scales), form, nb, bs, tokens, hkv, d)
+
+
+def kv_quant_store_rope(q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, k_scales, v_scales,
+                        magnitude: float = 1.0, interleaved: bool = False, out=None):
+    """attn_rope of q and k and kv_quant_store of the rotated k and of v, in
+    one launch.  Returns the rotated q: a new tensor, or ``out``, which may be
+    q itself."""
+    done = (_CALLS or _calls()).kv_quant_store_rope(q, k, v, positions, slot_mapping, freqs, k_cache, v_cache,
+                                                    k_scales, v_scales, magnitude, interleaved, out)
+    if done is not None:
+        return done
+    import torch
+    dev, (nb, bs, hkv, d), form, tokens = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _int32(slot_mapping, "slot_mapping", (None,), dev)
+    n = slot_mapping.shape[0]
+    new = (n, hkv, d)
+    ks, vs = _heads_rows(k, "k", new, dev), _heads_rows(v, "v", new, dev)
+    qs = _rows_of(q, "q", n, dev)
+    hq = q.shape[1]
+    if q.shape[2] != d:
+        raise ValueError("head_dim of q and caches differ")
+    _rope_tensors(positions, freqs, n, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    os_ = _rows_of(out, "out", n, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _call(dev.index, library().kv_quant_store_rope, q.data_ptr(), qs, k.data_ptr(), v.data_ptr(), ks, vs,
+          positions.data_ptr(), slot_mapping.data_ptr(), n, freqs.data_ptr(), 2 * freqs.shape[0], int(interleaved),
+          float(magnitude), hq, out.data_ptr(), os_, *_pointers(k_cache, v_cache, k_scales, v_scales), form, nb, bs,
+          tokens, hkv, d)
+    return out
+
+
+def kv_quant_load(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, starts, max_context_len: int,
+                  num_rows: int | None = None, out=None):
+    """Sequences of an 8-bit cache as bf16 rows (see include/kvpaged.h): token
+    p of sequence b becomes row starts[b] + p.  Returns (k, v): new tensors of
+    ``num_rows`` rows (rows that no token goes to are not written), or ``out``,
+    two tensors."""
+    done = (_CALLS or _calls()).kv_quant_load(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                              starts, max_context_len, num_rows, out)
+    if done is not None:
+        return done
+    import torch
+    dev, (nb, bs, hkv, d), form, tokens = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _int32(block_tables, "block_tables", (None, None), dev)
+    b, width = block_tables.shape
+    _int32(context_lens, "context_lens", (b,), dev)
+    _int32(starts, "starts", (b,), dev)
+    if out is None:
+        if num_rows is None:
+            raise ValueError("num_rows or out must be given")
+        out = tuple(torch.empty((num_rows, hkv, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    k, v = out
+    rows = k.shape[0] if num_rows is None else num_rows
+    ks, vs = (_heads_rows(t, name, (rows, hkv, d), dev) for t, name in ((k, "out k"), (v, "out v")))
+    _call(dev.index, library().kv_quant_load, *_pointers(k_cache, v_cache, k_scales, v_scales), form, nb, bs, tokens,
+          block_tables.data_ptr(), width, context_lens.data_ptr(), starts.data_ptr(), b, int(max_context_len), hkv, d,
+          rows, k.data_ptr(), ks, v.data_ptr(), vs)
+    return k, v
+
+
+def attn_decode_quant_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_context_len: int, device=None) -> int:
+    return _sized("attn_decode_quant_workspace_size", device, num_seqs, num_heads, num_kv_heads, head_dim,
+                  max_context_len)
+
+
+def attn_decode_quant(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len: int,
+                      softmax_scale: float | None = None, workspace=None, out=None):
+    """attn_decode_paged over an 8-bit cache (see include/kvpaged.h)."""
+    done = (_CALLS or _calls()).attn_decode_quant(q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                                                  context_lens, max_context_len, softmax_scale, workspace, out)
+    if done is not None:
+        return done
+    import torch
+    dev, (nb, bs, hkv, d), form, tokens = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _require(q, "q", torch.bfloat16, 3, dev)
+    b, hq, _ = q.shape
+    if q.shape[2] != d:
+        raise ValueError("head_dim of q and caches differ")
+    qs = _heads_rows(q, "q", q.shape, dev)
+    _int32(block_tables, "block_tables", (b, None), dev)
+    _int32(context_lens, "context_lens", (b,), dev)
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=dev)
+    os_ = _heads_rows(out, "out", q.shape, dev)
+    workspace = _scratch(workspace, "workspace",
+                         lambda: attn_decode_quant_workspace_size(b, hq, hkv, d, int(max_context_len), dev), dev)
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _call(dev.index, library().attn_decode_quant, q.data_ptr(), qs,
+          *_pointers(k_cache, v_cache, k_scales, v_scales), form, nb, bs, tokens, block_tables.data_ptr(),
+          block_tables.shape[1], context_lens.data_ptr(), b, int(max_context_len), hq, hkv, d, scale,
+          workspace.data_ptr(), workspace.numel(), out.data_ptr(), os_)
     return out

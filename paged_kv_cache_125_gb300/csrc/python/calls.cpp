@@ -1,5 +1,6 @@
 // The Python binding's quick way into the calls that run once per layer or
-// step beside kernels of a few microseconds (shared decode, page operators).
+// step beside kernels of a few microseconds (shared decode, page operators,
+// rotary positions, the 8-bit cache).
 //
 // Each function takes the arguments of the Python function of the same name,
 // all by position.  When every tensor is of the kind that the call takes it
@@ -394,6 +395,281 @@ PyObject* pages_compact(PyObject*, PyObject* const* o, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------- rotary positions, the 8-bit cache
+
+// The arrays of an 8-bit cache, from argument i on: k_cache, v_cache, k_scales, v_scales.
+struct QuantPool {
+  const at::Tensor *k = nullptr, *v = nullptr, *ks = nullptr, *vs = nullptr;
+  int64_t blocks = 0, block_size = 0, heads = 0, d = 0, tokens = 0;
+  int format = 0;
+};
+QuantPool quant_pool(Args& a, int i) {
+  QuantPool p;
+  if (!a.ok || !THPVariable_Check(a.o[i])) {
+    a.fail();
+    return p;
+  }
+  const at::ScalarType type = THPVariable_Unpack(a.o[i]).scalar_type();
+  if (type != at::kFloat8_e4m3fn && type != at::kChar) {
+    a.fail();
+    return p;
+  }
+  p.format = type == at::kChar ? KVP_INT8 : KVP_E4M3;
+  p.k = a.dense(i, type, {-1, -1, -1, -1});
+  if (!p.k) return p;
+  p.blocks = p.k->size(0), p.block_size = p.k->size(1), p.heads = p.k->size(2), p.d = p.k->size(3);
+  p.v = a.dense(i + 1, type, {p.blocks, p.block_size, p.heads, p.d});
+  p.ks = a.dense(i + 2, at::kFloat, {p.blocks, -1, p.heads});
+  if (!p.ks || p.ks->size(1) == 0 || p.block_size % p.ks->size(1)) {
+    a.fail();
+    return p;
+  }
+  p.vs = a.dense(i + 3, at::kFloat, {p.blocks, p.ks->size(1), p.heads});
+  p.tokens = p.block_size / p.ks->size(1);
+  if (!fits_int(p.block_size) || !fits_int(p.heads) || !fits_int(p.d)) a.fail();
+  return p;
+}
+
+// bf16 rows [n, any heads, d]
+const at::Tensor* any_rows(Args& a, int i, int64_t n, int64_t d) {
+  const at::Tensor* t = a.tensor(i, at::kBFloat16);
+  if (!t || t->dim() != 3 || (n >= 0 && t->size(0) != n) || (d >= 0 && t->size(2) != d) || t->stride(2) != 1 ||
+      t->stride(1) != t->size(2) || !fits_int(t->size(1)) || !fits_int(t->size(2)))
+    return a.fail();
+  return t;
+}
+
+double number(Args& a, int i) {
+  if (a.ok && PyFloat_Check(a.o[i])) return PyFloat_AS_DOUBLE(a.o[i]);
+  a.ok = false;
+  return 0;
+}
+int truth(Args& a, int i) {
+  if (a.o[i] != Py_True && a.o[i] != Py_False) a.ok = false;
+  return a.o[i] == Py_True;
+}
+
+const uint64_t* turns(const at::Tensor& t) { return at_<uint64_t>(t); }
+
+// q, k (or None), positions, freqs, magnitude, interleaved, out (None or two tensors)
+PyObject* rope(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc(n, 7)) return nullptr;
+  Args a{o};
+  const at::Tensor* q = any_rows(a, 0, -1, -1);
+  if (!q) Py_RETURN_NONE;
+  const int64_t rows = q->size(0), hq = q->size(1), d = q->size(2);
+  const bool with_k = o[1] != Py_None;
+  const at::Tensor* k = with_k ? any_rows(a, 1, rows, d) : nullptr;
+  const at::Tensor* pos = a.dense(2, at::kLong, {rows});
+  const at::Tensor* freqs = a.dense(3, at::kLong, {-1});
+  const double magnitude = number(a, 4);
+  const int interleaved = truth(a, 5);
+  if (!a.ok || freqs->size(0) > 512) Py_RETURN_NONE;
+  const int64_t hkv = with_k ? k->size(1) : 0;
+  at::Tensor qo, ko;
+  if (o[6] != Py_None) {
+    if (!PyTuple_CheckExact(o[6]) || PyTuple_GET_SIZE(o[6]) != 2) Py_RETURN_NONE;
+    Args b{PySequence_Fast_ITEMS(o[6]), a.idx};
+    const at::Tensor* x = b.rows(0, rows, hq, d);
+    const at::Tensor* y = with_k ? b.rows(1, rows, hkv, d) : nullptr;
+    if (!b.ok) Py_RETURN_NONE;
+    qo = *x;
+    if (with_k) ko = *y;
+  }
+  c10::cuda::CUDAGuard guard((c10::DeviceIndex)a.idx);
+  if (!qo.defined()) {
+    qo = fresh({rows, hq, d}, at::kBFloat16, a.idx);
+    if (with_k) ko = fresh({rows, hkv, d}, at::kBFloat16, a.idx);
+  }
+  const int rc = unlocked([&] {
+    return attn_rope(halves(*q), q->stride(0), with_k ? halves(*k) : nullptr, with_k ? k->stride(0) : 0,
+                     at_<int64_t>(*pos), rows, turns(*freqs), 2 * (int)freqs->size(0), interleaved, (float)magnitude,
+                     (int)hq, (int)hkv, (int)d, halves(qo), qo.stride(0), with_k ? halves(ko) : nullptr,
+                     with_k ? ko.stride(0) : 0, stream_of(a.idx));
+  });
+  if (rc) return failed(rc);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyObject* x = THPVariable_Wrap(qo);
+  PyObject* y = with_k ? THPVariable_Wrap(ko) : given(Py_None);
+  if (!x || !y) {
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_DECREF(r);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(r, 0, x);
+  PyTuple_SET_ITEM(r, 1, y);
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales -> True
+PyObject* quant_store(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc(n, 7)) return nullptr;
+  Args a{o};
+  const QuantPool p = quant_pool(a, 3);
+  if (!a.ok) Py_RETURN_NONE;
+  const at::Tensor* slots = a.dense(2, at::kInt, {-1});
+  if (!slots) Py_RETURN_NONE;
+  const int64_t rows = slots->size(0);
+  const at::Tensor* k = a.rows(0, rows, p.heads, p.d);
+  const at::Tensor* v = a.rows(1, rows, p.heads, p.d);
+  if (!a.ok) Py_RETURN_NONE;
+  c10::cuda::CUDAGuard guard((c10::DeviceIndex)a.idx);
+  const int rc = unlocked([&] {
+    return kv_quant_store(halves(*k), halves(*v), k->stride(0), v->stride(0), ints(*slots), rows, p.k->data_ptr(),
+                          p.v->data_ptr(), at_<float>(*p.ks), at_<float>(*p.vs), p.format, p.blocks,
+                          (int)p.block_size, (int)p.tokens, (int)p.heads, (int)p.d, stream_of(a.idx));
+  });
+  if (rc) return failed(rc);
+  Py_RETURN_TRUE;
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, k_scales, v_scales,
+// magnitude, interleaved, out
+PyObject* quant_store_rope(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc(n, 13)) return nullptr;
+  Args a{o};
+  const QuantPool p = quant_pool(a, 6);
+  if (!a.ok) Py_RETURN_NONE;
+  const at::Tensor* slots = a.dense(4, at::kInt, {-1});
+  if (!slots) Py_RETURN_NONE;
+  const int64_t rows = slots->size(0);
+  const at::Tensor* q = any_rows(a, 0, rows, p.d);
+  const at::Tensor* k = a.rows(1, rows, p.heads, p.d);
+  const at::Tensor* v = a.rows(2, rows, p.heads, p.d);
+  const at::Tensor* pos = a.dense(3, at::kLong, {rows});
+  const at::Tensor* freqs = a.dense(5, at::kLong, {-1});
+  const double magnitude = number(a, 10);
+  const int interleaved = truth(a, 11);
+  if (!a.ok || freqs->size(0) > 512) Py_RETURN_NONE;
+  const int64_t hq = q->size(1);
+  const at::Tensor* out = o[12] == Py_None ? nullptr : a.rows(12, rows, hq, p.d);
+  if (!a.ok) Py_RETURN_NONE;
+  c10::cuda::CUDAGuard guard((c10::DeviceIndex)a.idx);
+  at::Tensor made;
+  if (!out) {
+    made = fresh({rows, hq, p.d}, at::kBFloat16, a.idx);
+    out = &made;
+  }
+  const int rc = unlocked([&] {
+    return kv_quant_store_rope(halves(*q), q->stride(0), halves(*k), halves(*v), k->stride(0), v->stride(0),
+                               at_<int64_t>(*pos), ints(*slots), rows, turns(*freqs), 2 * (int)freqs->size(0),
+                               interleaved, (float)magnitude, (int)hq, halves(*out), out->stride(0),
+                               p.k->data_ptr(), p.v->data_ptr(), at_<float>(*p.ks), at_<float>(*p.vs), p.format,
+                               p.blocks, (int)p.block_size, (int)p.tokens, (int)p.heads, (int)p.d,
+                               stream_of(a.idx));
+  });
+  if (rc) return failed(rc);
+  return made.defined() ? THPVariable_Wrap(made) : given(o[12]);
+  END_HANDLE_TH_ERRORS
+}
+
+// k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, starts,
+// max_context_len, num_rows, out (None or two tensors)
+PyObject* quant_load(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc(n, 10)) return nullptr;
+  Args a{o};
+  const QuantPool p = quant_pool(a, 0);
+  const at::Tensor* bt = a.dense(4, at::kInt, {-1, -1});
+  if (!a.ok || !fits_int(bt->size(0)) || !fits_int(bt->size(1))) Py_RETURN_NONE;
+  const int64_t b = bt->size(0);
+  const at::Tensor* ctx = a.dense(5, at::kInt, {b});
+  const at::Tensor* starts = a.dense(6, at::kInt, {b});
+  const int longest = a.small(7);
+  int64_t rows = o[8] == Py_None ? -1 : a.integer(8, 0, LLONG_MAX);
+  if (!a.ok) Py_RETURN_NONE;
+  at::Tensor k, v;
+  const bool theirs = o[9] != Py_None;
+  if (theirs) {
+    if (!PyTuple_CheckExact(o[9]) || PyTuple_GET_SIZE(o[9]) != 2) Py_RETURN_NONE;
+    Args c{PySequence_Fast_ITEMS(o[9]), a.idx};
+    const at::Tensor* x = c.tensor(0, at::kBFloat16);
+    if (!x || x->dim() != 3) Py_RETURN_NONE;
+    if (rows < 0) rows = x->size(0);
+    x = c.rows(0, rows, p.heads, p.d);
+    const at::Tensor* y = c.rows(1, rows, p.heads, p.d);
+    if (!c.ok) Py_RETURN_NONE;
+    k = *x, v = *y;
+  } else if (rows < 0) {
+    Py_RETURN_NONE;
+  }
+  c10::cuda::CUDAGuard guard((c10::DeviceIndex)a.idx);
+  if (!theirs) {
+    k = fresh({rows, p.heads, p.d}, at::kBFloat16, a.idx);
+    v = fresh({rows, p.heads, p.d}, at::kBFloat16, a.idx);
+  }
+  const int rc = unlocked([&] {
+    return kv_quant_load(p.k->data_ptr(), p.v->data_ptr(), at_<float>(*p.ks), at_<float>(*p.vs), p.format, p.blocks,
+                         (int)p.block_size, (int)p.tokens, ints(*bt), (int)bt->size(1), ints(*ctx), ints(*starts),
+                         (int)b, longest, (int)p.heads, (int)p.d, rows, halves(k), k.stride(0), halves(v),
+                         v.stride(0), stream_of(a.idx));
+  });
+  if (rc) return failed(rc);
+  if (theirs) return given(o[9]);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyObject *x = THPVariable_Wrap(k), *y = THPVariable_Wrap(v);
+  if (!x || !y) {
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_DECREF(r);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(r, 0, x);
+  PyTuple_SET_ITEM(r, 1, y);
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len,
+// softmax_scale, workspace, out
+PyObject* decode_quant(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc(n, 11)) return nullptr;
+  Args a{o};
+  const QuantPool p = quant_pool(a, 1);
+  if (!a.ok) Py_RETURN_NONE;
+  const at::Tensor* q = any_rows(a, 0, -1, p.d);
+  if (!q || !fits_int(q->size(0))) Py_RETURN_NONE;
+  const int64_t b = q->size(0), hq = q->size(1);
+  const at::Tensor* bt = a.dense(5, at::kInt, {b, -1});
+  const at::Tensor* ctx = a.dense(6, at::kInt, {b});
+  const int longest = a.small(7);
+  const double scale = o[8] == Py_None ? 1.0 / std::sqrt((double)p.d) : number(a, 8);
+  const at::Tensor* ws = a.scratch(9);
+  const at::Tensor* out = o[10] == Py_None ? nullptr : a.rows(10, b, hq, p.d);
+  if (!a.ok || !fits_int(bt->size(1))) Py_RETURN_NONE;
+  c10::cuda::CUDAGuard guard((c10::DeviceIndex)a.idx);
+  at::Tensor made_ws, made;
+  if (!ws) {
+    const size_t bytes = attn_decode_quant_workspace_size((int)b, (int)hq, (int)p.heads, (int)p.d, longest);
+    if (!bytes) return failed(KVP_ERR_INVALID_ARG);
+    made_ws = fresh({(int64_t)bytes}, at::kByte, a.idx);
+    ws = &made_ws;
+  }
+  if (!out) {
+    made = fresh({b, hq, p.d}, at::kBFloat16, a.idx);
+    out = &made;
+  }
+  const int rc = unlocked([&] {
+    return attn_decode_quant(halves(*q), q->stride(0), p.k->data_ptr(), p.v->data_ptr(), at_<float>(*p.ks),
+                             at_<float>(*p.vs), p.format, p.blocks, (int)p.block_size, (int)p.tokens, ints(*bt),
+                             (int)bt->size(1), ints(*ctx), (int)b, longest, (int)hq, (int)p.heads, (int)p.d,
+                             (float)scale, ws->data_ptr(), (size_t)ws->numel(), halves(*out), out->stride(0),
+                             stream_of(a.idx));
+  });
+  if (rc) return failed(rc);
+  return made.defined() ? THPVariable_Wrap(made) : given(o[10]);
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* set_check(PyObject*, PyObject* check) {
   Py_INCREF(check);
   Py_XSETREF(g_check, check);
@@ -411,6 +687,11 @@ PyMethodDef kMethods[] = {
     {"kv_pages_fork", fast(pages_fork), METH_FASTCALL, nullptr},
     {"kv_pages_extend", fast(pages_extend), METH_FASTCALL, nullptr},
     {"kv_pages_compact", fast(pages_compact), METH_FASTCALL, nullptr},
+    {"attn_rope", fast(rope), METH_FASTCALL, nullptr},
+    {"kv_quant_store", fast(quant_store), METH_FASTCALL, nullptr},
+    {"kv_quant_store_rope", fast(quant_store_rope), METH_FASTCALL, nullptr},
+    {"kv_quant_load", fast(quant_load), METH_FASTCALL, nullptr},
+    {"attn_decode_quant", fast(decode_quant), METH_FASTCALL, nullptr},
     {"set_check", set_check, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

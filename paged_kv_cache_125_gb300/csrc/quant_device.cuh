@@ -1,0 +1,112 @@
+// Device code shared by the kernels of the 8-bit cache: codes, scales, and
+// rotary angles.
+#pragma once
+
+#include "kvp_device.cuh"
+#include "quant.h"
+
+namespace kvp {
+
+constexpr float kLeastScale = 5.421010862427522e-20f;  // 2^-64
+
+// The largest code is 448 = 1.75 * 2^8 (e4m3) or 127 = 1.984375 * 2^6 (int8).
+template <int kFormat>
+__device__ __forceinline__ float largest_code() {
+  return kFormat == KVP_E4M3 ? 448.f : 127.f;
+}
+
+// The least power of two p with top <= p * (the largest code), and at least
+// 2^-64: exponent arithmetic, so exact.  Powers of two cost e4m3 nothing (its
+// precision is relative) and int8 at most one bit; in exchange a code is the
+// number's own rounding with no division's before it, and a block whose scale
+// grows keeps what its codes hold, up to one rounding of the new, larger step.
+template <int kFormat>
+__device__ __forceinline__ float scale_for(float top) {
+  const uint32_t bits = __float_as_uint(top);
+  const uint32_t part = bits & 0x7fffffu;
+  int e = (int)(bits >> 23) - 127;
+  e += kFormat == KVP_E4M3 ? (part > 0x600000u) - 8 : (part > 0x7e0000u) - 6;
+  return e <= -64 ? kLeastScale : __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two numbers, already divided by their scale, as two codes (ties to even,
+// infinities to the largest code, NaN to NaN in e4m3 and to 0 in int8).
+template <int kFormat>
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  if constexpr (kFormat == KVP_E4M3) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  } else {
+    int a, b;
+    asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(a) : "f"(lo));
+    asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(b) : "f"(hi));
+    a = a < -127 ? -127 : a;  // -infinity saturates to -128
+    b = b < -127 ? -127 : b;
+    return (uint32_t)(a & 0xff) | (uint32_t)(b & 0xff) << 8;
+  }
+}
+
+template <int kFormat>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  uint2 r;
+  r.x = encode2<kFormat>(x[0] * inv, x[1] * inv) | encode2<kFormat>(x[2] * inv, x[3] * inv) << 16;
+  r.y = encode2<kFormat>(x[4] * inv, x[5] * inv) | encode2<kFormat>(x[6] * inv, x[7] * inv) << 16;
+  return r;
+}
+
+// The two codes in the low half of w as two fp16 numbers (exact: e4m3 is a
+// subset of fp16, and so are -127 .. 127).
+template <int kFormat>
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
+  uint32_t r;
+  if constexpr (kFormat == KVP_E4M3) {
+    asm("{\n\t.reg .b16 x;\n\tmov.b32 {x, _}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(w));
+  } else {
+    // 1024 + (code + 128) has the biased code in its low bits
+    uint32_t biased;
+    asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(biased) : "r"(w ^ 0x8080u), "r"(0x64646464u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x64806480u));  // 1152
+  }
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
+  float2 r;
+  asm("{\n\t.reg .f16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
+}
+
+template <int kFormat>
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+  return f16x2_floats(codes_f16x2<kFormat>(w));
+}
+
+// Cosine and sine of position * freq.  The angle is held in turns as a 64-bit
+// fixed-point fraction, in which the product with a 64-bit position wraps as
+// the angle does: far positions lose nothing.  Its upper 32 bits, signed, give
+// an angle in [-pi, pi), where the fast functions are off by at most 2^-21:
+// 2^-12 of the step that the rotated numbers are rounded to.
+__device__ __forceinline__ float2 rope_turn(int64_t position, uint64_t freq, float magnitude) {
+  const int32_t half_turns = (int32_t)(uint32_t)(((uint64_t)position * freq) >> 32);
+  const float angle = (float)half_turns * 1.4629180792671596e-9f;  // pi * 2^-31
+  return make_float2(__cosf(angle) * magnitude, __sinf(angle) * magnitude);
+}
+
+__device__ __forceinline__ void bf16_floats(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16lo(w[i]);
+    x[2 * i + 1] = bf16hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 floats_bf16(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+}  // namespace kvp

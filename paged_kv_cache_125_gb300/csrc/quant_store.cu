@@ -1,0 +1,263 @@
+// kv_quant_store: a step's new K/V rows quantised into the 8-bit paged cache.
+//
+// A scale serves the scale_tokens tokens of a block of the page and one kv
+// head.  The rows of one call that fall into the same block stand next to one
+// another in slot_mapping, in ascending slots: a run.  The scale becomes
+//   max(the least power of two that holds the run's largest number,
+//       the block's present scale)
+// the latter only where the run does not begin the block (offset 0).  Where a
+// block's scale grows, the codes of its other tokens are rounded anew.
+//
+// Memory bound: a row is read once (bf16) and its codes are written once, so
+// the numbers of a run are held in registers between the search for the largest
+// one and the rounding.  A team of head_dim / 16 lanes has a row of one head,
+// two 16-byte chunks per lane, and at most four rows; a run is shared by as
+// many teams as its block needs, up to the 16 warps of a CTA.
+#include "rope_device.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kRows = 4;    // of a team
+constexpr int kTile = 32;   // most rows of slot_mapping that a CTA looks through
+
+struct StoreShape {
+  int tile;        // rows of slot_mapping per CTA
+  int teams;       // per run
+  unsigned ctas;   // that store; the others rotate q
+};
+
+__device__ __forceinline__ float magnitude_of(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;  // infinities and NaN do not count
+}
+
+// A lane's numbers of one row: chunks li and li + D / 16 of a head.
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t* src, int li, float (&x)[2][8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    bf16_floats(*reinterpret_cast<const uint4*>(src + (li + i * (D / 16)) * 8), x[i]);
+}
+
+// The same, rotated (in fp32: what is quantised is not rounded to bf16 before).
+template <int D>
+__device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, const RopeArgs& r, int64_t pos,
+                                                 float (&x)[2][8]) {
+  load_row<D>(src, li, x);
+  const int half = r.rotary_dim / 2;
+  if (r.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int pair = (li + i * (D / 16)) * 4 + p;
+        if (pair >= half) continue;
+        const float2 cs = rope_turn(pos, r.freqs[pair], r.magnitude);
+        const float a = x[i][2 * p], b = x[i][2 * p + 1];
+        x[i][2 * p] = a * cs.x - b * cs.y;
+        x[i][2 * p + 1] = b * cs.x + a * cs.y;
+      }
+    }
+    return;
+  }
+  if (half == D / 2) {  // both numbers of a pair are this lane's
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float2 cs = rope_turn(pos, r.freqs[li * 8 + p], r.magnitude);
+      const float a = x[0][p], b = x[1][p];
+      x[0][p] = a * cs.x - b * cs.y;
+      x[1][p] = b * cs.x + a * cs.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int e = (li + i * (D / 16)) * 8 + p;
+      if (e >= r.rotary_dim) continue;
+      const bool first = e < half;
+      const float2 cs = rope_turn(pos, r.freqs[first ? e : e - half], r.magnitude);
+      const float other = bf16lo(src[first ? e + half : e - half]);
+      x[i][p] = x[i][p] * cs.x + (first ? -other : other) * cs.y;
+    }
+  }
+}
+
+template <int kFormat, int D, bool kRope>
+__global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantStoreRows a, const QuantCache c,
+                                                                  const RopeArgs r, const RopeRows q,
+                                                                  const RopeShape qs, const StoreShape s,
+                                                                  int* status) {
+  constexpr int TL = D / 16;  // lanes of a team
+  if constexpr (kRope) {
+    if (blockIdx.x >= s.ctas) {
+      rope_thread(r, q, RopeRows{}, qs, (int64_t)(blockIdx.x - s.ctas) * (kWarps * 32) + threadIdx.x);
+      return;
+    }
+  }
+  __shared__ int leaders[kTile];
+  __shared__ int count;
+  __shared__ float tops[2][kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_v = blockIdx.x & 1;
+  const int64_t first = (int64_t)(blockIdx.x >> 1) * s.tile;
+  const int tokens = 1 << c.scale_shift;
+  const int64_t pool = c.num_blocks * c.block_size;
+
+  // The tile's rows that begin a run.
+  if (warp == 0) {
+    const int64_t i = first + lane;
+    bool leads = false;
+    if (lane < s.tile && i < a.num_tokens) {
+      const int64_t slot = a.slots[i];
+      leads = slot >= 0 && slot < pool;
+      if (slot >= pool) record_error(status, KVP_ERR_DEVICE_DATA);
+      if (leads && (slot & (tokens - 1)) && i > 0) leads = a.slots[i - 1] != slot - 1;
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, leads);
+    if (leads) leaders[__popc(mask & ((1u << lane) - 1))] = lane;
+    if (lane == 0) count = __popc(mask);
+  }
+  __syncthreads();
+
+  const int Hkv = c.num_kv_heads;
+  const int units = count * Hkv;  // (run, head)
+  const int lanes = s.teams * TL;                  // of a unit
+  const int unit_lane = threadIdx.x & (lanes - 1);  // (a power of two)
+  const int team = unit_lane / TL, li = unit_lane % TL;
+  const int per_round = kWarps * 32 / lanes;
+  const uint16_t* src = is_v ? a.v : a.k;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  uint8_t* codes = is_v ? c.v : c.k;
+  float* scales = is_v ? c.v_scales : c.k_scales;
+  const int warps = lanes > 32 ? lanes / 32 : 1;
+  const int in_warp = lanes < 32 ? lanes : 32;
+
+  for (int base = 0, round = 0; base < units; base += per_round, ++round) {
+    const int u = base + (int)(threadIdx.x / lanes);
+    const bool active = u < units;
+    int64_t row = 0, slot = 0;
+    int n = 0, head = 0;
+    if (active) {
+      const int lead = u / Hkv;
+      head = u - lead * Hkv;
+      row = first + leaders[lead];
+      slot = a.slots[row];
+      n = tokens - (int)(slot & (tokens - 1));
+      if (n > a.num_tokens - row) n = (int)(a.num_tokens - row);
+    }
+    // The run's length: up to the first row whose slot does not follow.
+    const int wl = threadIdx.x & (in_warp - 1);
+    for (int at = 0; at < tokens; at += in_warp) {
+      const int i = at + wl;
+      const bool ends = i < n && a.slots[row + i] != slot + i;
+      unsigned hit = __ballot_sync(0xffffffffu, ends) >> (lane & ~(in_warp - 1));
+      if (in_warp < 32) hit &= (1u << in_warp) - 1;
+      if (hit) n = at + __ffs(hit) - 1;
+    }
+    const int64_t group = slot >> c.scale_shift;
+    const bool fresh = (slot & (tokens - 1)) == 0;
+    float old = 0.f;
+    if (active && wl == 0 && !fresh) old = scales[group * Hkv + head];
+    float x[kRows][2][8];
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = team + j * s.teams;
+      if (i >= n) continue;
+      const uint16_t* p = src + (row + i) * stride + (int64_t)head * D;
+      if (kRope && !is_v)
+        load_row_rotated<D>(p, li, r, r.positions[row + i], x[j]);
+      else
+        load_row<D>(p, li, x[j]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(x[j][e >> 3][e & 7]));
+    }
+    for (int o = in_warp / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    old = __shfl_sync(0xffffffffu, old, lane & ~(in_warp - 1));
+    if (warps > 1) {
+      if (lane == 0) tops[round & 1][warp] = top;
+      named_barrier_sync(1 + warp / warps, warps * 32);
+      for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[round & 1][(warp & ~(warps - 1)) + w]);
+    }
+    if (!active) continue;
+    const float need = scale_for<kFormat>(top);
+    const float scale = fresh ? need : fmaxf(old, need);
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = team + j * s.teams;
+      if (i >= n) continue;
+      uint8_t* dst = codes + ((slot + i) * Hkv + head) * D;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<uint2*>(dst + (li + h * TL) * 8) = encode8<kFormat>(x[j][h], inv);
+    }
+    if (fresh || scale == old) {
+      if (fresh && unit_lane == 0) scales[group * Hkv + head] = scale;
+      continue;
+    }
+    // The block's other tokens, at the new scale (codes without a scale: zero).
+    if (unit_lane == 0) scales[group * Hkv + head] = scale;
+    const float ratio = old > 0.f ? old / scale : 0.f;
+    const int from = (int)(slot & (tokens - 1));
+    for (int i = team; i < tokens; i += s.teams) {
+      if (i >= from && i < from + n) continue;
+      uint8_t* dst = codes + (((group << c.scale_shift) + i) * Hkv + head) * D;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2* p = reinterpret_cast<uint2*>(dst + (li + h * TL) * 8);
+        const uint2 w = *p;
+        const float2 f[4] = {decode2<kFormat>(w.x), decode2<kFormat>(w.x >> 16), decode2<kFormat>(w.y),
+                             decode2<kFormat>(w.y >> 16)};
+        const float y[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+        *p = encode8<kFormat>(y, ratio);
+      }
+    }
+  }
+}
+
+template <int kFormat, int D, bool kRope>
+cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs& r, const RopeRows& q,
+                   int num_sms, int* status, cudaStream_t stream) {
+  StoreShape s;
+  // A run's teams: four rows for each, so that its numbers fit the registers.
+  const int tokens = 1 << c.scale_shift;
+  s.teams = tokens / kRows < 1 ? 1 : tokens / kRows;
+  // Rows of slot_mapping per CTA: few where that leaves SMs without any.
+  int64_t tile = rows.num_tokens / num_sms;
+  s.tile = (int)(tile < 1 ? 1 : tile > kTile ? kTile : tile);
+  int64_t ctas = 2 * ((rows.num_tokens + s.tile - 1) / s.tile);
+  s.ctas = (unsigned)ctas;
+  RopeShape qs{};
+  if (kRope) {
+    qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 1024);
+    ctas += (rows.num_tokens * qs.units * qs.slices + kWarps * 32 - 1) / (kWarps * 32);
+  }
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  quant_store_kernel<kFormat, D, kRope><<<(unsigned)ctas, kWarps * 32, 0, stream>>>(rows, c, r, q, qs, s, status);
+  return cudaGetLastError();
+}
+
+template <int kFormat, int D>
+cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs* rope, const RopeRows* q,
+                   int num_sms, int* status, cudaStream_t stream) {
+  if (rope) return launch<kFormat, D, true>(rows, c, *rope, *q, num_sms, status, stream);
+  return launch<kFormat, D, false>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_store(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs* rope,
+                               const RopeRows* q, int num_sms, int* status, cudaStream_t stream) {
+  if (c.format == KVP_E4M3)
+    return c.head_dim == 128 ? launch<KVP_E4M3, 128>(rows, c, rope, q, num_sms, status, stream)
+                             : launch<KVP_E4M3, 64>(rows, c, rope, q, num_sms, status, stream);
+  return c.head_dim == 128 ? launch<KVP_INT8, 128>(rows, c, rope, q, num_sms, status, stream)
+                           : launch<KVP_INT8, 64>(rows, c, rope, q, num_sms, status, stream);
+}
+
+}  // namespace kvp
