@@ -3,115 +3,768 @@
 //   out[b, h] = sum_p softmax_p(q[b, h] . kc_p * ks_p * scale) * vs_p * vc_p
 //
 // with codes kc, vc and the scales ks, vs of their block of tokens and kv head.
-// One CTA per (sequence, kv head): a warp takes every eighth token, a lane
-// head_dim / 32 numbers of it; the warps' softmax states are joined in shared
-// memory.
+// Memory bound: every code of a context is read once.
+//
+// * Work is counted in units: up to 16 tokens of one page (all kv heads).  The
+//   units of all sequences, end to end, are cut into equal contiguous shares, one
+//   per CTA, two CTAs per SM.  A sequence that a cut falls into leaves partial
+//   results, which the merge kernel joins.
+// * A producer warp streams units into a ring in shared memory: one tensor copy
+//   each for K and V lands a unit as [kv head][token][head_dim] bytes, swizzled
+//   so that the consumers' 16-byte loads fall in different banks; the tokens'
+//   scales come by 4-byte asynchronous copies that arrive on the same barrier.
+//   A lane looks up the pages of one unit, 32 units ahead at a time.
+// * Eight consumer warps: warp w has kv head w % Hkv of the stage's unit w / Hkv
+//   (a stage is 8 / Hkv units).  Codes become fp16, exactly, on their way from
+//   shared memory to the warp's matrix instructions (fp16 in, fp32 sums):
+//   S = q K^T:   m16n8k16, M = the query heads of the kv head, N = 8 tokens.  The
+//                numbers of head_dim may come in any order, the same in q and K,
+//                so a thread's operand is 32 (16) contiguous bytes of a token.
+//   O^T += V^T W: m16n8k16, M = 16 columns of head_dim, N = 8 heads, K = the 16
+//                tokens; which columns make a tile is free too, so a thread's
+//                operand is 16 (8) contiguous bytes of four tokens, whose bytes are
+//                paired by one permute.  The weights W are the thread's own S.
+//   q is scaled per head by a power of two to at most 2 in size, so fp16 holds
+//   what its 8 bits say to 2^-25 of the largest number.
+// * Softmax: m is a running reference for p * vs, l = sum p and O = sum (p vs) vc
+//   are both relative to it.  W = p * vs is rounded to fp16 (2^-11; at most 2^8 and
+//   mostly at most 1): V's scales, which may differ by any factor between
+//   blocks, thus stay out of fp16's range.  m moves, and O and l with it, only
+//   when a weight would exceed 2^8.
+#include <cudaTypedefs.h>
+
+#include "kvp_internal.h"
 #include "quant_device.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kConsumers = 8;
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kStages = 3;
+constexpr int kUnit = 16;  // tokens
 
+// A stage holds 8 (unit, kv head) pairs of K and of V.
+template <int D>
+__host__ __device__ constexpr int half_bytes() {
+  return kConsumers * kUnit * D;
+}
+constexpr int kStageScales = kConsumers * kUnit;  // of K, and as many of V
+
+// Warps of one kv head join their parts through shared memory, this many columns
+// of head_dim at a time, so that the ring keeps its three stages.
+template <int D, int G>
+__host__ __device__ constexpr int join_columns() {
+  return G == 8 ? 32 : G == 4 && D == 128 ? 64 : D;
+}
+
+enum : int { F_NEW = 1, F_LAST = 2, F_WHOLE = 4, F_ENTERED = 8, F_DONE = 16 };
+
+struct alignas(16) StageMeta {
+  int b;
+  int flags;
+  uint8_t n[8];  // tokens of each unit
+};
+
+// A sequence that is cut: its first and last CTA (last < first: not cut).
+struct Chain {
+  int b;
+  int first;
+  int last;
+};
+
+struct Args {
+  QuantDecodeArgs a;
+  int64_t num_blocks;
+  int block_size;
+  int page_units;  // units of a full page
+  int scale_shift;
+  int num_kv_heads;
+  const float* k_scales;
+  const float* v_scales;
+  float scale_log2;
+  float* part;    // [ctas][2][Hq][D + 4]: O[D], m, l
+  Chain* chains;  // per sequence, or per CTA that one begins in where those are fewer
+  bool by_seq;
+  int* status;
+};
+
+template <int D, int G>
+struct Smem {
+  uint8_t k[kStages][half_bytes<D>()];
+  uint8_t v[kStages][half_bytes<D>()];
+  float scales[kStages][2][kStageScales];
+  StageMeta meta[kStages];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t joined[kConsumers], taken[kConsumers];
+  float join[kConsumers - 1][G][join_columns<D, G>() + 2];
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// d += a b: m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
+  return r;
+}
+
+__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// An arrival on bar once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ int clamp_len(int c, int cap) { return c < 0 ? 0 : c > cap ? cap : c; }
+
+// Units of a sequence of n tokens.
+__device__ __forceinline__ int units_of(const Args& x, int n) {
+  const int pages = n / x.block_size, rest = n - pages * x.block_size;
+  return pages * x.page_units + (rest + kUnit - 1) / kUnit;
+}
+
+// ---------------------------------------------------------------- producer
+
+template <int D, int G>
+__device__ void produce(const Args& x, const CUtensorMap* mapK, const CUtensorMap* mapV, Smem<D, G>& sm) {
+  const int lane = threadIdx.x & 31;
+  const int Hkv = x.num_kv_heads, per_stage = kConsumers / Hkv;
+  const int cap = x.a.max_blocks * x.block_size;
+  const int me = blockIdx.x;
+  const uint32_t unit_bytes = (uint32_t)(kUnit * Hkv * D);
+
+  long long total = 0;
+  for (int i = lane; i < x.a.num_seqs; i += 32) {
+    const int c = x.a.context_lens[i];
+    if (c < 0 || c > cap) record_error(x.status, KVP_ERR_DEVICE_DATA);
+    total += units_of(x, clamp_len(c, cap));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  // CTAs that get a share: no more than leave each four units.
+  const long long P = total >= 4LL * gridDim.x ? gridDim.x : (total + 3) / 4;
+  const long long start = me < P ? total * me / P : total, end = me < P ? total * (me + 1) / P : total;
+
+  // Rows without a context are zero.
+  for (int b = me; b < x.a.num_seqs; b += gridDim.x) {
+    if (clamp_len(x.a.context_lens[b], cap) != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(x.a.out + (int64_t)b * x.a.out_stride);
+    for (int i = lane; i < x.a.num_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    if (x.by_seq && lane == 0) x.chains[b] = {b, 0, -1};
+  }
+  if (!x.by_seq && lane == 0) x.chains[me] = {0, 0, -1};
+
+  // The first sequence of the share, and the units before it.
+  int b = 0;
+  long long before = 0;
+  if (start < end) {
+    for (int base = 0; base < x.a.num_seqs; base += 32) {
+      const int i = base + lane;
+      const int c = i < x.a.num_seqs ? units_of(x, clamp_len(x.a.context_lens[i], cap)) : 0;
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, i < x.a.num_seqs && before + incl > start);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        b = base + l;
+        before += __shfl_sync(0xffffffffu, incl - c, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+
+  int s = 0;
+  uint32_t ph = 0, issued = 0, issued_ph = 0;
+  bool ok = true;
+  long long pos = start;
+  for (; ok && pos < end && b < x.a.num_seqs; ++b) {
+    const int len = clamp_len(x.a.context_lens[b], cap);
+    const int units = units_of(x, len);
+    if (units == 0) continue;
+    const int u0 = (int)(pos - before);
+    const int u1 = (int)((end < before + units ? end : before + units) - before);
+    const bool cut = u0 > 0 || u1 < units;
+    if (u0 == 0 && lane == 0) {  // it begins here: the CTA of its last unit
+      int last = me;
+      if (cut) {
+        last = (int)((before + units - 1) * P / total);
+        while (total * (last + 1) / P <= before + units - 1) ++last;
+      }
+      if (x.by_seq)
+        x.chains[b] = {b, me, cut ? last : me - 1};
+      else if (cut)
+        x.chains[me] = {b, me, last};
+    }
+    const int seg_flags = (cut ? 0 : F_WHOLE) | (u0 > 0 ? F_ENTERED : 0);
+    // This lane's unit of the present 32, and of the next.
+    int row = 0, n = 0, row_next, n_next;
+    auto look_up = [&](int u, int& r, int& m) {
+      r = m = 0;
+      if (u >= u1) return;
+      const int page = u / x.page_units, off = (u - page * x.page_units) * kUnit;
+      int block = x.a.block_tables[(int64_t)b * x.a.max_blocks + page];
+      if (block < 0 || block >= x.num_blocks) {
+        record_error(x.status, KVP_ERR_DEVICE_DATA);
+        block = 0;  // never read a page outside the pool
+      }
+      r = block * x.block_size + off;
+      m = x.block_size - off < kUnit ? x.block_size - off : kUnit;
+      const int left = len - page * x.block_size - off;
+      if (m > left) m = left;
+    };
+    look_up(u0 + lane, row_next, n_next);
+    for (int u = u0; ok && u < u1; u += per_stage) {
+      const int at = (u - u0) & 31;
+      if (at == 0) {
+        row = row_next;
+        n = n_next;
+        look_up(u + 32 + lane, row_next, n_next);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ph ^ 1u, x.status))) {
+        ok = false;
+        break;
+      }
+      const int unit = lane - at;  // of the stage
+      const bool mine = unit >= 0 && unit < per_stage;
+      if (mine) sm.meta[s].n[unit] = (uint8_t)n;
+      if (lane == 0) {
+        sm.meta[s].b = b;
+        sm.meta[s].flags = seg_flags | (u == u0 ? F_NEW : 0) | (u + per_stage >= u1 ? F_LAST : 0);
+      }
+      const int count = __popc(__ballot_sync(0xffffffffu, mine && n > 0));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * count * unit_bytes);
+      __syncwarp();
+      if (mine && n > 0) {
+        tma_load_3d(sm.k[s] + unit * unit_bytes, mapK, 0, row, 0, &sm.full[s]);
+        tma_load_3d(sm.v[s] + unit * unit_bytes, mapV, 0, row, 0, &sm.full[s]);
+      }
+      // Scales, [unit][head][token] as the codes.
+#pragma unroll
+      for (int j = 0; j < kStageScales / 32; ++j) {
+        const int i = j * 32 + lane;
+        const int su = i / (kUnit * Hkv), head = i / kUnit % Hkv, t = i % kUnit;
+        const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
+        if (t < m) {
+          const int64_t src = (int64_t)((r + t) >> x.scale_shift) * Hkv + head;
+          copy4_async(&sm.scales[s][0][i], x.k_scales + src);
+          copy4_async(&sm.scales[s][1][i], x.v_scales + src);
+        }
+      }
+      arrive_after_copies(&sm.full[s]);
+      issued |= 1u << s;
+      issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    before += units;
+    pos = before;
+  }
+  if (ok && __all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ph ^ 1u, x.status))) {
+    if (lane == 0) {
+      sm.meta[s].flags = F_DONE;
+      mbar_arrive(&sm.full[s]);
+    }
+    __syncwarp();
+    arrive_after_copies(&sm.full[s]);
+    return;
+  }
+  // A wait expired: let every copy this CTA issued land before the CTA exits.
+  for (int i = 0; i < kStages; ++i)
+    if (issued >> i & 1u) mbar_wait(&sm.full[i], issued_ph >> i & 1u, x.status);
+}
+
+// ---------------------------------------------------------------- consumers
+
+// Thread (r, c) of a warp (r = lane / 4, c = lane % 4) has head r's scores of
+// tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a unit and the sums of heads 2c, 2c + 1 in
+// columns D / 8 * r .. + D / 8 - 1: o[i][y + 2 z] is head 2c + y, column
+// D / 8 * r + 2 i + z.
 template <int kFormat, int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) quant_decode_kernel(const QuantDecodeArgs a, const QuantCache c,
-                                                                   int* status) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.x, g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cap = a.max_blocks * c.block_size;
-  int len = a.context_lens[b];
-  if (len < 0 || len > cap) {
-    if (threadIdx.x == 0) record_error(status, KVP_ERR_DEVICE_DATA);
-    len = len < 0 ? 0 : cap;
-  }
-  const int per_block = c.block_size >> c.scale_shift;
-  const float scale = a.softmax_scale * 1.4426950408889634f;
-  float q[G][E], acc[G][E], m[G], l[G];
+__device__ void consume(const Args& x, Smem<D, G>& sm) {
+  constexpr int KS = D / 16;  // k-steps of S; tiles of O
+  constexpr int W = D / 32;   // 4-byte words of a token's columns that a thread has
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hkv = x.num_kv_heads;
+  const int g = warp % Hkv, sub = warp / Hkv, subs = kConsumers / Hkv;
+  const int head0 = g * G;
+  const int r = lane >> 2, c = lane & 3;
+  const bool oc[2] = {2 * c < G, 2 * c + 1 < G};
+  const uint32_t region = (uint32_t)((sub * Hkv + g) * kUnit * D);
+  const uint32_t kbase = smem_u32(sm.k[0]) + region, vbase = smem_u32(sm.v[0]) + region;
+  // Byte offset of 16-byte chunk q of a token's row: the copies' swizzle.
+  auto chunk = [](int row, int q) {
+    return (uint32_t)(D == 128 ? row * 128 + ((q ^ (row & 7)) << 4) : row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+  };
+
+  uint32_t qa[KS][2];
+  float o[KS][4];
+  float m = -INFINITY, l = 0.f, cq = 0.f;
+  int b = 0, s = 0, seg = 0;
+  uint32_t ph = 0;
+
+  while (true) {
+    if (!mbar_wait(&sm.full[s], ph, x.status)) return;
+    const int flags = sm.meta[s].flags;
+    if (flags & F_DONE) break;
+    if (flags & F_NEW) {
+      b = sm.meta[s].b;
+      // 2 KS contiguous words of head r's query, at most 2 in size
+      float top = 0.f;
+      uint32_t raw[KS * 2];
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
+      for (int i = 0; i < KS / 2; ++i) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (r < G)
+          u = *reinterpret_cast<const uint4*>(x.a.q + (int64_t)b * x.a.q_stride + (int64_t)(head0 + r) * D +
+                                              c * (2 * KS * 2) + i * 8);
+        raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
+      }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[h][e] = bf16lo(a.q[b * a.q_stride + (int64_t)(g * G + h) * D + lane * E + e]) * scale;
-      acc[h][e] = 0.f;
+      for (int i = 0; i < KS * 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(raw[i])), fabsf(bf16hi(raw[i]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      uint32_t e = __float_as_uint(top) >> 23;
+      e = e < 1 ? 1 : e > 253 ? 253 : e;
+      const float down = __uint_as_float((254 - e) << 23);
+      cq = __uint_as_float(e << 23) * x.scale_log2;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) qa[i >> 1][i & 1] = pack_f16x2(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      m = -INFINITY;
+      l = 0.f;
     }
-  }
-  for (int t = warp; t < len; t += kWarps) {
-    const int page = t / c.block_size, off = t - page * c.block_size;
-    const int block = a.block_tables[(int64_t)b * a.max_blocks + page];
-    if (block < 0 || block >= c.num_blocks) {
-      if (lane == 0) record_error(status, KVP_ERR_DEVICE_DATA);
-      continue;
+    const int n = sm.meta[s].n[sub];
+    if (n > 0) {
+      const uint32_t kst = kbase + (uint32_t)(s * half_bytes<D>()), vst = vbase + (uint32_t)(s * half_bytes<D>());
+      float sc[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two sums halve the chain
+        const int row = j * 8 + r;
+#pragma unroll
+        for (int i = 0; i < KS / 4; ++i) {
+          const uint4 u = lds128(kst + chunk(row, c * (KS / 4) + i));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mma_f16(y & 1 ? s1 : s0, qa[4 * i + y][0], 0, qa[4 * i + y][1], 0, codes_f16x2<kFormat>(w[y]),
+                    codes_f16x2<kFormat>(w[y] >> 16));
+        }
+        sc[j][0] = s0[0] + s1[0];
+        sc[j][1] = s0[1] + s1[1];
+      }
+      const float* scales = sm.scales[s][0] + (sub * Hkv + g) * kUnit + 2 * c;
+      float vs[2][2], top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 ks = *reinterpret_cast<const float2*>(scales + 8 * j);
+        const float2 v2 = *reinterpret_cast<const float2*>(scales + kStageScales + 8 * j);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const bool valid = 8 * j + 2 * c + y < n;
+          sc[j][y] = valid ? sc[j][y] * cq * (y ? ks.y : ks.x) : -INFINITY;
+          vs[j][y] = valid ? (y ? v2.y : v2.x) : 0.f;
+          // log2 of the scale, rounded up; below 2^-64 it counts as that
+          const int e = (int)(__float_as_uint(vs[j][y]) >> 23) - 126;
+          top = fmaxf(top, sc[j][y] + (float)(e < -64 ? -64 : e));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool grow = top > m + 8.f;  // also a sequence's first unit
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? fast_exp2(m - top) : 1.f;
+        if (grow) {
+          m = top;
+          l *= alpha;
+        }
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a1;
+          o[i][2] *= a0;
+          o[i][3] *= a1;
+        }
+      }
+      uint32_t wt[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float p0 = fast_exp2(sc[j][0] - m), p1 = fast_exp2(sc[j][1] - m);
+        l += p0 + p1;
+        wt[j] = pack_f16x2(p0 * vs[j][0], p1 * vs[j][1]);
+      }
+      // Tokens 2c, 2c + 1, 2c + 8, 2c + 9: this thread's columns.
+      uint32_t vw[4][W];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = 2 * c + (t & 1) + (t >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 u = lds128(vst + chunk(row, r));
+          vw[t][0] = u.x, vw[t][1] = u.y, vw[t][2] = u.z, vw[t][3] = u.w;
+        } else {
+          const uint2 u = lds64(vst + chunk(row, r >> 1) + (r & 1) * 8);
+          vw[t][0] = u.x, vw[t][1] = u.y;
+        }
+        if (n < kUnit && row >= n) {  // what lies behind the context may be anything
+#pragma unroll
+          for (int i = 0; i < W; ++i) vw[t][i] = 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], y ? 0x7362 : 0x5140);
+          const uint32_t hi = __byte_perm(vw[2][i], vw[3][i], y ? 0x7362 : 0x5140);
+          mma_f16(o[2 * i + y], codes_f16x2<kFormat>(lo), codes_f16x2<kFormat>(lo >> 16), codes_f16x2<kFormat>(hi),
+                  codes_f16x2<kFormat>(hi >> 16), wt[0], wt[1]);
+        }
+      }
     }
-    const int64_t row = (((int64_t)block * c.block_size + off) * c.num_kv_heads + g) * D + lane * E;
-    const int64_t sc = ((int64_t)block * per_block + (off >> c.scale_shift)) * c.num_kv_heads + g;
-    float k[E], v[E];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = decode2<kFormat>(*reinterpret_cast<const uint16_t*>(c.k + row + e));
-      const float2 y = decode2<kFormat>(*reinterpret_cast<const uint16_t*>(c.v + row + e));
-      k[e] = x.x, k[e + 1] = x.y, v[e] = y.x, v[e + 1] = y.y;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[s]);
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1u;
     }
-    const float ks = c.k_scales[sc], vs = c.v_scales[sc];
+    if (!(flags & F_LAST)) continue;
+
+    // ---- the end of the CTA's part of sequence b: heads 2c, 2c + 1
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    float mh[2] = {__shfl_sync(0xffffffffu, m, 8 * c), __shfl_sync(0xffffffffu, m, 8 * c + 4)};
+    float lh[2] = {__shfl_sync(0xffffffffu, l, 8 * c), __shfl_sync(0xffffffffu, l, 8 * c + 4)};
+    if (subs > 1) {
+      // Warps of the same kv head: sub 0 takes the others' parts, some columns
+      // at a time (bounded waits both ways).
+      constexpr int C = join_columns<D, G>();
+      constexpr int T = C / 16;  // tiles of a round: 2 T columns of each r
+      float M[2], w0[2];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      float s = 0.f;
+      for (int i0 = 0; i0 < KS; i0 += T, ++seg) {
+        if (sub > 0) {
+          if (seg > 0 && !mbar_wait(&sm.taken[g], (uint32_t)((seg - 1) & 1), x.status)) return;
+          float(*mine)[C + 2] = sm.join[warp - Hkv];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += q[h][e] * k[e];
+          for (int y = 0; y < 2; ++y) {
+            if (!oc[y]) continue;
+            float* to = mine[2 * c + y];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= ks;
-      const float top = fmaxf(m[h], s), old = m[h] == top ? 1.f : exp2f(m[h] - top), p = exp2f(s - top);
-      m[h] = top;
-      l[h] = l[h] * old + p;
+            for (int i = 0; i < T; ++i)
+              *reinterpret_cast<float2*>(to + 2 * (r * T + i)) = make_float2(o[i0 + i][y], o[i0 + i][y + 2]);
+            if (r == 0) *reinterpret_cast<float2*>(to + C) = make_float2(mh[y], lh[y]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.joined[g]);
+        } else {
+          if (!mbar_wait(&sm.joined[g], (uint32_t)(seg & 1), x.status)) return;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[h][e] = acc[h][e] * old + p * vs * v[e];
+          for (int y = 0; y < 2; ++y) {
+            if (!oc[y]) continue;
+            if (i0 == 0) {
+              M[y] = mh[y];
+              for (int k = 1; k < subs; ++k) M[y] = fmaxf(M[y], sm.join[(k - 1) * Hkv + g][2 * c + y][C]);
+              w0[y] = mh[y] == -INFINITY ? 0.f : fast_exp2(mh[y] - M[y]);
+              lh[y] *= w0[y];
+            }
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+              o[i0 + i][y] *= w0[y];
+              o[i0 + i][y + 2] *= w0[y];
+            }
+            for (int k = 1; k < subs; ++k) {
+              const float* from = sm.join[(k - 1) * Hkv + g][2 * c + y];
+              const float2 ml = *reinterpret_cast<const float2*>(from + C);
+              const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M[y]);
+              if (i0 == 0) lh[y] += w * ml.y;
+#pragma unroll
+              for (int i = 0; i < T; ++i) {
+                const float2 u = *reinterpret_cast<const float2*>(from + 2 * (r * T + i));
+                o[i0 + i][y] += w * u.x;
+                o[i0 + i][y + 2] += w * u.y;
+              }
+            }
+            if (i0 + T >= KS) mh[y] = M[y];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.taken[g]);
+        }
+      }
+      if (sub > 0) continue;
     }
-  }
-  __shared__ float all[kWarps][G][D + 2];
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+    for (int y = 0; y < 2; ++y) {
+      if (!oc[y]) continue;
+      const int h = head0 + 2 * c + y;
+      if (flags & F_WHOLE) {
+        const float inv = 1.f / lh[y];
+        uint16_t* to = x.a.out + (int64_t)b * x.a.out_stride + (int64_t)h * D + r * (D / 8);
 #pragma unroll
-    for (int e = 0; e < E; ++e) all[warp][h][lane * E + e] = acc[h][e];
-    if (lane == 0) all[warp][h][D] = m[h], all[warp][h][D + 1] = l[h];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-    const int h = i / D, e = i - h * D;
-    float top = -INFINITY, num = 0.f, den = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, all[w][h][D]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float x = all[w][h][D] == -INFINITY ? 0.f : exp2f(all[w][h][D] - top);
-      num += x * all[w][h][e];
-      den += x * all[w][h][D + 1];
+        for (int i = 0; i < KS; i += 4)
+          *reinterpret_cast<uint4*>(to + 2 * i) =
+              make_uint4(pack_bf16x2(o[i][y] * inv, o[i][y + 2] * inv),
+                         pack_bf16x2(o[i + 1][y] * inv, o[i + 1][y + 2] * inv),
+                         pack_bf16x2(o[i + 2][y] * inv, o[i + 2][y + 2] * inv),
+                         pack_bf16x2(o[i + 3][y] * inv, o[i + 3][y + 2] * inv));
+      } else {
+        float* to = x.part + (((size_t)blockIdx.x * 2 + (flags & F_ENTERED ? 0 : 1)) * x.a.num_heads + h) * (D + 4);
+#pragma unroll
+        for (int i = 0; i < KS; i += 2)
+          *reinterpret_cast<float4*>(to + r * (D / 8) + 2 * i) =
+              make_float4(o[i][y], o[i][y + 2], o[i + 1][y], o[i + 1][y + 2]);
+        if (r == 0) *reinterpret_cast<float2*>(to + D) = make_float2(mh[y], lh[y]);
+      }
     }
-    const uint32_t r = pack_bf16x2(len == 0 ? 0.f : num / den, 0.f);
-    a.out[b * a.out_stride + (int64_t)(g * G + h) * D + e] = (uint16_t)r;
   }
 }
 
-template <int kFormat, int D>
-cudaError_t launch(const QuantDecodeArgs& a, const QuantCache& c, int* status, cudaStream_t stream) {
-  const dim3 grid(a.num_seqs, c.num_kv_heads);
-  switch (a.num_heads / c.num_kv_heads) {
-    case 1: quant_decode_kernel<kFormat, D, 1><<<grid, kWarps * 32, 0, stream>>>(a, c, status); break;
-    case 2: quant_decode_kernel<kFormat, D, 2><<<grid, kWarps * 32, 0, stream>>>(a, c, status); break;
-    case 4: quant_decode_kernel<kFormat, D, 4><<<grid, kWarps * 32, 0, stream>>>(a, c, status); break;
-    default: quant_decode_kernel<kFormat, D, 8><<<grid, kWarps * 32, 0, stream>>>(a, c, status); break;
+template <int kFormat, int D, int G>
+__global__ void __launch_bounds__(kThreads, 2)
+    quant_split_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                       const Args x) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<D, G>& sm = *reinterpret_cast<Smem<D, G>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 33);  // the copies' bytes, and the producer's 32 lanes' own copies
+      mbar_init(&sm.empty[i], kConsumers);
+    }
+    const int subs = kConsumers / x.num_kv_heads;
+    for (int i = 0; i < kConsumers; ++i) {
+      mbar_init(&sm.joined[i], subs > 1 ? subs - 1 : 1);
+      mbar_init(&sm.taken[i], 1);
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&mapK);
+    prefetch_tensormap(&mapV);
   }
-  return cudaGetLastError();
+  // Launched in the shadow of the stream's previous kernel: nothing of memory
+  // is touched before that one is done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x >> 5 == kConsumers)
+    produce<D, G>(x, &mapK, &mapV, sm);
+  else
+    consume<kFormat, D, G>(x, sm);
+}
+
+// Joins the parts of the sequences that are cut: block (i, j) has sequence (or
+// CTA) i and some heads.  A head has D / 4 lanes times `slices` of the parts.
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) quant_merge_kernel(const Args x, int slices) {
+  constexpr int L = D / 4;
+  __shared__ float4 acc[kMergeThreads];
+  __shared__ float2 ml[kMergeThreads / L];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Chain ch = x.chains[blockIdx.x];
+  if (ch.last < ch.first) return;
+  const int li = threadIdx.x % L, group = threadIdx.x / L;
+  const int slice = group % slices;
+  const int h = blockIdx.y * (kMergeThreads / L / slices) + group / slices;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (h < x.a.num_heads) {
+    constexpr int B = 4;  // parts in flight
+    for (int i = ch.first + slice; i <= ch.last; i += B * slices) {
+      float4 a[B];
+      float2 s[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const int part = i + k * slices;
+        s[k] = make_float2(-INFINITY, 0.f);
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (part > ch.last) continue;
+        const float* p = x.part + (((size_t)part * 2 + (part == ch.first ? 1 : 0)) * x.a.num_heads + h) * (D + 4);
+        a[k] = *reinterpret_cast<const float4*>(p + li * 4);
+        s[k] = *reinterpret_cast<const float2*>(p + D);
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < B; ++k) top = fmaxf(top, s[k].x);
+      if (top == -INFINITY) continue;
+      const float w = fast_exp2(m - top);
+      l *= w;
+      o.x *= w, o.y *= w, o.z *= w, o.w *= w;
+      m = top;
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const float y = fast_exp2(s[k].x - top);
+        l += y * s[k].y;
+        o.x += y * a[k].x, o.y += y * a[k].y, o.z += y * a[k].z, o.w += y * a[k].w;
+      }
+    }
+  }
+  if (slices > 1) {
+    acc[threadIdx.x] = o;
+    if (li == 0) ml[group] = make_float2(m, l);
+    __syncthreads();
+    if (slice > 0) return;
+    float top = m;
+    for (int k = 1; k < slices; ++k) top = fmaxf(top, ml[group + k].x);
+    float w = fast_exp2(m - top);
+    l *= w;
+    o.x *= w, o.y *= w, o.z *= w, o.w *= w;
+    for (int k = 1; k < slices; ++k) {
+      const float2 s = ml[group + k];
+      const float4 a = acc[threadIdx.x + k * L];
+      w = fast_exp2(s.x - top);
+      l += w * s.y;
+      o.x += w * a.x, o.y += w * a.y, o.z += w * a.z, o.w += w * a.w;
+    }
+  }
+  if (h >= x.a.num_heads) return;
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(x.a.out + (int64_t)ch.b * x.a.out_stride + (int64_t)h * D + li * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+// Map of a code array as (column, token row, kv head) with a box of one unit.
+bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t d = c.head_dim, heads = c.num_kv_heads;
+  const cuuint64_t dims[3] = {d, (cuuint64_t)(c.num_blocks * c.block_size), heads};
+  const cuuint64_t strides[2] = {heads * d, d};
+  const cuuint32_t box[3] = {(cuuint32_t)d, kUnit, (cuuint32_t)heads};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+  int ctas;
+  bool by_seq;
+  size_t part_bytes, total_bytes;
+};
+
+// Two CTAs per SM, or one for 64 tokens where the bound of the lengths leaves
+// fewer.
+Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int num_sms) {
+  Plan p;
+  long long ctas = ((long long)num_seqs * max_context_len + 63) / 64;
+  if (ctas > 2 * num_sms) ctas = 2 * num_sms;
+  p.ctas = ctas < 1 ? 1 : (int)ctas;
+  p.by_seq = num_seqs <= p.ctas;
+  p.part_bytes = (size_t)p.ctas * 2 * num_heads * (head_dim + 4) * sizeof(float);  // (a multiple of 16)
+  p.total_bytes = p.part_bytes + (size_t)p.ctas * sizeof(Chain) + 16;
+  return p;
+}
+
+template <typename... Params, typename... As>
+cudaError_t launch_shadow(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          As... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kFormat, int D, int G>
+cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!unit_map(&mk, c.k, c) || !unit_map(&mv, c.v, c)) return cudaErrorInvalidValue;
+  constexpr size_t smem = sizeof(Smem<D, G>) + 1024;
+  static_assert(smem <= 113 * 1024, "two CTAs per SM");
+  cudaError_t e = cudaFuncSetAttribute(quant_split_kernel<kFormat, D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_shadow(quant_split_kernel<kFormat, D, G>, dim3(p.ctas), kThreads, smem, stream, mk, mv, x);
+  if (e != cudaSuccess) return e;
+  // Slices of the parts for each head: as many as a cut sequence has parts,
+  // about.
+  constexpr int groups = kMergeThreads / (D / 4);
+  const int chains = p.by_seq ? x.a.num_seqs : p.ctas;
+  int slices = 1;
+  while (slices < groups && slices * chains < 2 * p.ctas) slices *= 2;
+  const int per_block = groups / slices;
+  return launch_shadow(quant_merge_kernel<D>, dim3(chains, (x.a.num_heads + per_block - 1) / per_block),
+                       kMergeThreads, 0, stream, x, slices);
+}
+
+template <int kFormat, int D>
+cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream_t stream) {
+  switch (x.a.num_heads / c.num_kv_heads) {
+    case 1: return launch<kFormat, D, 1>(x, c, p, stream);
+    case 2: return launch<kFormat, D, 2>(x, c, p, stream);
+    case 4: return launch<kFormat, D, 4>(x, c, p, stream);
+    default: return launch<kFormat, D, 8>(x, c, p, stream);
+  }
 }
 
 }  // namespace
 
-size_t quant_decode_workspace_bytes(int, int, int, int, int, int) { return 256; }
+size_t quant_decode_workspace_bytes(int num_seqs, int num_heads, int, int head_dim, int max_context_len,
+                                    int num_sms) {
+  return plan(num_seqs, num_heads, head_dim, max_context_len, num_sms).total_bytes;
+}
 
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, int num_sms, int* status,
                                 cudaStream_t stream) {
+  const Plan p = plan(a.num_seqs, a.num_heads, c.head_dim, a.max_context_len, num_sms);
+  Args x;
+  x.a = a;
+  x.num_blocks = c.num_blocks;
+  x.block_size = c.block_size;
+  x.page_units = (c.block_size + kUnit - 1) / kUnit;
+  x.scale_shift = c.scale_shift;
+  x.num_kv_heads = c.num_kv_heads;
+  x.k_scales = c.k_scales;
+  x.v_scales = c.v_scales;
+  x.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  x.part = static_cast<float*>(a.workspace);
+  x.chains = reinterpret_cast<Chain*>(static_cast<uint8_t*>(a.workspace) + p.part_bytes);
+  x.by_seq = p.by_seq;
+  x.status = status;
   if (c.format == KVP_E4M3)
-    return c.head_dim == 128 ? launch<KVP_E4M3, 128>(a, c, status, stream) : launch<KVP_E4M3, 64>(a, c, status, stream);
-  return c.head_dim == 128 ? launch<KVP_INT8, 128>(a, c, status, stream) : launch<KVP_INT8, 64>(a, c, status, stream);
+    return c.head_dim == 128 ? launch<KVP_E4M3, 128>(x, c, p, stream) : launch<KVP_E4M3, 64>(x, c, p, stream);
+  return c.head_dim == 128 ? launch<KVP_INT8, 128>(x, c, p, stream) : launch<KVP_INT8, 64>(x, c, p, stream);
 }
 
 }  // namespace kvp
