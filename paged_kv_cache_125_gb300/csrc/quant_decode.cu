@@ -13,24 +13,27 @@
 //   each for K and V lands a unit as [kv head][token][head_dim] bytes, swizzled
 //   so that the consumers' 16-byte loads fall in different banks; the tokens'
 //   scales come by 4-byte asynchronous copies that arrive on the same barrier.
-//   A lane looks up the pages of one unit, 32 units ahead at a time.
+//   A lane looks up the page of one unit, 32 units ahead at a time.
 // * Eight consumer warps: warp w has kv head w % Hkv of the stage's unit w / Hkv
-//   (a stage is 8 / Hkv units).  Codes become fp16, exactly, on their way from
-//   shared memory to the warp's matrix instructions (fp16 in, fp32 sums):
-//   S = q K^T:   m16n8k16, M = the query heads of the kv head, N = 8 tokens.  The
-//                numbers of head_dim may come in any order, the same in q and K,
-//                so a thread's operand is 32 (16) contiguous bytes of a token.
-//   O^T += V^T W: m16n8k16, M = 16 columns of head_dim, N = 8 heads, K = the 16
-//                tokens; which columns make a tile is free too, so a thread's
-//                operand is 16 (8) contiguous bytes of four tokens, whose bytes are
-//                paired by one permute.  The weights W are the thread's own S.
-//   q is scaled per head by a power of two to at most 2 in size, so fp16 holds
-//   what its 8 bits say to 2^-25 of the largest number.
+//   (a stage is 8 / Hkv units).
+//   S = q K^T, N = 8 tokens, the query heads of the kv head in M.  The numbers of
+//   head_dim may come in any order, the same in q and K, so a thread's operand is
+//   32 (16) contiguous bytes of a token.  e4m3: m16n8k32 on the codes as they lie;
+//   q, scaled per head by a power of two to at most 2^8, is the sum of two e4m3
+//   numbers (rows r and r + 8, the second times 2^4): all of bf16's 8 bits, to
+//   2^-21 of the head's largest number.  int8: m16n8k16 on codes made fp16.
+//   O^T += V^T W: m16n8k16 in fp16, M = 16 columns of head_dim, N = 8 heads, K = the
+//   unit's 16 tokens; the transposing 8-bit load gives a thread four tokens of a
+//   column, which two conversions make its operand.  The weights W are the
+//   thread's own S.
+//   Both kinds of instruction sum in fp32.
 // * Softmax: m is a running reference for p * vs, l = sum p and O = sum (p vs) vc
 //   are both relative to it.  W = p * vs is rounded to fp16 (2^-11; at most 2^8 and
 //   mostly at most 1): V's scales, which may differ by any factor between
 //   blocks, thus stay out of fp16's range.  m moves, and O and l with it, only
 //   when a weight would exceed 2^8.
+// * Where scale_tokens is 16 or more (kUniform), a unit has one scale of K and
+//   one of V per kv head.
 #include <cudaTypedefs.h>
 
 #include "kvp_internal.h"
@@ -63,7 +66,7 @@ enum : int { F_NEW = 1, F_LAST = 2, F_WHOLE = 4, F_ENTERED = 8, F_DONE = 16 };
 struct alignas(16) StageMeta {
   int b;
   int flags;
-  uint8_t n[8];  // tokens of each unit
+  uint8_t n[8];  // tokens of each unit (read as two words)
 };
 
 // A sequence that is cut: its first and last CTA (last < first: not cut).
@@ -80,6 +83,7 @@ struct Args {
   int page_units;  // units of a full page
   int scale_shift;
   int num_kv_heads;
+  int head_shift;  // log2 of num_kv_heads
   const float* k_scales;
   const float* v_scales;
   float scale_log2;
@@ -93,7 +97,7 @@ template <int D, int G>
 struct Smem {
   uint8_t k[kStages][half_bytes<D>()];
   uint8_t v[kStages][half_bytes<D>()];
-  float scales[kStages][2][kStageScales];
+  float scales[kStages][2][kStageScales];  // [kv head of a unit][token], or (K, V) of each
   StageMeta meta[kStages];
   uint64_t full[kStages], empty[kStages];
   uint64_t joined[kConsumers], taken[kConsumers];
@@ -127,10 +131,22 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
   return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
-  return r;
+
+// d += a b: m16n8k32, e4m3 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 byte matrices, transposed: lane l gives the address of row l % 16 of
+// matrix l / 16; thread (r, c) gets rows 4c .. 4c + 3 of columns r and r + 8.
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr));
 }
 
 __device__ __forceinline__ void copy4_async(void* dst, const void* src) {
@@ -151,7 +167,7 @@ __device__ __forceinline__ int units_of(const Args& x, int n) {
 
 // ---------------------------------------------------------------- producer
 
-template <int D, int G>
+template <int D, int G, bool kUniform>
 __device__ void produce(const Args& x, const CUtensorMap* mapK, const CUtensorMap* mapV, Smem<D, G>& sm) {
   const int lane = threadIdx.x & 31;
   const int Hkv = x.num_kv_heads, per_stage = kConsumers / Hkv;
@@ -270,16 +286,24 @@ __device__ void produce(const Args& x, const CUtensorMap* mapK, const CUtensorMa
         tma_load_3d(sm.k[s] + unit * unit_bytes, mapK, 0, row, 0, &sm.full[s]);
         tma_load_3d(sm.v[s] + unit * unit_bytes, mapV, 0, row, 0, &sm.full[s]);
       }
-      // Scales, [unit][head][token] as the codes.
-#pragma unroll
-      for (int j = 0; j < kStageScales / 32; ++j) {
-        const int i = j * 32 + lane;
-        const int su = i / (kUnit * Hkv), head = i / kUnit % Hkv, t = i % kUnit;
+      if constexpr (kUniform) {
+        const int i = lane & 7, su = i >> x.head_shift;
         const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
-        if (t < m) {
-          const int64_t src = (int64_t)((r + t) >> x.scale_shift) * Hkv + head;
-          copy4_async(&sm.scales[s][0][i], x.k_scales + src);
-          copy4_async(&sm.scales[s][1][i], x.v_scales + src);
+        if (lane < 16 && m > 0)
+          copy4_async(&sm.scales[s][0][2 * i + (lane >> 3)],
+                      (lane < 8 ? x.k_scales : x.v_scales) +
+                          ((int64_t)(r >> x.scale_shift) << x.head_shift) + (i & (Hkv - 1)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kStageScales / 32; ++j) {
+          const int i = j * 32 + lane, t = lane % kUnit, head = i / kUnit & (Hkv - 1);
+          const int su = i / kUnit >> x.head_shift;
+          const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
+          if (t < m) {
+            const int64_t src = ((int64_t)((r + t) >> x.scale_shift) << x.head_shift) + head;
+            copy4_async(&sm.scales[s][0][i], x.k_scales + src);
+            copy4_async(&sm.scales[s][1][i], x.v_scales + src);
+          }
         }
       }
       arrive_after_copies(&sm.full[s]);
@@ -309,28 +333,128 @@ __device__ void produce(const Args& x, const CUtensorMap* mapK, const CUtensorMa
 
 // ---------------------------------------------------------------- consumers
 
+// S of 8 tokens for the query heads; thread (r, c): head r, the tokens that the
+// lanes' rows 2c and 2c + 1 are.
+template <int kFormat, int D>
+struct Scores;
+
+template <int D>
+struct Scores<KVP_E4M3, D> {
+  uint32_t a[D / 32][4];
+
+  // raw: D / 8 words of bf16 of head r, largest below 2^e (e a biased exponent)
+  __device__ __forceinline__ float load(const uint32_t (&raw)[D / 8], uint32_t e) {
+    e = e < 8 ? 8 : e;
+    const float up = __uint_as_float((261 - e) << 23);  // to below 2^8
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float q0 = bf16lo(raw[2 * i + y]) * up, q1 = bf16hi(raw[2 * i + y]) * up;
+        const uint32_t h = encode2<KVP_E4M3>(q0, q1);
+        const float2 f = decode2<KVP_E4M3>(h);
+        hi |= h << 16 * y;
+        lo |= encode2<KVP_E4M3>((q0 - f.x) * 16.f, (q1 - f.y) * 16.f) << 16 * y;
+      }
+      a[i >> 1][2 * (i & 1)] = hi;
+      a[i >> 1][2 * (i & 1) + 1] = lo;
+    }
+    return __uint_as_float((e - 7) << 23);
+  }
+  // chunk(i): the i-th 16 bytes of this thread's part of its token
+  template <typename F>
+  __device__ __forceinline__ void of(F chunk, float& x0, float& x1) const {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 u = lds128(chunk(i));
+      mma_e4m3(s, a[2 * i], u.x, u.y);
+      mma_e4m3(s, a[2 * i + 1], u.z, u.w);
+    }
+    x0 = fmaf(s[2], 0.0625f, s[0]);
+    x1 = fmaf(s[3], 0.0625f, s[1]);
+  }
+};
+
+template <int D>
+struct Scores<KVP_INT8, D> {
+  uint32_t a[D / 16][2];
+
+  __device__ __forceinline__ float load(const uint32_t (&raw)[D / 8], uint32_t e) {
+    e = e < 1 ? 1 : e > 253 ? 253 : e;
+    const float down = __uint_as_float((254 - e) << 23);  // to below 2
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) a[i >> 1][i & 1] = pack_f16x2(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+    return __uint_as_float(e << 23);
+  }
+  template <typename F>
+  __device__ __forceinline__ void of(F chunk, float& x0, float& x1) const {
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two sums halve the chain
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 u = lds128(chunk(i));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        mma_f16(y & 1 ? s1 : s0, a[4 * i + y][0], 0, a[4 * i + y][1], 0, codes_f16x2<KVP_INT8>(w[y]),
+                codes_f16x2<KVP_INT8>(w[y] >> 16));
+    }
+    x0 = s0[0] + s1[0];
+    x1 = s0[1] + s1[1];
+  }
+};
+
+// O += V^T W over a unit's tokens (n of them, where kCut).
+template <int kFormat, int D, bool kCut>
+__device__ __forceinline__ void add_values(uint32_t addr, uint32_t swizzle, int n, int c, const uint32_t (&wt)[2],
+                                           float (&o)[D / 16][4]) {
+  const int left = n - 4 * c;  // what lies behind the context may be anything
+  const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << 8 * left) - 1;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t w[4];
+    ldsm_bytes_t(addr + ((uint32_t)(i << 5) ^ swizzle), w);
+    if constexpr (kCut) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) w[y] &= keep;
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      mma_f16(o[2 * i + y], codes_f16x2<kFormat>(w[2 * y]), codes_f16x2<kFormat>(w[2 * y + 1]),
+              codes_f16x2<kFormat>(w[2 * y] >> 16), codes_f16x2<kFormat>(w[2 * y + 1] >> 16), wt[0], wt[1]);
+  }
+}
+
+// log2 of a scale, rounded up; below 2^-64 a scale counts as that.
+__device__ __forceinline__ float log2_above(float scale) {
+  const int e = (int)(__float_as_uint(scale) >> 23) - 126;
+  return (float)(e < -64 ? -64 : e);
+}
+
 // Thread (r, c) of a warp (r = lane / 4, c = lane % 4) has head r's scores of
-// tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a unit and the sums of heads 2c, 2c + 1 in
-// columns D / 8 * r .. + D / 8 - 1: o[i][y + 2 z] is head 2c + y, column
-// D / 8 * r + 2 i + z.
-template <int kFormat, int D, int G>
+// tokens 4c .. 4c + 3 of a unit and the sums of heads 2c, 2c + 1 in columns
+// 16 i + r + 8 z: o[i][y + 2 z] is head 2c + y.
+template <int kFormat, int D, int G, bool kUniform>
 __device__ void consume(const Args& x, Smem<D, G>& sm) {
-  constexpr int KS = D / 16;  // k-steps of S; tiles of O
-  constexpr int W = D / 32;   // 4-byte words of a token's columns that a thread has
+  constexpr int KS = D / 16;  // tiles of O
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = x.num_kv_heads;
-  const int g = warp % Hkv, sub = warp / Hkv, subs = kConsumers / Hkv;
+  const int g = warp & (Hkv - 1), sub = warp >> x.head_shift, subs = kConsumers >> x.head_shift;
   const int head0 = g * G;
   const int r = lane >> 2, c = lane & 3;
   const bool oc[2] = {2 * c < G, 2 * c + 1 < G};
-  const uint32_t region = (uint32_t)((sub * Hkv + g) * kUnit * D);
+  const uint32_t region = (uint32_t)(warp * kUnit * D);
   const uint32_t kbase = smem_u32(sm.k[0]) + region, vbase = smem_u32(sm.v[0]) + region;
   // Byte offset of 16-byte chunk q of a token's row: the copies' swizzle.
   auto chunk = [](int row, int q) {
     return (uint32_t)(D == 128 ? row * 128 + ((q ^ (row & 7)) << 4) : row * 64 + ((q ^ (row >> 1 & 3)) << 4));
   };
+  // V: row lane % 16, chunk 2i + lane / 16.
+  const uint32_t vrow = (uint32_t)(lane & 15) * D;
+  const uint32_t vswizzle = (uint32_t)(((D == 128 ? lane & 7 : lane >> 1 & 3) ^ (lane >> 4)) << 4);
 
-  uint32_t qa[KS][2];
+  Scores<kFormat, D> q;
   float o[KS][4];
   float m = -INFINITY, l = 0.f, cq = 0.f;
   int b = 0, s = 0, seg = 0;
@@ -338,76 +462,69 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
 
   while (true) {
     if (!mbar_wait(&sm.full[s], ph, x.status)) return;
-    const int flags = sm.meta[s].flags;
+    const uint4 meta = *reinterpret_cast<const uint4*>(&sm.meta[s]);
+    const int flags = (int)meta.y;
     if (flags & F_DONE) break;
     if (flags & F_NEW) {
-      b = sm.meta[s].b;
-      // 2 KS contiguous words of head r's query, at most 2 in size
-      float top = 0.f;
-      uint32_t raw[KS * 2];
+      b = (int)meta.x;
+      // D / 4 contiguous numbers of head r's query
+      uint32_t raw[D / 8];
 #pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
+      for (int i = 0; i < D / 32; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
         if (r < G)
           u = *reinterpret_cast<const uint4*>(x.a.q + (int64_t)b * x.a.q_stride + (int64_t)(head0 + r) * D +
-                                              c * (2 * KS * 2) + i * 8);
+                                              c * (D / 4) + i * 8);
         raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
       }
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < KS * 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(raw[i])), fabsf(bf16hi(raw[i]))));
+      for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(raw[i])), fabsf(bf16hi(raw[i]))));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      uint32_t e = __float_as_uint(top) >> 23;
-      e = e < 1 ? 1 : e > 253 ? 253 : e;
-      const float down = __uint_as_float((254 - e) << 23);
-      cq = __uint_as_float(e << 23) * x.scale_log2;
-#pragma unroll
-      for (int i = 0; i < KS * 2; ++i) qa[i >> 1][i & 1] = pack_f16x2(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+      cq = q.load(raw, __float_as_uint(top) >> 23) * x.scale_log2;
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       m = -INFINITY;
       l = 0.f;
     }
-    const int n = sm.meta[s].n[sub];
+    const int n = (int)((sub < 4 ? meta.z : meta.w) >> 8 * (sub & 3)) & 0xff;
     if (n > 0) {
       const uint32_t kst = kbase + (uint32_t)(s * half_bytes<D>()), vst = vbase + (uint32_t)(s * half_bytes<D>());
-      float sc[2][4];
+      float sc[4];  // tokens 4c + i
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two sums halve the chain
-        const int row = j * 8 + r;
-#pragma unroll
-        for (int i = 0; i < KS / 4; ++i) {
-          const uint4 u = lds128(kst + chunk(row, c * (KS / 4) + i));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            mma_f16(y & 1 ? s1 : s0, qa[4 * i + y][0], 0, qa[4 * i + y][1], 0, codes_f16x2<kFormat>(w[y]),
-                    codes_f16x2<kFormat>(w[y] >> 16));
-        }
-        sc[j][0] = s0[0] + s1[0];
-        sc[j][1] = s0[1] + s1[1];
+        const int row = (r >> 1) * 4 + 2 * j + (r & 1);
+        q.of([&](int i) { return kst + chunk(row, c * (D / 64) + i); }, sc[2 * j], sc[2 * j + 1]);
       }
-      const float* scales = sm.scales[s][0] + (sub * Hkv + g) * kUnit + 2 * c;
-      float vs[2][2], top = -INFINITY;
+      float vs[4], lv[4];
+      if constexpr (kUniform) {
+        const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * warp]);
+        const float kq = scale.x * cq;
+        const float lu = log2_above(scale.y);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 ks = *reinterpret_cast<const float2*>(scales + 8 * j);
-        const float2 v2 = *reinterpret_cast<const float2*>(scales + kStageScales + 8 * j);
+        for (int i = 0; i < 4; ++i) sc[i] *= kq, vs[i] = scale.y, lv[i] = lu;
+      } else {
+        const float4 ks = *reinterpret_cast<const float4*>(&sm.scales[s][0][warp * kUnit + 4 * c]);
+        const float4 v4 = *reinterpret_cast<const float4*>(&sm.scales[s][1][warp * kUnit + 4 * c]);
+        sc[0] *= cq * ks.x, sc[1] *= cq * ks.y, sc[2] *= cq * ks.z, sc[3] *= cq * ks.w;
+        vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const bool valid = 8 * j + 2 * c + y < n;
-          sc[j][y] = valid ? sc[j][y] * cq * (y ? ks.y : ks.x) : -INFINITY;
-          vs[j][y] = valid ? (y ? v2.y : v2.x) : 0.f;
-          // log2 of the scale, rounded up; below 2^-64 it counts as that
-          const int e = (int)(__float_as_uint(vs[j][y]) >> 23) - 126;
-          top = fmaxf(top, sc[j][y] + (float)(e < -64 ? -64 : e));
+        for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[i]);
+      }
+      if (n < kUnit) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool valid = 4 * c + i < n;
+          sc[i] = valid ? sc[i] : -INFINITY;
+          if (!kUniform && !valid) vs[i] = lv[i] = 0.f;
         }
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const bool grow = top > m + 8.f;  // also a sequence's first unit
-      if (__any_sync(0xffffffffu, grow)) {
+      float top = fmaxf(fmaxf(sc[0] + lv[0], sc[1] + lv[1]), fmaxf(sc[2] + lv[2], sc[3] + lv[3]));
+      if (__any_sync(0xffffffffu, top > m + 8.f)) {  // also a sequence's first unit
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const bool grow = top > m + 8.f;
         const float alpha = grow ? fast_exp2(m - top) : 1.f;
         if (grow) {
           m = top;
@@ -422,40 +539,14 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
           o[i][3] *= a1;
         }
       }
-      uint32_t wt[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float p0 = fast_exp2(sc[j][0] - m), p1 = fast_exp2(sc[j][1] - m);
-        l += p0 + p1;
-        wt[j] = pack_f16x2(p0 * vs[j][0], p1 * vs[j][1]);
-      }
-      // Tokens 2c, 2c + 1, 2c + 8, 2c + 9: this thread's columns.
-      uint32_t vw[4][W];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int row = 2 * c + (t & 1) + (t >> 1) * 8;
-        if constexpr (D == 128) {
-          const uint4 u = lds128(vst + chunk(row, r));
-          vw[t][0] = u.x, vw[t][1] = u.y, vw[t][2] = u.z, vw[t][3] = u.w;
-        } else {
-          const uint2 u = lds64(vst + chunk(row, r >> 1) + (r & 1) * 8);
-          vw[t][0] = u.x, vw[t][1] = u.y;
-        }
-        if (n < kUnit && row >= n) {  // what lies behind the context may be anything
-#pragma unroll
-          for (int i = 0; i < W; ++i) vw[t][i] = 0;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], y ? 0x7362 : 0x5140);
-          const uint32_t hi = __byte_perm(vw[2][i], vw[3][i], y ? 0x7362 : 0x5140);
-          mma_f16(o[2 * i + y], codes_f16x2<kFormat>(lo), codes_f16x2<kFormat>(lo >> 16), codes_f16x2<kFormat>(hi),
-                  codes_f16x2<kFormat>(hi >> 16), wt[0], wt[1]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) sc[i] = fast_exp2(sc[i] - m);
+      l += (sc[0] + sc[1]) + (sc[2] + sc[3]);
+      const uint32_t wt[2] = {pack_f16x2(sc[0] * vs[0], sc[1] * vs[1]), pack_f16x2(sc[2] * vs[2], sc[3] * vs[3])};
+      if (n == kUnit)
+        add_values<kFormat, D, false>(vst + vrow, vswizzle, n, c, wt, o);
+      else
+        add_values<kFormat, D, true>(vst + vrow, vswizzle, n, c, wt, o);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
@@ -474,7 +565,7 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
       // Warps of the same kv head: sub 0 takes the others' parts, some columns
       // at a time (bounded waits both ways).
       constexpr int C = join_columns<D, G>();
-      constexpr int T = C / 16;  // tiles of a round: 2 T columns of each r
+      constexpr int T = C / 16;  // tiles of a round
       float M[2], w0[2];
 #pragma unroll
       for (int i0 = 0; i0 < KS; i0 += T, ++seg) {
@@ -486,8 +577,10 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
             if (!oc[y]) continue;
             float* to = mine[2 * c + y];
 #pragma unroll
-            for (int i = 0; i < T; ++i)
-              *reinterpret_cast<float2*>(to + 2 * (r * T + i)) = make_float2(o[i0 + i][y], o[i0 + i][y + 2]);
+            for (int i = 0; i < T; ++i) {
+              to[16 * i + r] = o[i0 + i][y];
+              to[16 * i + r + 8] = o[i0 + i][y + 2];
+            }
             if (r == 0) *reinterpret_cast<float2*>(to + C) = make_float2(mh[y], lh[y]);
           }
           __syncwarp();
@@ -515,9 +608,8 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
               if (i0 == 0) lh[y] += w * ml.y;
 #pragma unroll
               for (int i = 0; i < T; ++i) {
-                const float2 u = *reinterpret_cast<const float2*>(from + 2 * (r * T + i));
-                o[i0 + i][y] += w * u.x;
-                o[i0 + i][y + 2] += w * u.y;
+                o[i0 + i][y] += w * from[16 * i + r];
+                o[i0 + i][y + 2] += w * from[16 * i + r + 8];
               }
             }
             if (i0 + T >= KS) mh[y] = M[y];
@@ -534,27 +626,27 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
       const int h = head0 + 2 * c + y;
       if (flags & F_WHOLE) {
         const float inv = 1.f / lh[y];
-        uint16_t* to = x.a.out + (int64_t)b * x.a.out_stride + (int64_t)h * D + r * (D / 8);
+        __nv_bfloat16* to =
+            reinterpret_cast<__nv_bfloat16*>(x.a.out + (int64_t)b * x.a.out_stride + (int64_t)h * D) + r;
 #pragma unroll
-        for (int i = 0; i < KS; i += 4)
-          *reinterpret_cast<uint4*>(to + 2 * i) =
-              make_uint4(pack_bf16x2(o[i][y] * inv, o[i][y + 2] * inv),
-                         pack_bf16x2(o[i + 1][y] * inv, o[i + 1][y + 2] * inv),
-                         pack_bf16x2(o[i + 2][y] * inv, o[i + 2][y + 2] * inv),
-                         pack_bf16x2(o[i + 3][y] * inv, o[i + 3][y + 2] * inv));
+        for (int i = 0; i < KS; ++i) {
+          to[16 * i] = __float2bfloat16_rn(o[i][y] * inv);
+          to[16 * i + 8] = __float2bfloat16_rn(o[i][y + 2] * inv);
+        }
       } else {
         float* to = x.part + (((size_t)blockIdx.x * 2 + (flags & F_ENTERED ? 0 : 1)) * x.a.num_heads + h) * (D + 4);
 #pragma unroll
-        for (int i = 0; i < KS; i += 2)
-          *reinterpret_cast<float4*>(to + r * (D / 8) + 2 * i) =
-              make_float4(o[i][y], o[i][y + 2], o[i + 1][y], o[i + 1][y + 2]);
+        for (int i = 0; i < KS; ++i) {
+          to[16 * i + r] = o[i][y];
+          to[16 * i + r + 8] = o[i][y + 2];
+        }
         if (r == 0) *reinterpret_cast<float2*>(to + D) = make_float2(mh[y], lh[y]);
       }
     }
   }
 }
 
-template <int kFormat, int D, int G>
+template <int kFormat, int D, int G, bool kUniform>
 __global__ void __launch_bounds__(kThreads, 2)
     quant_split_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                        const Args x) {
@@ -580,9 +672,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x >> 5 == kConsumers)
-    produce<D, G>(x, &mapK, &mapV, sm);
+    produce<D, G, kUniform>(x, &mapK, &mapV, sm);
   else
-    consume<kFormat, D, G>(x, sm);
+    consume<kFormat, D, G, kUniform>(x, sm);
 }
 
 // Joins the parts of the sequences that are cut: block (i, j) has sequence (or
@@ -712,10 +804,11 @@ cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream
   if (!unit_map(&mk, c.k, c) || !unit_map(&mv, c.v, c)) return cudaErrorInvalidValue;
   constexpr size_t smem = sizeof(Smem<D, G>) + 1024;
   static_assert(smem <= 113 * 1024, "two CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(quant_split_kernel<kFormat, D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  auto split = (1 << c.scale_shift) >= kUnit && c.block_size % kUnit == 0 ? quant_split_kernel<kFormat, D, G, true>
+                                                                           : quant_split_kernel<kFormat, D, G, false>;
+  cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch_shadow(quant_split_kernel<kFormat, D, G>, dim3(p.ctas), kThreads, smem, stream, mk, mv, x);
+  e = launch_shadow(split, dim3(p.ctas), kThreads, smem, stream, mk, mv, x);
   if (e != cudaSuccess) return e;
   // Slices of the parts for each head: as many as a cut sequence has parts,
   // about.
@@ -755,6 +848,8 @@ cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, i
   x.page_units = (c.block_size + kUnit - 1) / kUnit;
   x.scale_shift = c.scale_shift;
   x.num_kv_heads = c.num_kv_heads;
+  x.head_shift = 0;
+  while (1 << x.head_shift < c.num_kv_heads) ++x.head_shift;
   x.k_scales = c.k_scales;
   x.v_scales = c.v_scales;
   x.scale_log2 = a.softmax_scale * 1.4426950408889634f;
