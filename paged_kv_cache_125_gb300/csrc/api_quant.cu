@@ -285,6 +285,9 @@ int attn_decode_quant(const kvp_bf16* q, int64_t q_stride_tok, const void* k_cac
                               max_blocks_per_seq, context_lens, num_seqs, max_context_len, num_heads, num_kv_heads,
                               head_dim, out, out_stride_tok);
   if (rc || num_seqs == 0) return rc;
+  // The kernel counts work in units of up to 16 tokens of a page.
+  if ((int64_t)num_seqs * max_blocks_per_seq * ((block_size + 15) / 16) >= (int64_t)1 << 31)
+    return set_last_error(KVP_ERR_UNSUPPORTED, "%s: tables of 2^31 or more units of 16 tokens", fn);
   const kvp::QuantCache c = cache_of(k_cache, v_cache, k_scales, v_scales, format, num_blocks, block_size,
                                      scale_tokens, num_kv_heads, head_dim);
   rc = check_cache_pointers(fn, c);

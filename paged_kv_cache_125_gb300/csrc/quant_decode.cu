@@ -7,13 +7,14 @@
 //
 // * Work is counted in units: up to 16 tokens of one page (all kv heads).  The
 //   units of all sequences, end to end, are cut into equal contiguous shares, one
-//   per CTA, two CTAs per SM.  A sequence that a cut falls into leaves partial
+//   per CTA, one CTA per SM.  A sequence that a cut falls into leaves partial
 //   results, which the merge kernel joins.
-// * A producer warp streams units into a ring in shared memory: one tensor copy
-//   each for K and V lands a unit as [kv head][token][head_dim] bytes, swizzled
-//   so that the consumers' 16-byte loads fall in different banks; the tokens'
-//   scales come by 4-byte asynchronous copies that arrive on the same barrier.
-//   A lane looks up the page of one unit, 32 units ahead at a time.
+// * A producer warp streams units through a ring of five stages in shared memory:
+//   one tensor copy each for K and V lands a unit as [kv head][token][head_dim]
+//   bytes, swizzled so that the consumers' 16-byte loads fall in different banks;
+//   the tokens' scales come by 4-byte asynchronous copies that arrive on the same
+//   barrier.  A lane looks up the page of one unit, 32 units ahead at a time.
+//   Codes are marked as read once: L2 drops them first.
 // * Eight consumer warps: warp w has kv head w % Hkv of the stage's unit w / Hkv
 //   (a stage is 8 / Hkv units).
 //   S = q K^T, N = 8 tokens, the query heads of the kv head in M.  The numbers of
@@ -44,8 +45,10 @@ namespace {
 
 constexpr int kConsumers = 8;
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kStages = 3;
+constexpr int kStages = 5;
 constexpr int kUnit = 16;  // tokens
+constexpr int kTold = 8;   // segments that the producer may be ahead by, at most
+static_assert(kStages + 2 <= kTold, "a segment is told over one that all warps have finished");
 
 // A stage holds 8 (unit, kv head) pairs of K and of V.
 template <int D>
@@ -54,19 +57,12 @@ __host__ __device__ constexpr int half_bytes() {
 }
 constexpr int kStageScales = kConsumers * kUnit;  // of K, and as many of V
 
-// Warps of one kv head join their parts through shared memory, this many columns
-// of head_dim at a time, so that the ring keeps its three stages.
-template <int D, int G>
-__host__ __device__ constexpr int join_columns() {
-  return G == 8 ? 32 : G == 4 && D == 128 ? 64 : D;
-}
-
-enum : int { F_NEW = 1, F_LAST = 2, F_WHOLE = 4, F_ENTERED = 8, F_DONE = 16 };
+enum : int { F_LAST = 1, F_WHOLE = 2, F_ENTERED = 4 };
 
 struct alignas(16) StageMeta {
-  int b;
-  int flags;
   uint8_t n[8];  // tokens of each unit (read as two words)
+  int flags;
+  int pad;
 };
 
 // A sequence that is cut: its first and last CTA (last < first: not cut).
@@ -76,11 +72,21 @@ struct Chain {
   int last;
 };
 
+// Quotients of n < 2^31 by a number that the host knows: with 2^s >= d and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(m n / 2^32)) >> s.
+struct Divisor {
+  uint32_t m, s;
+};
+__device__ __forceinline__ int quotient(int n, Divisor d) {
+  return (int)(((uint32_t)n + __umulhi(d.m, (uint32_t)n)) >> d.s);
+}
+
 struct Args {
   QuantDecodeArgs a;
   int64_t num_blocks;
   int block_size;
   int page_units;  // units of a full page
+  Divisor by_block, by_page_units;
   int scale_shift;
   int num_kv_heads;
   int head_shift;  // log2 of num_kv_heads
@@ -93,15 +99,25 @@ struct Args {
   int* status;
 };
 
+// Units start .. end - 1 of the batch: CTA i has `each` of them, and one more where
+// i < more.  The first are units skip, skip + 1, ... of sequence seq.
+struct Share {
+  int start, end, each, more;
+  int seq, skip, len;
+};
+
 template <int D, int G>
 struct Smem {
-  uint8_t k[kStages][half_bytes<D>()];
-  uint8_t v[kStages][half_bytes<D>()];
-  float scales[kStages][2][kStageScales];  // [kv head of a unit][token], or (K, V) of each
-  StageMeta meta[kStages];
-  uint64_t full[kStages], empty[kStages];
+  alignas(1024) uint8_t k[kStages][half_bytes<D>()];
+  alignas(1024) uint8_t v[kStages][half_bytes<D>()];
+  alignas(16) float scales[kStages][2][kStageScales];  // [kv head of a unit][token], or (K, V) of each
+  alignas(16) StageMeta meta[kStages];
+  alignas(8) float join[kConsumers - 1][G][D + 2];  // O, m, l
+  alignas(8) uint64_t full[kStages], empty[kStages], told[kTold];
   uint64_t joined[kConsumers], taken[kConsumers];
-  float join[kConsumers - 1][G][join_columns<D, G>() + 2];
+  int2 warp_sums[kConsumers + 1];  // units and sequences that have any, of each warp's run
+  Share share;
+  int seg_seq[kTold];  // the sequence of segment i at i % kTold
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -161,175 +177,241 @@ __device__ __forceinline__ int clamp_len(int c, int cap) { return c < 0 ? 0 : c 
 
 // Units of a sequence of n tokens.
 __device__ __forceinline__ int units_of(const Args& x, int n) {
-  const int pages = n / x.block_size, rest = n - pages * x.block_size;
+  if (x.page_units * kUnit == x.block_size) return (n + kUnit - 1) / kUnit;
+  const int pages = quotient(n, x.by_block), rest = n - pages * x.block_size;
   return pages * x.page_units + (rest + kUnit - 1) / kUnit;
+}
+
+// ---------------------------------------------------------------- shares
+
+// This CTA's share of the batch's units, found by all of its threads at once (one
+// trip to the context lengths): each has a run of neighbouring sequences.
+template <int D, int G>
+__device__ void find_share(const Args& x, Smem<D, G>& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x;
+  const int cap = x.a.max_blocks * x.block_size;
+  const int per = x.a.num_seqs <= kThreads ? 1 : (x.a.num_seqs + kThreads - 1) / kThreads;
+  const int b0 = threadIdx.x * per, b1 = b0 + per < x.a.num_seqs ? b0 + per : x.a.num_seqs;
+  int mine = 0, live = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int c = x.a.context_lens[b];
+    if (c < 0 || c > cap) record_error(x.status, KVP_ERR_DEVICE_DATA);
+    const int u = units_of(x, clamp_len(c, cap));
+    mine += u;
+    live += u > 0;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 31) sm.warp_sums[warp] = make_int2(incl, live);
+  __syncthreads();
+  int before = incl - mine, total = 0;
+  live = 0;
+#pragma unroll
+  for (int w = 0; w <= kConsumers; ++w) {
+    const int2 y = sm.warp_sums[w];
+    if (w < warp) before += y.x;
+    total += y.x;
+    live += y.y;
+  }
+  // CTAs that get a share: one for four units or one for a sequence, whichever
+  // are more.
+  int ctas = (total + 3) / 4 > live ? (total + 3) / 4 : live;
+  if (ctas > (int)gridDim.x) ctas = gridDim.x;
+  if (ctas < 1) ctas = 1;
+  const int q = (unsigned)total / (unsigned)ctas, rest = total - q * ctas;
+  const int start = me < ctas ? me * q + (me < rest ? me : rest) : total;
+  const int end = me < ctas ? start + q + (me < rest) : total;
+  if (threadIdx.x == 0) sm.share = {start, end, q, rest, 0, 0, 0};
+  __syncthreads();
+  if (start < end && before <= start && start < before + mine) {  // one thread
+    for (int b = b0; b < b1; ++b) {
+      const int len = clamp_len(x.a.context_lens[b], cap), u = units_of(x, len);
+      if (start < before + u) {
+        sm.share.seq = b;
+        sm.share.skip = start - before;
+        sm.share.len = len;
+        break;
+      }
+      before += u;
+    }
+  }
+  __syncthreads();
+}
+
+// Rows without a context are zero, and not cut.
+template <int D>
+__device__ void empty_rows(const Args& x) {
+  const int cap = x.a.max_blocks * x.block_size;
+  for (int b = blockIdx.x + gridDim.x * (threadIdx.x >> 5); b < x.a.num_seqs; b += gridDim.x * (kThreads / 32)) {
+    if (clamp_len(x.a.context_lens[b], cap) != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(x.a.out + (int64_t)b * x.a.out_stride);
+    for (int j = threadIdx.x & 31; j < x.a.num_heads * D / 8; j += 32) o[j] = make_uint4(0, 0, 0, 0);
+    if (x.by_seq && (threadIdx.x & 31) == 0) x.chains[b] = {b, 0, -1};
+  }
 }
 
 // ---------------------------------------------------------------- producer
 
 template <int D, int G, bool kUniform>
-__device__ void produce(const Args& x, const CUtensorMap* mapK, const CUtensorMap* mapV, Smem<D, G>& sm) {
-  const int lane = threadIdx.x & 31;
-  const int Hkv = x.num_kv_heads, per_stage = kConsumers / Hkv;
-  const int cap = x.a.max_blocks * x.block_size;
-  const int me = blockIdx.x;
-  const uint32_t unit_bytes = (uint32_t)(kUnit * Hkv * D);
-
-  long long total = 0;
-  for (int i = lane; i < x.a.num_seqs; i += 32) {
-    const int c = x.a.context_lens[i];
-    if (c < 0 || c > cap) record_error(x.status, KVP_ERR_DEVICE_DATA);
-    total += units_of(x, clamp_len(c, cap));
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  // CTAs that get a share: no more than leave each four units.
-  const long long P = total >= 4LL * gridDim.x ? gridDim.x : (total + 3) / 4;
-  const long long start = me < P ? total * me / P : total, end = me < P ? total * (me + 1) / P : total;
-
-  // Rows without a context are zero.
-  for (int b = me; b < x.a.num_seqs; b += gridDim.x) {
-    if (clamp_len(x.a.context_lens[b], cap) != 0) continue;
-    uint4* o = reinterpret_cast<uint4*>(x.a.out + (int64_t)b * x.a.out_stride);
-    for (int i = lane; i < x.a.num_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-    if (x.by_seq && lane == 0) x.chains[b] = {b, 0, -1};
-  }
-  if (!x.by_seq && lane == 0) x.chains[me] = {0, 0, -1};
-
-  // The first sequence of the share, and the units before it.
-  int b = 0;
-  long long before = 0;
-  if (start < end) {
-    for (int base = 0; base < x.a.num_seqs; base += 32) {
-      const int i = base + lane;
-      const int c = i < x.a.num_seqs ? units_of(x, clamp_len(x.a.context_lens[i], cap)) : 0;
-      long long incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, i < x.a.num_seqs && before + incl > start);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        b = base + l;
-        before += __shfl_sync(0xffffffffu, incl - c, l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-  }
-
+struct Producer {
+  const Args& x;
+  Smem<D, G>& sm;
+  const CUtensorMap *mapK, *mapV;
+  int left;     // units of the share behind the present segment
+  int b, skip;  // the next segment: its sequence and first unit
+  int seq = 0, u = 0, u1 = 0, at = 0, len = 0, seg_flags = 0;
+  int row = 0, n = 0, row_next = 0, n_next = 0;  // this lane's unit of the present 32, and of the next
   int s = 0;
-  uint32_t ph = 0, issued = 0, issued_ph = 0;
-  bool ok = true;
-  long long pos = start;
-  for (; ok && pos < end && b < x.a.num_seqs; ++b) {
-    const int len = clamp_len(x.a.context_lens[b], cap);
-    const int units = units_of(x, len);
-    if (units == 0) continue;
-    const int u0 = (int)(pos - before);
-    const int u1 = (int)((end < before + units ? end : before + units) - before);
-    const bool cut = u0 > 0 || u1 < units;
-    if (u0 == 0 && lane == 0) {  // it begins here: the CTA of its last unit
-      int last = me;
-      if (cut) {
-        last = (int)((before + units - 1) * P / total);
-        while (total * (last + 1) / P <= before + units - 1) ++last;
-      }
-      if (x.by_seq)
-        x.chains[b] = {b, me, cut ? last : me - 1};
-      else if (cut)
-        x.chains[me] = {b, me, last};
+  uint32_t ph = 0, segs = 0, issued = 0, issued_ph = 0;
+  const uint64_t once = policy_evict_first();
+  bool more = true;
+
+  __device__ __forceinline__ Producer(const Args& x_, Smem<D, G>& sm_, const CUtensorMap* k, const CUtensorMap* v)
+      : x(x_), sm(sm_), mapK(k), mapV(v) {
+    left = sm.share.end - sm.share.start;
+    b = sm.share.seq;
+    skip = sm.share.skip;
+    len = sm.share.len;
+  }
+
+  __device__ __forceinline__ void look_up(int unit, int& r, int& m) {
+    r = m = 0;
+    if (unit >= u1) return;
+    const int page = quotient(unit, x.by_page_units), off = (unit - page * x.page_units) * kUnit;
+    int block = x.a.block_tables[(int64_t)seq * x.a.max_blocks + page];
+    if (block < 0 || block >= x.num_blocks) {
+      record_error(x.status, KVP_ERR_DEVICE_DATA);
+      block = 0;  // never read a page outside the pool
     }
-    const int seg_flags = (cut ? 0 : F_WHOLE) | (u0 > 0 ? F_ENTERED : 0);
-    // This lane's unit of the present 32, and of the next.
-    int row = 0, n = 0, row_next, n_next;
-    auto look_up = [&](int u, int& r, int& m) {
-      r = m = 0;
-      if (u >= u1) return;
-      const int page = u / x.page_units, off = (u - page * x.page_units) * kUnit;
-      int block = x.a.block_tables[(int64_t)b * x.a.max_blocks + page];
-      if (block < 0 || block >= x.num_blocks) {
-        record_error(x.status, KVP_ERR_DEVICE_DATA);
-        block = 0;  // never read a page outside the pool
+    r = block * x.block_size + off;
+    m = x.block_size - off < kUnit ? x.block_size - off : kUnit;
+    const int rest = len - page * x.block_size - off;
+    if (m > rest) m = rest;
+  }
+
+  // Tells the consumers the next segment's sequence (-1: no more), whose query they
+  // fetch while its first unit is on its way.  Nothing reads slot segs % kTold any more:
+  // of the segments that came after the one in it, all stages but the last
+  // kStages were given back, and seven segments have seven stages or more.
+  __device__ __forceinline__ void tell(int sequence) {
+    if ((threadIdx.x & 31) == 0) {
+      sm.seg_seq[segs & (kTold - 1)] = sequence;
+      mbar_arrive(&sm.told[segs & (kTold - 1)]);
+    }
+    ++segs;
+  }
+
+  __device__ __forceinline__ void next_segment() {
+    const int lane = threadIdx.x & 31, cap = x.a.max_blocks * x.block_size;
+    int units = 0;
+    if (segs == 0 && left > 0) {
+      units = units_of(x, len);
+    } else {
+      for (; left > 0 && b < x.a.num_seqs; ++b) {
+        len = clamp_len(x.a.context_lens[b], cap);
+        units = units_of(x, len);
+        if (units) break;
       }
-      r = block * x.block_size + off;
-      m = x.block_size - off < kUnit ? x.block_size - off : kUnit;
-      const int left = len - page * x.block_size - off;
-      if (m > left) m = left;
-    };
-    look_up(u0 + lane, row_next, n_next);
-    for (int u = u0; ok && u < u1; u += per_stage) {
-      const int at = (u - u0) & 31;
-      if (at == 0) {
-        row = row_next;
-        n = n_next;
-        look_up(u + 32 + lane, row_next, n_next);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ph ^ 1u, x.status))) {
-        ok = false;
-        break;
-      }
-      const int unit = lane - at;  // of the stage
-      const bool mine = unit >= 0 && unit < per_stage;
-      if (mine) sm.meta[s].n[unit] = (uint8_t)n;
-      if (lane == 0) {
-        sm.meta[s].b = b;
-        sm.meta[s].flags = seg_flags | (u == u0 ? F_NEW : 0) | (u + per_stage >= u1 ? F_LAST : 0);
-      }
-      const int count = __popc(__ballot_sync(0xffffffffu, mine && n > 0));
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * count * unit_bytes);
-      __syncwarp();
-      if (mine && n > 0) {
-        tma_load_3d(sm.k[s] + unit * unit_bytes, mapK, 0, row, 0, &sm.full[s]);
-        tma_load_3d(sm.v[s] + unit * unit_bytes, mapV, 0, row, 0, &sm.full[s]);
-      }
-      if constexpr (kUniform) {
-        const int i = lane & 7, su = i >> x.head_shift;
-        const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
-        if (lane < 16 && m > 0)
-          copy4_async(&sm.scales[s][0][2 * i + (lane >> 3)],
-                      (lane < 8 ? x.k_scales : x.v_scales) +
-                          ((int64_t)(r >> x.scale_shift) << x.head_shift) + (i & (Hkv - 1)));
-      } else {
+    }
+    if (!units) {
+      more = false;
+      tell(-1);
+      return;
+    }
+    tell(b);
+    const int begins = sm.share.end - left - skip;  // the sequence's first unit among all
+    const int take = left < units - skip ? left : units - skip;
+    seq = b++;
+    u = skip;
+    u1 = u + take;
+    left -= take;
+    skip = 0;
+    at = 0;
+    look_up(u + lane, row_next, n_next);
+    const bool cut = u > 0 || u1 < units;
+    if (u == 0 && lane == 0) {  // it begins here: the CTA of its last unit
+      const int end = begins + units - 1, each = sm.share.each, longer = sm.share.more * (each + 1);
+      const int last = !cut ? (int)blockIdx.x - 1
+                            : end < longer ? end / (each + 1) : sm.share.more + (end - longer) / each;
+      if (x.by_seq)
+        x.chains[seq] = {seq, (int)blockIdx.x, last};
+      else if (cut)
+        x.chains[blockIdx.x] = {seq, (int)blockIdx.x, last};
+    }
+    seg_flags = (cut ? 0 : F_WHOLE) | (u > 0 ? F_ENTERED : 0);
+  }
+
+  // Copies of one stage, once its slot is given back.  False: a wait expired.
+  __device__ __forceinline__ bool step() {
+    if (!more) return true;
+    if (u >= u1) {
+      next_segment();
+      if (!more) return true;
+    }
+    const int lane = threadIdx.x & 31;
+    const int Hkv = x.num_kv_heads, per_stage = kConsumers >> x.head_shift;
+    const uint32_t unit_bytes = (uint32_t)(kUnit * Hkv * D);
+    if (at == 0) {
+      row = row_next;
+      n = n_next;
+      look_up(u + 32 + lane, row_next, n_next);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ph ^ 1u, x.status))) return false;
+    const int unit = lane - at;  // of the stage
+    const bool mine = unit >= 0 && unit < per_stage;
+    if (mine) sm.meta[s].n[unit] = (uint8_t)n;
+    if (lane == 0) sm.meta[s].flags = seg_flags | (u + per_stage >= u1 ? F_LAST : 0);
+    const int count = __popc(__ballot_sync(0xffffffffu, mine && n > 0));
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * count * unit_bytes);
+    __syncwarp();
+    if (mine && n > 0) {
+      tma_load_3d_hint(sm.k[s] + unit * unit_bytes, mapK, 0, row, 0, &sm.full[s], once);
+      tma_load_3d_hint(sm.v[s] + unit * unit_bytes, mapV, 0, row, 0, &sm.full[s], once);
+    }
+    if constexpr (kUniform) {
+      const int i = lane & 7, su = i >> x.head_shift;
+      const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
+      if (lane < 16 && m > 0)
+        copy4_async(&sm.scales[s][0][2 * i + (lane >> 3)],
+                    (lane < 8 ? x.k_scales : x.v_scales) + ((int64_t)(r >> x.scale_shift) << x.head_shift) +
+                        (i & (Hkv - 1)));
+    } else {
 #pragma unroll
-        for (int j = 0; j < kStageScales / 32; ++j) {
-          const int i = j * 32 + lane, t = lane % kUnit, head = i / kUnit & (Hkv - 1);
-          const int su = i / kUnit >> x.head_shift;
-          const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
-          if (t < m) {
-            const int64_t src = ((int64_t)((r + t) >> x.scale_shift) << x.head_shift) + head;
-            copy4_async(&sm.scales[s][0][i], x.k_scales + src);
-            copy4_async(&sm.scales[s][1][i], x.v_scales + src);
-          }
+      for (int j = 0; j < kStageScales / 32; ++j) {
+        const int i = j * 32 + lane, t = lane % kUnit, head = i / kUnit & (Hkv - 1);
+        const int su = i / kUnit >> x.head_shift;
+        const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
+        if (t < m) {
+          const int64_t src = ((int64_t)((r + t) >> x.scale_shift) << x.head_shift) + head;
+          copy4_async(&sm.scales[s][0][i], x.k_scales + src);
+          copy4_async(&sm.scales[s][1][i], x.v_scales + src);
         }
       }
-      arrive_after_copies(&sm.full[s]);
-      issued |= 1u << s;
-      issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1u;
-      }
     }
-    before += units;
-    pos = before;
-  }
-  if (ok && __all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ph ^ 1u, x.status))) {
-    if (lane == 0) {
-      sm.meta[s].flags = F_DONE;
-      mbar_arrive(&sm.full[s]);
-    }
-    __syncwarp();
     arrive_after_copies(&sm.full[s]);
-    return;
+    issued |= 1u << s;
+    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1u;
+    }
+    u += per_stage;
+    at = (at + per_stage) & 31;
+    return true;
   }
-  // A wait expired: let every copy this CTA issued land before the CTA exits.
-  for (int i = 0; i < kStages; ++i)
-    if (issued >> i & 1u) mbar_wait(&sm.full[i], issued_ph >> i & 1u, x.status);
-}
+
+  // After an expired wait: let every copy that was issued land before the CTA exits.
+  __device__ void drain() {
+    for (int i = 0; i < kStages; ++i)
+      if (issued >> i & 1u) mbar_wait(&sm.full[i], issued_ph >> i & 1u, x.status);
+  }
+};
 
 // ---------------------------------------------------------------- consumers
 
@@ -407,14 +489,14 @@ struct Scores<KVP_INT8, D> {
 
 // O += V^T W over a unit's tokens (n of them, where kCut).
 template <int kFormat, int D, bool kCut>
-__device__ __forceinline__ void add_values(uint32_t addr, uint32_t swizzle, int n, int c, const uint32_t (&wt)[2],
+__device__ __forceinline__ void add_values(uint32_t addr, int n, int c, const uint32_t (&wt)[2],
                                            float (&o)[D / 16][4]) {
   const int left = n - 4 * c;  // what lies behind the context may be anything
   const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << 8 * left) - 1;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     uint32_t w[4];
-    ldsm_bytes_t(addr + ((uint32_t)(i << 5) ^ swizzle), w);
+    ldsm_bytes_t(addr ^ (uint32_t)(i << 5), w);
     if constexpr (kCut) {
 #pragma unroll
       for (int y = 0; y < 4; ++y) w[y] &= keep;
@@ -436,7 +518,7 @@ __device__ __forceinline__ float log2_above(float scale) {
 // tokens 4c .. 4c + 3 of a unit and the sums of heads 2c, 2c + 1 in columns
 // 16 i + r + 8 z: o[i][y + 2 z] is head 2c + y.
 template <int kFormat, int D, int G, bool kUniform>
-__device__ void consume(const Args& x, Smem<D, G>& sm) {
+__device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
   constexpr int KS = D / 16;  // tiles of O
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = x.num_kv_heads;
@@ -446,28 +528,27 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
   const bool oc[2] = {2 * c < G, 2 * c + 1 < G};
   const uint32_t region = (uint32_t)(warp * kUnit * D);
   const uint32_t kbase = smem_u32(sm.k[0]) + region, vbase = smem_u32(sm.v[0]) + region;
-  // Byte offset of 16-byte chunk q of a token's row: the copies' swizzle.
-  auto chunk = [](int row, int q) {
-    return (uint32_t)(D == 128 ? row * 128 + ((q ^ (row & 7)) << 4) : row * 64 + ((q ^ (row >> 1 & 3)) << 4));
-  };
-  // V: row lane % 16, chunk 2i + lane / 16.
-  const uint32_t vrow = (uint32_t)(lane & 15) * D;
-  const uint32_t vswizzle = (uint32_t)(((D == 128 ? lane & 7 : lane >> 1 & 3) ^ (lane >> 4)) << 4);
+  // A thread's 16 bytes: chunk q of row t is at chunk q ^ (t & 7) (D 64: t >> 1 & 3),
+  // the copies' swizzle.  K: rows krow (tokens of scores 0, 1) and krow + 2, chunks
+  // D / 64 * c + i.  V: row lane % 16, chunks 2i + lane / 16.
+  const int krow = (r >> 1) * 4 + (r & 1);
+  const uint32_t koff = (uint32_t)(krow * D + ((c * (D / 64) ^ (D == 128 ? krow & 7 : krow >> 1 & 3)) << 4));
+  const uint32_t voff =
+      (uint32_t)((lane & 15) * D + (((D == 128 ? lane & 7 : lane >> 1 & 3) ^ (lane >> 4)) << 4));
+  constexpr uint32_t kRowFlip = D == 128 ? 32 : 16;  // of the swizzle from krow to krow + 2
 
   Scores<kFormat, D> q;
   float o[KS][4];
-  float m = -INFINITY, l = 0.f, cq = 0.f;
-  int b = 0, s = 0, seg = 0;
+  int s = 0;
   uint32_t ph = 0;
 
-  while (true) {
-    if (!mbar_wait(&sm.full[s], ph, x.status)) return;
-    const uint4 meta = *reinterpret_cast<const uint4*>(&sm.meta[s]);
-    const int flags = (int)meta.y;
-    if (flags & F_DONE) break;
-    if (flags & F_NEW) {
-      b = (int)meta.x;
-      // D / 4 contiguous numbers of head r's query
+  for (uint32_t seg = 0;; ++seg) {
+    float m = -INFINITY, l = 0.f, cq;
+    {
+      // The segment's query: D / 4 contiguous numbers of head r.
+      if (!mbar_wait(&sm.told[seg & (kTold - 1)], seg / kTold & 1, x.status)) return;
+      const int b = sm.seg_seq[seg & (kTold - 1)];
+      if (b < 0) return;
       uint32_t raw[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -485,76 +566,78 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
       cq = q.load(raw, __float_as_uint(top) >> 23) * x.scale_log2;
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      m = -INFINITY;
-      l = 0.f;
     }
-    const int n = (int)((sub < 4 ? meta.z : meta.w) >> 8 * (sub & 3)) & 0xff;
-    if (n > 0) {
-      const uint32_t kst = kbase + (uint32_t)(s * half_bytes<D>()), vst = vbase + (uint32_t)(s * half_bytes<D>());
-      float sc[4];  // tokens 4c + i
+    int flags;
+    do {
+      if (!mbar_wait(&sm.full[s], ph, x.status)) return;
+      const uint4 meta = *reinterpret_cast<const uint4*>(&sm.meta[s]);
+      flags = (int)meta.z;
+      const int n = (int)((sub < 4 ? meta.x : meta.y) >> 8 * (sub & 3)) & 0xff;
+      if (n > 0) {
+        const uint32_t kst = kbase + (uint32_t)(s * half_bytes<D>()), vst = vbase + (uint32_t)(s * half_bytes<D>());
+        float sc[4];  // tokens 4c + i
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = (r >> 1) * 4 + 2 * j + (r & 1);
-        q.of([&](int i) { return kst + chunk(row, c * (D / 64) + i); }, sc[2 * j], sc[2 * j + 1]);
-      }
-      float vs[4], lv[4];
-      if constexpr (kUniform) {
-        const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * warp]);
-        const float kq = scale.x * cq;
-        const float lu = log2_above(scale.y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] *= kq, vs[i] = scale.y, lv[i] = lu;
-      } else {
-        const float4 ks = *reinterpret_cast<const float4*>(&sm.scales[s][0][warp * kUnit + 4 * c]);
-        const float4 v4 = *reinterpret_cast<const float4*>(&sm.scales[s][1][warp * kUnit + 4 * c]);
-        sc[0] *= cq * ks.x, sc[1] *= cq * ks.y, sc[2] *= cq * ks.z, sc[3] *= cq * ks.w;
-        vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[i]);
-      }
-      if (n < kUnit) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool valid = 4 * c + i < n;
-          sc[i] = valid ? sc[i] : -INFINITY;
-          if (!kUniform && !valid) vs[i] = lv[i] = 0.f;
+        for (int j = 0; j < 2; ++j) {
+          q.of([&](int i) { return ((kst + koff) ^ (j * kRowFlip ^ i << 4)) + 2 * j * D; }, sc[2 * j], sc[2 * j + 1]);
         }
-      }
-      float top = fmaxf(fmaxf(sc[0] + lv[0], sc[1] + lv[1]), fmaxf(sc[2] + lv[2], sc[3] + lv[3]));
-      if (__any_sync(0xffffffffu, top > m + 8.f)) {  // also a sequence's first unit
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool grow = top > m + 8.f;
-        const float alpha = grow ? fast_exp2(m - top) : 1.f;
-        if (grow) {
-          m = top;
-          l *= alpha;
-        }
-        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+        float vs[4], lv[4];
+        if constexpr (kUniform) {
+          const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * warp]);
+          const float kq = scale.x * cq;
+          const float lu = log2_above(scale.y);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a1;
-          o[i][2] *= a0;
-          o[i][3] *= a1;
-        }
-      }
+          for (int i = 0; i < 4; ++i) sc[i] *= kq, vs[i] = scale.y, lv[i] = lu;
+        } else {
+          const float4 ks = *reinterpret_cast<const float4*>(&sm.scales[s][0][warp * kUnit + 4 * c]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&sm.scales[s][1][warp * kUnit + 4 * c]);
+          sc[0] *= cq * ks.x, sc[1] *= cq * ks.y, sc[2] *= cq * ks.z, sc[3] *= cq * ks.w;
+          vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = fast_exp2(sc[i] - m);
-      l += (sc[0] + sc[1]) + (sc[2] + sc[3]);
-      const uint32_t wt[2] = {pack_f16x2(sc[0] * vs[0], sc[1] * vs[1]), pack_f16x2(sc[2] * vs[2], sc[3] * vs[3])};
-      if (n == kUnit)
-        add_values<kFormat, D, false>(vst + vrow, vswizzle, n, c, wt, o);
-      else
-        add_values<kFormat, D, true>(vst + vrow, vswizzle, n, c, wt, o);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.empty[s]);
-    if (++s == kStages) {
-      s = 0;
-      ph ^= 1u;
-    }
-    if (!(flags & F_LAST)) continue;
+          for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[i]);
+        }
+        if (n < kUnit) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool valid = 4 * c + i < n;
+            sc[i] = valid ? sc[i] : -INFINITY;
+            if (!kUniform && !valid) vs[i] = lv[i] = 0.f;
+          }
+        }
+        float top = fmaxf(fmaxf(sc[0] + lv[0], sc[1] + lv[1]), fmaxf(sc[2] + lv[2], sc[3] + lv[3]));
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {  // also a sequence's first unit
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const bool grow = top > m + 8.f;
+          const float alpha = grow ? fast_exp2(m - top) : 1.f;
+          if (grow) {
+            m = top;
+            l *= alpha;
+          }
+          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[i][0] *= a0;
+            o[i][1] *= a1;
+            o[i][2] *= a0;
+            o[i][3] *= a1;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = fast_exp2(sc[i] - m);
+        l += (sc[0] + sc[1]) + (sc[2] + sc[3]);
+        const uint32_t wt[2] = {pack_f16x2(sc[0] * vs[0], sc[1] * vs[1]), pack_f16x2(sc[2] * vs[2], sc[3] * vs[3])};
+        if (n == kUnit)
+          add_values<kFormat, D, false>(vst + voff, n, c, wt, o);
+        else
+          add_values<kFormat, D, true>(vst + voff, n, c, wt, o);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[s]);
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    } while (!(flags & F_LAST));
 
     // ---- the end of the CTA's part of sequence b: heads 2c, 2c + 1
     l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -562,64 +645,55 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
     float mh[2] = {__shfl_sync(0xffffffffu, m, 8 * c), __shfl_sync(0xffffffffu, m, 8 * c + 4)};
     float lh[2] = {__shfl_sync(0xffffffffu, l, 8 * c), __shfl_sync(0xffffffffu, l, 8 * c + 4)};
     if (subs > 1) {
-      // Warps of the same kv head: sub 0 takes the others' parts, some columns
-      // at a time (bounded waits both ways).
-      constexpr int C = join_columns<D, G>();
-      constexpr int T = C / 16;  // tiles of a round
-      float M[2], w0[2];
+      // Warps of the same kv head: sub 0 takes the others' parts (bounded waits
+      // both ways).
+      if (sub > 0) {
+        if (seg > 0 && !mbar_wait(&sm.taken[g], (seg - 1) & 1, x.status)) return;
 #pragma unroll
-      for (int i0 = 0; i0 < KS; i0 += T, ++seg) {
-        if (sub > 0) {
-          if (seg > 0 && !mbar_wait(&sm.taken[g], (uint32_t)((seg - 1) & 1), x.status)) return;
-          float(*mine)[C + 2] = sm.join[warp - Hkv];
+        for (int y = 0; y < 2; ++y) {
+          if (!oc[y]) continue;
+          float* to = sm.join[warp - Hkv][2 * c + y];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (!oc[y]) continue;
-            float* to = mine[2 * c + y];
-#pragma unroll
-            for (int i = 0; i < T; ++i) {
-              to[16 * i + r] = o[i0 + i][y];
-              to[16 * i + r + 8] = o[i0 + i][y + 2];
-            }
-            if (r == 0) *reinterpret_cast<float2*>(to + C) = make_float2(mh[y], lh[y]);
+          for (int i = 0; i < KS; ++i) {
+            to[16 * i + r] = o[i][y];
+            to[16 * i + r + 8] = o[i][y + 2];
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.joined[g]);
-        } else {
-          if (!mbar_wait(&sm.joined[g], (uint32_t)(seg & 1), x.status)) return;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (!oc[y]) continue;
-            if (i0 == 0) {
-              M[y] = mh[y];
-              for (int k = 1; k < subs; ++k) M[y] = fmaxf(M[y], sm.join[(k - 1) * Hkv + g][2 * c + y][C]);
-              w0[y] = mh[y] == -INFINITY ? 0.f : fast_exp2(mh[y] - M[y]);
-              lh[y] *= w0[y];
-            }
-#pragma unroll
-            for (int i = 0; i < T; ++i) {
-              o[i0 + i][y] *= w0[y];
-              o[i0 + i][y + 2] *= w0[y];
-            }
-            for (int k = 1; k < subs; ++k) {
-              const float* from = sm.join[(k - 1) * Hkv + g][2 * c + y];
-              const float2 ml = *reinterpret_cast<const float2*>(from + C);
-              const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M[y]);
-              if (i0 == 0) lh[y] += w * ml.y;
-#pragma unroll
-              for (int i = 0; i < T; ++i) {
-                o[i0 + i][y] += w * from[16 * i + r];
-                o[i0 + i][y + 2] += w * from[16 * i + r + 8];
-              }
-            }
-            if (i0 + T >= KS) mh[y] = M[y];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.taken[g]);
+          if (r == 0) *reinterpret_cast<float2*>(to + D) = make_float2(mh[y], lh[y]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.joined[g]);
+        continue;
       }
-      if (sub > 0) continue;
+      if (!mbar_wait(&sm.joined[g], seg & 1, x.status)) return;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (!oc[y]) continue;
+        float top = mh[y];
+        for (int k = 1; k < subs; ++k) top = fmaxf(top, sm.join[(k - 1) * Hkv + g][2 * c + y][D]);
+        float w = mh[y] == -INFINITY ? 0.f : fast_exp2(mh[y] - top);
+        lh[y] *= w;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          o[i][y] *= w;
+          o[i][y + 2] *= w;
+        }
+        for (int k = 1; k < subs; ++k) {
+          const float* from = sm.join[(k - 1) * Hkv + g][2 * c + y];
+          const float2 ml = *reinterpret_cast<const float2*>(from + D);
+          w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+          lh[y] += w * ml.y;
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[i][y] += w * from[16 * i + r];
+            o[i][y + 2] += w * from[16 * i + r + 8];
+          }
+        }
+        mh[y] = top;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.taken[g]);
     }
+    const int b = sm.seg_seq[seg & (kTold - 1)];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       if (!oc[y]) continue;
@@ -647,7 +721,7 @@ __device__ void consume(const Args& x, Smem<D, G>& sm) {
 }
 
 template <int kFormat, int D, int G, bool kUniform>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     quant_split_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                        const Args x) {
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -657,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&sm.full[i], 33);  // the copies' bytes, and the producer's 32 lanes' own copies
       mbar_init(&sm.empty[i], kConsumers);
     }
+    for (int i = 0; i < kTold; ++i) mbar_init(&sm.told[i], 1);
     const int subs = kConsumers / x.num_kv_heads;
     for (int i = 0; i < kConsumers; ++i) {
       mbar_init(&sm.joined[i], subs > 1 ? subs - 1 : 1);
@@ -671,10 +746,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x >> 5 == kConsumers)
-    produce<D, G, kUniform>(x, &mapK, &mapV, sm);
-  else
+  find_share<D, G>(x, sm);
+  if (!x.by_seq && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1};  // before the producer's
+  if (threadIdx.x >> 5 == kConsumers) {
+    Producer<D, G, kUniform> feed(x, sm, &mapK, &mapV);
+    bool ok = true;
+    while (ok && feed.more) ok = feed.step();
+    if (!ok) feed.drain();
+  } else {
     consume<kFormat, D, G, kUniform>(x, sm);
+  }
+  empty_rows<D>(x);
 }
 
 // Joins the parts of the sequences that are cut: block (i, j) has sequence (or
@@ -763,18 +845,25 @@ bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1u << s) < d) ++s;
+  return {(uint32_t)((((uint64_t)1 << 32) * ((1u << s) - d)) / d + 1), s};
+}
+
 struct Plan {
   int ctas;
   bool by_seq;
   size_t part_bytes, total_bytes;
 };
 
-// Two CTAs per SM, or one for 64 tokens where the bound of the lengths leaves
-// fewer.
+// One CTA per SM, or as many as the bound of the lengths gives a share (64 tokens
+// or a sequence each).
 Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int num_sms) {
   Plan p;
   long long ctas = ((long long)num_seqs * max_context_len + 63) / 64;
-  if (ctas > 2 * num_sms) ctas = 2 * num_sms;
+  if (ctas < num_seqs) ctas = num_seqs;
+  if (ctas > num_sms) ctas = num_sms;
   p.ctas = ctas < 1 ? 1 : (int)ctas;
   p.by_seq = num_seqs <= p.ctas;
   p.part_bytes = (size_t)p.ctas * 2 * num_heads * (head_dim + 4) * sizeof(float);  // (a multiple of 16)
@@ -802,8 +891,8 @@ template <int kFormat, int D, int G>
 cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream_t stream) {
   CUtensorMap mk, mv;
   if (!unit_map(&mk, c.k, c) || !unit_map(&mv, c.v, c)) return cudaErrorInvalidValue;
-  constexpr size_t smem = sizeof(Smem<D, G>) + 1024;
-  static_assert(smem <= 113 * 1024, "two CTAs per SM");
+  constexpr size_t smem = sizeof(Smem<D, G>) + 1024;  // (the struct begins at a multiple of 1024)
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   auto split = (1 << c.scale_shift) >= kUnit && c.block_size % kUnit == 0 ? quant_split_kernel<kFormat, D, G, true>
                                                                            : quant_split_kernel<kFormat, D, G, false>;
   cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -846,6 +935,8 @@ cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, i
   x.num_blocks = c.num_blocks;
   x.block_size = c.block_size;
   x.page_units = (c.block_size + kUnit - 1) / kUnit;
+  x.by_block = divisor(c.block_size);
+  x.by_page_units = divisor(x.page_units);
   x.scale_shift = c.scale_shift;
   x.num_kv_heads = c.num_kv_heads;
   x.head_shift = 0;
