@@ -8,6 +8,36 @@
 
 namespace kvp {
 
+// Quotients of n < 2^31 by a number that the host knows: with 2^s >= d and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(m n / 2^32)) >> s.
+struct Divisor {
+  uint32_t m, s;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((1u << s) < d) ++s;
+  return {(uint32_t)((((uint64_t)1 << 32) * ((1u << s) - d)) / d + 1), s};
+}
+
+// Launches a kernel in the shadow of the stream's previous one: it may become
+// resident while that one drains, and waits (griddepcontrol.wait) before it
+// touches memory.
+template <typename... Params, typename... As>
+inline cudaError_t launch_shadow(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          As... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Rotary positions (rope.cu): freqs[i] is pair i's angle per position in turns,
 // as a fraction of 2^64.
 struct RopeArgs {

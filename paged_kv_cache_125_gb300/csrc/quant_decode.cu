@@ -72,15 +72,6 @@ struct Chain {
   int last;
 };
 
-// Quotients of n < 2^31 by a number that the host knows: with 2^s >= d and
-// m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(m n / 2^32)) >> s.
-struct Divisor {
-  uint32_t m, s;
-};
-__device__ __forceinline__ int quotient(int n, Divisor d) {
-  return (int)(((uint32_t)n + __umulhi(d.m, (uint32_t)n)) >> d.s);
-}
-
 struct Args {
   QuantDecodeArgs a;
   int64_t num_blocks;
@@ -741,11 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&mapK);
     prefetch_tensormap(&mapV);
   }
-  // Launched in the shadow of the stream's previous kernel: nothing of memory
-  // is touched before that one is done.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  out_of_shadow();
   __syncthreads();
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   find_share<D, G>(x, sm);
   if (!x.by_seq && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1};  // before the producer's
   if (threadIdx.x >> 5 == kConsumers) {
@@ -845,12 +833,6 @@ bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-Divisor divisor(uint32_t d) {
-  uint32_t s = 0;
-  while ((1u << s) < d) ++s;
-  return {(uint32_t)((((uint64_t)1 << 32) * ((1u << s) - d)) / d + 1), s};
-}
-
 struct Plan {
   int ctas;
   bool by_seq;
@@ -869,22 +851,6 @@ Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int nu
   p.part_bytes = (size_t)p.ctas * 2 * num_heads * (head_dim + 4) * sizeof(float);  // (a multiple of 16)
   p.total_bytes = p.part_bytes + (size_t)p.ctas * sizeof(Chain) + 16;
   return p;
-}
-
-template <typename... Params, typename... As>
-cudaError_t launch_shadow(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                          As... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int kFormat, int D, int G>

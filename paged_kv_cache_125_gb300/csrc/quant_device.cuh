@@ -7,6 +7,27 @@
 
 namespace kvp {
 
+__device__ __forceinline__ int quotient(int n, Divisor d) {
+  return (int)(((uint32_t)n + __umulhi(d.m, (uint32_t)n)) >> d.s);
+}
+
+// The start of a kernel launched in the shadow of the one before: nothing of
+// memory is touched before that one is done, and the next may come up.
+__device__ __forceinline__ void out_of_shadow() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// 16 bytes that pass through once.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 constexpr float kLeastScale = 5.421010862427522e-20f;  // 2^-64
 
 // The largest code is 448 = 1.75 * 2^8 (e4m3) or 127 = 1.984375 * 2^6 (int8).
@@ -47,9 +68,23 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
   }
 }
 
+// The same for four finite numbers times inv, none above the largest code: int8 by
+// adding 1.5 * 2^23, whose last place is 1 (the conversion instruction runs at a
+// quarter of that rate).
+__device__ __forceinline__ uint32_t encode4_int8(float a, float b, float c, float d, float inv) {
+  const uint32_t w[4] = {__float_as_uint(fmaf(a, inv, 12582912.f)), __float_as_uint(fmaf(b, inv, 12582912.f)),
+                         __float_as_uint(fmaf(c, inv, 12582912.f)), __float_as_uint(fmaf(d, inv, 12582912.f))};
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
 template <int kFormat>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv, bool finite = false) {
   uint2 r;
+  if (kFormat == KVP_INT8 && finite) {
+    r.x = encode4_int8(x[0], x[1], x[2], x[3], inv);
+    r.y = encode4_int8(x[4], x[5], x[6], x[7], inv);
+    return r;
+  }
   r.x = encode2<kFormat>(x[0] * inv, x[1] * inv) | encode2<kFormat>(x[2] * inv, x[3] * inv) << 16;
   r.y = encode2<kFormat>(x[4] * inv, x[5] * inv) | encode2<kFormat>(x[6] * inv, x[7] * inv) << 16;
   return r;

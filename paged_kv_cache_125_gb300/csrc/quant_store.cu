@@ -12,25 +12,38 @@
 // the numbers of a run are held in registers between the search for the largest
 // one and the rounding.  A team of head_dim / 16 lanes has a row of one head,
 // two 16-byte chunks per lane, and at most four rows; a run is shared by as
-// many teams as its block needs, up to the 16 warps of a CTA.
+// many teams as its block needs.  A CTA has some rows of slot_mapping, one of K
+// and V, and some of the heads: few enough that its warps hold a full block's
+// runs at once.
 #include "rope_device.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kRows = 4;    // of a team
-constexpr int kTile = 32;   // most rows of slot_mapping that a CTA looks through
+constexpr int kThreads = 256, kMostThreads = 512;  // of a CTA: 512 where a run needs them
+constexpr int kRows = 4;   // of a team
+constexpr int kTile = 32;  // most rows of slot_mapping that a CTA looks through
 
 struct StoreShape {
   int tile;        // rows of slot_mapping per CTA
   int teams;       // per run
+  int heads;       // per CTA
+  int groups;      // of that many heads
   unsigned ctas;   // that store; the others rotate q
 };
 
 __device__ __forceinline__ float magnitude_of(float x) {
   const float a = fabsf(x);
   return a < INFINITY ? a : 0.f;  // infinities and NaN do not count
+}
+
+// The two largest |x| of four words of bf16, each among the words' lower or upper
+// halves, as bits.
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  return top;
 }
 
 // A lane's numbers of one row: chunks li and li + D / 16 of a head.
@@ -87,23 +100,26 @@ __device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, co
 }
 
 template <int kFormat, int D, bool kRope>
-__global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantStoreRows a, const QuantCache c,
-                                                                  const RopeArgs r, const RopeRows q,
-                                                                  const RopeShape qs, const StoreShape s,
-                                                                  int* status) {
+__global__ void __launch_bounds__(kMostThreads)
+    quant_store_kernel(const QuantStoreRows a, const QuantCache c, const RopeArgs r, const RopeRows q,
+                       const RopeShape qs, const StoreShape s, int* status) {
   constexpr int TL = D / 16;  // lanes of a team
+  out_of_shadow();
   if constexpr (kRope) {
     if (blockIdx.x >= s.ctas) {
-      rope_thread(r, q, RopeRows{}, qs, (int64_t)(blockIdx.x - s.ctas) * (kWarps * 32) + threadIdx.x);
+      rope_thread(r, q, RopeRows{}, qs, (int64_t)(blockIdx.x - s.ctas) * blockDim.x + threadIdx.x);
       return;
     }
   }
   __shared__ int leaders[kTile];
   __shared__ int count;
-  __shared__ float tops[2][kWarps];
+  __shared__ float tops[2][kMostThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.x & 1;
-  const int64_t first = (int64_t)(blockIdx.x >> 1) * s.tile;
+  const unsigned cta = blockIdx.x >> 1;
+  const int64_t first = (int64_t)(cta / s.groups) * s.tile;
+  const int head0 = (int)(cta % s.groups) * s.heads;
+  const int heads = c.num_kv_heads - head0 < s.heads ? c.num_kv_heads - head0 : s.heads;
   const int tokens = 1 << c.scale_shift;
   const int64_t pool = c.num_blocks * c.block_size;
 
@@ -112,10 +128,9 @@ __global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantSto
     const int64_t i = first + lane;
     bool leads = false;
     if (lane < s.tile && i < a.num_tokens) {
-      const int64_t slot = a.slots[i];
-      leads = slot >= 0 && slot < pool;
+      const int64_t slot = a.slots[i], before = i > 0 ? a.slots[i - 1] : -1;
+      leads = slot >= 0 && slot < pool && (!(slot & (tokens - 1)) || i == 0 || before != slot - 1);
       if (slot >= pool) record_error(status, KVP_ERR_DEVICE_DATA);
-      if (leads && (slot & (tokens - 1)) && i > 0) leads = a.slots[i - 1] != slot - 1;
     }
     const unsigned mask = __ballot_sync(0xffffffffu, leads);
     if (leads) leaders[__popc(mask & ((1u << lane) - 1))] = lane;
@@ -123,34 +138,34 @@ __global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantSto
   }
   __syncthreads();
 
-  const int Hkv = c.num_kv_heads;
-  const int units = count * Hkv;  // (run, head)
-  const int lanes = s.teams * TL;                  // of a unit
-  const int unit_lane = threadIdx.x & (lanes - 1);  // (a power of two)
+  const int units = count * heads;                 // (run, head)
+  const int lanes = s.teams * TL;                  // of a unit, a power of two
+  const int unit_lane = threadIdx.x & (lanes - 1);
   const int team = unit_lane / TL, li = unit_lane % TL;
-  const int per_round = kWarps * 32 / lanes;
+  const int per_round = (int)blockDim.x / lanes;
   const uint16_t* src = is_v ? a.v : a.k;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   uint8_t* codes = is_v ? c.v : c.k;
   float* scales = is_v ? c.v_scales : c.k_scales;
   const int warps = lanes > 32 ? lanes / 32 : 1;
   const int in_warp = lanes < 32 ? lanes : 32;
+  const int wl = threadIdx.x & (in_warp - 1);
+  const bool turns = kRope && !is_v;
 
   for (int base = 0, round = 0; base < units; base += per_round, ++round) {
-    const int u = base + (int)(threadIdx.x / lanes);
+    const int u = base + (int)threadIdx.x / lanes;
     const bool active = u < units;
     int64_t row = 0, slot = 0;
     int n = 0, head = 0;
     if (active) {
-      const int lead = u / Hkv;
-      head = u - lead * Hkv;
+      const int lead = u / heads;
+      head = head0 + u - lead * heads;
       row = first + leaders[lead];
       slot = a.slots[row];
       n = tokens - (int)(slot & (tokens - 1));
       if (n > a.num_tokens - row) n = (int)(a.num_tokens - row);
     }
     // The run's length: up to the first row whose slot does not follow.
-    const int wl = threadIdx.x & (in_warp - 1);
     for (int at = 0; at < tokens; at += in_warp) {
       const int i = at + wl;
       const bool ends = i < n && a.slots[row + i] != slot + i;
@@ -161,20 +176,48 @@ __global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantSto
     const int64_t group = slot >> c.scale_shift;
     const bool fresh = (slot & (tokens - 1)) == 0;
     float old = 0.f;
-    if (active && wl == 0 && !fresh) old = scales[group * Hkv + head];
-    float x[kRows][2][8];
+    if (active && wl == 0 && !fresh) old = scales[group * c.num_kv_heads + head];
+    // Rows as they are, or rotated (then held in fp32).
+    uint4 raw[kRows][2];
+    float x[kRope ? kRows : 1][2][8];
     float top = 0.f;
+    bool finite = false;
+    if (turns) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int i = team + j * s.teams;
-      if (i >= n) continue;
-      const uint16_t* p = src + (row + i) * stride + (int64_t)head * D;
-      if (kRope && !is_v)
-        load_row_rotated<D>(p, li, r, r.positions[row + i], x[j]);
-      else
-        load_row<D>(p, li, x[j]);
+      for (int j = 0; j < kRows; ++j) {
+        const int i = team + j * s.teams;
+        if (i >= n) continue;
+        float(&y)[2][8] = x[kRope ? j : 0];
+        load_row_rotated<D>(src + (row + i) * stride + (int64_t)head * D, li, r, r.positions[row + i], y);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(x[j][e >> 3][e & 7]));
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(y[e >> 3][e & 7]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int i = team + j * s.teams;
+        raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+        if (i >= n) continue;
+        const uint16_t* p = src + (row + i) * stride + (int64_t)head * D;
+        raw[j][0] = load_once(p + li * 8);
+        raw[j][1] = load_once(p + (li + TL) * 8);
+      }
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) bits = top_bits(top_bits(bits, raw[j][0]), raw[j][1]);
+      const uint32_t most = max(bits & 0xffffu, bits >> 16);
+      if (most < 0x7f80u) {
+        top = __uint_as_float(most << 16);
+        finite = true;
+      } else {  // infinities or NaN among them
+#pragma unroll
+        for (int j = 0; j < 2 * kRows; ++j) {
+          float y[8];
+          bf16_floats(raw[j >> 1][j & 1], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, magnitude_of(y[e]));
+        }
+      }
     }
     for (int o = in_warp / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     old = __shfl_sync(0xffffffffu, old, lane & ~(in_warp - 1));
@@ -191,22 +234,28 @@ __global__ void __launch_bounds__(kWarps * 32) quant_store_kernel(const QuantSto
     for (int j = 0; j < kRows; ++j) {
       const int i = team + j * s.teams;
       if (i >= n) continue;
-      uint8_t* dst = codes + ((slot + i) * Hkv + head) * D;
+      uint8_t* dst = codes + ((slot + i) * c.num_kv_heads + head) * D;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<uint2*>(dst + (li + h * TL) * 8) = encode8<kFormat>(x[j][h], inv);
+      for (int h = 0; h < 2; ++h) {
+        float y[8];
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[kRope ? j : 0][h][e];
+        } else {
+          bf16_floats(raw[j][h], y);
+        }
+        *reinterpret_cast<uint2*>(dst + (li + h * TL) * 8) = encode8<kFormat>(y, inv, finite);
+      }
     }
-    if (fresh || scale == old) {
-      if (fresh && unit_lane == 0) scales[group * Hkv + head] = scale;
-      continue;
-    }
+    if (scale == old) continue;
+    if (unit_lane == 0) scales[group * c.num_kv_heads + head] = scale;
+    if (fresh) continue;
     // The block's other tokens, at the new scale (codes without a scale: zero).
-    if (unit_lane == 0) scales[group * Hkv + head] = scale;
     const float ratio = old > 0.f ? old / scale : 0.f;
     const int from = (int)(slot & (tokens - 1));
     for (int i = team; i < tokens; i += s.teams) {
       if (i >= from && i < from + n) continue;
-      uint8_t* dst = codes + (((group << c.scale_shift) + i) * Hkv + head) * D;
+      uint8_t* dst = codes + (((group << c.scale_shift) + i) * c.num_kv_heads + head) * D;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint2* p = reinterpret_cast<uint2*>(dst + (li + h * TL) * 8);
@@ -227,19 +276,26 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   // A run's teams: four rows for each, so that its numbers fit the registers.
   const int tokens = 1 << c.scale_shift;
   s.teams = tokens / kRows < 1 ? 1 : tokens / kRows;
-  // Rows of slot_mapping per CTA: few where that leaves SMs without any.
-  int64_t tile = rows.num_tokens / num_sms;
+  const int threads = s.teams * (D / 16) > kThreads ? kMostThreads : kThreads;
+  const int slots = threads / (s.teams * (D / 16));  // runs of one head that a CTA holds at once
+  // Rows of slot_mapping per CTA: a block's, or as many as fill the CTA where
+  // blocks are short, but few where that leaves SMs without any.
+  int64_t tile = slots > c.num_kv_heads ? (int64_t)tokens * (slots / c.num_kv_heads) : tokens;
+  if (tile > rows.num_tokens / num_sms) tile = rows.num_tokens / num_sms;
   s.tile = (int)(tile < 1 ? 1 : tile > kTile ? kTile : tile);
-  int64_t ctas = 2 * ((rows.num_tokens + s.tile - 1) / s.tile);
-  s.ctas = (unsigned)ctas;
+  s.heads = slots < c.num_kv_heads ? slots : c.num_kv_heads;
+  s.groups = (c.num_kv_heads + s.heads - 1) / s.heads;
+  int64_t ctas = 2 * s.groups * ((rows.num_tokens + s.tile - 1) / s.tile);
   RopeShape qs{};
+  const int64_t store_ctas = ctas;
   if (kRope) {
     qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 1024);
-    ctas += (rows.num_tokens * qs.units * qs.slices + kWarps * 32 - 1) / (kWarps * 32);
+    ctas += (rows.num_tokens * qs.units * qs.slices + threads - 1) / threads;
   }
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  quant_store_kernel<kFormat, D, kRope><<<(unsigned)ctas, kWarps * 32, 0, stream>>>(rows, c, r, q, qs, s, status);
-  return cudaGetLastError();
+  s.ctas = (unsigned)store_ctas;
+  return launch_shadow(quant_store_kernel<kFormat, D, kRope>, dim3((unsigned)ctas), threads, 0, stream, rows, c, r,
+                       q, qs, s, status);
 }
 
 template <int kFormat, int D>

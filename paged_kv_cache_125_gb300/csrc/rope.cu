@@ -21,6 +21,7 @@ constexpr int kRopeThreads = 256;
 
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs r, const RopeRows q, const RopeRows k,
                                                             const RopeShape s) {
+  out_of_shadow();
   rope_thread(r, q, k, s, (int64_t)blockIdx.x * kRopeThreads + threadIdx.x);
 }
 
@@ -57,8 +58,7 @@ cudaError_t launch_rope(const RopeArgs& r, const RopeRows& q, const RopeRows& k,
   const RopeShape s = rope_shape(r, q, k, num_tokens, head_dim, (int64_t)num_sms * 4 * kRopeThreads);
   const int64_t ctas = (num_tokens * s.units * s.slices + kRopeThreads - 1) / kRopeThreads;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  rope_kernel<<<(unsigned)ctas, kRopeThreads, 0, stream>>>(r, q, k, s);
-  return cudaGetLastError();
+  return launch_shadow(rope_kernel, dim3((unsigned)ctas), kRopeThreads, 0, stream, r, q, k, s);
 }
 
 }  // namespace kvp

@@ -50,35 +50,52 @@ __device__ __forceinline__ void rope_vec(const RopeArgs& r, const RopeRows& q, c
     }
     return;
   }
-  constexpr int kPairs = kInterleaved ? 4 : 8;
+  // Four heads at a time; the first batch's loads are on their way while the angles
+  // are made.
+  constexpr int kPairs = kInterleaved ? 4 : 8, kBatch = 4;
+  const int e = unit * 8, e2 = e + r.rotary_dim / 2;
+  uint4 a4[kBatch], b4[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (h + j >= h1) break;
+      const Head x = head_of(q, k, t, h + j, d);
+      a4[j] = load_once(x.in + e);
+      if (!kInterleaved) b4[j] = load_once(x.in + e2);
+    }
+  };
+  load(h0);
   float2 cs[kPairs];
   const int64_t pos = r.positions[t];
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) cs[p] = rope_turn(pos, r.freqs[unit * kPairs + p], r.magnitude);
-  const int e = unit * 8, e2 = e + r.rotary_dim / 2;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const Head x = head_of(q, k, t, h, d);
-    float a[8], b[8];
-    bf16_floats(*reinterpret_cast<const uint4*>(x.in + e), a);
-    if constexpr (kInterleaved) {
+  for (int h = h0;;) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        b[2 * p] = a[2 * p] * cs[p].x - a[2 * p + 1] * cs[p].y;
-        b[2 * p + 1] = a[2 * p + 1] * cs[p].x + a[2 * p] * cs[p].y;
-      }
-      *reinterpret_cast<uint4*>(x.out + e) = floats_bf16(b);
-    } else {
-      bf16_floats(*reinterpret_cast<const uint4*>(x.in + e2), b);
-      float c[8];
+    for (int j = 0; j < kBatch; ++j) {
+      if (h + j >= h1) break;
+      const Head x = head_of(q, k, t, h + j, d);
+      float a[8], b[8], c[8];
+      bf16_floats(a4[j], a);
+      if constexpr (kInterleaved) {
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        c[p] = a[p] * cs[p].x - b[p] * cs[p].y;
-        b[p] = b[p] * cs[p].x + a[p] * cs[p].y;
+        for (int p = 0; p < 4; ++p) {
+          c[2 * p] = a[2 * p] * cs[p].x - a[2 * p + 1] * cs[p].y;
+          c[2 * p + 1] = a[2 * p + 1] * cs[p].x + a[2 * p] * cs[p].y;
+        }
+      } else {
+        bf16_floats(b4[j], b);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          c[p] = a[p] * cs[p].x - b[p] * cs[p].y;
+          b[p] = b[p] * cs[p].x + a[p] * cs[p].y;
+        }
+        *reinterpret_cast<uint4*>(x.out + e2) = floats_bf16(b);
       }
       *reinterpret_cast<uint4*>(x.out + e) = floats_bf16(c);
-      *reinterpret_cast<uint4*>(x.out + e2) = floats_bf16(b);
     }
+    h += kBatch;
+    if (h >= h1) return;
+    load(h);
   }
 }
 
