@@ -20,9 +20,10 @@
 namespace kvp {
 namespace {
 
-constexpr int kThreads = 256, kMostThreads = 512;  // of a CTA: 512 where a run needs them
-constexpr int kRows = 4;   // of a team
-constexpr int kTile = 32;  // most rows of slot_mapping that a CTA looks through
+constexpr int kThreads = 256, kMostThreads = 512;  // of a CTA: more where a run needs them
+constexpr int kRows = 4;    // of a team
+constexpr int kTile = 64;   // most rows of slot_mapping that a CTA looks through
+constexpr int kWords = (kTile + 256) / 32;  // of the rows that its runs may reach
 
 struct StoreShape {
   int tile;        // rows of slot_mapping per CTA
@@ -30,6 +31,7 @@ struct StoreShape {
   int heads;       // per CTA
   int groups;      // of that many heads
   unsigned ctas;   // that store; the others rotate q
+  Divisor by_pairs;
 };
 
 __device__ __forceinline__ float magnitude_of(float x) {
@@ -55,9 +57,10 @@ __device__ __forceinline__ void load_row(const uint16_t* src, int li, float (&x)
 }
 
 // The same, rotated (in fp32: what is quantised is not rounded to bf16 before).
+// turns: the row's cosines and sines.
 template <int D>
-__device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, const RopeArgs& r, int64_t pos,
-                                                 float (&x)[2][8]) {
+__device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, const RopeArgs& r,
+                                                 const float2* turns, float (&x)[2][8]) {
   load_row<D>(src, li, x);
   const int half = r.rotary_dim / 2;
   if (r.interleaved) {
@@ -67,34 +70,32 @@ __device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, co
       for (int p = 0; p < 4; ++p) {
         const int pair = (li + i * (D / 16)) * 4 + p;
         if (pair >= half) continue;
-        const float2 cs = rope_turn(pos, r.freqs[pair], r.magnitude);
+        const float2 cs = turns[pair];
         const float a = x[i][2 * p], b = x[i][2 * p + 1];
         x[i][2 * p] = a * cs.x - b * cs.y;
         x[i][2 * p + 1] = b * cs.x + a * cs.y;
       }
     }
-    return;
-  }
-  if (half == D / 2) {  // both numbers of a pair are this lane's
+  } else if (half == D / 2) {  // both numbers of a pair are this lane's
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      const float2 cs = rope_turn(pos, r.freqs[li * 8 + p], r.magnitude);
+      const float2 cs = turns[li * 8 + p];
       const float a = x[0][p], b = x[1][p];
       x[0][p] = a * cs.x - b * cs.y;
       x[1][p] = b * cs.x + a * cs.y;
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int e = (li + i * (D / 16)) * 8 + p;
-      if (e >= r.rotary_dim) continue;
-      const bool first = e < half;
-      const float2 cs = rope_turn(pos, r.freqs[first ? e : e - half], r.magnitude);
-      const float other = bf16lo(src[first ? e + half : e - half]);
-      x[i][p] = x[i][p] * cs.x + (first ? -other : other) * cs.y;
+      for (int p = 0; p < 8; ++p) {
+        const int e = (li + i * (D / 16)) * 8 + p;
+        if (e >= r.rotary_dim) continue;
+        const bool first = e < half;
+        const float2 cs = turns[first ? e : e - half];
+        const float other = bf16lo(src[first ? e + half : e - half]);
+        x[i][p] = x[i][p] * cs.x + (first ? -other : other) * cs.y;
+      }
     }
   }
 }
@@ -111,8 +112,9 @@ __global__ void __launch_bounds__(kMostThreads)
       return;
     }
   }
-  __shared__ int leaders[kTile];
-  __shared__ int count;
+  __shared__ int slots[kTile], leaders[kTile];
+  __shared__ uint32_t begins[kWords + 1];  // bit i: row first + i continues no run
+  __shared__ int count, end;  // runs that begin in the tile; the row behind the last of them
   __shared__ float tops[2][kMostThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.x & 1;
@@ -123,20 +125,59 @@ __global__ void __launch_bounds__(kMostThreads)
   const int tokens = 1 << c.scale_shift;
   const int64_t pool = c.num_blocks * c.block_size;
 
-  // The tile's rows that begin a run.
-  if (warp == 0) {
-    const int64_t i = first + lane;
-    bool leads = false;
-    if (lane < s.tile && i < a.num_tokens) {
-      const int64_t slot = a.slots[i], before = i > 0 ? a.slots[i - 1] : -1;
-      leads = slot >= 0 && slot < pool && (!(slot & (tokens - 1)) || i == 0 || before != slot - 1);
+  // The tile's rows and those that its runs may reach: which of them go on where the
+  // row before left off, in the same block.
+  const int words = (s.tile + tokens + 31) / 32;
+  for (int w = warp; w < words; w += (int)blockDim.x / 32) {
+    const int i = w * 32 + lane;
+    const int64_t row = first + i;
+    const int64_t slot = row < a.num_tokens ? a.slots[row] : -1;
+    const int64_t before = row > 0 && row < a.num_tokens ? a.slots[row - 1] : -2;
+    const bool follows = slot > 0 && slot < pool && (slot & (tokens - 1)) && before == slot - 1;
+    const unsigned mask = __ballot_sync(0xffffffffu, !follows);
+    if (lane == 0) begins[w] = mask;
+    if (i < s.tile) {
+      slots[i] = slot >= 0 && slot < pool ? (int)slot : -1;
       if (slot >= pool) record_error(status, KVP_ERR_DEVICE_DATA);
     }
-    const unsigned mask = __ballot_sync(0xffffffffu, leads);
-    if (leads) leaders[__popc(mask & ((1u << lane) - 1))] = lane;
-    if (lane == 0) count = __popc(mask);
   }
   __syncthreads();
+  // Where the run of row i ends: the next row that continues none.
+  auto run_end = [&](int i) {
+    int w = (i + 1) / 32;
+    uint32_t rest = w < words ? begins[w] & (0xffffffffu << ((i + 1) & 31)) : 1u;
+    while (!rest && ++w < words) rest = begins[w];
+    return w * 32 + (rest ? __ffs(rest) - 1 : 0);
+  };
+  if (warp == 0) {
+    int n = 0;
+    for (int at = 0; at < s.tile; at += 32) {
+      const int i = at + lane;
+      const bool leads = i < s.tile && slots[i] >= 0 && (begins[i / 32] >> lane & 1);
+      const unsigned mask = __ballot_sync(0xffffffffu, leads);
+      if (leads) leaders[n + __popc(mask & ((1u << lane) - 1))] = i;
+      n += __popc(mask);
+    }
+    if (lane == 0) {
+      count = n;
+      end = n ? run_end(leaders[n - 1]) : 0;
+    }
+  }
+  __syncthreads();
+  if (count == 0) return;
+
+  // Cosines and sines of the runs' rows, for all heads.
+  extern __shared__ float2 table[];
+  const int pairs = kRope ? r.rotary_dim / 2 : 0, table_row = pairs + 1;
+  const int row0 = leaders[0];
+  if (kRope && !is_v) {
+    const int rows = end - row0;
+    for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
+      const int j = quotient(i, s.by_pairs), p = i - j * pairs;
+      table[j * table_row + p] = rope_turn(r.positions[first + row0 + j], r.freqs[p], r.magnitude);
+    }
+    __syncthreads();
+  }
 
   const int units = count * heads;                 // (run, head)
   const int lanes = s.teams * TL;                  // of a unit, a power of two
@@ -158,20 +199,11 @@ __global__ void __launch_bounds__(kMostThreads)
     int64_t row = 0, slot = 0;
     int n = 0, head = 0;
     if (active) {
-      const int lead = u / heads;
+      const int lead = u / heads, i = leaders[lead];
       head = head0 + u - lead * heads;
-      row = first + leaders[lead];
-      slot = a.slots[row];
-      n = tokens - (int)(slot & (tokens - 1));
-      if (n > a.num_tokens - row) n = (int)(a.num_tokens - row);
-    }
-    // The run's length: up to the first row whose slot does not follow.
-    for (int at = 0; at < tokens; at += in_warp) {
-      const int i = at + wl;
-      const bool ends = i < n && a.slots[row + i] != slot + i;
-      unsigned hit = __ballot_sync(0xffffffffu, ends) >> (lane & ~(in_warp - 1));
-      if (in_warp < 32) hit &= (1u << in_warp) - 1;
-      if (hit) n = at + __ffs(hit) - 1;
+      row = first + i;
+      slot = slots[i];
+      n = run_end(i) - i;
     }
     const int64_t group = slot >> c.scale_shift;
     const bool fresh = (slot & (tokens - 1)) == 0;
@@ -188,7 +220,8 @@ __global__ void __launch_bounds__(kMostThreads)
         const int i = team + j * s.teams;
         if (i >= n) continue;
         float(&y)[2][8] = x[kRope ? j : 0];
-        load_row_rotated<D>(src + (row + i) * stride + (int64_t)head * D, li, r, r.positions[row + i], y);
+        load_row_rotated<D>(src + (row + i) * stride + (int64_t)head * D, li, r,
+                            table + (int)(row + i - first - row0) * table_row, y);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(y[e >> 3][e & 7]));
       }
@@ -273,10 +306,10 @@ template <int kFormat, int D, bool kRope>
 cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs& r, const RopeRows& q,
                    int num_sms, int* status, cudaStream_t stream) {
   StoreShape s;
-  // A run's teams: four rows for each, so that its numbers fit the registers.
+  // A run's teams: few rows for each, so that its numbers fit the registers.
   const int tokens = 1 << c.scale_shift;
   s.teams = tokens / kRows < 1 ? 1 : tokens / kRows;
-  const int threads = s.teams * (D / 16) > kThreads ? kMostThreads : kThreads;
+  const int threads = s.teams * (D / 16) > kThreads ? s.teams * (D / 16) : kThreads;
   const int slots = threads / (s.teams * (D / 16));  // runs of one head that a CTA holds at once
   // Rows of slot_mapping per CTA: a block's, or as many as fill the CTA where
   // blocks are short, but few where that leaves SMs without any.
@@ -289,13 +322,21 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   RopeShape qs{};
   const int64_t store_ctas = ctas;
   if (kRope) {
-    qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 1024);
+    qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 512);
     ctas += (rows.num_tokens * qs.units * qs.slices + threads - 1) / threads;
   }
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   s.ctas = (unsigned)store_ctas;
-  return launch_shadow(quant_store_kernel<kFormat, D, kRope>, dim3((unsigned)ctas), threads, 0, stream, rows, c, r,
-                       q, qs, s, status);
+  size_t table = 0;
+  if (kRope) {
+    s.by_pairs = divisor(r.rotary_dim / 2);
+    table = (size_t)(s.tile + tokens) * (r.rotary_dim / 2 + 1) * sizeof(float2);  // at most 166 KB
+    const cudaError_t e = cudaFuncSetAttribute(quant_store_kernel<kFormat, D, kRope>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_shadow(quant_store_kernel<kFormat, D, kRope>, dim3((unsigned)ctas), threads, table, stream, rows, c,
+                       r, q, qs, s, status);
 }
 
 template <int kFormat, int D>
