@@ -87,6 +87,7 @@ struct Args {
   float* part;    // [ctas][2][Hq][D + 4]: O[D], m, l
   Chain* chains;  // per sequence, or per CTA that one begins in where those are fewer
   bool by_seq;
+  bool whole;     // CTA i has sequences i, i + CTAs, ...: none is cut
   int* status;
 };
 
@@ -242,7 +243,7 @@ __device__ void empty_rows(const Args& x) {
     if (clamp_len(x.a.context_lens[b], cap) != 0) continue;
     uint4* o = reinterpret_cast<uint4*>(x.a.out + (int64_t)b * x.a.out_stride);
     for (int j = threadIdx.x & 31; j < x.a.num_heads * D / 8; j += 32) o[j] = make_uint4(0, 0, 0, 0);
-    if (x.by_seq && (threadIdx.x & 31) == 0) x.chains[b] = {b, 0, -1};
+    if (x.by_seq && !x.whole && (threadIdx.x & 31) == 0) x.chains[b] = {b, 0, -1};
   }
 }
 
@@ -264,9 +265,9 @@ struct Producer {
 
   __device__ __forceinline__ Producer(const Args& x_, Smem<D, G>& sm_, const CUtensorMap* k, const CUtensorMap* v)
       : x(x_), sm(sm_), mapK(k), mapV(v) {
-    left = sm.share.end - sm.share.start;
-    b = sm.share.seq;
-    skip = sm.share.skip;
+    left = x.whole ? 1 << 30 : sm.share.end - sm.share.start;
+    b = x.whole ? (int)blockIdx.x : sm.share.seq;
+    skip = x.whole ? 0 : sm.share.skip;
     len = sm.share.len;
   }
 
@@ -300,11 +301,13 @@ struct Producer {
   __device__ __forceinline__ void next_segment() {
     const int lane = threadIdx.x & 31, cap = x.a.max_blocks * x.block_size;
     int units = 0;
-    if (segs == 0 && left > 0) {
+    if (segs == 0 && left > 0 && !x.whole) {
       units = units_of(x, len);
     } else {
-      for (; left > 0 && b < x.a.num_seqs; ++b) {
-        len = clamp_len(x.a.context_lens[b], cap);
+      for (; left > 0 && b < x.a.num_seqs; b += x.whole ? gridDim.x : 1) {
+        const int c = x.a.context_lens[b];
+        if (x.whole && (c < 0 || c > cap)) record_error(x.status, KVP_ERR_DEVICE_DATA);
+        len = clamp_len(c, cap);
         units = units_of(x, len);
         if (units) break;
       }
@@ -317,15 +320,16 @@ struct Producer {
     tell(b);
     const int begins = sm.share.end - left - skip;  // the sequence's first unit among all
     const int take = left < units - skip ? left : units - skip;
-    seq = b++;
+    seq = b;
+    b += x.whole ? gridDim.x : 1;
     u = skip;
     u1 = u + take;
-    left -= take;
+    if (!x.whole) left -= take;
     skip = 0;
     at = 0;
     look_up(u + lane, row_next, n_next);
     const bool cut = u > 0 || u1 < units;
-    if (u == 0 && lane == 0) {  // it begins here: the CTA of its last unit
+    if (u == 0 && lane == 0 && !x.whole) {  // it begins here: the CTA of its last unit
       const int end = begins + units - 1, each = sm.share.each, longer = sm.share.more * (each + 1);
       const int last = !cut ? (int)blockIdx.x - 1
                             : end < longer ? end / (each + 1) : sm.share.more + (end - longer) / each;
@@ -469,9 +473,11 @@ struct Scores<KVP_INT8, D> {
       const uint4 u = lds128(chunk(i));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
-        mma_f16(y & 1 ? s1 : s0, a[4 * i + y][0], 0, a[4 * i + y][1], 0, codes_f16x2<KVP_INT8>(w[y]),
-                codes_f16x2<KVP_INT8>(w[y] >> 16));
+      for (int y = 0; y < 4; ++y) {
+        uint32_t lo, hi;
+        codes_f16x4<KVP_INT8>(w[y], lo, hi);
+        mma_f16(y & 1 ? s1 : s0, a[4 * i + y][0], 0, a[4 * i + y][1], 0, lo, hi);
+      }
     }
     x0 = s0[0] + s1[0];
     x1 = s0[1] + s1[1];
@@ -493,9 +499,12 @@ __device__ __forceinline__ void add_values(uint32_t addr, int n, int c, const ui
       for (int y = 0; y < 4; ++y) w[y] &= keep;
     }
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-      mma_f16(o[2 * i + y], codes_f16x2<kFormat>(w[2 * y]), codes_f16x2<kFormat>(w[2 * y + 1]),
-              codes_f16x2<kFormat>(w[2 * y] >> 16), codes_f16x2<kFormat>(w[2 * y + 1] >> 16), wt[0], wt[1]);
+    for (int y = 0; y < 2; ++y) {
+      uint32_t a[4];
+      codes_f16x4<kFormat>(w[2 * y], a[0], a[2]);
+      codes_f16x4<kFormat>(w[2 * y + 1], a[1], a[3]);
+      mma_f16(o[2 * i + y], a[0], a[1], a[2], a[3], wt[0], wt[1]);
+    }
   }
 }
 
@@ -734,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   out_of_shadow();
   __syncthreads();
-  find_share<D, G>(x, sm);
-  if (!x.by_seq && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1};  // before the producer's
+  if (!x.whole) find_share<D, G>(x, sm);
+  if (!x.by_seq && !x.whole && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1};  // before the producer's
   if (threadIdx.x >> 5 == kConsumers) {
     Producer<D, G, kUniform> feed(x, sm, &mapK, &mapV);
     bool ok = true;
@@ -835,16 +844,20 @@ bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c) {
 
 struct Plan {
   int ctas;
-  bool by_seq;
+  bool by_seq, whole;
   size_t part_bytes, total_bytes;
 };
 
 // One CTA per SM, or as many as the bound of the lengths gives a share (64 tokens
-// or a sequence each).
+// or a sequence each).  Where no sequence is longer than kWholeTokens none is cut:
+// a second kernel for the cut ones takes longer than the units it would spread.
+constexpr int kWholeTokens = 256;
+
 Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int num_sms) {
   Plan p;
+  p.whole = max_context_len <= kWholeTokens;
   long long ctas = ((long long)num_seqs * max_context_len + 63) / 64;
-  if (ctas < num_seqs) ctas = num_seqs;
+  if (ctas < num_seqs || p.whole) ctas = num_seqs;
   if (ctas > num_sms) ctas = num_sms;
   p.ctas = ctas < 1 ? 1 : (int)ctas;
   p.by_seq = num_seqs <= p.ctas;
@@ -864,7 +877,7 @@ cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream
   cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_shadow(split, dim3(p.ctas), kThreads, smem, stream, mk, mv, x);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   // Slices of the parts for each head: as many as a cut sequence has parts,
   // about.
   constexpr int groups = kMergeThreads / (D / 4);
@@ -913,6 +926,7 @@ cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, i
   x.part = static_cast<float*>(a.workspace);
   x.chains = reinterpret_cast<Chain*>(static_cast<uint8_t*>(a.workspace) + p.part_bytes);
   x.by_seq = p.by_seq;
+  x.whole = p.whole;
   x.status = status;
   if (c.format == KVP_E4M3)
     return c.head_dim == 128 ? launch<KVP_E4M3, 128>(x, c, p, stream) : launch<KVP_E4M3, 64>(x, c, p, stream);

@@ -106,6 +106,20 @@ __device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
   return r;
 }
 
+// All four codes of w: lo has the first two.
+template <int kFormat>
+__device__ __forceinline__ void codes_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kFormat == KVP_E4M3) {
+    lo = codes_f16x2<KVP_E4M3>(w);
+    hi = codes_f16x2<KVP_E4M3>(w >> 16);
+  } else {
+    const uint32_t biased = w ^ 0x80808080u;
+    uint32_t a = __byte_perm(biased, 0x64646464u, 0x4140), b = __byte_perm(biased, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+  }
+}
+
 __device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
   float2 r;
   asm("{\n\t.reg .f16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
