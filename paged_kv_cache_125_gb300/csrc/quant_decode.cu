@@ -66,10 +66,11 @@ struct alignas(16) StageMeta {
 };
 
 // A sequence that is cut: its first and last CTA (last < first: not cut).
-struct Chain {
+struct alignas(16) Chain {
   int b;
   int first;
   int last;
+  int pad;
 };
 
 struct Args {
@@ -243,7 +244,7 @@ __device__ void empty_rows(const Args& x) {
     if (clamp_len(x.a.context_lens[b], cap) != 0) continue;
     uint4* o = reinterpret_cast<uint4*>(x.a.out + (int64_t)b * x.a.out_stride);
     for (int j = threadIdx.x & 31; j < x.a.num_heads * D / 8; j += 32) o[j] = make_uint4(0, 0, 0, 0);
-    if (x.by_seq && !x.whole && (threadIdx.x & 31) == 0) x.chains[b] = {b, 0, -1};
+    if (x.by_seq && !x.whole && (threadIdx.x & 31) == 0) x.chains[b] = {b, 0, -1, 0};
   }
 }
 
@@ -334,9 +335,9 @@ struct Producer {
       const int last = !cut ? (int)blockIdx.x - 1
                             : end < longer ? end / (each + 1) : sm.share.more + (end - longer) / each;
       if (x.by_seq)
-        x.chains[seq] = {seq, (int)blockIdx.x, last};
+        x.chains[seq] = {seq, (int)blockIdx.x, last, 0};
       else if (cut)
-        x.chains[blockIdx.x] = {seq, (int)blockIdx.x, last};
+        x.chains[blockIdx.x] = {seq, (int)blockIdx.x, last, 0};
     }
     seg_flags = (cut ? 0 : F_WHOLE) | (u > 0 ? F_ENTERED : 0);
   }
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   out_of_shadow();
   __syncthreads();
   if (!x.whole) find_share<D, G>(x, sm);
-  if (!x.by_seq && !x.whole && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1};  // before the producer's
+  if (!x.by_seq && !x.whole && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1, 0};  // before the producer's
   if (threadIdx.x >> 5 == kConsumers) {
     Producer<D, G, kUniform> feed(x, sm, &mapK, &mapV);
     bool ok = true;
@@ -756,76 +757,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   empty_rows<D>(x);
 }
 
-// Joins the parts of the sequences that are cut: block (i, j) has sequence (or
-// CTA) i and some heads.  A head has D / 4 lanes times `slices` of the parts.
-constexpr int kMergeThreads = 256;
+// Joins the parts of the sequences that are cut.  A warp has one head of one chain,
+// or a slice of its parts (then the block's warps join theirs in shared memory).
+// Small blocks of few registers: one comes up on every SM beside the split
+// kernel's CTA and waits there for that grid's end; then two dependent trips to L2
+// (the chain, its parts) remain.
+constexpr int kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) quant_merge_kernel(const Args x, int slices) {
-  constexpr int L = D / 4;
-  __shared__ float4 acc[kMergeThreads];
-  __shared__ float2 ml[kMergeThreads / L];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Chain ch = x.chains[blockIdx.x];
-  if (ch.last < ch.first) return;
-  const int li = threadIdx.x % L, group = threadIdx.x / L;
-  const int slice = group % slices;
-  const int h = blockIdx.y * (kMergeThreads / L / slices) + group / slices;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (h < x.a.num_heads) {
-    constexpr int B = 4;  // parts in flight
-    for (int i = ch.first + slice; i <= ch.last; i += B * slices) {
-      float4 a[B];
-      float2 s[B];
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
+    quant_merge_kernel(const Args x, int chains, int head_shift, int slice_shift) {
+  constexpr int E = D / 32, kBatch = 8;  // parts in flight
+  __shared__ float all[kMergeWarps][D + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = (blockIdx.x * kMergeWarps + warp) >> slice_shift, slice = warp & ((1 << slice_shift) - 1);
+  const int chain = item >> head_shift, h = item & ((1 << head_shift) - 1);
+  out_of_shadow();
+  Chain ch{0, 0, -1, 0};
+  if (chain < chains) {
+    const int4 c = *reinterpret_cast<const int4*>(&x.chains[chain]);
+    ch = {c.x, c.y, c.z, c.w};
+  }
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  for (int i = ch.first + slice; i <= ch.last; i += kBatch << slice_shift) {
+    float a[kBatch][E];
+    float2 s[kBatch];
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const int part = i + k * slices;
-        s[k] = make_float2(-INFINITY, 0.f);
-        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (part > ch.last) continue;
-        const float* p = x.part + (((size_t)part * 2 + (part == ch.first ? 1 : 0)) * x.a.num_heads + h) * (D + 4);
-        a[k] = *reinterpret_cast<const float4*>(p + li * 4);
-        s[k] = *reinterpret_cast<const float2*>(p + D);
+    for (int k = 0; k < kBatch; ++k) {
+      const int part = i + (k << slice_shift);
+      s[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[k][e] = 0.f;
+      if (part > ch.last) continue;
+      const float* p = x.part + (((size_t)part * 2 + (part == ch.first ? 1 : 0)) * x.a.num_heads + h) * (D + 4);
+      if constexpr (E == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p + lane * 4);
+        a[k][0] = u.x, a[k][1] = u.y, a[k][2] = u.z, a[k][3] = u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(p + lane * 2);
+        a[k][0] = u.x, a[k][1] = u.y;
       }
-      float top = m;
+      s[k] = *reinterpret_cast<const float2*>(p + D);
+    }
+    float top = m;
 #pragma unroll
-      for (int k = 0; k < B; ++k) top = fmaxf(top, s[k].x);
-      if (top == -INFINITY) continue;
-      const float w = fast_exp2(m - top);
-      l *= w;
-      o.x *= w, o.y *= w, o.z *= w, o.w *= w;
-      m = top;
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
+    if (top == -INFINITY) continue;
+    const float w = fast_exp2(m - top);
+    l *= w;
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const float y = fast_exp2(s[k].x - top);
-        l += y * s[k].y;
-        o.x += y * a[k].x, o.y += y * a[k].y, o.z += y * a[k].z, o.w += y * a[k].w;
-      }
+    for (int e = 0; e < E; ++e) o[e] *= w;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float y = fast_exp2(s[k].x - top);
+      l += y * s[k].y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += y * a[k][e];
     }
   }
-  if (slices > 1) {
-    acc[threadIdx.x] = o;
-    if (li == 0) ml[group] = make_float2(m, l);
+  if (slice_shift > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) all[warp][lane * E + e] = o[e];
+    if (lane == 0) all[warp][D] = m, all[warp][D + 1] = l;
     __syncthreads();
     if (slice > 0) return;
     float top = m;
-    for (int k = 1; k < slices; ++k) top = fmaxf(top, ml[group + k].x);
+    for (int k = 1; k < 1 << slice_shift; ++k) top = fmaxf(top, all[warp + k][D]);
     float w = fast_exp2(m - top);
     l *= w;
-    o.x *= w, o.y *= w, o.z *= w, o.w *= w;
-    for (int k = 1; k < slices; ++k) {
-      const float2 s = ml[group + k];
-      const float4 a = acc[threadIdx.x + k * L];
-      w = fast_exp2(s.x - top);
-      l += w * s.y;
-      o.x += w * a.x, o.y += w * a.y, o.z += w * a.z, o.w += w * a.w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= w;
+    for (int k = 1; k < 1 << slice_shift; ++k) {
+      w = fast_exp2(all[warp + k][D] - top);
+      l += w * all[warp + k][D + 1];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += w * all[warp + k][lane * E + e];
     }
   }
-  if (h >= x.a.num_heads) return;
+  if (ch.last < ch.first) return;
   const float inv = 1.f / l;
-  *reinterpret_cast<uint2*>(x.a.out + (int64_t)ch.b * x.a.out_stride + (int64_t)h * D + li * 4) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  uint32_t* to = reinterpret_cast<uint32_t*>(x.a.out + (int64_t)ch.b * x.a.out_stride + (int64_t)h * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) to[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
 }
 
 // Map of a code array as (column, token row, kv head) with a box of one unit.
@@ -878,15 +892,14 @@ cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream
   if (e != cudaSuccess) return e;
   e = launch_shadow(split, dim3(p.ctas), kThreads, smem, stream, mk, mv, x);
   if (e != cudaSuccess || p.whole) return e;
-  // Slices of the parts for each head: as many as a cut sequence has parts,
-  // about.
-  constexpr int groups = kMergeThreads / (D / 4);
+  // Warps for each head of a chain: one for eight parts that it may have.
   const int chains = p.by_seq ? x.a.num_seqs : p.ctas;
-  int slices = 1;
-  while (slices < groups && slices * chains < 2 * p.ctas) slices *= 2;
-  const int per_block = groups / slices;
-  return launch_shadow(quant_merge_kernel<D>, dim3(chains, (x.a.num_heads + per_block - 1) / per_block),
-                       kMergeThreads, 0, stream, x, slices);
+  int slice_shift = 0, head_shift = 0;
+  while (slice_shift < 3 && (8 << slice_shift) * chains < p.ctas) ++slice_shift;
+  while (1 << head_shift < x.a.num_heads) ++head_shift;
+  const int blocks = (int)((((int64_t)chains << head_shift << slice_shift) + kMergeWarps - 1) / kMergeWarps);
+  return launch_shadow(quant_merge_kernel<D>, dim3(blocks), kMergeWarps * 32, 0, stream, x, chains, head_shift,
+                       slice_shift);
 }
 
 template <int kFormat, int D>
