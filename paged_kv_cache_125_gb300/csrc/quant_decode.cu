@@ -747,6 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!x.whole) find_share<D, G>(x, sm);
   if (!x.by_seq && !x.whole && threadIdx.x == kThreads - 32) x.chains[blockIdx.x] = {0, 0, -1, 0};  // before the producer's
   if (threadIdx.x >> 5 == kConsumers) {
+    // The tensor copies read what kernels before this one stored.
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     Producer<D, G, kUniform> feed(x, sm, &mapK, &mapV);
     bool ok = true;
     while (ok && feed.more) ok = feed.step();

@@ -135,13 +135,20 @@ __device__ __forceinline__ float2 decode2(uint32_t w) {
 
 // Cosine and sine of position * freq.  The angle is held in turns as a 64-bit
 // fixed-point fraction, in which the product with a 64-bit position wraps as
-// the angle does: far positions lose nothing.  Its upper 32 bits, signed, give
-// an angle in [-pi, pi), where the fast functions are off by at most 2^-21:
-// 2^-12 of the step that the rotated numbers are rounded to.
+// the angle does: far positions lose nothing.  Its upper 32 bits, signed, are
+// the angle in units of pi * 2^-31.  The fast functions are off by at most 2^-21,
+// 2^-12 of the step that bf16 rows are rounded to (16384 tokens of 40 heads: 54.4
+// us, with the full ones 56.6); keys that become codes get the full ones, as the
+// fast ones' error rounds a few in a million the other way.
+template <bool kFast>
 __device__ __forceinline__ float2 rope_turn(int64_t position, uint64_t freq, float magnitude) {
-  const int32_t half_turns = (int32_t)(uint32_t)(((uint64_t)position * freq) >> 32);
-  const float angle = (float)half_turns * 1.4629180792671596e-9f;  // pi * 2^-31
-  return make_float2(__cosf(angle) * magnitude, __sinf(angle) * magnitude);
+  const float half_turns = (float)(int32_t)(uint32_t)(((uint64_t)position * freq) >> 32);
+  float s, c;
+  if constexpr (kFast)
+    __sincosf(half_turns * 1.4629180792671596e-9f, &s, &c);  // pi * 2^-31
+  else
+    sincospif(half_turns * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  return make_float2(c * magnitude, s * magnitude);
 }
 
 __device__ __forceinline__ void bf16_floats(const uint4& u, float (&x)[8]) {

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMostThreads)
     const int rows = end - row0;
     for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
       const int j = quotient(i, s.by_pairs), p = i - j * pairs;
-      table[j * table_row + p] = rope_turn(r.positions[first + row0 + j], r.freqs[p], r.magnitude);
+      table[j * table_row + p] = rope_turn<false>(r.positions[first + row0 + j], r.freqs[p], r.magnitude);
     }
     __syncthreads();
   }

@@ -15,8 +15,8 @@ struct RopeShape {
   int per_slice;   // heads in each
 };
 
-// What a launch of threads of this shape needs for the rows; more threads than
-// `fill` only shorten a thread's run of heads.
+// The shape of a launch for these rows (rope.cu).  A thread has fewer heads where
+// that makes up to `fill` threads.
 RopeShape rope_shape(const RopeArgs& r, const RopeRows& q, const RopeRows& k, int64_t num_tokens, int head_dim,
                      int64_t fill);
 
@@ -68,7 +68,7 @@ __device__ __forceinline__ void rope_vec(const RopeArgs& r, const RopeRows& q, c
   float2 cs[kPairs];
   const int64_t pos = r.positions[t];
 #pragma unroll
-  for (int p = 0; p < kPairs; ++p) cs[p] = rope_turn(pos, r.freqs[unit * kPairs + p], r.magnitude);
+  for (int p = 0; p < kPairs; ++p) cs[p] = rope_turn<true>(pos, r.freqs[unit * kPairs + p], r.magnitude);
   for (int h = h0;;) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -113,7 +113,7 @@ __device__ __forceinline__ void rope_any(const RopeArgs& r, const RopeRows& q, c
   const bool turns = unit < half;
   const int e = !turns ? half + unit : r.interleaved ? 2 * unit : unit;
   const int e2 = r.interleaved ? e + 1 : e + half;
-  const float2 cs = turns ? rope_turn(r.positions[t], r.freqs[unit], r.magnitude) : make_float2(0.f, 0.f);
+  const float2 cs = turns ? rope_turn<true>(r.positions[t], r.freqs[unit], r.magnitude) : make_float2(0.f, 0.f);
   for (int h = h0; h < h1; ++h) {
     const Head x = head_of(q, k, t, h, s.head_dim);
     if (!turns) {
