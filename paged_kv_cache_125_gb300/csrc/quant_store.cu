@@ -48,20 +48,14 @@ __device__ __forceinline__ uint32_t top_bits(uint32_t top, const uint4& u) {
   return top;
 }
 
-// A lane's numbers of one row: chunks li and li + D / 16 of a head.
+// A lane's numbers of one row (chunks li and li + D / 16 of a head, at src), rotated
+// by the row's cosines and sines, in fp32: what is quantised is not rounded to bf16
+// before.
 template <int D>
-__device__ __forceinline__ void load_row(const uint16_t* src, int li, float (&x)[2][8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    bf16_floats(*reinterpret_cast<const uint4*>(src + (li + i * (D / 16)) * 8), x[i]);
-}
-
-// The same, rotated (in fp32: what is quantised is not rounded to bf16 before).
-// turns: the row's cosines and sines.
-template <int D>
-__device__ __forceinline__ void load_row_rotated(const uint16_t* src, int li, const RopeArgs& r,
-                                                 const float2* turns, float (&x)[2][8]) {
-  load_row<D>(src, li, x);
+__device__ __forceinline__ void rotate_row(const uint4 (&raw)[2], const uint16_t* src, int li, const RopeArgs& r,
+                                           const float2* turns, float (&x)[2][8]) {
+  bf16_floats(raw[0], x[0]);
+  bf16_floats(raw[1], x[1]);
   const int half = r.rotary_dim / 2;
   if (r.interleaved) {
 #pragma unroll
@@ -116,6 +110,8 @@ __global__ void __launch_bounds__(kMostThreads)
   __shared__ uint32_t begins[kWords + 1];  // bit i: row first + i continues no run
   __shared__ int count, end;  // runs that begin in the tile; the row behind the last of them
   __shared__ float tops[2][kMostThreads / 32];
+  __shared__ int64_t positions[kRope ? kWords * 32 : 1];
+  __shared__ uint64_t freqs[kRope ? D / 2 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.x & 1;
   const unsigned cta = blockIdx.x >> 1;
@@ -125,6 +121,9 @@ __global__ void __launch_bounds__(kMostThreads)
   const int tokens = 1 << c.scale_shift;
   const int64_t pool = c.num_blocks * c.block_size;
 
+  const bool turns = kRope && !is_v;
+  const int pairs = kRope ? r.rotary_dim / 2 : 0;
+  if (turns && threadIdx.x < pairs) freqs[kRope ? threadIdx.x : 0] = r.freqs[threadIdx.x];
   // The tile's rows and those that its runs may reach: which of them go on where the
   // row before left off, in the same block.
   const int words = (s.tile + tokens + 31) / 32;
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(kMostThreads)
     const bool follows = slot > 0 && slot < pool && (slot & (tokens - 1)) && before == slot - 1;
     const unsigned mask = __ballot_sync(0xffffffffu, !follows);
     if (lane == 0) begins[w] = mask;
+    if (turns && row < a.num_tokens) positions[kRope ? i : 0] = r.positions[row];
     if (i < s.tile) {
       slots[i] = slot >= 0 && slot < pool ? (int)slot : -1;
       if (slot >= pool) record_error(status, KVP_ERR_DEVICE_DATA);
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kMostThreads)
       if (leads) leaders[n + __popc(mask & ((1u << lane) - 1))] = i;
       n += __popc(mask);
     }
+    __syncwarp();
     if (lane == 0) {
       count = n;
       end = n ? run_end(leaders[n - 1]) : 0;
@@ -168,16 +169,7 @@ __global__ void __launch_bounds__(kMostThreads)
 
   // Cosines and sines of the runs' rows, for all heads.
   extern __shared__ float2 table[];
-  const int pairs = kRope ? r.rotary_dim / 2 : 0, table_row = pairs + 1;
-  const int row0 = leaders[0];
-  if (kRope && !is_v) {
-    const int rows = end - row0;
-    for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
-      const int j = quotient(i, s.by_pairs), p = i - j * pairs;
-      table[j * table_row + p] = rope_turn<false>(r.positions[first + row0 + j], r.freqs[p], r.magnitude);
-    }
-    __syncthreads();
-  }
+  const int table_row = pairs + 1, row0 = leaders[0];
 
   const int units = count * heads;                 // (run, head)
   const int lanes = s.teams * TL;                  // of a unit, a power of two
@@ -191,7 +183,6 @@ __global__ void __launch_bounds__(kMostThreads)
   const int warps = lanes > 32 ? lanes / 32 : 1;
   const int in_warp = lanes < 32 ? lanes : 32;
   const int wl = threadIdx.x & (in_warp - 1);
-  const bool turns = kRope && !is_v;
 
   for (int base = 0, round = 0; base < units; base += per_round, ++round) {
     const int u = base + (int)threadIdx.x / lanes;
@@ -209,32 +200,38 @@ __global__ void __launch_bounds__(kMostThreads)
     const bool fresh = (slot & (tokens - 1)) == 0;
     float old = 0.f;
     if (active && wl == 0 && !fresh) old = scales[group * c.num_kv_heads + head];
-    // Rows as they are, or rotated (then held in fp32).
     uint4 raw[kRows][2];
-    float x[kRope ? kRows : 1][2][8];
+    const uint16_t* at = src + row * stride + (int64_t)head * D;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int i = team + j * s.teams;
+      raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+      if (i >= n) continue;
+      raw[j][0] = load_once(at + i * stride + li * 8);
+      raw[j][1] = load_once(at + i * stride + (li + TL) * 8);
+    }
+    if (turns && round == 0) {  // while the first rows are on their way
+      for (int i = threadIdx.x; i < (end - row0) * pairs; i += blockDim.x) {
+        const int j = quotient(i, s.by_pairs), p = i - j * pairs;
+        table[j * table_row + p] = rope_turn<false>(positions[row0 + j], freqs[p], r.magnitude);
+      }
+      __syncthreads();
+    }
+    float x[kRope ? kRows : 1][2][8];  // rotated rows
     float top = 0.f;
     bool finite = false;
     if (turns) {
+      const float2* row_turns = table + ((int)(row - first) - row0) * table_row;
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         const int i = team + j * s.teams;
         if (i >= n) continue;
         float(&y)[2][8] = x[kRope ? j : 0];
-        load_row_rotated<D>(src + (row + i) * stride + (int64_t)head * D, li, r,
-                            table + (int)(row + i - first - row0) * table_row, y);
+        rotate_row<D>(raw[j], at + i * stride, li, r, row_turns + i * table_row, y);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(y[e >> 3][e & 7]));
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int i = team + j * s.teams;
-        raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
-        if (i >= n) continue;
-        const uint16_t* p = src + (row + i) * stride + (int64_t)head * D;
-        raw[j][0] = load_once(p + li * 8);
-        raw[j][1] = load_once(p + (li + TL) * 8);
-      }
       uint32_t bits = 0;
 #pragma unroll
       for (int j = 0; j < kRows; ++j) bits = top_bits(top_bits(bits, raw[j][0]), raw[j][1]);
