@@ -4,7 +4,7 @@
 // rounded once to bf16.  Memory bound: a code is read once, a number written
 // once.  A thread turns 16 codes (one 16-byte load) into 16 numbers (two 16-byte
 // stores that pass L2 by); the codes of a token's heads are contiguous, so a
-// warp's loads and stores are too.  A CTA has 16 tokens of K or of V: with both
+// warp's loads and stores are too.  A CTA has 8 or 16 tokens of K or of V: with both
 // in one CTA, or with several tokens' loads of a thread in flight together, a
 // sequence of 131072 tokens took 143 to 162 us; so it takes 130 (93% of the
 // copy's rate).
@@ -14,11 +14,11 @@ namespace kvp {
 namespace {
 
 constexpr int kLoadThreads = 256;
-constexpr int kTile = 16;  // tokens of a CTA's step
 
 struct LoadShape {
   int columns;    // threads of a row: of its chunks of 16 codes, as many as fit a CTA
   int rows;       // of a CTA's pass
+  int tile;       // tokens of a CTA's step
   Divisor by_columns, by_block;
 };
 
@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(kLoadThreads) quant_load_kernel(const QuantLoa
   const float* scales = is_v ? c.v_scales : c.k_scales;
   uint16_t* to = is_v ? a.v : a.k;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  for (int t0 = blockIdx.x * kTile; t0 < len; t0 += gridDim.x * kTile) {
+  for (int t0 = blockIdx.x * s.tile; t0 < len; t0 += gridDim.x * s.tile) {
 #pragma unroll 1
-    for (int i = y; i < kTile; i += s.rows) {
+    for (int i = y; i < s.tile; i += s.rows) {
       const int t = t0 + i;
       if (t >= len) break;
       const int page = quotient(t, s.by_block);
@@ -82,7 +82,11 @@ cudaError_t launch_quant_load(const QuantLoadArgs& a, const QuantCache& c, int n
   s.rows = kLoadThreads / s.columns;
   s.by_columns = divisor(s.columns);
   s.by_block = divisor(c.block_size);
-  const int tiles = (a.max_context_len + kTile - 1) / kTile;
+  // 16 tokens for a CTA; 8 where that leaves each SM fewer than 16 CTAs (five
+  // sequences of up to 1400 tokens: 18.1 us for 19.7 with the store before; one of
+  // 131072: 131.9 for 135.9 the other way).
+  s.tile = (int64_t)a.num_seqs * a.max_context_len < (int64_t)num_sms * 128 ? 8 : 16;
+  const int tiles = (a.max_context_len + s.tile - 1) / s.tile;
   const dim3 grid(tiles < 1 ? 1 : tiles, a.num_seqs, 2);
   return launch_shadow(c.format == KVP_E4M3 ? quant_load_kernel<KVP_E4M3> : quant_load_kernel<KVP_INT8>, grid,
                        kLoadThreads, 0, stream, a, c, s, status);
