@@ -5,18 +5,18 @@
 // with codes kc, vc and the scales ks, vs of their block of tokens and kv head.
 // Memory bound: every code of a context is read once.
 //
-// * Work is counted in units: up to 16 tokens of one page (all kv heads).  The
-//   units of all sequences, end to end, are cut into equal contiguous shares, one
-//   per CTA, one CTA per SM.  A sequence that a cut falls into leaves partial
-//   results, which the merge kernel joins.
-// * A producer warp streams units through a ring of five stages in shared memory:
+// * Work is counted in units of one page: 16 tokens of eight kv heads, up to 128 of
+//   fewer where pages are long enough.  The units of all sequences, end to end, are
+//   cut into equal contiguous shares, one per CTA, one CTA per SM.  A sequence that a
+//   cut falls into leaves partial results, which the merge kernel joins.
+// * A producer warp streams units through a ring of stages in shared memory:
 //   one tensor copy each for K and V lands a unit as [kv head][token][head_dim]
 //   bytes, swizzled so that the consumers' 16-byte loads fall in different banks;
 //   the tokens' scales come by 4-byte asynchronous copies that arrive on the same
 //   barrier.  A lane looks up the page of one unit, 32 units ahead at a time.
 //   Codes are marked as read once: L2 drops them first.
-// * Eight consumer warps: warp w has kv head w % Hkv of the stage's unit w / Hkv
-//   (a stage is 8 / Hkv units).
+// * Eight consumer warps: warp w has one piece of 16 tokens of a stage (two of
+//   head_dim 64) of kv head w % Hkv.
 //   S = q K^T, N = 8 tokens, the query heads of the kv head in M.  The numbers of
 //   head_dim may come in any order, the same in q and K, so a thread's operand is
 //   32 (16) contiguous bytes of a token.  e4m3: m16n8k32 on the codes as they lie;
@@ -45,24 +45,38 @@ namespace {
 
 constexpr int kConsumers = 8;
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kStages = 5;
-constexpr int kUnit = 16;  // tokens
-constexpr int kTold = 8;   // segments that the producer may be ahead by, at most
-static_assert(kStages + 2 <= kTold, "a segment is told over one that all warps have finished");
+constexpr int kPiece = 16;  // tokens of a warp's step
+// Stages of the ring: as many as fit beside the join's buffer.  (Four and six of
+// head_dim 128 measured 1 to 2% slower at decode B512, two CTAs of three 12%.)
+template <int D>
+__host__ __device__ constexpr int stages() {
+  return 5;
+}
+constexpr int kTold = 16;  // segments that the producer may be ahead by, at most
+static_assert(stages<64>() + 2 <= kTold, "a segment is told over one that all warps have finished");
 
-// A stage holds 8 (unit, kv head) pairs of K and of V.
+// Pieces that a warp takes from a stage: two of head_dim 64, whose 1 KB would not pay
+// for the stage's waits (64 sequences of 16384 tokens, 16/8/64 e4m3: 170 us; with one
+// 208).
+template <int D>
+__host__ __device__ constexpr int warp_pieces() {
+  return D == 128 ? 1 : 2;
+}
+// Pieces of a stage, each of one kv head, of K and of V.
+template <int D>
+__host__ __device__ constexpr int stage_pieces() {
+  return kConsumers * warp_pieces<D>();
+}
 template <int D>
 __host__ __device__ constexpr int half_bytes() {
-  return kConsumers * kUnit * D;
+  return stage_pieces<D>() * kPiece * D;
 }
-constexpr int kStageScales = kConsumers * kUnit;  // of K, and as many of V
 
 enum : int { F_LAST = 1, F_WHOLE = 2, F_ENTERED = 4 };
 
-struct alignas(16) StageMeta {
-  uint8_t n[8];  // tokens of each unit (read as two words)
+struct StageMeta {
+  uint8_t n[16];  // tokens of each unit
   int flags;
-  int pad;
 };
 
 // A sequence that is cut: its first and last CTA (last < first: not cut).
@@ -77,6 +91,9 @@ struct Args {
   QuantDecodeArgs a;
   int64_t num_blocks;
   int block_size;
+  int unit;        // tokens of a unit: 16 << piece_shift
+  int piece_shift;
+  int least;       // units of the smallest share
   int page_units;  // units of a full page
   Divisor by_block, by_page_units;
   int scale_shift;
@@ -101,12 +118,12 @@ struct Share {
 
 template <int D, int G>
 struct Smem {
-  alignas(1024) uint8_t k[kStages][half_bytes<D>()];
-  alignas(1024) uint8_t v[kStages][half_bytes<D>()];
-  alignas(16) float scales[kStages][2][kStageScales];  // [kv head of a unit][token], or (K, V) of each
-  alignas(16) StageMeta meta[kStages];
+  alignas(1024) uint8_t k[stages<D>()][half_bytes<D>()];
+  alignas(1024) uint8_t v[stages<D>()][half_bytes<D>()];
+  alignas(16) float scales[stages<D>()][2][stage_pieces<D>() * kPiece];  // [piece][token], or (K, V) of each
+  alignas(16) StageMeta meta[stages<D>()];
   alignas(8) float join[kConsumers - 1][G][D + 2];  // O, m, l
-  alignas(8) uint64_t full[kStages], empty[kStages], told[kTold];
+  alignas(8) uint64_t full[stages<D>()], empty[stages<D>()], told[kTold];
   uint64_t joined[kConsumers], taken[kConsumers];
   int2 warp_sums[kConsumers + 1];  // units and sequences that have any, of each warp's run
   Share share;
@@ -170,9 +187,9 @@ __device__ __forceinline__ int clamp_len(int c, int cap) { return c < 0 ? 0 : c 
 
 // Units of a sequence of n tokens.
 __device__ __forceinline__ int units_of(const Args& x, int n) {
-  if (x.page_units * kUnit == x.block_size) return (n + kUnit - 1) / kUnit;
+  if (x.page_units * x.unit == x.block_size) return (n + x.unit - 1) >> (4 + x.piece_shift);
   const int pages = quotient(n, x.by_block), rest = n - pages * x.block_size;
-  return pages * x.page_units + (rest + kUnit - 1) / kUnit;
+  return pages * x.page_units + ((rest + x.unit - 1) >> (4 + x.piece_shift));
 }
 
 // ---------------------------------------------------------------- shares
@@ -211,9 +228,10 @@ __device__ void find_share(const Args& x, Smem<D, G>& sm) {
     total += y.x;
     live += y.y;
   }
-  // CTAs that get a share: one for four units or one for a sequence, whichever
-  // are more.
-  int ctas = (total + 3) / 4 > live ? (total + 3) / 4 : live;
+  // CTAs that get a share: one for 64 tokens (a unit, where those are longer) or one
+  // for a sequence, whichever are more.
+  int ctas = (int)((unsigned)(total + x.least - 1) / (unsigned)x.least);
+  if (ctas < live) ctas = live;
   if (ctas > (int)gridDim.x) ctas = gridDim.x;
   if (ctas < 1) ctas = 1;
   const int q = (unsigned)total / (unsigned)ctas, rest = total - q * ctas;
@@ -275,14 +293,14 @@ struct Producer {
   __device__ __forceinline__ void look_up(int unit, int& r, int& m) {
     r = m = 0;
     if (unit >= u1) return;
-    const int page = quotient(unit, x.by_page_units), off = (unit - page * x.page_units) * kUnit;
+    const int page = quotient(unit, x.by_page_units), off = (unit - page * x.page_units) * x.unit;
     int block = x.a.block_tables[(int64_t)seq * x.a.max_blocks + page];
     if (block < 0 || block >= x.num_blocks) {
       record_error(x.status, KVP_ERR_DEVICE_DATA);
       block = 0;  // never read a page outside the pool
     }
     r = block * x.block_size + off;
-    m = x.block_size - off < kUnit ? x.block_size - off : kUnit;
+    m = x.block_size - off < x.unit ? x.block_size - off : x.unit;
     const int rest = len - page * x.block_size - off;
     if (m > rest) m = rest;
   }
@@ -290,9 +308,10 @@ struct Producer {
   // Tells the consumers the next segment's sequence (-1: no more), whose query they
   // fetch while its first unit is on its way.  Nothing reads slot segs % kTold any more:
   // of the segments that came after the one in it, all stages but the last
-  // kStages were given back, and seven segments have seven stages or more.
+  // stages() were given back, and kTold - 1 segments have as many stages or more.
   __device__ __forceinline__ void tell(int sequence) {
-    if ((threadIdx.x & 31) == 0) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
       sm.seg_seq[segs & (kTold - 1)] = sequence;
       mbar_arrive(&sm.told[segs & (kTold - 1)]);
     }
@@ -350,8 +369,9 @@ struct Producer {
       if (!more) return true;
     }
     const int lane = threadIdx.x & 31;
-    const int Hkv = x.num_kv_heads, per_stage = kConsumers >> x.head_shift;
-    const uint32_t unit_bytes = (uint32_t)(kUnit * Hkv * D);
+    const int Hkv = x.num_kv_heads, per_stage = stage_pieces<D>() >> x.head_shift >> x.piece_shift;
+    const uint32_t unit_bytes = (uint32_t)(x.unit * Hkv * D);
+    const int pieces = (1 << x.piece_shift) - 1;  // of a unit, less one
     if (at == 0) {
       row = row_next;
       n = n_next;
@@ -371,18 +391,21 @@ struct Producer {
       tma_load_3d_hint(sm.v[s] + unit * unit_bytes, mapV, 0, row, 0, &sm.full[s], once);
     }
     if constexpr (kUniform) {
-      const int i = lane & 7, su = i >> x.head_shift;
-      const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
-      if (lane < 16 && m > 0)
-        copy4_async(&sm.scales[s][0][2 * i + (lane >> 3)],
-                    (lane < 8 ? x.k_scales : x.v_scales) + ((int64_t)(r >> x.scale_shift) << x.head_shift) +
+      constexpr int kPieces = stage_pieces<D>();  // 8 or 16: K's and V's scales are a warp's at most
+      const int i = lane & (kPieces - 1), sub = i >> x.head_shift, off = (sub & pieces) * kPiece;
+      const int r = __shfl_sync(0xffffffffu, row, at + (sub >> x.piece_shift)) + off;
+      const int m = __shfl_sync(0xffffffffu, n, at + (sub >> x.piece_shift)) - off;
+      if (lane < 2 * kPieces && m > 0)
+        copy4_async(&sm.scales[s][0][2 * i + lane / kPieces],
+                    (lane < kPieces ? x.k_scales : x.v_scales) + ((int64_t)(r >> x.scale_shift) << x.head_shift) +
                         (i & (Hkv - 1)));
     } else {
 #pragma unroll
-      for (int j = 0; j < kStageScales / 32; ++j) {
-        const int i = j * 32 + lane, t = lane % kUnit, head = i / kUnit & (Hkv - 1);
-        const int su = i / kUnit >> x.head_shift;
-        const int r = __shfl_sync(0xffffffffu, row, at + su), m = __shfl_sync(0xffffffffu, n, at + su);
+      for (int j = 0; j < stage_pieces<D>() * kPiece / 32; ++j) {
+        const int i = j * 32 + lane, sub = i / kPiece >> x.head_shift, head = i / kPiece & (Hkv - 1);
+        const int t = (sub & pieces) * kPiece + lane % kPiece;
+        const int r = __shfl_sync(0xffffffffu, row, at + (sub >> x.piece_shift));
+        const int m = __shfl_sync(0xffffffffu, n, at + (sub >> x.piece_shift));
         if (t < m) {
           const int64_t src = ((int64_t)((r + t) >> x.scale_shift) << x.head_shift) + head;
           copy4_async(&sm.scales[s][0][i], x.k_scales + src);
@@ -393,7 +416,7 @@ struct Producer {
     arrive_after_copies(&sm.full[s]);
     issued |= 1u << s;
     issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
-    if (++s == kStages) {
+    if (++s == stages<D>()) {
       s = 0;
       ph ^= 1u;
     }
@@ -404,7 +427,7 @@ struct Producer {
 
   // After an expired wait: let every copy that was issued land before the CTA exits.
   __device__ void drain() {
-    for (int i = 0; i < kStages; ++i)
+    for (int i = 0; i < stages<D>(); ++i)
       if (issued >> i & 1u) mbar_wait(&sm.full[i], issued_ph >> i & 1u, x.status);
   }
 };
@@ -527,8 +550,12 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
   const int head0 = g * G;
   const int r = lane >> 2, c = lane & 3;
   const bool oc[2] = {2 * c < G, 2 * c + 1 < G};
-  const uint32_t region = (uint32_t)(warp * kUnit * D);
-  const uint32_t kbase = smem_u32(sm.k[0]) + region, vbase = smem_u32(sm.v[0]) + region;
+  // This warp's pieces: sub * PW, sub * PW + 1, ... of kv head g.
+  constexpr int PW = warp_pieces<D>();
+  auto place = [&](int p) {  // of one in a stage half
+    const int piece = sub * PW + p, unit = piece >> x.piece_shift;
+    return (uint32_t)(((unit * Hkv + g) * x.unit + (piece - (unit << x.piece_shift)) * kPiece) * D);
+  };
   // A thread's 16 bytes: chunk q of row t is at chunk q ^ (t & 7) (D 64: t >> 1 & 3),
   // the copies' swizzle.  K: rows krow (tokens of scores 0, 1) and krow + 2, chunks
   // D / 64 * c + i.  V: row lane % 16, chunks 2i + lane / 16.
@@ -571,40 +598,52 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
     int flags;
     do {
       if (!mbar_wait(&sm.full[s], ph, x.status)) return;
-      const uint4 meta = *reinterpret_cast<const uint4*>(&sm.meta[s]);
-      flags = (int)meta.z;
-      const int n = (int)((sub < 4 ? meta.x : meta.y) >> 8 * (sub & 3)) & 0xff;
-      if (n > 0) {
-        const uint32_t kst = kbase + (uint32_t)(s * half_bytes<D>()), vst = vbase + (uint32_t)(s * half_bytes<D>());
-        float sc[4];  // tokens 4c + i
+      flags = sm.meta[s].flags;
+      int n[PW];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          q.of([&](int i) { return ((kst + koff) ^ (j * kRowFlip ^ i << 4)) + 2 * j * D; }, sc[2 * j], sc[2 * j + 1]);
+      for (int p = 0; p < PW; ++p) {
+        const int piece = sub * PW + p, unit = piece >> x.piece_shift;
+        n[p] = (int)sm.meta[s].n[unit] - (piece - (unit << x.piece_shift)) * kPiece;
+      }
+      if (n[0] > 0) {
+        const uint32_t half = (uint32_t)(s * half_bytes<D>());
+        float sc[PW][4], vs[PW][4];  // tokens 4c + i
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < PW; ++p) {
+          const uint32_t at = (smem_u32(sm.k[0]) + half + place(p)) + koff;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            q.of([&](int i) { return (at ^ (j * kRowFlip ^ i << 4)) + 2 * j * D; }, sc[p][2 * j], sc[p][2 * j + 1]);
         }
-        float vs[4], lv[4];
-        if constexpr (kUniform) {
-          const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * warp]);
-          const float kq = scale.x * cq;
-          const float lu = log2_above(scale.y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] *= kq, vs[i] = scale.y, lv[i] = lu;
-        } else {
-          const float4 ks = *reinterpret_cast<const float4*>(&sm.scales[s][0][warp * kUnit + 4 * c]);
-          const float4 v4 = *reinterpret_cast<const float4*>(&sm.scales[s][1][warp * kUnit + 4 * c]);
-          sc[0] *= cq * ks.x, sc[1] *= cq * ks.y, sc[2] *= cq * ks.z, sc[3] *= cq * ks.w;
-          vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
+        for (int p = 0; p < PW; ++p) {
+          const int at = ((sub * PW + p) << x.head_shift) + g;
+          float lv[4];
+          if constexpr (kUniform) {
+            const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * at]);
+            const float kq = scale.x * cq, v = PW == 1 || n[p] > 0 ? scale.y : 0.f;
+            const float lu = log2_above(v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[i]);
-        }
-        if (n < kUnit) {
+            for (int i = 0; i < 4; ++i) sc[p][i] *= kq, vs[p][i] = v, lv[i] = lu;
+          } else {
+            const float4 ks = *reinterpret_cast<const float4*>(&sm.scales[s][0][at * kPiece + 4 * c]);
+            const float4 v4 = *reinterpret_cast<const float4*>(&sm.scales[s][1][at * kPiece + 4 * c]);
+            sc[p][0] *= cq * ks.x, sc[p][1] *= cq * ks.y, sc[p][2] *= cq * ks.z, sc[p][3] *= cq * ks.w;
+            vs[p][0] = v4.x, vs[p][1] = v4.y, vs[p][2] = v4.z, vs[p][3] = v4.w;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool valid = 4 * c + i < n;
-            sc[i] = valid ? sc[i] : -INFINITY;
-            if (!kUniform && !valid) vs[i] = lv[i] = 0.f;
+            for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[p][i]);
           }
+          if (n[p] < kPiece) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool valid = 4 * c + i < n[p];
+              sc[p][i] = valid ? sc[p][i] : -INFINITY;
+              if (!kUniform && !valid) vs[p][i] = lv[i] = 0.f;
+            }
+          }
+          top = fmaxf(top, fmaxf(fmaxf(sc[p][0] + lv[0], sc[p][1] + lv[1]), fmaxf(sc[p][2] + lv[2], sc[p][3] + lv[3])));
         }
-        float top = fmaxf(fmaxf(sc[0] + lv[0], sc[1] + lv[1]), fmaxf(sc[2] + lv[2], sc[3] + lv[3]));
         if (__any_sync(0xffffffffu, top > m + 8.f)) {  // also a sequence's first unit
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -624,17 +663,22 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = fast_exp2(sc[i] - m);
-        l += (sc[0] + sc[1]) + (sc[2] + sc[3]);
-        const uint32_t wt[2] = {pack_f16x2(sc[0] * vs[0], sc[1] * vs[1]), pack_f16x2(sc[2] * vs[2], sc[3] * vs[3])};
-        if (n == kUnit)
-          add_values<kFormat, D, false>(vst + voff, n, c, wt, o);
-        else
-          add_values<kFormat, D, true>(vst + voff, n, c, wt, o);
+        for (int p = 0; p < PW; ++p) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[p][i] = fast_exp2(sc[p][i] - m);
+          l += (sc[p][0] + sc[p][1]) + (sc[p][2] + sc[p][3]);
+          const uint32_t wt[2] = {pack_f16x2(sc[p][0] * vs[p][0], sc[p][1] * vs[p][1]),
+                                  pack_f16x2(sc[p][2] * vs[p][2], sc[p][3] * vs[p][3])};
+          const uint32_t at = (smem_u32(sm.v[0]) + half + place(p)) + voff;
+          if (n[p] >= kPiece)
+            add_values<kFormat, D, false>(at, n[p], c, wt, o);
+          else
+            add_values<kFormat, D, true>(at, n[p], c, wt, o);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[s]);
-      if (++s == kStages) {
+      if (++s == stages<D>()) {
         s = 0;
         ph ^= 1u;
       }
@@ -728,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D, G>& sm = *reinterpret_cast<Smem<D, G>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < stages<D>(); ++i) {
       mbar_init(&sm.full[i], 33);  // the copies' bytes, and the producer's 32 lanes' own copies
       mbar_init(&sm.empty[i], kConsumers);
     }
@@ -845,13 +889,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
 }
 
 // Map of a code array as (column, token row, kv head) with a box of one unit.
-bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c) {
+bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c, int unit) {
   auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t d = c.head_dim, heads = c.num_kv_heads;
   const cuuint64_t dims[3] = {d, (cuuint64_t)(c.num_blocks * c.block_size), heads};
   const cuuint64_t strides[2] = {heads * d, d};
-  const cuuint32_t box[3] = {(cuuint32_t)d, kUnit, (cuuint32_t)heads};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)unit, (cuuint32_t)heads};
   const cuuint32_t ones[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -885,10 +929,10 @@ Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int nu
 template <int kFormat, int D, int G>
 cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream_t stream) {
   CUtensorMap mk, mv;
-  if (!unit_map(&mk, c.k, c) || !unit_map(&mv, c.v, c)) return cudaErrorInvalidValue;
+  if (!unit_map(&mk, c.k, c, x.unit) || !unit_map(&mv, c.v, c, x.unit)) return cudaErrorInvalidValue;
   constexpr size_t smem = sizeof(Smem<D, G>) + 1024;  // (the struct begins at a multiple of 1024)
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  auto split = (1 << c.scale_shift) >= kUnit && c.block_size % kUnit == 0 ? quant_split_kernel<kFormat, D, G, true>
+  auto split = (1 << c.scale_shift) >= kPiece && c.block_size % kPiece == 0 ? quant_split_kernel<kFormat, D, G, true>
                                                                            : quant_split_kernel<kFormat, D, G, false>;
   cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -928,7 +972,15 @@ cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, i
   x.a = a;
   x.num_blocks = c.num_blocks;
   x.block_size = c.block_size;
-  x.page_units = (c.block_size + kUnit - 1) / kUnit;
+  // A unit fills a stage where a page has room for that: few copies, and long ones.
+  // (64 sequences of 65536 tokens, 8/1/128 e4m3: 160 us; with units of 16 tokens 220.)
+  x.piece_shift = 0;
+  const int pieces = c.head_dim == 128 ? stage_pieces<128>() : stage_pieces<64>();
+  while (x.piece_shift < 3 && 2 * c.num_kv_heads << x.piece_shift <= pieces && c.block_size % (2 * kPiece << x.piece_shift) == 0)
+    ++x.piece_shift;
+  x.unit = kPiece << x.piece_shift;
+  x.least = 64 / x.unit > 1 ? 64 / x.unit : 1;
+  x.page_units = (c.block_size + x.unit - 1) / x.unit;
   x.by_block = divisor(c.block_size);
   x.by_page_units = divisor(x.page_units);
   x.scale_shift = c.scale_shift;
