@@ -543,6 +543,112 @@ def test_caches_past_two_billion_numbers():
                   torch.tensor([[0, 1, 2]], dtype=i32), [n], d ** -0.5)
 
 
+def test_more_sequences_than_threads():
+    """Lengths in runs of several for a thread; empty rows in front, between and behind."""
+    lens = [0] * 5 + [(i * 7) % 41 for i in range(1200)] + [0] * 9
+    q, host, dev, tables = decode_case(2, 1, 64, 16, 16, INT8, lens, 22, poison=False)
+    for longest in (40, 300):  # none cut; cut where shares end
+        out = run_decode(q[:, :2], dev, tables, lens, longest=longest)
+        assert_decode(out, q[:, :2], host, tables, lens, 0.125)
+        assert not out[torch.tensor(lens) == 0].any()
+    assert kvp.device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(8, 1, 128, 256), (8, 1, 128, 16), (4, 2, 64, 64), (2, 1, 64, 2048), (16, 8, 64, 32)])
+def test_decode_many_short_segments(hq, hkv, d, bs):
+    """More segments in a CTA than the producer tells ahead, in one launch and in two."""
+    lens = [1 + (i * 13) % 50 for i in range(152 * 20)]
+    q, host, dev, tables = decode_case(hq, hkv, d, bs, 16, E4M3, lens, 23, poison=False)
+    for longest in (50, 1000):
+        out = run_decode(q[:, :hq], dev, tables, lens, longest=longest)
+        some = slice(0, None, 61)
+        assert_decode(out[some], q[some, :hq], host, tables[some], lens[some], d ** -0.5)
+        assert bool(torch.isfinite(out).all())
+    assert kvp.device_status() == 0
+
+
+def test_store_rows_of_other_calls_stay():
+    """What a call does not name stays as it was: blocks behind the last run, and pages between."""
+    for dtype in (E4M3, INT8):
+        codes, scales = cache_arrays(9, 32, 8, 3, 128, dtype, gen(24))
+        dev = [to_dev(codes.clone(), scales.clone()) for _ in range(2)]
+        slots = torch.cat((torch.arange(70, 83), torch.arange(160, 161), torch.arange(200, 216))).to(i32)
+        x = randn((len(slots), 3, 128), gen(25))
+        kvp.kv_quant_store(x.to(DEV), x.to(DEV), slots.to(DEV), dev[0][0], dev[1][0], dev[0][1], dev[1][1])
+        touched = torch.zeros(9 * 32 // 8, dtype=torch.bool)
+        touched[slots.long() // 8] = True
+        for got, old in ((dev[0][0], codes), (dev[1][0], codes)):
+            assert torch.equal(bits(got).view(-1, 8 * 3 * 128)[~touched], bits(old).view(-1, 8 * 3 * 128)[~touched])
+        for got in (dev[0][1], dev[1][1]):
+            assert torch.equal(got.cpu().view(-1, 3)[~touched], scales.view(-1, 3)[~touched])
+
+
+def test_calls_without_the_extension_module(monkeypatch):
+    """The same results where the binding makes the calls itself."""
+    lens = [33, 0, 70]
+    q, host, dev, tables = decode_case(4, 2, 64, 32, 16, INT8, lens, 26, poison=False)
+    rows = randn((3, 4 + 2 + 2, 64), gen(27)).to(DEV)
+    freqs, _ = kvp.attn_rope_freqs(64, device=DEV)
+    pos = torch.tensor([32, 5, 69], device=DEV)
+    slots = torch.tensor([int(tables[0, 1]) * 32, -1, int(tables[2, 2]) * 32 + 5], dtype=i32, device=DEV)
+    st, ctx = torch.tensor([0, 40, 50], dtype=i32, device=DEV), torch.tensor(lens, dtype=i32, device=DEV)
+
+    def everything():
+        cache = [t.clone() for t in (dev[0][0], dev[1][0], dev[0][1], dev[1][1])]
+        got = list(kvp.attn_rope(rows[:, :4], rows[:, 4:6], pos, freqs, 1.25, True))
+        kvp.kv_quant_store(rows[:, 4:6], rows[:, 6:], slots, *cache)
+        got += [t.clone() for t in cache]
+        got.append(kvp.kv_quant_store_rope(rows[:, :4], rows[:, 4:6], rows[:, 6:], pos, slots, freqs, *cache, 1.25, True))
+        out = tuple(torch.zeros((120, 2, 64), dtype=bf16, device=DEV) for _ in range(2))
+        got += list(kvp.kv_quant_load(*cache, tables.to(DEV), ctx, st, 70, out=out))
+        got.append(kvp.attn_decode_quant(rows[:, :4], *cache, tables.to(DEV), ctx, 70))
+        return got + cache
+
+    want = everything()
+    monkeypatch.setattr(kvp, "_CALLS", kvp._NoCalls())
+    for a, b in zip(everything(), want):
+        assert torch.equal(bits(a.contiguous()), bits(b.contiguous()))
+
+
+def test_binding_refusals():
+    """What the calls do not take, with device tensors."""
+    _, _, dev, tables = decode_case(4, 2, 64, 32, 16, INT8, [33, 70], 28, poison=False)
+    arrays = (dev[0][0], dev[1][0], dev[0][1], dev[1][1])
+    x = torch.zeros((2, 2, 64), dtype=bf16, device=DEV)
+    slots = torch.tensor([1, 2], dtype=i32, device=DEV)
+    tab, ctx = tables.to(DEV), torch.tensor([33, 70], dtype=i32, device=DEV)
+    freqs, _ = kvp.attn_rope_freqs(64, device=DEV)
+    pos = torch.tensor([0, 1], device=DEV)
+    with pytest.raises(ValueError, match="rows|row per"):
+        kvp.kv_quant_store(x[:1], x, slots, *arrays)
+    with pytest.raises(ValueError, match="head_dim|must be"):
+        kvp.attn_decode_quant(torch.zeros((2, 4, 128), dtype=bf16, device=DEV), *arrays, tab, ctx, 70)
+    with pytest.raises(ValueError, match="k_scales"):
+        kvp.kv_quant_store(x, x, slots, arrays[0], arrays[1], arrays[2][:, :1, :1], arrays[3])
+    with pytest.raises(TypeError, match="float32"):
+        kvp.kv_quant_store(x, x, slots, arrays[0], arrays[1], arrays[2].half(), arrays[3])
+    with pytest.raises(TypeError, match="int8"):
+        kvp.kv_quant_store(x, x, slots, arrays[0], arrays[1].view(E4M3), *arrays[2:])
+    with pytest.raises(ValueError, match="contiguous"):
+        kvp.kv_quant_store(x, x, slots, arrays[0].transpose(1, 2), arrays[1], *arrays[2:])
+    with pytest.raises(ValueError, match="num_rows"):
+        kvp.kv_quant_load(*arrays, tab, ctx, slots, 70)
+    with pytest.raises(ValueError, match="positions"):
+        kvp.attn_rope(x, x, pos[:1], freqs)
+    with pytest.raises(ValueError, match="head_dim"):
+        kvp.attn_rope(x, torch.zeros((2, 2, 128), dtype=bf16, device=DEV), pos, freqs)
+    with pytest.raises(kvp.KvpError, match="rotary_dim"):
+        kvp.attn_rope(x[..., :32].contiguous(), None, pos, freqs)
+    with pytest.raises(kvp.KvpError, match="bad shape"):  # the workspace that it would need
+        kvp.attn_decode_quant(torch.zeros((2, 6, 64), dtype=bf16, device=DEV), *arrays, tab, ctx, 70)
+    with pytest.raises(kvp.KvpError, match="scale_tokens"):
+        kvp.kv_quant_store(x, x, slots, *(torch.zeros((2, 48, 2, 64), dtype=torch.int8, device=DEV) for _ in range(2)),
+                           *(torch.zeros((2, 2, 2), device=DEV) for _ in range(2)))
+    kvp.kv_quant_store(x[:0], x[:0], slots[:0], *arrays)  # no rows: nothing to do
+    assert kvp.attn_decode_quant(torch.zeros((0, 4, 64), dtype=bf16, device=DEV), *arrays, tab[:0], ctx[:0], 70).shape[0] == 0
+    kvp.attn_rope(x[:0], None, pos[:0], freqs)
+
+
 # ------------------------------------------------------- streams, graphs, a whole run
 
 def test_another_stream_and_a_graph():

@@ -181,6 +181,7 @@ def test_decode_refusals(lib):
     for kw in (dict(qs=2040), dict(os=2040)):
         assert _decode(lib, b=1, **kw) == INVALID and "stride" in _err(lib)
     assert _decode(lib, mb=1 << 23) == UNSUPPORTED and "capacity" in _err(lib)
+    assert _decode(lib, b=1 << 11, bs=16, mb=1 << 20) == UNSUPPORTED and "2^31" in _err(lib)
     for args in ((-1, 16, 8, 128, 10), (1, 24, 8, 128, 10), (1, 16, 8, 96, 10), (1, 16, 8, 128, -1)):
         with pytest.raises(kvp.KvpError, match="bad shape"):
             kvp.attn_decode_quant_workspace_size(*args)
