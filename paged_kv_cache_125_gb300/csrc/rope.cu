@@ -17,7 +17,7 @@
 namespace kvp {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs r, const RopeRows q, const RopeRows k,
                                                             const RopeShape s) {
