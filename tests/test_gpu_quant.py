@@ -425,9 +425,22 @@ def test_decode(hq, hkv, d, bs, t, dtype):
     lens = [1, 0, 15, 16, 17, 300, 2, 33, 64, 0, 129, 1000]
     q, host, dev, tables = decode_case(hq, hkv, d, bs, t, dtype, lens, hq + d + bs)
     host = [(torch.nan_to_num(h[0].to(f32)), torch.nan_to_num(h[1])) for h in host]
-    out = run_decode(q[:, :hq], dev, tables, lens)
+    for longest in (1000, 100000, 256):  # in shares, of few and of all CTAs; not cut
+        out = run_decode(q[:, :hq], dev, tables, lens, longest=longest)
+        assert_decode(out, q[:, :hq], host, tables, lens, d ** -0.5)
+        assert not out[1].any() and not out[9].any()
+    assert kvp.device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (1, 1, 64), (2, 1, 128), (64, 8, 128), (8, 4, 64), (4, 2, 128)])
+@pytest.mark.parametrize("lens", [[1], [17], [0, 300, 0], [129, 128, 127], [2048] * 15, [1, 2047] * 7, [1024, 5, 600] * 11])
+def test_decode_small_batches(hq, hkv, d, lens):
+    """Fewer units than CTAs, empty sequences between, and the same result twice."""
+    q, host, dev, tables = decode_case(hq, hkv, d, 64, 16, E4M3, lens, 29 + len(lens), poison=False)
+    out = run_decode(q[:, :hq], dev, tables, lens, longest=max(max(lens), 257))
     assert_decode(out, q[:, :hq], host, tables, lens, d ** -0.5)
-    assert not out[1].any() and not out[9].any()
+    again = run_decode(q[:, :hq], dev, tables, lens, longest=max(max(lens), 257))
+    assert torch.equal(out, again)
     assert kvp.device_status() == 0
 
 
