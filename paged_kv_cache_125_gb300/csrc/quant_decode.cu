@@ -908,14 +908,18 @@ struct Plan {
   size_t part_bytes, total_bytes;
 };
 
-// One CTA per SM, or as many as the bound of the lengths gives a share (64 tokens
-// or a sequence each).  Where no sequence is longer than kWholeTokens none is cut:
-// a second kernel for the cut ones takes longer than the units it would spread.
-constexpr int kWholeTokens = 256;
+// Stages (0.62 us each for a CTA alone) of the longest sequence up to which none is cut:
+// the second kernel for the cut ones takes 3 us more.  With 16/8/128, a stage of 16
+// tokens: one sequence of 64 tokens 5.7 us whole and 7.7 cut, of 128 8.1 and 8.6, of
+// 192 10.6 and 8.7; 64 sequences of 256 14.1 and 15.1, as the SMs have their own.
+constexpr int kWholeStages = 6, kWholeStagesOfMany = 16, kMany = 48;
 
-Plan plan(int num_seqs, int num_heads, int head_dim, int max_context_len, int num_sms) {
+// One CTA per SM, or as many as the bound of the lengths gives a share (64 tokens
+// or a sequence each).
+Plan plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len, int num_sms) {
   Plan p;
-  p.whole = max_context_len <= kWholeTokens;
+  const int stage_tokens = kPiece * (head_dim == 128 ? stage_pieces<128>() : stage_pieces<64>()) / num_kv_heads;
+  p.whole = max_context_len <= stage_tokens * (num_seqs >= kMany ? kWholeStagesOfMany : kWholeStages);
   long long ctas = ((long long)num_seqs * max_context_len + 63) / 64;
   if (ctas < num_seqs || p.whole) ctas = num_seqs;
   if (ctas > num_sms) ctas = num_sms;
@@ -960,14 +964,14 @@ cudaError_t launch(const Args& x, const QuantCache& c, const Plan& p, cudaStream
 
 }  // namespace
 
-size_t quant_decode_workspace_bytes(int num_seqs, int num_heads, int, int head_dim, int max_context_len,
+size_t quant_decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len,
                                     int num_sms) {
-  return plan(num_seqs, num_heads, head_dim, max_context_len, num_sms).total_bytes;
+  return plan(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, num_sms).total_bytes;
 }
 
 cudaError_t launch_quant_decode(const QuantDecodeArgs& a, const QuantCache& c, int num_sms, int* status,
                                 cudaStream_t stream) {
-  const Plan p = plan(a.num_seqs, a.num_heads, c.head_dim, a.max_context_len, num_sms);
+  const Plan p = plan(a.num_seqs, a.num_heads, c.num_kv_heads, c.head_dim, a.max_context_len, num_sms);
   Args x;
   x.a = a;
   x.num_blocks = c.num_blocks;
