@@ -742,7 +742,8 @@ int kv_quant_store_rope(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 
  *                     num_rows - 1 is skipped and records KVP_ERR_DEVICE_DATA, as
  *                     are tokens of a page id outside the pool
  *   k, v              [num_rows, num_kv_heads, head_dim] bf16, 16-byte aligned,
- *                     row strides in multiples of 8 elements
+ *                     row strides in multiples of 8 elements; no two tokens of
+ *                     the call go to one row, and the outputs overlap nothing else
  * At most 65535 sequences.
  */
 int kv_quant_load(const void *k_cache, const void *v_cache, const float *k_scales, const float *v_scales,
@@ -764,9 +765,10 @@ size_t attn_decode_quant_workspace_size(int num_seqs, int num_heads, int num_kv_
  * Arguments as attn_decode_paged, with the cache's arrays and a workspace of
  * attn_decode_quant_workspace_size() bytes.  Scales of tokens within a context
  * are finite and not negative (kv_quant_store's are); codes and scales beyond a
- * context may be anything.
+ * context may be anything.  A head whose query holds an infinity or a NaN gets
+ * NaN.  Calls that may run at the same time need workspaces of their own.
  * Supported: num_kv_heads in {1, 2, 4, 8}; num_heads / num_kv_heads in
- * {1, 2, 4, 8}.
+ * {1, 2, 4, 8}; num_seqs * max_blocks_per_seq * ceil(block_size / 16) below 2^31.
  */
 int attn_decode_quant(const kvp_bf16 *q, int64_t q_stride_tok, const void *k_cache, const void *v_cache,
                       const float *k_scales, const float *v_scales, int format, int64_t num_blocks, int block_size,

@@ -24,7 +24,7 @@
 //   numbers (rows r and r + 8, the second times 2^4): all of bf16's 8 bits, to
 //   2^-21 of the head's largest number.  int8: m16n8k16 on codes made fp16.
 //   O^T += V^T W: m16n8k16 in fp16, M = 16 columns of head_dim, N = 8 heads, K = the
-//   unit's 16 tokens; the transposing 8-bit load gives a thread four tokens of a
+//   piece's 16 tokens; the transposing 8-bit load gives a thread four tokens of a
 //   column, which two conversions make its operand.  The weights W are the
 //   thread's own S.
 //   Both kinds of instruction sum in fp32.
@@ -591,7 +591,11 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
       for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(raw[i])), fabsf(bf16hi(raw[i]))));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      cq = q.load(raw, __float_as_uint(top) >> 23) * x.scale_log2;
+      const uint32_t e = __float_as_uint(top) >> 23;
+      cq = q.load(raw, e) * x.scale_log2;
+      // An infinity in q: every score is infinite or NaN, and the softmax NaN.  (A NaN's
+      // own code is one.)
+      if (e == 255) cq = __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }

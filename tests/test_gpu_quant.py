@@ -494,6 +494,40 @@ def test_decode_q_of_any_size():
         assert_decode(out, q[:, :2], host, tables, [90], scale)
 
 
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("hq,hkv,d,t", [(16, 8, 128, 16), (8, 1, 64, 4)])
+def test_decode_q_not_finite(hq, hkv, d, t, dtype):
+    """An infinite score's softmax is NaN; the other heads keep their numbers, in a sequence that is one CTA's, in one
+    that many share, and in one without a context."""
+    lens = [40, 4000, 0]
+    q, _, dev, tables = decode_case(hq, hkv, d, 64, t, dtype, lens, 16, poison=False)
+    q = q[:, :hq].contiguous()
+    want = run_decode(q, dev, tables, lens)
+    heads = {0: math.inf, 3: -math.inf, hq - 1: math.nan}
+    for h, x in heads.items():
+        q[:, h, h % d] = x
+    out = run_decode(q, dev, tables, lens)
+    for h in range(hq):
+        if h in heads:
+            assert bool(torch.isnan(out[:2, h]).all()) and not out[2, h].any()
+        else:
+            assert torch.equal(out[:, h], want[:, h])
+
+
+def test_bounds_far_above_the_lengths():
+    """max_context_len may be any bound: work is sized by the tables where that is less."""
+    lens, most = [70, 3], 2 ** 31 - 1
+    q, host, dev, tables = decode_case(8, 8, 128, 16, 16, E4M3, lens, 17, poison=False)
+    q = q[:, :8].contiguous()
+    assert_decode(run_decode(q, dev, tables, lens, longest=most), q, host, tables, lens, 128 ** -0.5)
+    rows = [[torch.zeros((80, 8, 128), dtype=bf16, device=DEV) for _ in range(2)] for _ in range(2)]
+    for out, longest in zip(rows, (70, most)):
+        kvp.kv_quant_load(dev[0][0], dev[1][0], dev[0][1], dev[1][1], tables.to(DEV),
+                          torch.tensor(lens, dtype=i32, device=DEV), torch.tensor([0, 72], dtype=i32, device=DEV),
+                          longest, out=tuple(out))
+    assert all(torch.equal(a, b) for a, b in zip(*rows))
+
+
 def test_decode_bad_pages_and_lengths():
     lens = [40, 40]
     q, host, dev, tables = decode_case(2, 1, 64, 16, 16, E4M3, lens, 16, poison=False)
