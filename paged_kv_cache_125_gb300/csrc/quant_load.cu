@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kLoadThreads) quant_load_kernel(const QuantLoa
 cudaError_t launch_quant_load(const QuantLoadArgs& a, const QuantCache& c, int num_sms, int* status,
                               cudaStream_t stream) {
   const int vecs = c.num_kv_heads * c.head_dim / 16;
+  // (no sequence is longer than its row of the table: up to 2^30 tokens)
+  const int cap = a.max_blocks * c.block_size, longest = a.max_context_len < cap ? a.max_context_len : cap;
   LoadShape s;
   s.columns = vecs < kLoadThreads ? vecs : kLoadThreads;
   s.rows = kLoadThreads / s.columns;
@@ -85,8 +87,8 @@ cudaError_t launch_quant_load(const QuantLoadArgs& a, const QuantCache& c, int n
   // 16 tokens for a CTA; 8 where that leaves each SM fewer than 16 CTAs (five
   // sequences of up to 1400 tokens: 18.1 us for 19.7 with the store before; one of
   // 131072: 131.9 for 135.9 the other way).
-  s.tile = (int64_t)a.num_seqs * a.max_context_len < (int64_t)num_sms * 128 ? 8 : 16;
-  const int tiles = (a.max_context_len + s.tile - 1) / s.tile;
+  s.tile = (int64_t)a.num_seqs * longest < (int64_t)num_sms * 128 ? 8 : 16;
+  const int tiles = (longest + s.tile - 1) / s.tile;
   const dim3 grid(tiles < 1 ? 1 : tiles, a.num_seqs, 2);
   return launch_shadow(c.format == KVP_E4M3 ? quant_load_kernel<KVP_E4M3> : quant_load_kernel<KVP_INT8>, grid,
                        kLoadThreads, 0, stream, a, c, s, status);
