@@ -831,15 +831,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   float m = -INFINITY, l = 0.f, o[E] = {};
   for (int i = ch.first + slice; i <= ch.last; i += kBatch << slice_shift) {
     float a[kBatch][E];
-    float2 s[kBatch];
+    float2 s = make_float2(-INFINITY, 0.f);  // lane k: part k's m and l
+    auto of = [&](int part) {  // (at most 5.2 million numbers)
+      return x.part + ((part * 2 + (part == ch.first ? 1 : 0)) * x.a.num_heads + h) * (D + 4);
+    };
+    if (lane < kBatch && i + (lane << slice_shift) <= ch.last)
+      s = *reinterpret_cast<const float2*>(of(i + (lane << slice_shift)) + D);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int part = i + (k << slice_shift);
-      s[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) a[k][e] = 0.f;
       if (part > ch.last) continue;
-      const float* p = x.part + (((size_t)part * 2 + (part == ch.first ? 1 : 0)) * x.a.num_heads + h) * (D + 4);
+      const float* p = of(part);
       if constexpr (E == 4) {
         const float4 u = *reinterpret_cast<const float4*>(p + lane * 4);
         a[k][0] = u.x, a[k][1] = u.y, a[k][2] = u.z, a[k][3] = u.w;
@@ -847,25 +851,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
         const float2 u = *reinterpret_cast<const float2*>(p + lane * 2);
         a[k][0] = u.x, a[k][1] = u.y;
       }
-      s[k] = *reinterpret_cast<const float2*>(p + D);
     }
-    float top = m;
+    float top = s.x;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
+    for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(m, __shfl_sync(0xffffffffu, top, 0));
     if (top == -INFINITY) continue;
-    const float w = fast_exp2(m - top);
-    l *= w;
+    const float w = fast_exp2(m - top), share = fast_exp2(s.x - top);
+    l = l * w + share * s.y;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= w;
     m = top;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const float y = fast_exp2(s[k].x - top);
-      l += y * s[k].y;
+      const float y = __shfl_sync(0xffffffffu, share, k);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += y * a[k][e];
     }
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (slice_shift > 0) {
 #pragma unroll
     for (int e = 0; e < E; ++e) all[warp][lane * E + e] = o[e];

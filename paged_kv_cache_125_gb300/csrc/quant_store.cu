@@ -319,7 +319,10 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   RopeShape qs{};
   const int64_t store_ctas = ctas;
   if (kRope) {
-    qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 512);
+    // Fewer threads for q than attn_rope's: the stores' fill the SMs already (five chunks
+    // of up to 900 tokens, 16/8/128: 17.6 us with the load behind; 18.2 with twice as
+    // many, 20.4 with four times).
+    qs = rope_shape(r, q, RopeRows{}, rows.num_tokens, c.head_dim, (int64_t)num_sms * 256);
     ctas += (rows.num_tokens * qs.units * qs.slices + threads - 1) / threads;
   }
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
