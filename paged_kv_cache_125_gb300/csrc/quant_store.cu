@@ -21,8 +21,8 @@ namespace kvp {
 namespace {
 
 constexpr int kThreads = 256, kMostThreads = 512;  // of a CTA: more where a run needs them
-constexpr int kRows = 4;    // of a team
-constexpr int kTile = 64;   // most rows of slot_mapping that a CTA looks through
+constexpr int kTile = 256;   // most rows of slot_mapping that a CTA looks through
+constexpr int kRotatedTile = 64;  // where their cosines are kept
 constexpr int kWords = (kTile + 256) / 32;  // of the rows that its runs may reach
 
 struct StoreShape {
@@ -31,7 +31,7 @@ struct StoreShape {
   int heads;       // per CTA
   int groups;      // of that many heads
   unsigned ctas;   // that store; the others rotate q
-  Divisor by_pairs;
+  Divisor by_heads, by_pairs;
 };
 
 __device__ __forceinline__ float magnitude_of(float x) {
@@ -94,11 +94,21 @@ __device__ __forceinline__ void rotate_row(const uint4 (&raw)[2], const uint16_t
   }
 }
 
-template <int kFormat, int D, bool kRope>
-__global__ void __launch_bounds__(kMostThreads)
+// Registers for four CTAs of 256 threads per SM (9216 rows of 32/8/128: 10.1 us; with as
+// many registers as the compiler likes, and three CTAs, 12.7), for three where runs are
+// one row (16 us; 18.5 with two), for two where rows are rotated.
+__host__ __device__ constexpr int most_threads(int rows) { return rows == 1 ? kThreads : kMostThreads; }
+__host__ __device__ constexpr int least_ctas(bool rope, int rows) {
+  return rows == 1 ? (rope ? 2 : 3) : (rope ? 1 : 2);
+}
+
+// kRows rows of a team's run, kRuns runs at once.
+template <int kFormat, int D, bool kRope, int kRows>
+__global__ void __launch_bounds__(most_threads(kRows), least_ctas(kRope, kRows))
     quant_store_kernel(const QuantStoreRows a, const QuantCache c, const RopeArgs r, const RopeRows q,
                        const RopeShape qs, const StoreShape s, int* status) {
   constexpr int TL = D / 16;  // lanes of a team
+  constexpr int kRuns = 4 / kRows;
   out_of_shadow();
   if constexpr (kRope) {
     if (blockIdx.x >= s.ctas) {
@@ -184,31 +194,37 @@ __global__ void __launch_bounds__(kMostThreads)
   const int in_warp = lanes < 32 ? lanes : 32;
   const int wl = threadIdx.x & (in_warp - 1);
 
-  for (int base = 0, round = 0; base < units; base += per_round, ++round) {
-    const int u = base + (int)threadIdx.x / lanes;
-    const bool active = u < units;
-    int64_t row = 0, slot = 0;
-    int n = 0, head = 0;
-    if (active) {
-      const int lead = u / heads, i = leaders[lead];
-      head = head0 + u - lead * heads;
-      row = first + i;
-      slot = slots[i];
-      n = run_end(i) - i;
-    }
-    const int64_t group = slot >> c.scale_shift;
-    const bool fresh = (slot & (tokens - 1)) == 0;
-    float old = 0.f;
-    if (active && wl == 0 && !fresh) old = scales[group * c.num_kv_heads + head];
-    uint4 raw[kRows][2];
-    const uint16_t* at = src + row * stride + (int64_t)head * D;
+  for (int base = 0, round = 0; base < units; base += per_round * kRuns, ++round) {
+    bool active[kRuns];
+    int64_t row[kRuns], slot[kRuns];
+    int n[kRuns], head[kRuns];
+    float old[kRuns];
+    uint4 raw[kRuns][kRows][2];
+    auto at = [&](int m) { return src + row[m] * stride + (int64_t)head[m] * D; };
+    auto group = [&](int m) { return (slot[m] >> c.scale_shift) * c.num_kv_heads + head[m]; };
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int i = team + j * s.teams;
-      raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
-      if (i >= n) continue;
-      raw[j][0] = load_once(at + i * stride + li * 8);
-      raw[j][1] = load_once(at + i * stride + (li + TL) * 8);
+    for (int m = 0; m < kRuns; ++m) {
+      const int u = base + m * per_round + (int)threadIdx.x / lanes;
+      active[m] = u < units;
+      row[m] = slot[m] = 0;
+      n[m] = head[m] = 0;
+      if (active[m]) {
+        const int lead = heads == s.heads ? quotient(u, s.by_heads) : u / heads, i = leaders[lead];
+        head[m] = head0 + u - lead * heads;
+        row[m] = first + i;
+        slot[m] = slots[i];
+        n[m] = run_end(i) - i;
+      }
+      old[m] = 0.f;
+      if (active[m] && wl == 0 && (slot[m] & (tokens - 1))) old[m] = scales[group(m)];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int i = team + j * s.teams;
+        raw[m][j][0] = raw[m][j][1] = make_uint4(0, 0, 0, 0);
+        if (i >= n[m]) continue;
+        raw[m][j][0] = load_once(at(m) + i * stride + li * 8);
+        raw[m][j][1] = load_once(at(m) + i * stride + (li + TL) * 8);
+      }
     }
     if (turns && round == 0) {  // while the first rows are on their way
       for (int i = threadIdx.x; i < (end - row0) * pairs; i += blockDim.x) {
@@ -217,89 +233,94 @@ __global__ void __launch_bounds__(kMostThreads)
       }
       __syncthreads();
     }
-    float x[kRope ? kRows : 1][2][8];  // rotated rows
-    float top = 0.f;
-    bool finite = false;
-    if (turns) {
-      const float2* row_turns = table + ((int)(row - first) - row0) * table_row;
+#pragma unroll
+    for (int m = 0; m < kRuns; ++m) {
+      float x[kRope ? kRows : 1][2][8];  // rotated rows
+      float top = 0.f;
+      bool finite = false;
+      if (turns) {
+        const float2* row_turns = table + ((int)(row[m] - first) - row0) * table_row;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          const int i = team + j * s.teams;
+          if (i >= n[m]) continue;
+          float(&y)[2][8] = x[kRope ? j : 0];
+          rotate_row<D>(raw[m][j], at(m) + i * stride, li, r, row_turns + i * table_row, y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(y[e >> 3][e & 7]));
+        }
+      } else {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) bits = top_bits(top_bits(bits, raw[m][j][0]), raw[m][j][1]);
+        const uint32_t most = max(bits & 0xffffu, bits >> 16);
+        if (most < 0x7f80u) {
+          top = __uint_as_float(most << 16);
+          finite = true;
+        } else {  // infinities or NaN among them
+#pragma unroll
+          for (int j = 0; j < 2 * kRows; ++j) {
+            float y[8];
+            bf16_floats(raw[m][j >> 1][j & 1], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, magnitude_of(y[e]));
+          }
+        }
+      }
+      for (int o = in_warp / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float before = __shfl_sync(0xffffffffu, old[m], lane & ~(in_warp - 1));
+      if (warps > 1) {
+        const int turn = (round * kRuns + m) & 1;
+        if (lane == 0) tops[turn][warp] = top;
+        named_barrier_sync(1 + warp / warps, warps * 32);
+        for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[turn][(warp & ~(warps - 1)) + w]);
+      }
+      if (!active[m]) continue;
+      const bool fresh = (slot[m] & (tokens - 1)) == 0;
+      const float need = scale_for<kFormat>(top);
+      const float scale = fresh ? need : fmaxf(before, need);
+      const float inv = 1.f / scale;
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         const int i = team + j * s.teams;
-        if (i >= n) continue;
-        float(&y)[2][8] = x[kRope ? j : 0];
-        rotate_row<D>(raw[j], at + i * stride, li, r, row_turns + i * table_row, y);
+        if (i >= n[m]) continue;
+        uint8_t* dst = codes + ((slot[m] + i) * c.num_kv_heads + head[m]) * D;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, magnitude_of(y[e >> 3][e & 7]));
-      }
-    } else {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) bits = top_bits(top_bits(bits, raw[j][0]), raw[j][1]);
-      const uint32_t most = max(bits & 0xffffu, bits >> 16);
-      if (most < 0x7f80u) {
-        top = __uint_as_float(most << 16);
-        finite = true;
-      } else {  // infinities or NaN among them
-#pragma unroll
-        for (int j = 0; j < 2 * kRows; ++j) {
+        for (int h = 0; h < 2; ++h) {
           float y[8];
-          bf16_floats(raw[j >> 1][j & 1], y);
+          if (turns) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, magnitude_of(y[e]));
+            for (int e = 0; e < 8; ++e) y[e] = x[kRope ? j : 0][h][e];
+          } else {
+            bf16_floats(raw[m][j][h], y);
+          }
+          *reinterpret_cast<uint2*>(dst + (li + h * TL) * 8) = encode8<kFormat>(y, inv, finite);
         }
       }
-    }
-    for (int o = in_warp / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    old = __shfl_sync(0xffffffffu, old, lane & ~(in_warp - 1));
-    if (warps > 1) {
-      if (lane == 0) tops[round & 1][warp] = top;
-      named_barrier_sync(1 + warp / warps, warps * 32);
-      for (int w = 0; w < warps; ++w) top = fmaxf(top, tops[round & 1][(warp & ~(warps - 1)) + w]);
-    }
-    if (!active) continue;
-    const float need = scale_for<kFormat>(top);
-    const float scale = fresh ? need : fmaxf(old, need);
-    const float inv = 1.f / scale;
+      if (scale == before) continue;
+      if (unit_lane == 0) scales[group(m)] = scale;
+      if (fresh) continue;
+      // The block's other tokens, at the new scale (codes without a scale: zero).
+      const float ratio = before > 0.f ? before / scale : 0.f;
+      const int from = (int)(slot[m] & (tokens - 1));
+      for (int i = team; i < tokens; i += s.teams) {
+        if (i >= from && i < from + n[m]) continue;
+        uint8_t* dst = codes + ((slot[m] - from + i) * c.num_kv_heads + head[m]) * D;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int i = team + j * s.teams;
-      if (i >= n) continue;
-      uint8_t* dst = codes + ((slot + i) * c.num_kv_heads + head) * D;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float y[8];
-        if (turns) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[kRope ? j : 0][h][e];
-        } else {
-          bf16_floats(raw[j][h], y);
+        for (int h = 0; h < 2; ++h) {
+          uint2* p = reinterpret_cast<uint2*>(dst + (li + h * TL) * 8);
+          const uint2 w = *p;
+          const float2 f[4] = {decode2<kFormat>(w.x), decode2<kFormat>(w.x >> 16), decode2<kFormat>(w.y),
+                               decode2<kFormat>(w.y >> 16)};
+          const float y[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+          *p = encode8<kFormat>(y, ratio);
         }
-        *reinterpret_cast<uint2*>(dst + (li + h * TL) * 8) = encode8<kFormat>(y, inv, finite);
-      }
-    }
-    if (scale == old) continue;
-    if (unit_lane == 0) scales[group * c.num_kv_heads + head] = scale;
-    if (fresh) continue;
-    // The block's other tokens, at the new scale (codes without a scale: zero).
-    const float ratio = old > 0.f ? old / scale : 0.f;
-    const int from = (int)(slot & (tokens - 1));
-    for (int i = team; i < tokens; i += s.teams) {
-      if (i >= from && i < from + n) continue;
-      uint8_t* dst = codes + (((group << c.scale_shift) + i) * c.num_kv_heads + head) * D;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2* p = reinterpret_cast<uint2*>(dst + (li + h * TL) * 8);
-        const uint2 w = *p;
-        const float2 f[4] = {decode2<kFormat>(w.x), decode2<kFormat>(w.x >> 16), decode2<kFormat>(w.y),
-                             decode2<kFormat>(w.y >> 16)};
-        const float y[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-        *p = encode8<kFormat>(y, ratio);
       }
     }
   }
 }
 
-template <int kFormat, int D, bool kRope>
+template <int kFormat, int D, bool kRope, int kRows>
 cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs& r, const RopeRows& q,
                    int num_sms, int* status, cudaStream_t stream) {
   StoreShape s;
@@ -307,14 +328,22 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   const int tokens = 1 << c.scale_shift;
   s.teams = tokens / kRows < 1 ? 1 : tokens / kRows;
   const int threads = s.teams * (D / 16) > kThreads ? s.teams * (D / 16) : kThreads;
-  const int slots = threads / (s.teams * (D / 16));  // runs of one head that a CTA holds at once
+  const int slots = threads / (s.teams * (D / 16)) * (4 / kRows);  // runs of one head that a CTA holds at once
+  s.heads = slots < c.num_kv_heads ? slots : c.num_kv_heads;
+  auto groups = [&] { return (c.num_kv_heads + s.heads - 1) / s.heads; };
+  // Two rounds of heads for a CTA where full blocks leave each SM its four CTAs all the same
+  // (9216 rows of 32/8/128, blocks of 64: 12.4 us; with one round 13.4, with four 19.5).
+  if (2 * groups() * (rows.num_tokens / tokens) >= (int64_t)num_sms * 7)
+    s.heads = 2 * s.heads < c.num_kv_heads ? 2 * s.heads : c.num_kv_heads;
+  s.groups = groups();
+  s.by_heads = divisor(s.heads);
   // Rows of slot_mapping per CTA: a block's, or as many as fill the CTA where
   // blocks are short, but few where that leaves SMs without any.
   int64_t tile = slots > c.num_kv_heads ? (int64_t)tokens * (slots / c.num_kv_heads) : tokens;
-  if (tile > rows.num_tokens / num_sms) tile = rows.num_tokens / num_sms;
-  s.tile = (int)(tile < 1 ? 1 : tile > kTile ? kTile : tile);
-  s.heads = slots < c.num_kv_heads ? slots : c.num_kv_heads;
-  s.groups = (c.num_kv_heads + s.heads - 1) / s.heads;
+  const int64_t few = rows.num_tokens * (s.groups > 2 ? s.groups : 2) / (2 * num_sms);
+  if (tile > few) tile = few;
+  const int most = kRope ? kRotatedTile : kTile;
+  s.tile = (int)(tile < 1 ? 1 : tile > most ? most : tile);
   int64_t ctas = 2 * s.groups * ((rows.num_tokens + s.tile - 1) / s.tile);
   RopeShape qs{};
   const int64_t store_ctas = ctas;
@@ -331,19 +360,24 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   if (kRope) {
     s.by_pairs = divisor(r.rotary_dim / 2);
     table = (size_t)(s.tile + tokens) * (r.rotary_dim / 2 + 1) * sizeof(float2);  // at most 166 KB
-    const cudaError_t e = cudaFuncSetAttribute(quant_store_kernel<kFormat, D, kRope>,
+    const cudaError_t e = cudaFuncSetAttribute(quant_store_kernel<kFormat, D, kRope, kRows>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_shadow(quant_store_kernel<kFormat, D, kRope>, dim3((unsigned)ctas), threads, table, stream, rows, c,
+  return launch_shadow(quant_store_kernel<kFormat, D, kRope, kRows>, dim3((unsigned)ctas), threads, table, stream, rows, c,
                        r, q, qs, s, status);
 }
 
 template <int kFormat, int D>
 cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs* rope, const RopeRows* q,
                    int num_sms, int* status, cudaStream_t stream) {
-  if (rope) return launch<kFormat, D, true>(rows, c, *rope, *q, num_sms, status, stream);
-  return launch<kFormat, D, false>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream);
+  // Four rows of a run for a team; one row of four runs where runs are of one or two.
+  const bool longer = c.scale_shift > 1;
+  if (rope)
+    return longer ? launch<kFormat, D, true, 4>(rows, c, *rope, *q, num_sms, status, stream)
+                  : launch<kFormat, D, true, 1>(rows, c, *rope, *q, num_sms, status, stream);
+  return longer ? launch<kFormat, D, false, 4>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream)
+                : launch<kFormat, D, false, 1>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream);
 }
 
 }  // namespace
