@@ -293,6 +293,74 @@ def test_store_rope(hkv, d, bs, t, r, interleaved, dtype):
     assert again.data_ptr() == q.data_ptr() and torch.equal(q, oq)
 
 
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("hkv,d,bs,t,rotate", [
+    (8, 128, 256, 64, False), (8, 128, 256, 256, False), (8, 128, 64, 1, False), (3, 64, 48, 2, False),
+    (6, 128, 64, 16, False), (8, 128, 256, 16, True), (5, 64, 64, 1, True), (8, 128, 256, 256, True),
+    (2, 128, 32, 32, True)])
+def test_store_many_rows(hkv, d, bs, t, rotate, dtype):
+    """More rows than the CTAs that run at once: sequences end to end, each from the start of a page, some rows
+    without a slot; the same bits as calls of a sequence each, and the formula's numbers.  The rows without a slot cut
+    a block's run in two, which leaves that block undefined, and only that one."""
+    g = gen(t + d)
+    lens = [3700, 1, 2049, 0, 1600, 1023, 255, 800]
+    n, hq = sum(lens), hkv
+    pages = [-(-x // bs) for x in lens]
+    blocks = sum(pages) + 2
+    ids = torch.randperm(blocks, generator=g)
+    slots, first = [], 0
+    for x, m in zip(lens, pages):
+        p = torch.arange(x)
+        slots.append(ids[first:first + m][p // bs] * bs + p % bs)
+        first += m
+    slots = torch.cat(slots).to(i32)
+    slots[5000:5003] = -1
+    x = randn((n, hq + 2 * hkv, d), g).to(DEV)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    pos = torch.arange(n, device=DEV) + 77
+    freqs, magnitude = kvp.attn_rope_freqs(d, device=DEV)
+    host = [cache_arrays(blocks, bs, t, hkv, d, dtype, g) for _ in range(2)]
+    dev, parts = ([to_dev(*h) for h in host] for _ in range(2))
+    out = [torch.zeros((n, hq, d), dtype=bf16, device=DEV) for _ in range(2)]
+
+    def store(a, b, arrays, to):
+        cache = (arrays[0][0], arrays[1][0], arrays[0][1], arrays[1][1])
+        if rotate:
+            kvp.kv_quant_store_rope(q[a:b], k[a:b], v[a:b], pos[a:b], slots[a:b].to(DEV), freqs, *cache, magnitude,
+                                    out=to[a:b])
+        else:
+            kvp.kv_quant_store(k[a:b], v[a:b], slots[a:b].to(DEV), *cache)
+
+    store(0, n, dev, out[0])
+    a = 0
+    for m in lens:
+        store(a, a + m, parts, out[1])
+        a += m
+    cut = slots[4999].item() // t
+    if cut != slots[5003].item() // t:
+        cut = None
+
+    def without_cut(codes, scales):
+        if cut is not None:
+            codes.view(-1, t, hkv, d)[cut] = 0
+            scales.view(-1, hkv)[cut] = 0
+        return codes, scales
+
+    for one, many in zip(dev, parts):
+        for arrays in (one, many):
+            without_cut(arrays[0].view(torch.uint8), arrays[1])
+        assert torch.equal(bits(one[0]), bits(many[0])) and torch.equal(one[1], many[1])
+    assert torch.equal(*out)
+    for rows, h, arrays in ((k, host[0], dev[0]), (v, host[1], dev[1])):
+        if rotate and rows is k:
+            continue
+        want = (h[0].to(f32).to(f64), h[1].to(f64))
+        ref.store(rows.cpu().to(f64), slots, *want, dtype)
+        without_cut(*want)
+        assert_store(arrays, want, dtype)
+    assert kvp.device_status() == 0
+
+
 # ------------------------------------------------------------------------ load
 
 def batch(lens, bs, spare, g, width=None):
