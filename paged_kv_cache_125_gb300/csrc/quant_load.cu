@@ -6,8 +6,9 @@
 // stores that pass L2 by); the codes of a token's heads are contiguous, so a
 // warp's loads and stores are too.  A CTA has 8 or 16 tokens of K or of V: with both
 // in one CTA, or with several tokens' loads of a thread in flight together, a
-// sequence of 131072 tokens took 143 to 162 us; so it takes 130 (93% of the
-// copy's rate).
+// sequence of 131072 tokens took 143 to 162 us; so it takes 131 (93% of the
+// copy's rate).  Eight prefixes of 100 .. 2048 tokens, 53 MB: 11.8 us (4.5 TB/s),
+// three dependent trips (length, page, codes) and a start in it.
 #include "quant_device.cuh"
 
 namespace kvp {

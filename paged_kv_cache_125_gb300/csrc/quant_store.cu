@@ -11,10 +11,14 @@
 // Memory bound: a row is read once (bf16) and its codes are written once, so
 // the numbers of a run are held in registers between the search for the largest
 // one and the rounding.  A team of head_dim / 16 lanes has a row of one head,
-// two 16-byte chunks per lane, and at most four rows; a run is shared by as
-// many teams as its block needs.  A CTA has some rows of slot_mapping, one of K
-// and V, and some of the heads: few enough that its warps hold a full block's
-// runs at once.
+// two 16-byte chunks per lane, and four rows (of one run, or of four runs where
+// blocks have one or two tokens); a run is shared by as many teams as its block
+// needs.  A CTA has some rows of slot_mapping, one of K and V, and some of the
+// heads: few enough that its warps hold a full block's runs in one or two rounds.
+// Eight prompts of 256 .. 2048 tokens (9216 rows of 32/8/128, int8, blocks of 64):
+// 12.3 us, 4.6 TB/s of the 6.7 that a copy reaches; 40000 rows 44 us, 5.6 TB/s.
+// What remains is the start and two dependent trips, to the slots and to the rows.
+// 64 decode rows: 3.2 us, a launch.
 #include "rope_device.cuh"
 
 namespace kvp {

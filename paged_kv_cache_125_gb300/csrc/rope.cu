@@ -11,7 +11,8 @@
 // cosines and sines of one 16-byte chunk's pairs (of two chunks' in the half
 // layout, where x and y stand in different ones) in registers and applies them
 // to several heads, so that a head costs two or four 16-byte accesses and the
-// rotation itself.  Neighbouring threads have neighbouring chunks.
+// rotation itself.  Neighbouring threads have neighbouring chunks.  16384 tokens
+// of 32/8/128: 51.6 us, 6.5 TB/s (a copy: 6.7).
 #include "rope_device.cuh"
 
 namespace kvp {
