@@ -19,6 +19,8 @@
 // 12.3 us, 4.6 TB/s of the 6.7 that a copy reaches; 40000 rows 44 us, 5.6 TB/s.
 // What remains is the start and two dependent trips, to the slots and to the rows.
 // 64 decode rows: 3.2 us, a launch.
+#include <type_traits>
+
 #include "rope_device.cuh"
 
 namespace kvp {
@@ -100,10 +102,10 @@ __device__ __forceinline__ void rotate_row(const uint4 (&raw)[2], const uint16_t
 
 // Registers for four CTAs of 256 threads per SM (9216 rows of 32/8/128: 10.1 us; with as
 // many registers as the compiler likes, and three CTAs, 12.7), for three where runs are
-// one row (16 us; 18.5 with two), for two where rows are rotated.
-__host__ __device__ constexpr int most_threads(int rows) { return rows == 1 ? kThreads : kMostThreads; }
+// one or two rows (16 us; 18.5 with two, and four make 2300 rows 8.3 for 6.7), for two where rows are rotated.
+__host__ __device__ constexpr int most_threads(int rows) { return rows < 4 ? kThreads : kMostThreads; }
 __host__ __device__ constexpr int least_ctas(bool rope, int rows) {
-  return rows == 1 ? (rope ? 2 : 3) : (rope ? 1 : 2);
+  return rows < 4 ? (rope ? 2 : 3) : (rope ? 1 : 2);
 }
 
 // kRows rows of a team's run, kRuns runs at once.
@@ -342,7 +344,9 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   s.groups = groups();
   s.by_heads = divisor(s.heads);
   // Rows of slot_mapping per CTA: a block's, or as many as fill the CTA where
-  // blocks are short, but few where that leaves SMs without any.
+  // blocks are short, but few where that leaves SMs without any.  (A window shorter
+  // than a block leaves CTAs without a run's start: 9216 rows, blocks of 256 13.8 us, in
+  // windows of 60 rows 21.2.)
   int64_t tile = slots > c.num_kv_heads ? (int64_t)tokens * (slots / c.num_kv_heads) : tokens;
   const int64_t few = rows.num_tokens * (s.groups > 2 ? s.groups : 2) / (2 * num_sms);
   if (tile > few) tile = few;
@@ -375,13 +379,17 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
 template <int kFormat, int D>
 cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs* rope, const RopeRows* q,
                    int num_sms, int* status, cudaStream_t stream) {
-  // Four rows of a run for a team; one row of four runs where runs are of one or two.
-  const bool longer = c.scale_shift > 1;
-  if (rope)
-    return longer ? launch<kFormat, D, true, 4>(rows, c, *rope, *q, num_sms, status, stream)
-                  : launch<kFormat, D, true, 1>(rows, c, *rope, *q, num_sms, status, stream);
-  return longer ? launch<kFormat, D, false, 4>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream)
-                : launch<kFormat, D, false, 1>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream);
+  // Four rows for a team: of one run, or of four or two where runs are of one or two
+  // (9216 rows of 32/8/128: 15.9 us for 21.0 with one run of one row, 11.7 for 15.4 with
+  // one run of two).
+  auto with = [&](auto rows_of_run) {
+    constexpr int R = decltype(rows_of_run)::value;
+    return rope ? launch<kFormat, D, true, R>(rows, c, *rope, *q, num_sms, status, stream)
+                : launch<kFormat, D, false, R>(rows, c, RopeArgs{}, RopeRows{}, num_sms, status, stream);
+  };
+  if (c.scale_shift == 0) return with(std::integral_constant<int, 1>());
+  if (c.scale_shift == 1) return with(std::integral_constant<int, 2>());
+  return with(std::integral_constant<int, 4>());
 }
 
 }  // namespace
