@@ -33,10 +33,14 @@
 //   thread's own S.
 //   Both kinds of instruction sum in fp32.
 // * Softmax: m is a running reference for p * vs, l = sum p and O = sum (p vs) vc
-//   are both relative to it.  W = p * vs is rounded to fp16 (2^-11; at most 2^8 and
-//   mostly at most 1): V's scales, which may differ by any factor between
-//   blocks, thus stay out of fp16's range.  m moves, and O and l with it, only
-//   when a weight would exceed 2^8.
+//   are both relative to it.  W = p * vs is rounded to fp16: V's scales, which may
+//   differ by any factor between blocks, thus stay out of fp16's range.  m moves, and O
+//   and l with it, only when a weight would exceed 2^15, and then to where that one
+//   is 2^11 .. 2^12.  So fp16's range lies below the largest weight: one down to 2^-25
+//   of it is off by 2^-11 of itself, a smaller one by 2^-36 of the largest, and what
+//   lies behind a key that takes nearly all of the weight keeps its bits.  (A step
+//   whose weights are below 1/2 could be raised apart: 5 to 10% of the time for all
+//   calls, and 25% for those.)
 // * Where scale_tokens is 16 or more (kUniform), a unit has one scale of K and
 //   one of V per kv head.
 #include <cudaTypedefs.h>
@@ -536,6 +540,9 @@ __device__ __forceinline__ void add_values(uint32_t addr, int n, int c, const ui
   }
 }
 
+// log2 of the largest weight that there may be, and of the one that m moves for.
+constexpr float kMostWeight = 15.f, kFirstWeight = 12.f;
+
 // log2 of a scale, rounded up; below 2^-64 a scale counts as that.
 __device__ __forceinline__ float log2_above(float scale) {
   const int e = (int)(__float_as_uint(scale) >> 23) - 126;
@@ -652,13 +659,13 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
           }
           top = fmaxf(top, fmaxf(fmaxf(sc[p][0] + lv[0], sc[p][1] + lv[1]), fmaxf(sc[p][2] + lv[2], sc[p][3] + lv[3])));
         }
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {  // also a sequence's first unit
+        if (__any_sync(0xffffffffu, top > m + kMostWeight)) {  // also a sequence's first unit
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const bool grow = top > m + 8.f;
-          const float alpha = grow ? fast_exp2(m - top) : 1.f;
+          const bool grow = top > m + kMostWeight;
+          const float to = top - kFirstWeight, alpha = grow ? fast_exp2(m - to) : 1.f;
           if (grow) {
-            m = top;
+            m = to;
             l *= alpha;
           }
           const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);

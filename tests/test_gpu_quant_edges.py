@@ -1,0 +1,74 @@
+"""The 8-bit cache where its numbers lie far apart, on the GPU against 64-bit
+definitions.
+
+Tolerances of decode: bf16 output 2^-8 |out|; weights p * scale rounded to fp16, by
+2^-11 of each, so 2^-11 sum p |v|; and the same again for the scores' own error (below
+2^-13 here) and for weights beyond 2^-25 of the largest, which a gap of 26 has some of:
+2^-36 of it, 2^-9 of themselves, in either direction.  Nothing in them grows with the
+context.
+"""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_125_gb300 as kvp
+import quant_reference as ref
+from test_gpu_quant import DEV, E4M3, INT8, bf16, clean_status, f32, f64, i32  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------- decode: one dominant key
+
+def dominated(hq, hkv, d, t, dtype, n, at, gap, seed, v_scale=None):
+    """One sequence whose key `at` counts about 2^gap times as much as any other; its values are zero in the first
+    half of the columns, the others' have a mean of a half.  -> q of three rows, arrays, tables, softmax scale."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    bs = 256
+    blocks = -(-n // bs)
+    size = 1.0 if dtype == E4M3 else 0.25
+    k_scale, v_scale = 2.0 ** -5 / size, v_scale or 2.0 ** -6 / size
+
+    def codes(mean, spread):
+        x = torch.empty((blocks * bs, hkv, d), device=DEV).normal_(mean, spread, generator=g)
+        return x.clamp_(-ref.LIMIT[dtype], ref.LIMIT[dtype])
+
+    # scores (natural): 2 * k[0] and a spread of a half
+    k, v = codes(0.0, 8.0 * size), codes(32.0 * size, 64.0 * size)
+    k[at], k[at, :, 0] = 0.0, gap * math.log(2) / 2 / k_scale
+    v[at, :, :d // 2] = 0.0
+    arrays = [(x.round() if dtype == INT8 else x).to(dtype).view(blocks, bs, hkv, d) for x in (k, v)]
+    scales = [torch.full((blocks, bs // t, hkv), s, device=DEV) for s in (k_scale, v_scale)]
+    q = torch.empty((3, hq, d), device=DEV).normal_(generator=g)
+    q[:, :, 0] = 16.0
+    tables = torch.randperm(blocks, generator=g, device=DEV).to(i32)[None]
+    for x in arrays + scales:  # pages in the table's order
+        x.view(torch.uint8)[tables[0].long()] = x.view(torch.uint8).clone()
+    return q.to(bf16), arrays, scales, tables, 0.125
+
+
+def check_dominated(q, arrays, scales, tables, scale, n):
+    """One sequence shared by many CTAs, and as many sequences as CTAs, none of them cut."""
+    want, size, _ = ref.decode(q, *((c.to(f32), s) for c, s in zip(arrays, scales)), tables.expand(3, -1), [n] * 3, scale)
+    tol = 2.0 ** -8 * want.abs() + 2 * 2.0 ** -11 * size
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for rows in (1, sms):
+        out = kvp.attn_decode_quant(q[torch.arange(rows, device=DEV) % 3], *arrays, *scales,
+                                    tables.expand(rows, -1).contiguous(),
+                                    torch.full((rows,), n, dtype=i32, device=DEV), n, softmax_scale=scale)
+        for b in {0, rows // 2, rows - 1}:
+            off = (out[b].cpu().to(f64) - want[b % 3]).abs()
+            assert bool((off <= tol[b % 3]).all()), (rows, b, (off / size[b % 3]).max().item())
+    assert kvp.device_status() == 0
+
+
+@pytest.mark.parametrize("gap", [8, 18, 22, 24, 26])
+@pytest.mark.parametrize("hq,hkv,d,t,dtype,n,at", [
+    (8, 8, 64, 16, E4M3, 131072, 0), (16, 8, 128, 4, INT8, 65536, 0), (8, 1, 128, 16, E4M3, 131072, 0),
+    (32, 8, 128, 16, E4M3, 40000, 20000), (64, 8, 64, 32, INT8, 30001, 30000), (4, 4, 128, 1, E4M3, 32768, 100)])
+def test_decode_one_key_outweighs_a_long_context(hq, hkv, d, t, dtype, n, at, gap):
+    """What lies behind a key that takes nearly all of the weight: each of the other weights keeps its bits, however
+    many they are."""
+    q, arrays, scales, tables, scale = dominated(hq, hkv, d, t, dtype, n, at, gap, n + gap)
+    check_dominated(q, arrays, scales, tables, scale, n)
