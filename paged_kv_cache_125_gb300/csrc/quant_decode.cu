@@ -543,10 +543,15 @@ __device__ __forceinline__ void add_values(uint32_t addr, int n, int c, const ui
 // log2 of the largest weight that there may be, and of the one that m moves for.
 constexpr float kMostWeight = 15.f, kFirstWeight = 12.f;
 
-// log2 of a scale, rounded up; below 2^-64 a scale counts as that.
+// V's scales are taken times 2^-16, and outputs times 2^16: the largest p is then
+// 2^(27 - e) .. 2^(30 - e) for scales of 2^e, between 2^95 and 2^-100 whatever they are
+// (sums over a context stay finite, and a p counts down to 2^-26 of it at least).
+constexpr float kValueUnit = 1.52587890625e-05f;
+
+// log2 of a scale times 2^-16, rounded up; a scale below 2^-64 counts as that.
 __device__ __forceinline__ float log2_above(float scale) {
   const int e = (int)(__float_as_uint(scale) >> 23) - 126;
-  return (float)(e < -64 ? -64 : e);
+  return (float)(e < -80 ? -80 : e);
 }
 
 // Thread (r, c) of a warp (r = lane / 4, c = lane % 4) has head r's scores of
@@ -637,7 +642,7 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
           float lv[4];
           if constexpr (kUniform) {
             const float2 scale = *reinterpret_cast<const float2*>(&sm.scales[s][0][2 * at]);
-            const float kq = scale.x * cq, v = PW == 1 || n[p] > 0 ? scale.y : 0.f;
+            const float kq = scale.x * cq, v = PW == 1 || n[p] > 0 ? scale.y * kValueUnit : 0.f;
             const float lu = log2_above(v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[p][i] *= kq, vs[p][i] = v, lv[i] = lu;
@@ -647,7 +652,7 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
             sc[p][0] *= cq * ks.x, sc[p][1] *= cq * ks.y, sc[p][2] *= cq * ks.z, sc[p][3] *= cq * ks.w;
             vs[p][0] = v4.x, vs[p][1] = v4.y, vs[p][2] = v4.z, vs[p][3] = v4.w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lv[i] = log2_above(vs[p][i]);
+            for (int i = 0; i < 4; ++i) vs[p][i] *= kValueUnit, lv[i] = log2_above(vs[p][i]);
           }
           if (n[p] < kPiece) {
 #pragma unroll
@@ -759,7 +764,7 @@ __device__ __forceinline__ void consume(const Args& x, Smem<D, G>& sm) {
       if (!oc[y]) continue;
       const int h = head0 + 2 * c + y;
       if (flags & F_WHOLE) {
-        const float inv = 1.f / lh[y];
+        const float inv = 1.f / kValueUnit / lh[y];
         __nv_bfloat16* to =
             reinterpret_cast<__nv_bfloat16*>(x.a.out + (int64_t)b * x.a.out_stride + (int64_t)h * D) + r;
 #pragma unroll
@@ -902,7 +907,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     }
   }
   if (ch.last < ch.first) return;
-  const float inv = 1.f / l;
+  const float inv = 1.f / kValueUnit / l;
   uint32_t* to = reinterpret_cast<uint32_t*>(x.a.out + (int64_t)ch.b * x.a.out_stride + (int64_t)h * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) to[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);

@@ -72,3 +72,12 @@ def test_decode_one_key_outweighs_a_long_context(hq, hkv, d, t, dtype, n, at, ga
     many they are."""
     q, arrays, scales, tables, scale = dominated(hq, hkv, d, t, dtype, n, at, gap, n + gap)
     check_dominated(q, arrays, scales, tables, scale, n)
+
+
+@pytest.mark.parametrize("dtype,power", [(E4M3, 60), (E4M3, 100), (E4M3, 119), (INT8, 100), (INT8, 120), (E4M3, -64), (INT8, -60)])
+@pytest.mark.parametrize("gap", [7, 20])
+def test_decode_values_of_any_size(dtype, power, gap):
+    """V's scales from the least to the largest that bf16 rows give."""
+    for hq, hkv, d, t in ((16, 8, 128, 16), (2, 2, 64, 4)):
+        q, arrays, scales, tables, scale = dominated(hq, hkv, d, t, dtype, 20000, 0, gap, power, v_scale=2.0 ** power)
+        check_dominated(q, arrays, scales, tables, scale, 20000)
