@@ -753,7 +753,8 @@ int kv_quant_load(const void *k_cache, const void *v_cache, const float *k_scale
                   int64_t k_stride_tok, kvp_bf16 *v, int64_t v_stride_tok, kvp_stream_t stream);
 
 /* Bytes of device workspace attn_decode_quant needs for this shape on the
- * current device (0 on error; see kvp_last_error). */
+ * current device (0 on error; see kvp_last_error).  Never less for more
+ * sequences or a larger bound: that of a loop's largest batch serves them all. */
 size_t attn_decode_quant_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                         int max_context_len);
 

@@ -928,7 +928,7 @@ bool unit_map(CUtensorMap* map, const void* codes, const QuantCache& c, int unit
 }
 
 struct Plan {
-  int ctas;
+  int ctas, most;  // most: with cuts; the workspace is sized by it
   bool by_seq, whole;
   size_t part_bytes, total_bytes;
 };
@@ -940,18 +940,21 @@ struct Plan {
 constexpr int kWholeStages = 6, kWholeStagesOfMany = 16, kMany = 48;
 
 // One CTA per SM, or as many as the bound of the lengths gives a share (64 tokens
-// or a sequence each).
+// or a sequence each).  The workspace is that of a batch that is cut even where none
+// is: it then never shrinks as sequences or the bound grow, and that of the largest
+// batch serves the others.
 Plan plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_context_len, int num_sms) {
   Plan p;
   const int stage_tokens = kPiece * (head_dim == 128 ? stage_pieces<128>() : stage_pieces<64>()) / num_kv_heads;
   p.whole = max_context_len <= stage_tokens * (num_seqs >= kMany ? kWholeStagesOfMany : kWholeStages);
   long long ctas = ((long long)num_seqs * max_context_len + 63) / 64;
-  if (ctas < num_seqs || p.whole) ctas = num_seqs;
+  if (ctas < num_seqs) ctas = num_seqs;
   if (ctas > num_sms) ctas = num_sms;
-  p.ctas = ctas < 1 ? 1 : (int)ctas;
+  p.most = ctas < 1 ? 1 : (int)ctas;
+  p.ctas = p.whole && num_seqs < p.most ? (num_seqs < 1 ? 1 : num_seqs) : p.most;
   p.by_seq = num_seqs <= p.ctas;
-  p.part_bytes = (size_t)p.ctas * 2 * num_heads * (head_dim + 4) * sizeof(float);  // (a multiple of 16)
-  p.total_bytes = p.part_bytes + (size_t)p.ctas * sizeof(Chain) + 16;
+  p.part_bytes = (size_t)p.most * 2 * num_heads * (head_dim + 4) * sizeof(float);  // (a multiple of 16)
+  p.total_bytes = p.part_bytes + (size_t)p.most * sizeof(Chain) + 16;
   return p;
 }
 

@@ -14,7 +14,8 @@ import torch
 
 import paged_kv_cache_125_gb300 as kvp
 import quant_reference as ref
-from test_gpu_quant import DEV, E4M3, INT8, bf16, clean_status, f32, f64, i32  # noqa: F401
+from test_gpu_quant import (DEV, E4M3, INT8, assert_decode, bf16, clean_status, decode_case, f32, f64, i32,  # noqa: F401
+                            run_decode)
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +82,27 @@ def test_decode_values_of_any_size(dtype, power, gap):
     for hq, hkv, d, t in ((16, 8, 128, 16), (2, 2, 64, 4)):
         q, arrays, scales, tables, scale = dominated(hq, hkv, d, t, dtype, 20000, 0, gap, power, v_scale=2.0 ** power)
         check_dominated(q, arrays, scales, tables, scale, 20000)
+
+
+# ------------------------------------------------------------- decode: workspace
+
+@pytest.mark.parametrize("heads", [(16, 8, 128), (8, 1, 128), (2, 1, 64), (64, 8, 64)])
+def test_decode_workspace_of_a_larger_batch_serves(heads):
+    """No smaller batch, and none of shorter contexts, needs more."""
+    bounds = [0, 1, 16, 64, 96, 97, 192, 256, 257, 512, 1024, 2048, 4096, 100000]
+    below = [0] * len(bounds)
+    for n in range(0, 400):
+        need = [kvp.attn_decode_quant_workspace_size(n, *heads, bound) for bound in bounds]
+        assert need == sorted(need), n
+        assert all(a <= b for a, b in zip(below, need)), n
+        below = need
+
+
+def test_decode_batches_in_one_workspace():
+    ws = torch.empty((kvp.attn_decode_quant_workspace_size(64, 16, 8, 128, 256),), dtype=torch.uint8, device=DEV)
+    for n in (64, 48, 47, 32, 1):
+        lens = [256 - 3 * i for i in range(n)]
+        q, host, dev, tables = decode_case(16, 8, 128, 64, 16, E4M3, lens, n, poison=False)
+        out = run_decode(q[:, :16], dev, tables, lens, longest=256, workspace=ws)
+        assert_decode(out, q[:, :16], host, tables, lens, 128 ** -0.5)
+    assert kvp.device_status() == 0
