@@ -691,8 +691,9 @@ enum {
  * scale is the least power of two, 2^-64 or more, with which no number of the
  * run exceeds the largest code; a run that does not begin its block (offset 0)
  * takes the block's present scale where that is larger.  Where a block's scale
- * grows, the codes of its other tokens are rounded anew at the new scale
- * (a present scale that is not above 0 leaves them zero).  A run at offset 0
+ * grows, the codes of its other tokens are rounded anew at the new scale.  A
+ * present scale that is zero, negative, infinite or NaN counts as none, and the
+ * block's other codes become zero, NaN among them.  A run at offset 0
  * begins the block: other tokens' codes stay as they are and mean nothing until
  * they are stored.  Codes are rounded to nearest, ties to even.  Infinities and
  * NaN do not count for the scale; infinities become the largest code, NaN is

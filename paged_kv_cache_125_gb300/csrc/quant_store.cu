@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(most_threads(kRows), least_ctas(kRope, kRows))
         }
       }
       for (int o = in_warp / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float before = __shfl_sync(0xffffffffu, old[m], lane & ~(in_warp - 1));
+      float before = __shfl_sync(0xffffffffu, old[m], lane & ~(in_warp - 1));
+      if (!(before > 0.f && before < INFINITY)) before = 0.f;  // no scale: its codes mean nothing
       if (warps > 1) {
         const int turn = (round * kRuns + m) & 1;
         if (lane == 0) tops[turn][warp] = top;
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(most_threads(kRows), least_ctas(kRope, kRows))
       if (scale == before) continue;
       if (unit_lane == 0) scales[group(m)] = scale;
       if (fresh) continue;
-      // The block's other tokens, at the new scale (codes without a scale: zero).
-      const float ratio = before > 0.f ? before / scale : 0.f;
+      // The block's other tokens, at the new scale (codes without a scale: zero, NaN too).
+      const float ratio = before / scale;
       const int from = (int)(slot[m] & (tokens - 1));
       for (int i = team; i < tokens; i += s.teams) {
         if (i >= from && i < from + n[m]) continue;
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(most_threads(kRows), least_ctas(kRope, kRows))
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint2* p = reinterpret_cast<uint2*>(dst + (li + h * TL) * 8);
-          const uint2 w = *p;
+          const uint2 w = before > 0.f ? *p : make_uint2(0, 0);
           const float2 f[4] = {decode2<kFormat>(w.x), decode2<kFormat>(w.x >> 16), decode2<kFormat>(w.y),
                                decode2<kFormat>(w.y >> 16)};
           const float y[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};

@@ -14,8 +14,8 @@ import torch
 
 import paged_kv_cache_125_gb300 as kvp
 import quant_reference as ref
-from test_gpu_quant import (DEV, E4M3, INT8, assert_decode, bf16, clean_status, decode_case, f32, f64, i32,  # noqa: F401
-                            run_decode)
+from test_gpu_quant import (DEV, E4M3, INT8, assert_decode, bf16, bits, clean_status, decode_case, f32, f64,  # noqa: F401
+                            gen, i32, randn, run_decode, to_dev)
 
 pytestmark = pytest.mark.gpu
 
@@ -105,4 +105,33 @@ def test_decode_batches_in_one_workspace():
         q, host, dev, tables = decode_case(16, 8, 128, 64, 16, E4M3, lens, n, poison=False)
         out = run_decode(q[:, :16], dev, tables, lens, longest=256, workspace=ws)
         assert_decode(out, q[:, :16], host, tables, lens, 128 ** -0.5)
+    assert kvp.device_status() == 0
+
+
+# -------------------------------------------------- store: scales that mean nothing
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("t", [2, 8, 64])
+def test_store_over_scales_that_mean_nothing(t, dtype):
+    """A block that is continued over a scale of NaN, zero, below zero or infinity: the new rows' own scale, and zeros
+    in the place of every other code, those that are NaN among them."""
+    present = torch.tensor([math.nan, 0.0, -1.0, math.inf, -math.inf, -0.0, -math.nan])
+    b, bs = len(present), 64
+    codes = torch.randint(0, 256, (b, bs, 2, 64), generator=gen(t), dtype=torch.uint8)
+    codes[:, 0], codes[:, bs - 1] = 0x7F, 0xFF
+    scales = present[:, None, None].expand(b, bs // t, 2).contiguous()
+    dev = [to_dev(codes.view(dtype), scales) for _ in range(2)]
+    x = randn((b, 4, 64), gen(t + 1)).to(DEV)
+    place = t - 1
+    slots = torch.arange(b, dtype=i32) * bs + place
+    kvp.kv_quant_store(x[:, :2], x[:, 2:], slots.to(DEV), dev[0][0], dev[1][0], dev[0][1], dev[1][1])
+    for (c, s), rows in zip(dev, (x[:, :2], x[:, 2:])):
+        rows = rows.cpu().to(f64)
+        need = torch.tensor([[ref.scale_for(r.abs().max().item(), dtype) for r in head] for head in rows], dtype=f64)
+        assert torch.equal(s[:, 0].cpu().to(f64), need)
+        got = c.cpu()[:, :t].to(f32).to(f64)
+        assert torch.equal(got[:, place], ref.encode(rows / need[..., None], dtype))
+        assert not got[:, :place].any() and not torch.isnan(got).any()
+        if t < bs:
+            assert torch.equal(bits(c)[:, t:], codes[:, t:])
     assert kvp.device_status() == 0
