@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
 #pragma unroll
     for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(m, __shfl_sync(0xffffffffu, top, 0));
-    if (top == -INFINITY) continue;
+    // (A part has tokens, so m is -inf only of keys that are all NaN, and so is the sum.)
     const float w = fast_exp2(m - top), share = fast_exp2(s.x - top);
     l = l * w + share * s.y;
 #pragma unroll

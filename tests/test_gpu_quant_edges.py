@@ -135,3 +135,22 @@ def test_store_over_scales_that_mean_nothing(t, dtype):
         if t < bs:
             assert torch.equal(bits(c)[:, t:], codes[:, t:])
     assert kvp.device_status() == 0
+
+
+# -------------------------------------------------------- decode: keys that are NaN
+
+def test_decode_keys_that_are_nan():
+    """A NaN key makes its kv head's outputs NaN, also where it fills the parts of many CTAs and no other."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * 64  # four units of 16 tokens for each CTA
+    q, host, dev, tables = decode_case(16, 8, 128, 256, 16, E4M3, [n], 61, poison=False)
+    want = run_decode(q[:, :16], dev, tables, [n])
+    codes = dev[0][0].view(torch.uint8)
+    for first, last in ((0, 64 * 64), (5, 6), (n - 1, n), (0, n)):
+        held = codes.clone()
+        for p in range(first, last):
+            codes[int(tables[0, p // 256]), p % 256, 3] = 0x7F
+        out = run_decode(q[:, :16], dev, tables, [n])
+        assert bool(torch.isnan(out[0, 6:8]).all()), (first, last)
+        assert torch.equal(out[0, :6], want[0, :6]) and torch.equal(out[0, 8:], want[0, 8:])
+        codes.copy_(held)
