@@ -674,9 +674,17 @@ int attn_rope(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k, int64_
  * steps of 1/127 of a block's largest number to twice that.
  *   scale_tokens  a power of two up to 256 that divides block_size
  * Supported: head_dim in {64, 128}; a pool of fewer than 2^31 slots.
- * A page is copied, moved or freed like one of a bf16 cache: kv_copy_blocks and
- * the page calls take the code arrays as 16-bit numbers of half the head_dim;
- * kv_copy_blocks takes the scale arrays likewise.
+ * kv_copy_blocks copies pages of each array: codes as 16-bit numbers of half the
+ * head_dim, scales as two of them each (block_elems = 2 * (block_size /
+ * scale_tokens) * num_kv_heads).  kv_pages_fork and kv_pages_compact move the
+ * pages of the one pool that they are given, so K's and V's codes are planes of
+ * one allocation there; the scales do not move with them.  The caller copies
+ * those of each page that moved, before anything reads it, with kv_copy_blocks:
+ *   after kv_pages_compact   p to places[p], for every page p with places[p]
+ *                            neither -1 nor p
+ *   after kv_pages_fork      block_tables[parents[r]][j] to out_tables[r][j], for
+ *                            every new row r whose last page, j, is not filled,
+ *                            where the two differ
  */
 enum {
   KVP_E4M3 = 0, /* 8-bit floats: 4 exponent bits, 3 of mantissa, up to 448 */

@@ -14,8 +14,8 @@ import torch
 
 import paged_kv_cache_125_gb300 as kvp
 import quant_reference as ref
-from test_gpu_quant import (DEV, E4M3, INT8, assert_decode, bf16, bits, clean_status, decode_case, f32, f64,  # noqa: F401
-                            gen, i32, randn, run_decode, to_dev)
+from test_gpu_quant import (DEV, E4M3, INT8, assert_decode, bf16, bits, cache_arrays, clean_status,  # noqa: F401
+                            decode_case, f32, f64, gen, i32, randn, run_decode, to_dev)
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,76 @@ def test_decode_keys_that_are_nan():
         assert bool(torch.isnan(out[0, 6:8]).all()), (first, last)
         assert torch.equal(out[0, :6], want[0, :6]) and torch.equal(out[0, 8:], want[0, 8:])
         codes.copy_(held)
+
+
+# ----------------------------------------------------------------- pages of the cache
+
+def stacked_cache(blocks, bs, t, hkv, d, dtype, g):
+    """K and V as planes of one allocation: codes [2, blocks, ...], scales [2, blocks, ...]."""
+    (kc, ks), (vc, vs) = (cache_arrays(blocks, bs, t, hkv, d, dtype, g) for _ in range(2))
+    return torch.stack((kc.view(torch.uint8), vc.view(torch.uint8))).to(DEV), torch.stack((ks, vs)).to(DEV)
+
+
+def decode_stacked(q, codes, scales, dtype, tables, lens):
+    return kvp.attn_decode_quant(q, codes[0].view(dtype), codes[1].view(dtype), scales[0], scales[1], tables, lens, 100)
+
+
+def copy_scales(scales, pairs):
+    """kv_copy_blocks of the scales, as 16-bit numbers of planes [blocks, scale blocks, kv heads, 2]."""
+    pairs = torch.tensor(pairs, dtype=i32, device=DEV).view(-1, 2)
+    kvp.kv_copy_blocks(scales.view(bf16).view(*scales.shape, 2), pairs)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("hkv,d,bs,t", [(2, 64, 32, 8), (1, 128, 16, 16), (3, 64, 48, 1)])
+def test_pages_forked_and_compacted(hkv, d, bs, t, dtype):
+    """kv_pages_fork and kv_pages_compact move the codes; the caller copies the scales of the pages that moved."""
+    g = gen(bs + t)
+    hq = hkv if hkv == 3 else 2 * hkv
+    blocks, lens = 16, [bs + 5, 3, 2 * bs, 0]
+    codes, scales = stacked_cache(blocks, bs, t, hkv, d, dtype, g)
+    tables = torch.tensor([[9, 4, -1], [11, -1, -1], [2, 13, -1], [-1, -1, -1]], dtype=i32)
+    counts = torch.zeros((blocks,), dtype=i32)
+    counts[[9, 4, 11, 2, 13]] = 1
+    lens_dev = torch.tensor(lens, dtype=i32, device=DEV)
+    x = randn((6, hq + 2 * hkv, d), g).to(DEV)
+    parents = [0, 0, 1, 2, 1, 0]
+
+    def attend(tab, ctx, q):  # (decode takes 1, 2, 4 or 8 kv heads: otherwise the rows themselves)
+        if hkv != 3:
+            return decode_stacked(q, codes, scales, dtype, tab, ctx)
+        n = ctx.tolist()
+        starts = torch.tensor([sum(n[:i]) for i in range(len(n))], dtype=i32, device=DEV)
+        k, v = kvp.kv_quant_load(codes[0].view(dtype), codes[1].view(dtype), *scales, tab, ctx, starts, max(n), num_rows=sum(n))
+        return [torch.cat((k[a:a + m], v[a:a + m])) for a, m in zip(starts.tolist(), n)]
+
+    want = attend(tables.to(DEV), lens_dev, x[:4, :hq])
+    pool = codes.view(bf16)
+    tab, ctx, cnt = kvp.kv_pages_fork(pool, tables.to(DEV), lens_dev, counts.to(DEV),
+                                      torch.tensor(parents, dtype=i32, device=DEV))
+    # a forked row whose last page is another than its parent's has a copy of it
+    pairs = []
+    for r, (p, n) in enumerate(zip(parents, ctx.tolist())):
+        last = (n - 1) // bs
+        src, dst = int(tables[p, last]), int(tab[r, last])
+        if src != dst:
+            pairs.append((src, dst))
+    assert len(pairs) == 3
+    copy_scales(scales, pairs)
+    got = attend(tab, ctx, x[parents, :hq])
+    for r, p in enumerate(parents):
+        assert torch.equal(got[r], want[p]), r
+    # each goes on by itself
+    slots = torch.tensor([int(tab[r, n // bs]) * bs + n % bs if n % bs else -1 for r, n in enumerate(ctx.tolist())],
+                         dtype=i32, device=DEV)
+    kvp.kv_quant_store(8 * x[:, hq:hq + hkv], 8 * x[:, hq + hkv:], slots, codes[0].view(dtype), codes[1].view(dtype), *scales)
+    ctx = ctx + (slots >= 0).to(i32)
+    want = attend(tab, ctx, x[:, :hq])
+    assert not torch.equal(want[0], want[1])
+    # compact: places has the new id of every page
+    tab, cnt, places = kvp.kv_pages_compact(pool, tab, ctx, cnt)
+    copy_scales(scales, [(p, q) for p, q in enumerate(places.tolist()) if q >= 0 and q != p])
+    got = attend(tab, ctx, x[:, :hq])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert kvp.device_status() == 0
