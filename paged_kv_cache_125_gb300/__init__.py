@@ -788,9 +788,12 @@ def attn_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none
         raise ValueError(f"scaling must be one of {', '.join(_ROPE_SCALINGS)}, got {scaling!r}")
     turns = _ROPE_TURNS.get(scaling, (0.0, 0.0))
     low, high = (turns[0] if low is None else low), (turns[1] if high is None else high)
-    freqs = (ctypes.c_uint64 * max(1, int(rotary_dim) // 2))()
+    rotary_dim = int(rotary_dim)
+    if not 2 <= rotary_dim <= 1024:  # before room is made for it, or ctypes cuts it to an int
+        raise KvpError(-1, f"attn_rope_freqs: rotary_dim {rotary_dim} is not even or not in 2 .. 1024")
+    freqs = (ctypes.c_uint64 * (rotary_dim // 2))()
     magnitude = ctypes.c_float()
-    _check(library().attn_rope_freqs(int(rotary_dim), float(base), _ROPE_SCALINGS[scaling], float(factor),
+    _check(library().attn_rope_freqs(rotary_dim, float(base), _ROPE_SCALINGS[scaling], float(factor),
                                      float(original_len), float(low), float(high), freqs,
                                      ctypes.byref(magnitude)))
     return torch.tensor(list(freqs), dtype=torch.int64, device=device), magnitude.value

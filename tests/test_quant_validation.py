@@ -62,6 +62,13 @@ def test_frequency_refusals(lib):
         kvp.attn_rope_freqs(65, device="cpu")
 
 
+@pytest.mark.parametrize("r", [1026, 1 << 20, (1 << 32) + 64, -(1 << 32) + 64, 1 << 70, -5])
+def test_frequencies_of_a_size_that_no_head_has(r):
+    """Refused at once: no room is made for them, and no size wraps round to one that is taken."""
+    with pytest.raises(kvp.KvpError, match="rotary_dim"):
+        kvp.attn_rope_freqs(r, device="cpu")
+
+
 # ---------------------------------------------------------------- C ABI
 
 def _rope(lib, **kw):
