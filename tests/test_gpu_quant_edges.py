@@ -227,3 +227,45 @@ def test_pages_forked_and_compacted(hkv, d, bs, t, dtype):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert kvp.device_status() == 0
+
+
+# ---------------------------------------------------------- decode: none of them cut
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("hq,hkv,d,bs,t", [(16, 8, 128, 256, 16), (8, 8, 128, 24, 8), (64, 8, 64, 64, 32), (16, 4, 128, 128, 128),
+                                           (8, 1, 128, 256, 64), (2, 1, 64, 16, 1), (8, 2, 64, 512, 256)])
+@pytest.mark.parametrize("seqs,stages", [(12, 6), (60, 16)])
+def test_decode_short_contexts_in_one_launch(hq, hkv, d, bs, t, dtype, seqs, stages):
+    """Up to six stages of a sequence (16, where sequences are many) no sequence is cut: a stage holds 8 pieces of 16
+    tokens and a kv head of 128, or 16 of 64."""
+    longest = stages * 16 * (8 if d == 128 else 16) // hkv
+    lens = [(longest - 5 * i) % (longest + 1) for i in range(seqs - 2)] + [0, 1]
+    q, host, dev, tables = decode_case(hq, hkv, d, bs, t, dtype, lens, seqs + d)
+    host = [(torch.nan_to_num(h[0].to(f32)), torch.nan_to_num(h[1])) for h in host]
+    for bound in (longest, longest + 1):  # the largest that is not cut, the least that is
+        out = run_decode(q[:, :hq], dev, tables, lens, longest=bound)
+        assert_decode(out, q[:, :hq], host, tables, lens, d ** -0.5)
+    assert kvp.device_status() == 0
+
+
+# ------------------------------------------------------------- the rotating store
+
+def test_store_rope_without_queries():
+    """num_heads 0 of the C call: only k and v; the same codes as with queries beside them."""
+    g = gen(71)
+    n, hkv, d, t, bs = 40, 2, 64, 8, 32
+    x = randn((n, 3 * hkv, d), g).to(DEV)
+    q, k, v = x[:, :hkv], x[:, hkv:2 * hkv], x[:, 2 * hkv:]
+    pos, slots = torch.arange(n, device=DEV), torch.arange(n, dtype=i32, device=DEV)
+    freqs, magnitude = kvp.attn_rope_freqs(d, device=DEV)
+    host = [cache_arrays(3, bs, t, hkv, d, E4M3, g) for _ in range(2)]
+    both, alone = ([to_dev(*h) for h in host] for _ in range(2))
+    kvp.kv_quant_store_rope(q, k, v, pos, slots, freqs, both[0][0], both[1][0], both[0][1], both[1][1], magnitude)
+    rc = kvp.library().kv_quant_store_rope(
+        None, 0, k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), pos.data_ptr(), slots.data_ptr(), n,
+        freqs.data_ptr(), d, 0, magnitude, 0, None, 0, alone[0][0].data_ptr(), alone[1][0].data_ptr(),
+        alone[0][1].data_ptr(), alone[1][1].data_ptr(), 0, 3, bs, t, hkv, d, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for a, b in zip(both, alone):
+        assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(a[1], b[1])
+    assert kvp.device_status() == 0
