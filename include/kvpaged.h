@@ -620,8 +620,9 @@ enum {
   KVP_ROPE_LINEAR = 1,    /* w_i / factor */
   KVP_ROPE_NTK = 2,       /* base * factor^(rotary_dim / (rotary_dim - 2)) */
   KVP_ROPE_YARN = 3,      /* w_i and w_i / factor, blended over the pairs: w_i up to the pair that turns `high`
-                           * times over original_len tokens (rounded down), w_i / factor from the one that turns
-                           * `low` times on (rounded up); cosines and sines times 0.1 ln(factor) + 1 */
+                           * times over original_len tokens (rounded down, 0 at least), w_i / factor from the one
+                           * that turns `low` times on (rounded up, rotary_dim - 1 at most; pair 0 is not
+                           * stretched); cosines and sines times 0.1 ln(factor) + 1 */
   KVP_ROPE_WAVELENGTH = 4 /* w_i and w_i / factor, blended over the pairs' turns t in original_len tokens: w_i
                            * from t = high on, w_i / factor up to t = low, by (t - low) / (high - low) between */
 };
@@ -667,7 +668,8 @@ int attn_rope(const kvp_bf16 *q, int64_t q_stride_tok, const kvp_bf16 *k, int64_
  * The cache in 8 bits.  One layer's cache is four arrays:
  *   k_cache, v_cache    [num_blocks, block_size, num_kv_heads, head_dim] codes
  *   k_scales, v_scales  [num_blocks, block_size / scale_tokens, num_kv_heads] fp32
- * all contiguous and 16-byte aligned.  The number at (slot, head, e) is its
+ * all contiguous and 16-byte aligned (a layer's scales within a larger array too:
+ * their number there has to be a multiple of 4).  The number at (slot, head, e) is its
  * code times the scale of the scale_tokens tokens around the slot and the head.
  * Half the bytes of a bf16 cache (and 4 / (scale_tokens * head_dim) more for the
  * scales); e4m3 keeps 4 significant bits of each number whatever its size, int8

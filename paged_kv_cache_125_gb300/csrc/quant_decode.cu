@@ -4,10 +4,10 @@
 //
 // with codes kc, vc and the scales ks, vs of their block of tokens and kv head.
 // Memory bound: every code of a context is read once.  512 sequences of 1000 ..
-// 8000 tokens (32/8/128, e4m3, 4.7 GB): 655 us, 7.2 TB/s, more than a copy's 6.7
-// (reads alone are faster).  64 of 512 .. 4096 (16/8/128, 294 MB): 50 us, 5.9 TB/s,
+// 8000 tokens (32/8/128, e4m3, 4.7 GB): 659 us, 7.2 TB/s, more than a copy's 6.7
+// (reads alone are faster).  64 of 512 .. 4096 (16/8/128, 294 MB): 50 us, 5.8 TB/s,
 // of which the split kernel's stream is 42 us, its start 3 and the merge 4.  One of
-// 131071 (64/8/128, int8): 51.6 us, of which the merge of 152 parts is 6.
+// 131071 (64/8/128, int8): 51.5 us, of which the merge of 152 parts is 6.
 //
 // * Work is counted in units of one page: 16 tokens of eight kv heads, up to 128 of
 //   fewer where pages are long enough.  The units of all sequences, end to end, are
@@ -64,7 +64,7 @@ constexpr int kTold = 16;  // segments that the producer may be ahead by, at mos
 static_assert(stages<64>() + 2 <= kTold, "a segment is told over one that all warps have finished");
 
 // Pieces that a warp takes from a stage: two of head_dim 64, whose 1 KB would not pay
-// for the stage's waits (64 sequences of 16384 tokens, 16/8/64 e4m3: 170 us; with one
+// for the stage's waits (64 sequences of 16384 tokens, 16/8/64 e4m3: 172 us; with one
 // 208).
 template <int D>
 __host__ __device__ constexpr int warp_pieces() {

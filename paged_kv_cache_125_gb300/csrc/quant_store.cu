@@ -16,9 +16,12 @@
 // needs.  A CTA has some rows of slot_mapping, one of K and V, and some of the
 // heads: few enough that its warps hold a full block's runs in one or two rounds.
 // Eight prompts of 256 .. 2048 tokens (9216 rows of 32/8/128, int8, blocks of 64):
-// 12.3 us, 4.6 TB/s of the 6.7 that a copy reaches; 40000 rows 44 us, 5.6 TB/s.
+// 12.5 us, 4.5 TB/s of the 6.7 that a copy reaches; 40000 rows 44 us, 5.6 TB/s.
 // What remains is the start and two dependent trips, to the slots and to the rows.
-// 64 decode rows: 3.2 us, a launch.
+// 64 decode rows: 3.3 us, a launch.
+// The comparisons below, where they name rows alone, are of one prompt stored again and
+// again to the same blocks of a cache, which L2 holds: 1 to 2 us less than with two
+// sets of rows and blocks in turn, as above (9216 rows, blocks of 64: 10.6 and 11.5).
 #include <type_traits>
 
 #include "rope_device.cuh"
@@ -339,14 +342,14 @@ cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeAr
   s.heads = slots < c.num_kv_heads ? slots : c.num_kv_heads;
   auto groups = [&] { return (c.num_kv_heads + s.heads - 1) / s.heads; };
   // Two rounds of heads for a CTA where full blocks leave each SM its four CTAs all the same
-  // (9216 rows of 32/8/128, blocks of 64: 12.4 us; with one round 13.4, with four 19.5).
+  // (the eight prompts above: 12.5 us; with one round 13.4, with four 19.5).
   if (2 * groups() * (rows.num_tokens / tokens) >= (int64_t)num_sms * 7)
     s.heads = 2 * s.heads < c.num_kv_heads ? 2 * s.heads : c.num_kv_heads;
   s.groups = groups();
   s.by_heads = divisor(s.heads);
   // Rows of slot_mapping per CTA: a block's, or as many as fill the CTA where
   // blocks are short, but few where that leaves SMs without any.  (A window shorter
-  // than a block leaves CTAs without a run's start: 9216 rows, blocks of 256 13.8 us, in
+  // than a block leaves CTAs without a run's start: 9216 rows, blocks of 256 13.6 us, in
   // windows of 60 rows 21.2.)
   int64_t tile = slots > c.num_kv_heads ? (int64_t)tokens * (slots / c.num_kv_heads) : tokens;
   const int64_t few = rows.num_tokens * (s.groups > 2 ? s.groups : 2) / (2 * num_sms);
@@ -381,7 +384,7 @@ template <int kFormat, int D>
 cudaError_t launch(const QuantStoreRows& rows, const QuantCache& c, const RopeArgs* rope, const RopeRows* q,
                    int num_sms, int* status, cudaStream_t stream) {
   // Four rows for a team: of one run, or of four or two where runs are of one or two
-  // (9216 rows of 32/8/128: 15.9 us for 21.0 with one run of one row, 11.7 for 15.4 with
+  // (9216 rows of 32/8/128: 16.3 us for 21.0 with one run of one row, 11.9 for 15.4 with
   // one run of two).
   auto with = [&](auto rows_of_run) {
     constexpr int R = decltype(rows_of_run)::value;
