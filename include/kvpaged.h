@@ -778,7 +778,7 @@ size_t attn_decode_quant_workspace_size(int num_seqs, int num_heads, int num_kv_
  * attn_decode_quant_workspace_size() bytes.  Scales of tokens within a context
  * are finite and not negative (kv_quant_store's are); codes and scales beyond a
  * context may be anything.  A head whose query holds an infinity or a NaN gets
- * NaN.  Calls that may run at the same time need workspaces of their own.
+ * NaN, and so does every head over a key with a NaN.  Calls that may run at the same time need workspaces of their own.
  * Supported: num_kv_heads in {1, 2, 4, 8}; num_heads / num_kv_heads in
  * {1, 2, 4, 8}; num_seqs * max_blocks_per_seq * ceil(block_size / 16) below 2^31.
  */
